@@ -241,6 +241,144 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
                                 uint32_t *d_counts, uint32_t *d_offsets, ss_stream_t stream);
 
 /*
+ * A paged key-value cache, with the attention of one new token per sequence
+ * that reads it and the eviction that compacts it.
+ *
+ * The pool (ss_kv_pages): num_pages pages, each holding page_size tokens of
+ * every key-value head.  Element d of the key of head h at slot s of page p
+ * is k[p * page_stride + h * head_stride + s * slot_stride + d] (strides in
+ * elements; [page][head][slot][dim] and [page][slot][head][dim] are both
+ * strides of this), and the same offset in v.  An SS_E4M3 cache holds
+ * value / scale: k_scale and v_scale are device arrays of kv_heads floats
+ * (NULL: 1), and must be NULL for the other types.  `weight` (device,
+ * contiguous [page][head][slot] floats, NULL: none) holds the attention that
+ * each cached token has gathered.
+ *
+ * The sequences (ss_kv_table): position i of sequence b lives at slot
+ * i % page_size of page pages[b * row_stride + i / page_size].  lens[b] is
+ * its length; entries of `pages` past the length are not read.  max_len is
+ * an upper bound on the lengths known to the host (0: max_pages *
+ * page_size); it sizes launches and scratch.
+ *
+ * Shared rules:
+ *   - head_dim is at most 256 and head_dim * element size a multiple of 16
+ *     bytes, as are the strides; k, v and the rows of new tokens, q and out
+ *     are 16-byte aligned (evict and append take up to 2^20 kv_heads *
+ *     batch rows; attend 2^31 of any product that it forms).
+ *   - Lengths and page numbers are device data, checked on the device: a
+ *     length below 0 or above max_len (or max_pages * page_size) is clamped,
+ *     a page number outside [0, num_pages) is not followed, and either is
+ *     reported by the next ss_stream_status() as SS_ERR_INVALID_ARG with the
+ *     sequence in *failing_tile; the outputs of that sequence are then
+ *     undefined, and nothing outside the arrays is touched.
+ *   - batch == 0 is a no-op.  Results do not change from run to run.
+ */
+typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2 } ss_elem;
+
+typedef struct ss_kv_pages {
+    ss_elem type;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int64_t num_pages;
+    void *k;
+    void *v;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+    const float *k_scale;
+    const float *v_scale;
+    float *weight;
+} ss_kv_pages;
+
+typedef struct ss_kv_table {
+    const int32_t *pages;
+    int64_t row_stride;
+    int32_t max_pages;
+    int32_t batch;
+    int32_t *lens;
+    int32_t max_len;
+} ss_kv_table;
+
+/*
+ * Appends new tokens' keys and values.  Sequence b has the new tokens
+ * offsets[b] .. offsets[b+1] - 1 of k_new and v_new (offsets NULL: one token
+ * each, token b), and lens[b] already counts them: they become its last
+ * positions, in order.  Token t's row of head h starts at k_new + t *
+ * token_stride + h * head_stride (elements of `type`, SS_BF16 or SS_F16;
+ * the strides serve a fused projection's output in place).  The cache holds
+ * `type`, or SS_E4M3: each element is then x / scale[h] (fp32 division)
+ * clamped to [-448, 448] and rounded to the nearest e4m3, ties to even; NaN
+ * stays NaN.  The new slots' weights become 0 (where weight is not NULL).
+ *   offsets  device, batch + 1 int32, offsets[0] = 0, non-decreasing, or NULL.
+ *   tokens   offsets[batch]; batch where offsets is NULL.
+ * No two sequences may share a page that is appended to.
+ */
+ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_elem type, const void *k_new,
+                       const void *v_new, int64_t token_stride, int64_t head_stride, const int32_t *offsets,
+                       size_t tokens, ss_stream_t stream);
+
+/*
+ * Attention of one token per sequence over its cached positions.  Query head
+ * j of q_heads = group * kv_heads reads key-value head j / group.  With s(p)
+ * = scale * (q . k(p)) over the visible positions {p < len : window <= 0 or p
+ * < sinks or p >= len - window}:
+ *   out = sum_p exp(s(p) - lse) v(p),   lse = log sum_p exp(s(p)),
+ *   weight_out(h, p) = weight_in(h, p) + sum over h's query heads of
+ *                      exp(s(p) - lse), for every position p < len.
+ * A row with no visible position, or all of whose scores are -inf, gives
+ * out = 0 and lse = -inf and adds no weight.  A NaN in a visible row spreads
+ * as in the formula; rows that are not visible are not read.
+ *   type        of q and out, SS_BF16 or SS_F16: the cache's, or either with
+ *               an SS_E4M3 cache.
+ *   q, out      row (b, j) at b * seq_stride + j * head_stride (each its own
+ *               strides); must not overlap each other or the cache.
+ *   lse         device, batch * q_heads floats (natural logarithm), or NULL.
+ *   weight_out  device, the layout of ss_kv_pages.weight, or NULL: no weights.
+ *   weight_in   the same layout, or NULL (zeros).  weight_in == weight_out
+ *               accumulates in place; a partial overlap is not allowed.
+ * Scores, softmax and sums are fp32; out is rounded once.
+ */
+typedef struct ss_kv_attention {
+    ss_elem type;
+    int32_t q_heads;
+    const void *q;
+    int64_t q_seq_stride;
+    int64_t q_head_stride;
+    void *out;
+    int64_t out_seq_stride;
+    int64_t out_head_stride;
+    float scale;
+    int32_t window;
+    int32_t sinks;
+    float *lse;
+    const float *weight_in;
+    float *weight_out;
+} ss_kv_attention;
+ss_status ss_kv_attend(const ss_kv_pages *cache, const ss_kv_table *seqs, const ss_kv_attention *args,
+                       ss_stream_t stream);
+
+/*
+ * Evicts the least attended tokens: an order-preserving compaction of every
+ * (sequence, head) of `src` into the pages of `dst`.  Of a sequence of n
+ * positions m = min(n, keep) stay: the first `sinks`, the last `recent`, and
+ * of the others those of the largest src weight; equal weights go to the
+ * lower position first (-0 equals +0; NaN ranks below -inf).  Kept row i, in
+ * the order of positions, goes to position i of the destination: k, v (bit
+ * for bit) and, where dst->weight is not NULL, the weight.  Heads choose
+ * independently.  dst_seqs->lens receives m.  `dst` has src's type, heads,
+ * head_dim and scales (not moved); its page_size and strides are its own,
+ * and it may be the same pool.  The destination pages must not be pages that
+ * any sequence of src reads; source pages may be shared.
+ *   kept  device, batch x kv_heads x keep int32, or NULL: the source position
+ *         of each kept row, -1 from m on.
+ *   0 <= sinks, 0 <= recent, sinks + recent <= keep, 1 <= keep.
+ */
+ss_status ss_kv_evict(const ss_kv_pages *src, const ss_kv_table *src_seqs, const ss_kv_pages *dst,
+                      const ss_kv_table *dst_seqs, int32_t keep, int32_t sinks, int32_t recent, int32_t *kept,
+                      ss_stream_t stream);
+
+/*
  * Generic scan entry: dtype, inclusive (0/1) and algorithm chosen at run
  * time.  Same argument rules as the named scans.  The reduce-then-scan
  * algorithms ("Prefix sum and other parallel patterns", three passes with

@@ -40,6 +40,8 @@ SS_ALGO_RTS_BLELLOCH_PAD2 = 4
 
 SS_WIDE_U32_U64, SS_WIDE_I32_I64, SS_WIDE_I64, SS_WIDE_F64 = 0, 1, 2, 3
 
+SS_BF16, SS_F16, SS_E4M3 = 0, 1, 2
+
 
 class LibraryMissing(ImportError):
     pass
@@ -50,6 +52,27 @@ class StreamScanError(RuntimeError):
         super().__init__(f"{where}: status {status} ({detail})")
         self.status = status
         self.detail = detail
+
+
+class _KvPages(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p)]
+
+
+class _KvTable(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("lens", ctypes.c_void_p), ("max_len", ctypes.c_int32)]
+
+
+class _KvAttention(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("q_heads", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_seq_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_seq_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("lse", ctypes.c_void_p),
+                ("weight_in", ctypes.c_void_p), ("weight_out", ctypes.c_void_p)]
 
 
 _lib = None
@@ -96,6 +119,9 @@ def _declare(lib):
         "ss_scan_temp_bytes": [SZ, ctypes.POINTER(SZ)],
         "ss_scan_ws": [I, I, P, P, SZ, P, SZ, P],
         "ss_temp_status": [P, P, ctypes.POINTER(I64)],
+        "ss_kv_append": [P, P, I, P, P, I64, I64, P, SZ, P],
+        "ss_kv_attend": [P, P, P, P],
+        "ss_kv_evict": [P, P, P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -433,3 +459,119 @@ def ss_temp_status(temp, stream=None):
         stream = torch.cuda.current_stream()
     st = lib().ss_temp_status(_addr(temp), _stream(stream), ctypes.byref(tile))
     return st, tile.value
+
+
+def _elem(t) -> int:
+    """The library's element type of a torch tensor."""
+    name = str(t.dtype)
+    kinds = {"torch.bfloat16": SS_BF16, "torch.float16": SS_F16, "torch.float8_e4m3fn": SS_E4M3}
+    if name not in kinds:
+        raise TypeError(f"{name} is not a type of the key-value cache calls (bfloat16, float16, float8_e4m3fn)")
+    return kinds[name]
+
+
+def _like(name: str, t, shape, dtype: str):
+    """Checks an optional tensor argument's shape, type and (for contiguous
+    arguments) layout; the C ABI sees only addresses."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or str(t.dtype) != "torch." + dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{str(t.dtype)[6:]} {tuple(t.shape)}")
+
+
+class KVPages:
+    """The pool of a paged key-value cache (ss_kv_pages).
+
+    k, v    CUDA tensors of shape (num_pages, kv_heads, page_size, head_dim),
+            bfloat16, float16 or float8_e4m3fn, with the same strides (any
+            order of the first three dimensions; the last one contiguous).
+    weight  float32 (num_pages, kv_heads, page_size), contiguous, or None.
+    k_scale, v_scale  float32 (kv_heads,), for a float8 cache, or None (1).
+    The tensors are kept alive and may be updated in place.
+    """
+
+    def __init__(self, k, v, weight=None, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-dimensional, of one shape and type")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and a contiguous last dimension")
+        pages, heads, page, dim = k.shape
+        _like("weight", weight, (pages, heads, page), "float32")
+        _like("k_scale", k_scale, (heads,), "float32")
+        _like("v_scale", v_scale, (heads,), "float32")
+        self.k, self.v, self.weight, self.k_scale, self.v_scale = k, v, weight, k_scale, v_scale
+        self.kv_heads, self.head_dim = heads, dim
+        self._c = _KvPages(_elem(k), heads, dim, page, pages, _addr(k), _addr(v), k.stride(0), k.stride(1),
+                           k.stride(2), _addr(k_scale), _addr(v_scale), _addr(weight))
+        self._ref = ctypes.addressof(self._c)
+
+
+class KVTable:
+    """The sequences of a paged key-value cache (ss_kv_table).
+
+    pages    int32 (batch, max_pages): page numbers, rows may be strided.
+    lens     int32 (batch,): lengths, read by every call at the time it runs.
+    max_len  an upper bound on the lengths (default: max_pages * page_size);
+             set it to the longest length in use to size launches by it.
+    """
+
+    def __init__(self, pages, lens, max_len=None):
+        if pages.dim() != 2 or str(pages.dtype) != "torch.int32" or (pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise ValueError("pages must be a 2-dimensional int32 tensor with contiguous rows")
+        _like("lens", lens, (pages.shape[0],), "int32")
+        self.pages, self.lens, self.batch = pages, lens, pages.shape[0]
+        self._c = _KvTable(_addr(pages), pages.stride(0), pages.shape[1], pages.shape[0], _addr(lens),
+                           0 if max_len is None else max_len)
+        self._ref = ctypes.addressof(self._c)
+
+    @property
+    def max_len(self):
+        return self._c.max_len
+
+    @max_len.setter
+    def max_len(self, n):
+        self._c.max_len = n
+
+
+def ss_kv_append(cache: KVPages, seqs: KVTable, k_new, v_new, offsets=None, stream=None) -> None:
+    """Writes new tokens' rows, (tokens, kv_heads, head_dim) tensors of one
+    type and strides, to the last positions of their sequences; offsets is
+    int32 (batch + 1,), or None for one token per sequence."""
+    if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype or k_new.stride() != v_new.stride():
+        raise ValueError("k_new and v_new must be 3-dimensional, of one shape, type and strides")
+    if tuple(k_new.shape[1:]) != (cache.kv_heads, cache.head_dim) or k_new.stride(2) != 1:
+        raise ValueError(f"k_new must be (tokens, {cache.kv_heads}, {cache.head_dim}) with a contiguous last dimension")
+    _like("offsets", offsets, (seqs.batch + 1,), "int32")
+    _check(lib().ss_kv_append(cache._ref, seqs._ref, _elem(k_new), k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
+                              k_new.stride(1), _addr(offsets), k_new.shape[0], _stream(stream, k_new)), "ss_kv_append")
+
+
+def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int = 0, sinks: int = 0, lse=None,
+                 weight_in=None, weight_out=None, stream=None) -> None:
+    """Attention of q, (batch, q_heads, head_dim), over the cached positions
+    into out; scale defaults to head_dim ** -0.5.  lse: float32 (batch,
+    q_heads).  weight_out, weight_in: float32 tensors of the pool's weight
+    shape (weight_out = weight_in = cache.weight accumulates in place)."""
+    if q.dim() != 3 or q.shape != out.shape or q.dtype != out.dtype or q.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("q and out must be 3-dimensional, of one shape and type, with a contiguous last dimension")
+    if q.shape[0] != seqs.batch or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be ({seqs.batch}, q_heads, {cache.head_dim})")
+    _like("lse", lse, q.shape[:2], "float32")
+    if weight_in is not None or weight_out is not None:
+        shape = tuple(cache.k.shape[:3])
+        _like("weight_in", weight_in, shape, "float32")
+        _like("weight_out", weight_out, shape, "float32")
+    a = _KvAttention(_elem(q), q.shape[1], q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0),
+                     out.stride(1), cache.head_dim ** -0.5 if scale is None else scale, window, sinks, _addr(lse),
+                     _addr(weight_in), _addr(weight_out))
+    _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a), _stream(stream, q)), "ss_kv_attend")
+
+
+def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable, keep: int, sinks: int = 0,
+                recent: int = 0, kept=None, stream=None) -> None:
+    """Moves the kept rows of every sequence and head into dst's pages and
+    their number into dst_seqs.lens; kept: int32 (batch, kv_heads, keep)."""
+    _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32")
+    _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, _addr(kept),
+                             _stream(stream, src.k)), "ss_kv_evict")

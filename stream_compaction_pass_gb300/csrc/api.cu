@@ -2,6 +2,7 @@
 // per-(device, stream) workspaces, device status read-back and the
 // host-memory pipeline.  All arithmetic runs in the kernels of scan.cu,
 // compact.cu and ablations.cu.
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstring>
@@ -79,6 +80,8 @@ struct Workspace {
     size_t totals_cap = 0;  // bytes
     uint32_t* moe_acc = nullptr;  // MoE bin accumulator, kept all-zero between launches
     size_t moe_acc_cap = 0;       // words
+    void* kv = nullptr;           // scratch of the key-value cache calls
+    size_t kv_cap = 0;            // bytes
     uint64_t launches_since_clear = 0;
     HostPipe pipe;
     std::mutex pipe_mu;  // one host pipeline at a time per workspace
@@ -181,6 +184,22 @@ ss_status ensure_moe_acc(Workspace* w, size_t words) {
     e = cudaMemsetAsync(w->moe_acc, 0, cap * 4, w->stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     w->moe_acc_cap = cap;
+    return SS_OK;
+}
+
+ss_status ensure_kv(Workspace* w, size_t bytes) {
+    if (bytes <= w->kv_cap) return SS_OK;
+    if (w->kv) {
+        cudaError_t e = cudaFreeAsync(w->kv, w->stream);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync");
+        w->kv = nullptr;
+        w->kv_cap = 0;
+    }
+    cudaError_t e = cudaMallocAsync(&w->kv, bytes, w->stream);
+    if (e != cudaSuccess)
+        return e == cudaErrorMemoryAllocation ? fail(SS_ERR_NO_MEMORY, "key-value cache scratch")
+                                              : cuda_fail(e, "cudaMallocAsync");
+    w->kv_cap = bytes;
     return SS_OK;
 }
 
@@ -385,9 +404,175 @@ ss_status read_status_words(uint32_t* d_status, cudaStream_t s, int64_t* failing
     return SS_OK;
 }
 
+// ---- the paged key-value cache ----
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The public description as the kernels take it; `name` says which argument
+// an error is about.
+ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
+    const std::string who(name);
+    if (p == nullptr) return fail(SS_ERR_INVALID_ARG, who + " is null");
+    if (p->type != SS_BF16 && p->type != SS_F16 && p->type != SS_E4M3)
+        return fail(SS_ERR_UNSUPPORTED, who + ": unknown element type");
+    const int64_t size = p->type == SS_E4M3 ? 1 : 2;
+    if (p->kv_heads < 1 || p->page_size < 1 || p->num_pages < 1)
+        return fail(SS_ERR_INVALID_ARG, who + ": kv_heads, page_size and num_pages must be positive");
+    if (p->num_pages > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, who + ": num_pages must be below 2^31");
+    if (p->head_dim < 1 || p->head_dim > 256 || p->head_dim * size % 16 != 0)
+        return fail(SS_ERR_INVALID_ARG, who + ": head_dim must be at most 256 and a whole number of 16-byte vectors");
+    if (!p->k || !p->v) return fail(SS_ERR_INVALID_ARG, who + ": null k or v");
+    if (!aligned16(p->k) || !aligned16(p->v)) return fail(SS_ERR_INVALID_ARG, who + ": k and v must be 16-byte aligned");
+    if (p->page_stride * size % 16 || p->head_stride * size % 16 || p->slot_stride * size % 16)
+        return fail(SS_ERR_INVALID_ARG, who + ": strides must be multiples of 16 bytes");
+    if (p->page_stride < 0 || p->head_stride < 0 || p->slot_stride < 0)
+        return fail(SS_ERR_INVALID_ARG, who + ": strides must not be negative");
+    if (p->type != SS_E4M3 && (p->k_scale || p->v_scale))
+        return fail(SS_ERR_INVALID_ARG, who + ": scales belong to an SS_E4M3 cache");
+    if (!aligned4(p->k_scale) || !aligned4(p->v_scale) || !aligned4(p->weight))
+        return fail(SS_ERR_INVALID_ARG, who + ": scales and weight must be 4-byte aligned");
+    *out = ss::KvPages{static_cast<ss::KvElem>(p->type), p->kv_heads, p->head_dim, p->page_size, p->num_pages,
+                       static_cast<char*>(p->k), static_cast<char*>(p->v), p->page_stride, p->head_stride,
+                       p->slot_stride, p->k_scale, p->v_scale, p->weight};
+    return SS_OK;
+}
+
+ss_status kv_table(const ss_kv_table* t, const ss::KvPages& c, const char* name, ss::KvTable* out) {
+    const std::string who(name);
+    if (t == nullptr) return fail(SS_ERR_INVALID_ARG, who + " is null");
+    if (t->batch < 0 || t->max_pages < 0 || t->max_len < 0 || t->row_stride < 0)
+        return fail(SS_ERR_INVALID_ARG, who + ": negative batch, max_pages, max_len or row_stride");
+    if (t->batch > 0 && (!t->lens || (t->max_pages > 0 && !t->pages)))
+        return fail(SS_ERR_INVALID_ARG, who + ": null pages or lens");
+    if (!aligned4(t->pages) || !aligned4(t->lens))
+        return fail(SS_ERR_INVALID_ARG, who + ": pages and lens must be 4-byte aligned");
+    int64_t held = (int64_t)t->max_pages * c.page_size;
+    if (t->max_len > 0 && t->max_len < held) held = t->max_len;
+    if (held > 0x7fffffff - 4096) return fail(SS_ERR_INVALID_ARG, who + ": max_len must be below 2^31 - 4096");
+    *out = ss::KvTable{t->pages, t->row_stride, t->max_pages, t->batch, t->lens, (int)held};
+    return SS_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_elem type, const void* k_new,
+                       const void* v_new, int64_t token_stride, int64_t head_stride, const int32_t* offsets,
+                       size_t tokens, ss_stream_t stream) try {
+    ss::KvPages c;
+    ss::KvTable t;
+    ss_status st = kv_pages(cache, "cache", &c);
+    if (st != SS_OK) return st;
+    st = kv_table(seqs, c, "seqs", &t);
+    if (st != SS_OK) return st;
+    if (type != SS_BF16 && type != SS_F16) return fail(SS_ERR_UNSUPPORTED, "new tokens must be SS_BF16 or SS_F16");
+    if (cache->type != SS_E4M3 && cache->type != type)
+        return fail(SS_ERR_INVALID_ARG, "new tokens must have the cache's type, or the cache be SS_E4M3");
+    if (offsets == nullptr && tokens != (size_t)t.batch)
+        return fail(SS_ERR_INVALID_ARG, "without offsets there is one token for each sequence");
+    if (!aligned4(offsets)) return fail(SS_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
+    if (tokens > 0x7fffffff / (size_t)c.kv_heads) return fail(SS_ERR_INVALID_ARG, "tokens * kv_heads must be below 2^31");
+    if (tokens == 0 || t.batch == 0) return SS_OK;
+    if (!k_new || !v_new) return fail(SS_ERR_INVALID_ARG, "null k_new or v_new");
+    if (!aligned16(k_new) || !aligned16(v_new)) return fail(SS_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8)
+        return fail(SS_ERR_INVALID_ARG, "token_stride and head_stride must be non-negative multiples of 16 bytes");
+    if (c.head_dim % 8) return fail(SS_ERR_INVALID_ARG, "head_dim must be a multiple of 8");
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w);
+    if (st != SS_OK) return st;
+    cudaError_t e = ss::launch_kv_append(c, t, static_cast<ss::KvElem>(type), k_new, v_new, token_stride, head_stride,
+                                         offsets, (int64_t)tokens, ws_status(w), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "append launch");
+} catch (...) {
+    return SS_ERR_NO_MEMORY;
+}
+
+ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const ss_kv_attention* args,
+                       ss_stream_t stream) try {
+    ss::KvPages c;
+    ss::KvTable t;
+    ss_status st = kv_pages(cache, "cache", &c);
+    if (st != SS_OK) return st;
+    st = kv_table(seqs, c, "seqs", &t);
+    if (st != SS_OK) return st;
+    if (args == nullptr) return fail(SS_ERR_INVALID_ARG, "args is null");
+    const ss_kv_attention& a = *args;
+    if (a.type != SS_BF16 && a.type != SS_F16) return fail(SS_ERR_UNSUPPORTED, "q and out must be SS_BF16 or SS_F16");
+    if (cache->type != SS_E4M3 && cache->type != a.type)
+        return fail(SS_ERR_INVALID_ARG, "q must have the cache's type, or the cache be SS_E4M3");
+    if (a.q_heads < 1 || a.q_heads % c.kv_heads) return fail(SS_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
+    if (a.q_heads / c.kv_heads > 128) return fail(SS_ERR_INVALID_ARG, "at most 128 query heads per key-value head");
+    if (a.sinks < 0) return fail(SS_ERR_INVALID_ARG, "sinks must not be negative");
+    if (!(a.scale - a.scale == 0.0f)) return fail(SS_ERR_INVALID_ARG, "scale must be finite");
+    if (a.weight_in && !a.weight_out) return fail(SS_ERR_INVALID_ARG, "weight_in without weight_out");
+    if (!aligned4(a.lse) || !aligned4(a.weight_in) || !aligned4(a.weight_out))
+        return fail(SS_ERR_INVALID_ARG, "lse and weights must be 4-byte aligned");
+    const size_t pool = (size_t)c.num_pages * c.kv_heads * c.page_size * 4;
+    if (a.weight_in && a.weight_in != a.weight_out && overlaps(a.weight_in, pool, a.weight_out, pool))
+        return fail(SS_ERR_INVALID_ARG, "weight_in and weight_out partially overlap");
+    if (t.batch == 0) return SS_OK;
+    if (!a.q || !a.out) return fail(SS_ERR_INVALID_ARG, "null q or out");
+    if (!aligned16(a.q) || !aligned16(a.out)) return fail(SS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    const int64_t strides[] = {a.q_seq_stride, a.q_head_stride, a.out_seq_stride, a.out_head_stride};
+    for (int64_t x : strides)
+        if (x < 0 || x % 8) return fail(SS_ERR_INVALID_ARG, "strides of q and out must be non-negative multiples of 16 bytes");
+    const size_t qb = (size_t)((t.batch - 1) * strides[0] + (a.q_heads - 1) * strides[1] + c.head_dim) * 2;
+    const size_t ob = (size_t)((t.batch - 1) * strides[2] + (a.q_heads - 1) * strides[3] + c.head_dim) * 2;
+    if (overlaps(a.q, qb, a.out, ob)) return fail(SS_ERR_INVALID_ARG, "q and out overlap");
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w);
+    if (st != SS_OK) return st;
+    const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, a.q_seq_stride, a.q_head_stride, a.out,
+                            a.out_seq_stride, a.out_head_stride, a.scale, a.window, a.sinks, a.lse, a.weight_in,
+                            a.weight_out};
+    cudaError_t e = ss::launch_kv_attend(c, t, k, ws_status(w), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "attention launch");
+} catch (...) {
+    return SS_ERR_NO_MEMORY;
+}
+
+ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const ss_kv_pages* dst,
+                      const ss_kv_table* dst_seqs, int32_t keep, int32_t sinks, int32_t recent, int32_t* kept,
+                      ss_stream_t stream) try {
+    ss::KvPages c, d;
+    ss::KvTable t, dt;
+    ss_status st = kv_pages(src, "src", &c);
+    if (st != SS_OK) return st;
+    st = kv_table(src_seqs, c, "src_seqs", &t);
+    if (st != SS_OK) return st;
+    st = kv_pages(dst, "dst", &d);
+    if (st != SS_OK) return st;
+    st = kv_table(dst_seqs, d, "dst_seqs", &dt);
+    if (st != SS_OK) return st;
+    if (c.type != d.type || c.kv_heads != d.kv_heads || c.head_dim != d.head_dim)
+        return fail(SS_ERR_INVALID_ARG, "dst must have src's type, kv_heads and head_dim");
+    if (t.batch != dt.batch) return fail(SS_ERR_INVALID_ARG, "src_seqs and dst_seqs must have the same batch");
+    if (c.weight == nullptr) return fail(SS_ERR_INVALID_ARG, "src has no weights to evict by");
+    if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep)
+        return fail(SS_ERR_INVALID_ARG, "keep must be positive and at least sinks + recent, neither of them negative");
+    if (!aligned4(kept)) return fail(SS_ERR_INVALID_ARG, "kept must be 4-byte aligned");
+    if ((int64_t)t.batch * c.kv_heads > 1 << 20) return fail(SS_ERR_INVALID_ARG, "batch * kv_heads must be at most 2^20");
+    if (t.batch == 0) return SS_OK;
+    if (overlaps(t.lens, (size_t)t.batch * 4, dt.lens, (size_t)t.batch * 4))
+        return fail(SS_ERR_INVALID_ARG, "the lengths of src_seqs and dst_seqs overlap");
+    if (std::min(keep, t.max_len) > (int64_t)dt.max_pages * d.page_size)
+        return fail(SS_ERR_INVALID_ARG, "dst_seqs cannot hold the kept positions");
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w);
+    if (st != SS_OK) return st;
+    if (kept == nullptr) {
+        st = ensure_kv(w, (size_t)t.batch * c.kv_heads * keep * 4);
+        if (st != SS_OK) return st;
+        kept = static_cast<int32_t*>(w->kv);
+    }
+    cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, ws_status(w), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "eviction launch");
+} catch (...) {
+    return SS_ERR_NO_MEMORY;
+}
 
 ss_status scan_inclusive_i32(const int32_t* in, int32_t* out, size_t n, ss_stream_t stream) {
     return scan_lookback(Dtype::I32, true, in, out, n, nullptr, nullptr, (cudaStream_t)stream);
@@ -729,6 +914,10 @@ ss_status ss_stream_status(ss_stream_t stream, int64_t* failing_tile) {
         if (failing_tile) *failing_tile = words[1] ? (int64_t)words[1] - 1 : -1;
         return fail(SS_ERR_LOOKBACK_TIMEOUT, "a look-back wait ran out");
     }
+    if (words[0] & ss::kErrKvTable) {
+        if (failing_tile) *failing_tile = words[1] ? (int64_t)words[1] - 1 : -1;
+        return fail(SS_ERR_INVALID_ARG, "a length or page number of a key-value cache was out of range");
+    }
     return SS_OK;
 }
 
@@ -869,6 +1058,7 @@ void ss_shutdown(void) {
         if (w->desc) cudaFree(w->desc);
         if (w->totals) cudaFree(w->totals);
         if (w->moe_acc) cudaFree(w->moe_acc);
+        if (w->kv) cudaFree(w->kv);
         if (w->header) cudaFree(w->header);
         HostPipe& p = w->pipe;
         if (p.ready) {

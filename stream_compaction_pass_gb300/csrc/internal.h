@@ -14,6 +14,7 @@ enum class Dtype : int { I32 = 0, U32 = 1, F32 = 2 };
 constexpr uint32_t kErrLookbackTimeout = 1u;
 constexpr uint32_t kErrCounter = 2u;      // a CTA claimed a tile id past the grid
 constexpr uint32_t kErrBulkTimeout = 4u;  // a bulk copy into shared memory never completed
+constexpr uint32_t kErrKvTable = 8u;      // a length or page number of a key-value cache out of range
 
 // Device pointers into a workspace for the single-pass kernels.
 struct LookbackWs {
@@ -163,6 +164,48 @@ uint32_t moe_grid(size_t m, int sms);
 uint32_t reduce_grid(int sms);
 cudaError_t launch_reduce_sum(Dtype dt, const void* in, size_t n, void* partials, uint32_t* ticket, void* total,
                               uint32_t grid, cudaStream_t s);
+
+// The paged key-value cache (kv_append.cu, kv_attend.cu, kv_evict.cu): the
+// public descriptions as the kernels take them, checked by api.cu.  Strides
+// are in elements; max_len is resolved (never 0 unless nothing can be held).
+enum class KvElem : int { BF16 = 0, F16 = 1, E4M3 = 2 };
+inline int kv_elem_bytes(KvElem t) { return t == KvElem::E4M3 ? 1 : 2; }
+struct KvPages {
+    KvElem type;
+    int kv_heads, head_dim, page_size;
+    int64_t num_pages;
+    char *k, *v;
+    int64_t page_stride, head_stride, slot_stride;
+    const float *k_scale, *v_scale;
+    float* weight;
+};
+struct KvTable {
+    const int32_t* pages;
+    int64_t row_stride;
+    int max_pages, batch;
+    int32_t* lens;
+    int max_len;
+};
+struct KvAttention {
+    KvElem type;
+    int q_heads;
+    const void* q;
+    int64_t q_seq_stride, q_head_stride;
+    void* out;
+    int64_t out_seq_stride, out_head_stride;
+    float scale;
+    int window, sinks;
+    float* lse;
+    const float* weight_in;
+    float* weight_out;
+};
+cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, const void* k_new, const void* v_new,
+                             int64_t token_stride, int64_t head_stride, const int32_t* offsets, int64_t tokens,
+                             uint32_t* status, cudaStream_t s);
+cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, uint32_t* status,
+                             cudaStream_t s);
+cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
+                            int sinks, int recent, int32_t* kept, uint32_t* status, cudaStream_t s);
 
 // Ablations (reduce-then-scan, three kernels).  `totals` holds one value
 // per 4096-element tile.  tile_scan: 0 = register/shuffle tile scan,

@@ -1,0 +1,53 @@
+// kv.cuh -- what the paged key-value cache kernels share: the cache and its
+// page tables as the kernels see them, checked look-ups, and element types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "lookback.cuh"
+
+namespace ss {
+
+// The length of sequence b as every kernel reads it: clamped to what the
+// table can hold, and reported where it had to be.
+__device__ __forceinline__ int kv_len(const KvTable& t, int b, uint32_t* status) {
+    const int n = t.lens[b];
+    const int m = min(max(n, 0), t.max_len);
+    if (m != n) record_error(status, kErrKvTable, (uint32_t)b);
+    return m;
+}
+
+// The page of position `pos` of sequence b, or -1 (reported) if the table
+// names a page outside the pool.
+__device__ __forceinline__ int kv_page(const KvTable& t, int64_t num_pages, int b, int index, uint32_t* status) {
+    const int p = t.pages[(int64_t)b * t.row_stride + index];
+    if (p >= 0 && p < num_pages) return p;
+    record_error(status, kErrKvTable, (uint32_t)b);
+    return -1;
+}
+
+// A 16-byte vector through the non-coherent path, and one streamed out.
+__device__ __forceinline__ uint4 ldg_vec(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void stg_vec(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_fp8_e4m3 x) { return (float)x; }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// Weights in the order of eviction as 32-bit keys, best first: a larger
+// weight has the smaller key, -0 and +0 the same one, NaN the last.  Key 0 is
+// no number's: it stands for the positions that stay whatever their weight.
+__device__ __forceinline__ uint32_t evict_key(float w) {
+    if (w != w) return 0xffffffffu;
+    uint32_t u = __float_as_uint(w);
+    if (u == 0x80000000u) u = 0;
+    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // ascending in the weight
+    return ~u;
+}
+
+}  // namespace ss

@@ -1,0 +1,518 @@
+"""The paged key-value cache (append, attend, evict) against the definitions
+in 64 bits (tests/kv_helpers.py).
+
+Tolerances.  u = 2^-8 (bf16: 7 fraction bits) or 2^-11 (fp16: 10) is half a
+unit in the last place of the output type.  A score is a sum of `dim` products in fp32, so it is off
+by at most e = dim * 2^-23 * scale * sum |q k| (+ 1e-6 for the scaling), and a
+softmax weight by a factor 1 +- (2 e + 4e-6) with the exponential's and the
+sums' rounding.  out is then within u |out| + (2 e + 4e-6 + r) max |v| of the
+formula, where r bounds how weights are rounded for the product with v: 2^-16
+for 16-bit caches, 2^-11 for 8-bit ones.  Moved rows, kept positions and
+quantised values are exact."""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from kv_helpers import Cache, attend_reference, e4m3_reference, evict_reference, torch_type, visible
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import stream_compaction_pass_gb300 as m
+    return m
+
+
+def ok(ss, stream=None):
+    st, where = ss.ss_stream_status(stream=stream)
+    assert st == ss.SS_OK, (st, where, ss.ss_last_error_detail())
+
+
+def run_attend(ss, c, group, qkind, window=0, sinks=0, weights="add", scale=None, seed=5, strided=False, lse=True,
+               qscale=1.5):
+    import torch
+    gen = torch.Generator().manual_seed(seed)
+    B, QH = len(c.lens), c.heads * group
+    q_host = (torch.randn(B, QH, c.dim, generator=gen) * qscale).to(torch_type(qkind))
+    if strided:  # the query part of a fused projection, out inside a wider buffer
+        q = torch.full((B, QH + 5, c.dim + 16), math.nan, dtype=q_host.dtype, device="cuda")[:, :QH, :c.dim]
+        q.copy_(q_host)
+        wide = torch.full((QH, B, c.dim + 8), 7.0, dtype=q_host.dtype, device="cuda")
+        out = wide.transpose(0, 1)[:, :, :c.dim]
+    else:
+        q = q_host.cuda()
+        wide = None
+        out = torch.full_like(q, math.nan)
+    pages, table = c.ss(ss)
+    d_lse = torch.full((B, QH), math.nan, device="cuda") if lse else None
+    w_in = w_out = None
+    if weights == "add":
+        w_in = w_out = c.weight.clone()
+    elif weights == "new":
+        w_out = torch.full_like(c.weight, -3.0)
+    elif weights == "apart":
+        w_in, w_out = c.weight, torch.full_like(c.weight, -3.0)
+    ss.ss_kv_attend(pages, table, q, out, scale=scale, window=window, sinks=sinks, lse=d_lse, weight_in=w_in, weight_out=w_out)
+    ok(ss)
+    if wide is not None:
+        assert bool((wide[:, :, c.dim:] == 7.0).all()), "a store outside out's rows"
+    return q_host.float().numpy(), out.float().cpu().numpy(), None if d_lse is None else d_lse.cpu().numpy(), \
+        None if w_out is None else w_out.cpu().numpy()
+
+
+def check_attend(ss, c, group, qkind, window=0, sinks=0, weights="add", scale=None, **kw):
+    q, out, lse, w = run_attend(ss, c, group, qkind, window, sinks, weights, scale, **kw)
+    sc = c.dim ** -0.5 if scale is None else scale
+    want, want_lse, added = attend_reference(c, q, sc, window, sinks)
+    u = 2.0 ** -8 if qkind == "bf16" else 2.0 ** -11
+    r = 2.0 ** -11 if c.kind == "e4m3" else 2.0 ** -16
+    for b, n in enumerate(c.lens):
+        see = visible(n, window, sinks)
+        for j in range(out.shape[1]):
+            h = j // group
+            if not see.any():
+                assert (out[b, j] == 0).all() and (lse is None or lse[b, j] == -np.inf)
+                continue
+            k = np.abs(c.rows(c.k_host, b, h)[see]) * c.scale(c.ks, h)
+            v = np.abs(c.rows(c.v_host, b, h)[see]) * c.scale(c.vs, h)
+            e = c.dim * 2.0 ** -23 * abs(sc) * float((k @ np.abs(q[b, j]).astype(np.float64)).max()) + 1e-6
+            tol = u * np.abs(want[b, j]) + (2 * e + 4e-6 + r) * v.max()
+            bad = np.abs(out[b, j] - want[b, j]) > tol
+            assert not bad.any(), (b, j, n, float(np.abs(out[b, j] - want[b, j]).max()), float(tol.max()))
+            if lse is not None:
+                assert abs(lse[b, j] - want_lse[b, j]) <= e + 1e-6 * (1 + abs(want_lse[b, j])), (b, j, lse[b, j], want_lse[b, j])
+    if w is not None:
+        start = {"add": c.w_host, "apart": c.w_host, "new": np.zeros_like(c.w_host)}[weights]
+        kmax = np.nanmax(np.abs(c.k_host)) * (1.0 if c.ks is None else float(c.ks.max()))
+        e = c.dim * 2.0 ** -23 * abs(sc) * float(np.abs(q).sum(-1).max()) * kmax + 1e-6
+        for b in range(len(c.lens)):
+            for h in range(c.heads):
+                got, base, add = c.rows(w, b, h), c.rows(start, b, h), c.rows(added, b, h)
+                assert (np.abs(got - (base + add)) <= (2 * e + 4e-6) * add + 2.0 ** -22 * (base + add)).all(), (b, h)
+        untouched = np.isnan(c.w_host)
+        if weights == "add":
+            assert np.isnan(w[untouched]).all(), "a weight outside the sequences was written"
+        else:
+            assert (w[untouched] == -3.0).all(), "a weight outside the sequences was written"
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 100, 257]
+
+
+@pytest.mark.parametrize("kind,qkind", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("dim", [16, 64, 80, 128, 256])
+def test_attend_types_and_dims(ss, kind, qkind, dim):
+    check_attend(ss, Cache(LENS, heads=2, dim=dim, page=16, kind=kind, seed=dim), 4, qkind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [1, 2, 3, 8, 9, 16, 17, 40])
+def test_attend_groups(ss, kind, group):
+    check_attend(ss, Cache([77, 0, 18, 300], heads=3, dim=64, page=32, kind=kind, seed=group), group, "bf16")
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 64, 256])
+@pytest.mark.parametrize("layout", ["hnd", "nhd"])
+def test_attend_pages_and_layouts(ss, page, layout):
+    check_attend(ss, Cache([1, 50, 129, 500, 0, 63], heads=2, dim=128, page=page, kind="f16", seed=page, layout=layout), 2, "f16")
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (33, 0), (40, 17), (100, 100), (64, 1000), (5000, 3)])
+@pytest.mark.parametrize("weights", ["add", "apart"])
+def test_attend_window_and_sinks(ss, window, sinks, weights):
+    check_attend(ss, Cache([0, 1, 16, 40, 64, 65, 101, 333, 700], heads=2, dim=64, page=16, seed=3), 2, "bf16", window, sinks, weights)
+
+
+@pytest.mark.parametrize("weights", ["add", "new", "apart", None])
+def test_attend_weights_forms(ss, weights):
+    check_attend(ss, Cache([513, 4, 0, 90], heads=2, dim=128, page=32, seed=9), 8, "bf16", weights=weights, lse=weights != "new")
+
+
+@pytest.mark.parametrize("n,heads,group,dim,kind", [(20011, 1, 8, 128, "bf16"), (9001, 2, 1, 64, "f16"), (30000, 1, 5, 128, "e4m3"),
+                                                    (5003, 1, 2, 256, "bf16"), (12345, 1, 33, 64, "bf16")])
+def test_attend_one_long_sequence_split_and_joined(ss, n, heads, group, dim, kind):
+    check_attend(ss, Cache([n], heads=heads, dim=dim, page=64, kind=kind, seed=n), group, "f16" if kind == "f16" else "bf16")
+
+
+def test_attend_many_short_sequences(ss):
+    rng = np.random.default_rng(4)
+    check_attend(ss, Cache(rng.integers(0, 40, 1300).tolist(), heads=2, dim=64, page=8, seed=4), 2, "bf16")
+
+
+def test_attend_ragged_batch(ss):
+    check_attend(ss, Cache([3000, 1, 0, 16, 1500, 47, 0, 2222, 9], heads=4, dim=128, page=16, seed=8), 4, "bf16")
+
+
+def test_attend_strided_query_and_output(ss):
+    check_attend(ss, Cache([5, 90, 200], heads=2, dim=64, page=16, seed=6), 3, "bf16", strided=True)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_attend_scales(ss, scale):
+    # 2.0: a nearly one-hot softmax with scores in the hundreds
+    check_attend(ss, Cache([64, 301], heads=2, dim=64, page=16, kind="f16", seed=7), 2, "f16", scale=scale)
+
+
+def test_attend_large_values_in_an_8_bit_cache_with_large_queries(ss):
+    # q beyond fp16's range in bf16: the scores are as if it were fp32
+    check_attend(ss, Cache([40, 200], heads=2, dim=64, page=16, kind="e4m3", seed=10), 4, "bf16", qscale=3e5, scale=1e-6)
+
+
+def test_attend_infinities_and_nan_spread_as_in_the_formula(ss):
+    import torch
+    c = Cache([30, 30, 30, 30], heads=1, dim=64, page=16, seed=11)
+
+    def at(b, p):
+        return int(c.table_host[b, p // 16]), 0, p % 16
+
+    c.v[at(0, 7)] = math.nan      # sequence 0: out is NaN
+    c.k[at(1, 3)] = math.nan      # sequence 1: everything is NaN
+    for p in range(30):           # sequence 2: every score is -inf
+        c.k[at(2, p)] = 0.0
+        c.k[at(2, p) + (0,)] = -math.inf
+    c.k[at(3, 5) + (0,)] = -math.inf  # sequence 3: one position drops out
+    q = torch.ones(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pages, table = c.ss(ss)
+    out, lse, w = torch.empty_like(q), torch.empty(4, 2, device="cuda"), torch.zeros_like(c.weight)
+    ss.ss_kv_attend(pages, table, q, out, lse=lse, weight_out=w)
+    ok(ss)
+    assert bool(out[0].isnan().all()) and bool(torch.isfinite(lse[0]).all())
+    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+    assert all(float(w[at(2, p)]) == 0 for p in range(30))
+    assert bool(torch.isfinite(out[3]).all()) and float(w[at(3, 5)]) == 0.0
+    # the same rows where the window hides them change nothing
+    out2 = torch.empty_like(q)
+    c.v[at(3, 5)] = math.nan
+    ss.ss_kv_attend(pages, table, q, out2, window=20)
+    ok(ss)
+    assert bool(torch.isfinite(out2[[0, 1, 3]]).all())
+
+
+def test_attend_is_the_same_on_every_run_and_stream(ss):
+    import torch
+    c = Cache([4001, 17, 900], heads=4, dim=128, page=16, seed=12)
+    pages, table = c.ss(ss)
+    q = torch.randn(3, 16, 128, device="cuda").to(torch.bfloat16)
+    first = None
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            out, w = torch.empty_like(q), torch.zeros_like(c.weight)
+            for _ in range(3):
+                ss.ss_kv_attend(pages, table, q, out, weight_out=w, stream=stream)
+            stream.synchronize()
+            ok(ss, stream)
+        first = first or (out, w)
+        assert torch.equal(out, first[0]) and torch.equal(w, first[1])
+
+
+def test_attend_in_a_graph_reads_the_lengths_of_each_replay(ss):
+    import torch
+    c = Cache([600, 90], heads=2, dim=64, page=16, seed=13)
+    pages, table = c.ss(ss)
+    q = torch.randn(2, 4, 64, device="cuda").to(torch.bfloat16)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ss.ss_kv_attend(pages, table, q, out, stream=side)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            ss.ss_kv_attend(pages, table, q, out, stream=torch.cuda.current_stream())
+    for lens in ([600, 90], [33, 1], [0, 77]):
+        c.lens_dev.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        ss.ss_kv_attend(pages, table, q, want)
+        ok(ss)
+        assert torch.equal(out, want)
+
+
+def test_attend_reports_bad_lengths_and_pages_and_keeps_the_other_sequences(ss):
+    import torch
+    c = Cache([100, 50, 60], heads=2, dim=64, page=16, seed=14)
+    pages, table = c.ss(ss)
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    ss.ss_kv_attend(pages, table, q, want)
+    ok(ss)
+    good = c.table.clone()
+    for value in (-1, c.num_pages, 2 ** 31 - 1, -2 ** 31):
+        c.table.copy_(good)
+        c.table[1, 2] = value
+        ss.ss_kv_attend(pages, table, q, out)
+        st, where = ss.ss_stream_status()
+        assert (st, where) == (ss.SS_ERR_INVALID_ARG, 1)
+        assert torch.equal(out[[0, 2]], want[[0, 2]])
+    c.table.copy_(good)
+    for n in (-5, c.width * 16 + 1, 2 ** 31 - 1):
+        c.lens_dev[1] = n
+        c.table[1] = good[0, 0]  # every entry names a real page: only the length is wrong
+        ss.ss_kv_attend(pages, table, q, out)
+        st, where = ss.ss_stream_status()
+        assert (st, where) == (ss.SS_ERR_INVALID_ARG, 1)
+        assert torch.equal(out[[0, 2]], want[[0, 2]])
+
+
+def test_pool_past_32_bit_offsets(ss):
+    import torch
+    heads, dim, page = 8, 128, 64
+    pages = (1 << 31) // (heads * dim * page) + 40  # more than 2^31 elements in each of k and v
+    k = torch.zeros(pages, heads, page, dim, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    weight = torch.zeros(pages, heads, page, device="cuda")
+    n = 10 * page - 7
+    near, far = list(range(10)), list(range(pages - 10, pages))
+    k[near] = torch.randn(10, heads, page, dim, device="cuda").to(torch.bfloat16)
+    v[near] = torch.randn(10, heads, page, dim, device="cuda").to(torch.bfloat16)
+    weight[near] = torch.rand(10, heads, page, device="cuda")
+    for x in (k, v, weight):
+        x[far] = x[near]
+    cache = ss.KVPages(k, v, weight=weight)
+    seqs = ss.KVTable(torch.tensor([near, far], dtype=torch.int32, device="cuda"), torch.tensor([n, n], dtype=torch.int32, device="cuda"))
+    q = torch.randn(1, 16, dim, device="cuda").to(torch.bfloat16).expand(2, -1, -1).contiguous()
+    out, lse = torch.empty_like(q), torch.empty(2, 16, device="cuda")
+    ss.ss_kv_attend(cache, seqs, q, out, lse=lse)
+    ok(ss)
+    assert torch.allclose(out[0].float(), out[1].float(), rtol=2 ** -7, atol=1e-4) and float(out.float().abs().max()) > 0
+    dst = list(range(pages - 20, pages - 15)), list(range(20, 25))
+    new = ss.KVTable(torch.tensor(dst, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda"))
+    kept = torch.empty(2, heads, 300, dtype=torch.int32, device="cuda")
+    ss.ss_kv_evict(cache, seqs, cache, new, 300, sinks=4, recent=30, kept=kept)
+    ok(ss)
+    assert torch.equal(kept[0], kept[1]) and new.lens.tolist() == [300, 300]
+    rows = [x[d].transpose(1, 2).reshape(5 * page, heads, dim)[:300] for x in (k, v) for d in dst]
+    assert torch.equal(rows[0], rows[1]) and torch.equal(rows[2], rows[3])
+    idx = kept[0].long()
+    whole = k[near].transpose(1, 2).reshape(10 * page, heads, dim)
+    for h in range(heads):
+        assert torch.equal(rows[0][:, h], whole[idx[h], h])
+    x = torch.randn(2, heads, dim, device="cuda").to(torch.bfloat16)
+    ss.ss_kv_append(cache, seqs, x, x)
+    ok(ss)
+    for b, last in enumerate((near[9], far[9])):
+        assert torch.equal(k[last, :, (n - 1) % page], x[b]) and float(weight[last, :, (n - 1) % page].abs().max()) == 0.0
+
+
+# ---- eviction ----
+
+def run_evict(ss, c, weights, keep, sinks, recent, dst_page=None, dst_layout="hnd", with_kept=True, dst_weight=True):
+    """Evicts c with the given weight pool and compares everything with the reference."""
+    import torch
+    c.weight.copy_(torch.from_numpy(weights))
+    dst_page = dst_page or c.page
+    kept_lens = [min(n, keep) for n in c.lens]
+    d = Cache(kept_lens, heads=c.heads, dim=c.dim, page=dst_page, kind=c.kind, seed=77, layout=dst_layout, scales=False,
+              with_weight=dst_weight)
+    d.ks, d.vs = c.ks, c.vs
+    before = [x.float().clone() for x in (d.k, d.v)]
+    d.lens_dev.fill_(-9)
+    pages, table = c.ss(ss)
+    new_pages, new_table = d.ss(ss)
+    kept = torch.full((len(c.lens), c.heads, keep), 12345, dtype=torch.int32, device="cuda") if with_kept else None
+    ss.ss_kv_evict(pages, table, new_pages, new_table, keep, sinks=sinks, recent=recent, kept=kept)
+    ok(ss)
+    want = evict_reference(c, weights, keep, sinks, recent)
+    assert d.lens_dev.tolist() == kept_lens
+    if with_kept:
+        assert np.array_equal(kept.cpu().numpy(), want)
+    got = [x.float().cpu().numpy() for x in (d.k, d.v)]
+    new_w = d.weight.cpu().numpy() if dst_weight else None
+    touched = np.zeros(got[0].shape[:3], bool)
+    for b, m in enumerate(kept_lens):
+        j = np.arange(m)
+        for h in range(c.heads):
+            idx = want[b, h, :m]
+            to = d.table_host[b, j // dst_page], h, j % dst_page
+            touched[to] = True
+            for x, host in zip(got, (c.k_host, c.v_host)):
+                assert np.array_equal(x[to], c.rows(host, b, h)[idx])
+            if dst_weight:
+                assert np.array_equal(new_w[to].view(np.uint32), c.rows(weights, b, h)[idx].view(np.uint32))
+    for x, old in zip(got, before):
+        assert np.array_equal(x[~touched], old.cpu().numpy()[~touched], equal_nan=True), "a row outside the kept ones was written"
+
+
+def random_weights(c, seed, zeros=0.2, levels=None):
+    rng = np.random.default_rng(seed)
+    w = np.exp(2.5 * rng.standard_normal(c.w_host.shape) - 8).astype(np.float32)
+    if levels:
+        w = rng.integers(0, levels, w.shape).astype(np.float32)
+    w[rng.random(w.shape) < zeros] = 0.0
+    return w
+
+
+@pytest.mark.parametrize("kind,dim", [("bf16", 64), ("f16", 80), ("e4m3", 128), ("bf16", 256), ("e4m3", 16)])
+@pytest.mark.parametrize("keep,sinks,recent", [(64, 4, 16), (1, 0, 0), (1, 1, 0), (1, 0, 1), (37, 20, 17), (200, 0, 0), (1000, 4, 100)])
+def test_evict(ss, kind, dim, keep, sinks, recent):
+    c = Cache([0, 1, 63, 64, 65, 300, 999, 1001], heads=2, dim=dim, page=16, kind=kind, seed=keep)
+    run_evict(ss, c, random_weights(c, keep + dim), keep, sinks, recent)
+
+
+@pytest.mark.parametrize("levels,zeros", [(1, 0.0), (2, 0.0), (3, 0.5), (40, 0.0)])
+def test_evict_ties_go_to_the_lower_position(ss, levels, zeros):
+    c = Cache([1500, 700, 33], heads=3, dim=16, page=16, seed=levels)
+    run_evict(ss, c, random_weights(c, levels, zeros, levels), 301, 3, 50)
+
+
+def test_evict_infinities_nan_and_signed_zeros(ss):
+    c = Cache([800, 400], heads=2, dim=16, page=16, seed=2)
+    rng = np.random.default_rng(3)
+    w = rng.choice(np.array([np.nan, -np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-45, -1e-45, 1.0, -1.0, 3.4e38, -3.4e38], np.float32),
+                   c.w_host.shape).astype(np.float32)
+    for keep in (50, 399, 700):
+        run_evict(ss, c, w, keep, 2, 9)
+
+
+@pytest.mark.parametrize("page,layout,dst_page,dst_layout", [(16, "hnd", 64, "hnd"), (64, "nhd", 8, "hnd"), (7, "hnd", 3, "nhd"), (1, "nhd", 1, "nhd")])
+def test_evict_between_page_sizes_and_layouts(ss, page, layout, dst_page, dst_layout):
+    c = Cache([130, 257, 64], heads=2, dim=64, page=page, seed=page, layout=layout)
+    run_evict(ss, c, random_weights(c, 5), 100, 4, 30, dst_page, dst_layout)
+
+
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 33000, 70001, 131073])
+def test_evict_long(ss, n):
+    c = Cache([n, n // 3], heads=2, dim=16, page=64, seed=n, kind="e4m3")
+    run_evict(ss, c, random_weights(c, n), n // 4, 4, 1000)
+
+
+def test_evict_very_long(ss):
+    # longer than the keys of one row that shared memory can hold
+    c = Cache([500_003], heads=1, dim=16, page=128, seed=1, kind="e4m3")
+    run_evict(ss, c, random_weights(c, 1), 123_457, 4, 1000)
+
+
+def test_evict_many_rows(ss):
+    rng = np.random.default_rng(6)
+    c = Cache(rng.integers(0, 200, 150).tolist(), heads=8, dim=16, page=16, seed=6)
+    run_evict(ss, c, random_weights(c, 6), 48, 2, 8)
+
+
+def test_evict_without_optional_outputs(ss):
+    c = Cache([300, 20], heads=2, dim=64, page=16, seed=15)
+    run_evict(ss, c, random_weights(c, 15), 64, 4, 16, with_kept=False, dst_weight=False)
+    run_evict(ss, c, random_weights(c, 16), 64, 4, 16, with_kept=False)
+
+
+def test_evict_reports_bad_pages(ss):
+    import torch
+    c = Cache([300, 200], heads=2, dim=64, page=16, seed=16)
+    pages, table = c.ss(ss)
+    d = Cache([64, 64], heads=2, dim=64, page=16, seed=17)
+    new_pages, new_table = d.ss(ss)
+    c.table[1, 3] = c.num_pages
+    ss.ss_kv_evict(pages, table, new_pages, new_table, 64)
+    assert ss.ss_stream_status() == (ss.SS_ERR_INVALID_ARG, 1)
+    c.table[1, 3] = 0
+    d.table[0, 1] = -7
+    ss.ss_kv_evict(pages, table, new_pages, new_table, 64)
+    assert ss.ss_stream_status() == (ss.SS_ERR_INVALID_ARG, 0)
+    torch.cuda.synchronize()
+
+
+# ---- append ----
+
+def check_append(ss, lens, news, heads, dim, page, kind, src, layout="hnd", strided=False, offsets=True, values=None):
+    import torch
+    c = Cache(lens, heads=heads, dim=dim, page=page, kind=kind, seed=21, layout=layout)
+    before = [x.float().cpu().numpy() for x in (c.k, c.v)] + [c.weight.cpu().numpy()]
+    total = sum(news)
+    gen = torch.Generator().manual_seed(22)
+    if values is None:
+        host = (torch.randn(total, 3, heads, dim, generator=gen) * 0.8).to(torch_type(src))
+    else:
+        host = torch.from_numpy(np.resize(values, (total, 3, heads, dim)).astype(np.float32)).to(torch_type(src))
+    dev = host.cuda()
+    k_new, v_new = (dev[:, 1], dev[:, 2]) if strided else (dev[:, 1].contiguous(), dev[:, 2].contiguous())
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    pages, table = c.ss(ss)
+    ss.ss_kv_append(pages, table, k_new, v_new, offsets=torch.from_numpy(starts).cuda() if offsets else None)
+    ok(ss)
+    after = [x.float().cpu().numpy() for x in (c.k, c.v)] + [c.weight.cpu().numpy()]
+    want = [x.copy() for x in before]
+    for b, (n, m) in enumerate(zip(lens, news)):
+        p = np.arange(n - m, n)
+        at = c.table_host[b, p // page], slice(None), p % page
+        for i, scale in ((0, c.ks), (1, c.vs)):
+            x = host[starts[b]:starts[b + 1], i + 1].float().numpy()
+            if kind == "e4m3":
+                x = e4m3_reference(x / (np.float32(1) if scale is None else scale.numpy()[:, None]))
+            want[i][at] = x
+        want[2][at] = 0.0
+    for got, ref in zip(after, want):
+        assert np.array_equal(got, ref.astype(np.float32), equal_nan=True)
+
+
+@pytest.mark.parametrize("kind,src", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("dim,page", [(16, 16), (64, 1), (80, 7), (128, 16), (256, 64)])
+def test_append_prompts(ss, kind, src, dim, page):
+    check_append(ss, [100, 1, 0, 300, 64, 17], [100, 1, 0, 299, 5, 0], 3, dim, page, kind, src, strided=dim == 128)
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_append_one_token_each(ss, kind, layout):
+    check_append(ss, [1, 16, 17, 100, 333], [1] * 5, 8, 128, 16, kind, "bf16", layout, strided=True, offsets=False)
+
+
+def test_append_rounds_saturates_and_keeps_nan(ss):
+    steps = np.arange(-4096, 4096) / 512.0  # every neighbourhood of a tie at the small end
+    hard = np.concatenate([steps, [np.inf, -np.inf, np.nan, 447, 449, 464, 465, 480, 1e5, -1e5, 2.0 ** -10, 2.0 ** -9, 3 * 2.0 ** -11, 0.0, -0.0]])
+    check_append(ss, [200, 500], [200, 500], 2, 64, 16, "e4m3", "bf16", values=hard)
+    check_append(ss, [200, 500], [200, 500], 2, 64, 16, "e4m3", "f16", values=hard[np.abs(np.nan_to_num(hard, posinf=1.0, neginf=1.0)) < 6e4])
+
+
+def test_append_large_batch_of_prompts(ss):
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 700, 90).tolist()
+    check_append(ss, lens, [int(rng.integers(0, n + 1)) for n in lens], 4, 64, 32, "bf16", "bf16")
+
+
+def test_append_more_tokens_than_the_length_is_reported(ss):
+    import torch
+    c = Cache([10, 10], heads=1, dim=64, page=16, seed=23)
+    pages, table = c.ss(ss)
+    x = torch.zeros(16, 1, 64, dtype=torch.bfloat16, device="cuda")
+    ss.ss_kv_append(pages, table, x, x, offsets=torch.tensor([0, 4, 16], dtype=torch.int32, device="cuda"))
+    assert ss.ss_stream_status() == (ss.SS_ERR_INVALID_ARG, 1)
+
+
+def test_a_sequence_lives_through_append_attend_and_evict(ss):
+    """Weights gathered over steps decide what stays; attention over the
+    evicted cache is attention over the kept rows."""
+    import torch
+    heads, group, dim, page = 2, 4, 64, 16
+    c = Cache([120, 90], heads=heads, dim=dim, page=page, seed=31)
+    c.weight.zero_()
+    pages, table = c.ss(ss)
+    gen = torch.Generator().manual_seed(32)
+    expect = np.zeros(c.w_host.shape)
+    for step in range(4):
+        c.lens = [n + 1 for n in c.lens]
+        c.lens_dev.add_(1)
+        new = torch.randn(2, 2, heads, dim, generator=gen).to(torch.bfloat16)
+        ss.ss_kv_append(pages, table, new[:, 0].cuda(), new[:, 1].cuda())
+        for b in range(2):
+            p = c.lens[b] - 1
+            for host, i in ((c.k_host, 0), (c.v_host, 1)):
+                host[c.table_host[b, p // page], :, p % page] = new[b, i].float().numpy()
+        q = torch.randn(2, heads * group, dim, generator=gen).to(torch.bfloat16)
+        out = torch.empty_like(q, device="cuda")
+        ss.ss_kv_attend(pages, table, q.cuda(), out, weight_in=c.weight, weight_out=c.weight)
+        ok(ss)
+        want, _, added = attend_reference(c, q.float().numpy(), dim ** -0.5)
+        expect += added
+        assert np.abs(out.float().cpu().numpy() - want).max() <= 2.0 ** -8 * np.abs(want).max() + 2e-4
+    held = ~np.isnan(c.weight.cpu().numpy())
+    for b in range(2):
+        for h in range(heads):
+            assert np.allclose(c.rows(c.weight.cpu().numpy(), b, h), c.rows(expect, b, h), rtol=1e-4, atol=1e-7)
+    assert held.any()
+    weights = np.where(held, c.weight.cpu().numpy(), 0).astype(np.float32)
+    run_evict(ss, c, weights, 70, 4, 20)
