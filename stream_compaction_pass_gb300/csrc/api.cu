@@ -450,7 +450,7 @@ ss_status kv_table(const ss_kv_table* t, const ss::KvPages& c, const char* name,
     int64_t held = (int64_t)t->max_pages * c.page_size;
     if (t->max_len > 0 && t->max_len < held) held = t->max_len;
     if (held > 0x7fffffff - 4096) return fail(SS_ERR_INVALID_ARG, who + ": max_len must be below 2^31 - 4096");
-    *out = ss::KvTable{t->pages, t->row_stride, t->max_pages, t->batch, t->lens, (int)held};
+    *out = ss::KvTable{t->pages, t->row_stride, t->max_pages, t->batch, t->lens, (int)held, 0};
     return SS_OK;
 }
 
@@ -528,7 +528,12 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, a.q_seq_stride, a.q_head_stride, a.out,
                             a.out_seq_stride, a.out_head_stride, a.scale, a.window, a.sinks, a.lse, a.weight_in,
                             a.weight_out};
-    cudaError_t e = ss::launch_kv_attend(c, t, k, ws_status(w), (cudaStream_t)stream);
+    size_t bytes = 0;
+    cudaError_t e = ss::kv_attend_scratch(c, t, k, &bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "attention set-up");
+    st = ensure_kv(w, bytes);
+    if (st != SS_OK) return st;
+    e = ss::launch_kv_attend(c, t, k, w->kv, ws_status(w), (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "attention launch");
 } catch (...) {
     return SS_ERR_NO_MEMORY;

@@ -185,6 +185,7 @@ struct KvTable {
     int max_pages, batch;
     int32_t* lens;
     int max_len;
+    int first = 0;  // the caller's number of sequence 0, for error reports
 };
 struct KvAttention {
     KvElem type;
@@ -202,7 +203,9 @@ struct KvAttention {
 cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, const void* k_new, const void* v_new,
                              int64_t token_stride, int64_t head_stride, const int32_t* offsets, int64_t tokens,
                              uint32_t* status, cudaStream_t s);
-cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, uint32_t* status,
+// Device scratch of one attention call, in bytes.
+cudaError_t kv_attend_scratch(const KvPages& c, const KvTable& t, const KvAttention& a, size_t* bytes);
+cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, uint32_t* status,
                              cudaStream_t s);
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
                             int sinks, int recent, int32_t* kept, uint32_t* status, cudaStream_t s);

@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "lookback.cuh"
 
 namespace ss {
@@ -15,7 +17,7 @@ namespace ss {
 __device__ __forceinline__ int kv_len(const KvTable& t, int b, uint32_t* status) {
     const int n = t.lens[b];
     const int m = min(max(n, 0), t.max_len);
-    if (m != n) record_error(status, kErrKvTable, (uint32_t)b);
+    if (m != n) record_error(status, kErrKvTable, (uint32_t)(t.first + b));
     return m;
 }
 
@@ -24,7 +26,7 @@ __device__ __forceinline__ int kv_len(const KvTable& t, int b, uint32_t* status)
 __device__ __forceinline__ int kv_page(const KvTable& t, int64_t num_pages, int b, int index, uint32_t* status) {
     const int p = t.pages[(int64_t)b * t.row_stride + index];
     if (p >= 0 && p < num_pages) return p;
-    record_error(status, kErrKvTable, (uint32_t)b);
+    record_error(status, kErrKvTable, (uint32_t)(t.first + b));
     return -1;
 }
 
