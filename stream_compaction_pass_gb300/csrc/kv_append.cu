@@ -1,6 +1,9 @@
 // kv_append.cu -- new tokens' keys and values into their pages (streamscan.h,
 // ss_kv_append): a row copy, or a quantisation to e4m3 with one scale per
-// head.  Bound by memory: each row is read once and written once.
+// head.  Bound by memory: each row is read once and written once.  A CTA takes
+// a few (token, head) rows: one thread a row finds its page and slot, then all
+// threads move 16-byte vectors of the result, every load issued before the
+// first store.
 #include "kv.cuh"
 
 namespace ss {
@@ -8,50 +11,121 @@ namespace ss {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendVecs = 4;  // result vectors of a thread
 
-// One thread per element: simple, and right for every size.
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+template <typename T> __device__ __forceinline__ float2 open_pair(uint32_t u);
+template <> __device__ __forceinline__ float2 open_pair<__nv_bfloat16>(uint32_t u) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+template <> __device__ __forceinline__ float2 open_pair<__half>(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// 16 elements over the scale, as e4m3.  The quotient is the correctly rounded
+// fp32 one, as the definition has it, and is then rounded once more.
+template <typename T> __device__ __forceinline__ uint4 quant16(const uint4 (&x)[2], float scale) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = open_pair<T>(w[2 * i]), b = open_pair<T>(w[2 * i + 1]);
+        r[i] = quant4(__fdiv_rn(a.x, scale), __fdiv_rn(a.y, scale), __fdiv_rn(b.x, scale), __fdiv_rn(b.y, scale));
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 template <typename T, bool QUANT>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvPages c, KvTable t, const T* __restrict__ k_new,
                                                              const T* __restrict__ v_new, int64_t token_stride,
                                                              int64_t head_stride, const int32_t* __restrict__ offsets,
-                                                             int64_t rows, uint32_t* status) {
-    const int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-    if (i >= rows * c.head_dim) return;
-    const int64_t row = i / c.head_dim;
-    const int d = (int)(i % c.head_dim);
-    const int64_t tok = row / c.kv_heads;
-    const int h = (int)(row % c.kv_heads);
-    int b = (int)tok;
-    int64_t back = 1;  // positions before the end
-    if (offsets) {
-        int lo = 0, hi = t.batch;  // the sequence with offsets[b] <= tok < offsets[b + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (offsets[mid] <= tok) lo = mid; else hi = mid;
+                                                             int64_t rows, int per, int vecs, uint32_t* status) {
+    constexpr int kIn = QUANT ? 2 : 1;  // 16-byte vectors read for one written
+    constexpr int kBytes = QUANT ? 1 : 2;
+    __shared__ int64_t s_src[kAppendThreads], s_dst[kAppendThreads];  // byte offsets, dst -1: not written
+    __shared__ float s_scale[2][kAppendThreads];
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * per;
+    if (tid < per && row0 + tid < rows) {
+        const int64_t tok = (row0 + tid) / c.kv_heads;
+        const int h = (int)((row0 + tid) % c.kv_heads);
+        int b = (int)tok;
+        int64_t back = 1;  // positions before the end
+        if (offsets) {
+            int lo = 0, hi = t.batch;  // the last b with offsets[b] <= tok
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (offsets[mid] <= tok) lo = mid; else hi = mid;
+            }
+            b = lo;
+            back = offsets[b + 1] - tok;
         }
-        b = lo;
-        back = offsets[b + 1] - tok;
+        const int64_t pos = kv_len(t, b, status) - back;
+        int64_t dst = -1;
+        if (back < 1 || pos < 0) {
+            record_error(status, kErrKvTable, (uint32_t)(t.first + b));
+        } else {
+            const int page = kv_page(t, c.num_pages, b, (int)(pos / c.page_size), status);
+            const int slot = (int)(pos % c.page_size);
+            if (page >= 0) {
+                dst = ((int64_t)page * c.page_stride + (int64_t)h * c.head_stride + (int64_t)slot * c.slot_stride) * kBytes;
+                if (c.weight) c.weight[((int64_t)page * c.kv_heads + h) * c.page_size + slot] = 0.0f;
+            }
+        }
+        s_src[tid] = (tok * token_stride + h * head_stride) * 2;
+        s_dst[tid] = dst;
+        if (QUANT) {
+            s_scale[0][tid] = c.k_scale ? c.k_scale[h] : 1.0f;
+            s_scale[1][tid] = c.v_scale ? c.v_scale[h] : 1.0f;
+        }
     }
-    const int len = kv_len(t, b, status);
-    const int64_t pos = len - back;
-    if (back < 1 || pos < 0) {
-        record_error(status, kErrKvTable, (uint32_t)b);
-        return;
+    __syncthreads();
+    const int here = (int)min((int64_t)per, rows - row0);
+    const int half = here * vecs;  // k's vectors, then v's
+    for (int i0 = tid; i0 < 2 * half; i0 += kAppendThreads * kAppendVecs) {
+        uint4 x[kAppendVecs][kIn];
+        int64_t to[kAppendVecs];
+        int at[kAppendVecs];
+#pragma unroll
+        for (int l = 0; l < kAppendVecs; ++l) {
+            const int i = i0 + l * kAppendThreads;
+            to[l] = -1;
+            if (i >= 2 * half) continue;
+            const bool is_v = i >= half;
+            const int k = is_v ? i - half : i, r = k / vecs, v = k - r * vecs;
+            if (s_dst[r] < 0) continue;
+            const char* from = reinterpret_cast<const char*>(is_v ? v_new : k_new) + s_src[r] + v * (16 * kIn);
+#pragma unroll
+            for (int e = 0; e < kIn; ++e) x[l][e] = ldg_vec(from + 16 * e);
+            to[l] = s_dst[r] + v * 16;
+            at[l] = is_v ? r + kAppendThreads : r;
+        }
+#pragma unroll
+        for (int l = 0; l < kAppendVecs; ++l) {
+            if (to[l] < 0) continue;
+            uint4 y = x[l][0];
+            if constexpr (QUANT) y = quant16<T>(x[l], (&s_scale[0][0])[at[l]]);
+            stg_vec((at[l] >= kAppendThreads ? c.v : c.k) + to[l], y);
+        }
     }
-    const int page = kv_page(t, c.num_pages, b, (int)(pos / c.page_size), status);
-    if (page < 0) return;
-    const int slot = (int)(pos % c.page_size);
-    const int64_t src = tok * token_stride + h * head_stride + d;
-    const int64_t dst = page * c.page_stride + h * c.head_stride + slot * c.slot_stride + d;
-    if (QUANT) {
-        const float ks = c.k_scale ? c.k_scale[h] : 1.0f, vs = c.v_scale ? c.v_scale[h] : 1.0f;
-        reinterpret_cast<__nv_fp8_e4m3*>(c.k)[dst] = __nv_fp8_e4m3(__fdiv_rn(to_f32(k_new[src]), ks));
-        reinterpret_cast<__nv_fp8_e4m3*>(c.v)[dst] = __nv_fp8_e4m3(__fdiv_rn(to_f32(v_new[src]), vs));
-    } else {
-        reinterpret_cast<T*>(c.k)[dst] = k_new[src];
-        reinterpret_cast<T*>(c.v)[dst] = v_new[src];
-    }
-    if (d == 0 && c.weight) c.weight[((int64_t)page * c.kv_heads + h) * c.page_size + slot] = 0.0f;
+}
+
+template <typename T, bool QUANT>
+cudaError_t run(const KvPages& c, const KvTable& t, const void* k_new, const void* v_new, int64_t token_stride,
+                int64_t head_stride, const int32_t* offsets, int64_t tokens, uint32_t* status, cudaStream_t s) {
+    const int64_t rows = tokens * c.kv_heads;
+    const int vecs = c.head_dim * (QUANT ? 1 : 2) / 16;
+    int per = kAppendThreads * kAppendVecs / (2 * vecs);  // rows whose vectors are one round
+    per = per > kAppendThreads ? kAppendThreads : per;
+    const unsigned grid = (unsigned)((rows + per - 1) / per);
+    k_kv_append<T, QUANT><<<grid, kAppendThreads, 0, s>>>(c, t, static_cast<const T*>(k_new), static_cast<const T*>(v_new), token_stride,
+                                                          head_stride, offsets, rows, per, vecs, status);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -59,19 +133,12 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvPages c, KvTable
 cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, const void* k_new, const void* v_new,
                              int64_t token_stride, int64_t head_stride, const int32_t* offsets, int64_t tokens,
                              uint32_t* status, cudaStream_t s) {
-    const int64_t rows = tokens * c.kv_heads;
-    const unsigned grid = (unsigned)((rows * c.head_dim + kAppendThreads - 1) / kAppendThreads);
     const bool quant = c.type == KvElem::E4M3;
-    if (type == KvElem::BF16) {
-        const auto *k = static_cast<const __nv_bfloat16*>(k_new), *v = static_cast<const __nv_bfloat16*>(v_new);
-        if (quant) k_kv_append<__nv_bfloat16, true><<<grid, kAppendThreads, 0, s>>>(c, t, k, v, token_stride, head_stride, offsets, rows, status);
-        else k_kv_append<__nv_bfloat16, false><<<grid, kAppendThreads, 0, s>>>(c, t, k, v, token_stride, head_stride, offsets, rows, status);
-    } else {
-        const auto *k = static_cast<const __half*>(k_new), *v = static_cast<const __half*>(v_new);
-        if (quant) k_kv_append<__half, true><<<grid, kAppendThreads, 0, s>>>(c, t, k, v, token_stride, head_stride, offsets, rows, status);
-        else k_kv_append<__half, false><<<grid, kAppendThreads, 0, s>>>(c, t, k, v, token_stride, head_stride, offsets, rows, status);
-    }
-    return cudaGetLastError();
+    if (type == KvElem::BF16)
+        return quant ? run<__nv_bfloat16, true>(c, t, k_new, v_new, token_stride, head_stride, offsets, tokens, status, s)
+                     : run<__nv_bfloat16, false>(c, t, k_new, v_new, token_stride, head_stride, offsets, tokens, status, s);
+    return quant ? run<__half, true>(c, t, k_new, v_new, token_stride, head_stride, offsets, tokens, status, s)
+                 : run<__half, false>(c, t, k_new, v_new, token_stride, head_stride, offsets, tokens, status, s);
 }
 
 }  // namespace ss
