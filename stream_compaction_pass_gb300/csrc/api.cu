@@ -513,6 +513,8 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     const size_t pool = (size_t)c.num_pages * c.kv_heads * c.page_size * 4;
     if (a.weight_in && a.weight_in != a.weight_out && overlaps(a.weight_in, pool, a.weight_out, pool))
         return fail(SS_ERR_INVALID_ARG, "weight_in and weight_out partially overlap");
+    if ((int64_t)(t.max_len / 16 + 1) * a.q_heads > 0x7fffffff)
+        return fail(SS_ERR_INVALID_ARG, "max_len / 16 * q_heads must be below 2^31");
     if (t.batch == 0) return SS_OK;
     if (!a.q || !a.out) return fail(SS_ERR_INVALID_ARG, "null q or out");
     if (!aligned16(a.q) || !aligned16(a.out)) return fail(SS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");

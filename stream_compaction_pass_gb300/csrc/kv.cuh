@@ -12,6 +12,20 @@
 
 namespace ss {
 
+// Division of numbers below 2^31 by a fixed one, by a multiplication: with
+// 2^l >= d and m = floor(2^32 (2^l - d) / d) + 1, n / d = (n m / 2^32 + n) / 2^l
+// (Granlund and Montgomery, "Division by invariant integers using multiplication").
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d) : shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 // The length of sequence b as every kernel reads it: clamped to what the
 // table can hold, and reported where it had to be.
 __device__ __forceinline__ int kv_len(const KvTable& t, int b, uint32_t* status) {

@@ -31,43 +31,66 @@ namespace ss {
 
 namespace {
 
-constexpr int kTile = 16;       // positions per tile (a page may end inside it)
 constexpr int kMaxBatch = 512;  // sequences per launch: their tile counts' prefix sums are in shared memory
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
-constexpr int kWeightChunk = 512;  // positions per CTA of the weights' part
+constexpr int kWeightTiles = 16;  // tiles that a CTA of the weights' part takes at least
 constexpr int kMaxGroup = 128;
 constexpr size_t kMaxLogits = (size_t)2 << 30;  // bytes of scores one launch may leave in scratch
 
 // Which positions of a sequence are visible, and in which tiles they lie: the
-// tiles of the first tokens, then those of the window.
+// tiles (of 2^shift positions; a page may end inside one) of the first
+// tokens, then those of the window.
 struct Tiles {
     int len, start, sinks, nsink, first, count;
-    __device__ Tiles(int len_, int window, int sinks_) : len(len_), start(0), sinks(sinks_), nsink(0), first(0) {
+    __device__ __forceinline__ Tiles(int len_, int window, int sinks_, int shift) : len(len_), start(0), sinks(sinks_), nsink(0), first(0) {
+        const int up = (1 << shift) - 1;
         if (window > 0 && window < len) {
             start = len - window;
-            first = start / kTile;
-            nsink = min((min(sinks, start) + kTile - 1) / kTile, first);
+            first = start >> shift;
+            nsink = min((min(sinks, start) + up) >> shift, first);
         }
-        count = nsink + (len + kTile - 1) / kTile - first;
+        count = nsink + ((len + up) >> shift) - first;
     }
     __device__ __forceinline__ int tile(int j) const { return j < nsink ? j : first + j - nsink; }
     __device__ __forceinline__ bool visible(int p) const { return p < len && (p < sinks || p >= start); }
+    // Whether all of p .. p + n - 1 are visible.
+    __device__ __forceinline__ bool whole(int p, int n) const { return p + n <= len && (p + n <= sinks || p >= start); }
 };
 
 struct Scratch {
     int* pre;       // batch + 1: tiles of the sequences before, per unit
+    int* pre_all;   // the same of all positions, where those that are not visible get a weight too (else pre)
     float* lse2;    // batch x q_heads: R + log2 l of the rows the first launch finished
     float2* ml;     // workers x 2 x 16: (R, l) of a part
     float* o;       // workers x 2 x rows x DP: its O
     float* logits;  // per (sequence, key-value head) tile: group x 16 scores, log2 units; or null
     int group, units, rows, workers;  // units per sequence; rows = min(group, 16)
+    int shift;                        // tiles have 2^shift positions
+    FastDiv page;                     // by page_size
 };
 
-// Worker w of n takes the tiles [share(w), share(w + 1)) of `total`.
-__device__ __forceinline__ long long share_begin(int w, int n, long long total) { return (long long)w * total / n; }
-// The worker whose share holds tile t.
-__device__ __forceinline__ int share_of(long long t, int n, long long total) { return (int)(((t + 1) * n - 1) / total); }
+// A list of `total` tiles cut into n contiguous shares, the first ones a tile
+// longer.  Lists are shorter than 2^31 (the launcher sees to it).
+struct Shares {
+    int quot, rem;
+    __device__ __forceinline__ Shares(int total, int n) : quot(total / n), rem(total - total / n * n) {}
+    __device__ __forceinline__ int begin(int w) const { return w * quot + min(w, rem); }
+    __device__ __forceinline__ int holder(int t) const {  // the share that holds tile t
+        const int split = rem * (quot + 1);
+        return t < split ? t / (quot + 1) : rem + (t - split) / quot;
+    }
+};
+
+// The last b with pre[b] * per <= at, for at < pre[n] * per: never an empty sequence.
+__device__ __forceinline__ int find_sequence(const int* pre, int n, int per, int at) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pre[mid] * per <= at) lo = mid; else hi = mid;
+    }
+    return lo;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -131,6 +154,18 @@ template <typename T> __device__ __forceinline__ float2 open2(uint32_t u) {
     return Pair<T>::open(*reinterpret_cast<const typename Pair<T>::type*>(&u));
 }
 
+// x[1 .. n] become their running sums and x[0] zero, by one warp.
+__device__ __forceinline__ void prefix_sums(int* x, int n, int lane) {
+    int run = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int y = warp_inclusive_scan<int>(i < n ? x[i + 1] : 0, lane) + run;
+        if (i < n) x[i + 1] = y;
+        run = __shfl_sync(kFullMask, y, 31);
+    }
+    if (lane == 0) x[0] = 0;
+}
+
 // Two e4m3 bytes as two fp16 (exact).
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t lo16) {
     uint32_t r;
@@ -156,29 +191,32 @@ template <bool FP8, int DP> __device__ __forceinline__ int v_vec(int row, int v)
     return v ^ ((row >> 1) & 1) ^ (((row >> 2) & 1) << 2);
 }
 
-// A place in the list of tiles.
+// A place in the list of tiles: sequence, key-value head, 16 query heads of
+// its group, tile.
 struct Cursor {
-    int b, u, j;
+    int b, head, part, j;
     Tiles t;
-    __device__ Cursor() : b(0), u(0), j(0), t(0, 0, 0) {}
+    __device__ __forceinline__ Cursor() : b(0), head(0), part(0), j(0), t(0, 0, 0, 0) {}
 };
 
 // DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros in shared
-// memory).  NW warps of a CTA, S stages of each warp's ring.
-template <typename QT, bool FP8, int DP, int NW, int S>
+// memory).  T positions per tile (16 or 32), NW warps of a CTA, S stages of
+// each warp's ring.
+template <bool FP8, int DP, int T, int NW, int S>
 struct Shape {
     static constexpr int kBytes = FP8 ? 1 : 2;
     static constexpr int kRowBytes = DP * kBytes;
     static constexpr int kVecs = kRowBytes / 16;
-    static constexpr int kTileBytes = kTile * kRowBytes;    // of k, and of v
+    static constexpr int kTileBytes = T * kRowBytes;        // of k, and of v
     static constexpr bool kQShared = DP == 256;             // Q's fragments in shared memory: registers are short
     static constexpr int kQBytes = kQShared ? DP / 16 * 32 * 16 : 0;
     static constexpr size_t kSmem = (size_t)NW * (S * 2 * kTileBytes + kQBytes) + (kMaxBatch + 1) * 4;
 };
 
-template <typename QT, bool FP8, int DP, int NW, int S>
+template <typename QT, bool FP8, int DP, int T, int NW, int S>
 __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
-    using Sh = Shape<QT, FP8, DP, NW, S>;
+    using Sh = Shape<FP8, DP, T, NW, S>;
+    constexpr int kShift2 = T == 16 ? 4 : 5;
     // 8-bit caches multiply in fp16, which holds every e4m3 value; P is kept
     // below 2^15 by the reference so that small weights stay normal numbers.
     using MT = typename std::conditional<FP8, __half, QT>::type;
@@ -188,7 +226,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     // rounding of out (2^-16 against 2^-9 for bf16), except under bf16 outputs
     // of 8-bit caches, where one fp16 term (2^-12) is already finer than out.
     constexpr bool kTwo = !(FP8 && std::is_same<QT, __nv_bfloat16>::value);
-    constexpr int kKS = DP / 16, kNT = DP / 8;
+    constexpr int kKS = DP / 16, kNT = DP / 8, kPT = T / 8;  // steps along head_dim, products along it, along positions
 
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -197,84 +235,102 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
 
     // Prefix sums of the sequences' tile counts.
     int* pre = reinterpret_cast<int*>(smem + (size_t)NW * (S * 2 * Sh::kTileBytes + Sh::kQBytes));
-    for (int i = tid; i < t.batch; i += NW * 32) pre[i + 1] = Tiles(kv_len(t, i, status), a.window, a.sinks).count;
+    for (int i = tid; i < t.batch; i += NW * 32) pre[i + 1] = Tiles(kv_len(t, i, status), a.window, a.sinks, kShift2).count;
     __syncthreads();
-    if (warp == 0) {
-        int run = 0;
-        for (int i0 = 0; i0 < t.batch; i0 += 32) {
-            const int i = i0 + lane;
-            const int x = warp_inclusive_scan<int>(i < t.batch ? pre[i + 1] : 0, lane) + run;
-            if (i < t.batch) pre[i + 1] = x;
-            run = __shfl_sync(kFullMask, x, 31);
-        }
-        if (lane == 0) pre[0] = 0;
-    }
+    if (warp == 0) prefix_sums(pre, t.batch, lane);
     __syncthreads();
     if (blockIdx.x == 0)
         for (int i = tid; i <= t.batch; i += NW * 32) sc.pre[i] = pre[i];
+    if (blockIdx.x == 0 && warp == 0 && sc.pre_all != sc.pre) {
+        for (int i = lane; i < t.batch; i += 32) sc.pre_all[i + 1] = (kv_len(t, i, status) + T - 1) >> kShift2;
+        __syncwarp();
+        prefix_sums(sc.pre_all, t.batch, lane);
+    }
 
-    const long long total = (long long)pre[t.batch] * sc.units;
-    const int workers = (int)min((long long)gridDim.x * NW, total);
+    const int total = pre[t.batch] * sc.units;
+    const int workers = min((int)gridDim.x * NW, total);
     const int me = warp * gridDim.x + blockIdx.x;  // the first workers are on different SMs
     if (me >= workers) return;
-    const long long t0 = share_begin(me, workers, total);
-    const int n = (int)(share_begin(me + 1, workers, total) - t0);
+    const Shares shares(total, workers);
+    const int t0 = shares.begin(me), n = shares.begin(me + 1) - t0;
+    const int parts = sc.units / c.kv_heads;
 
     // The sequence, unit and tile at t0.
     Cursor cur;
     {
-        int lo = 0, hi = t.batch;
-        while (hi - lo > 1) {  // the last b with pre[b] units <= t0: never an empty one
-            const int mid = (lo + hi) / 2;
-            if ((long long)pre[mid] * sc.units <= t0) lo = mid; else hi = mid;
-        }
-        cur.b = lo;
-        cur.t = Tiles(kv_len(t, lo, status), a.window, a.sinks);
-        const long long r = t0 - (long long)pre[lo] * sc.units;
-        cur.u = (int)(r / cur.t.count);
-        cur.j = (int)(r % cur.t.count);
+        cur.b = find_sequence(pre, t.batch, sc.units, t0);
+        cur.t = Tiles(kv_len(t, cur.b, status), a.window, a.sinks, kShift2);
+        const int r = t0 - pre[cur.b] * sc.units, u = r / cur.t.count;
+        cur.j = r - u * cur.t.count;
+        cur.head = u / parts;
+        cur.part = u - cur.head * parts;
     }
     auto advance = [&](Cursor& x) {
         if (++x.j < x.t.count) return;
         x.j = 0;
-        if (++x.u < sc.units) return;
-        x.u = 0;
+        if (++x.part < parts) return;
+        x.part = 0;
+        if (++x.head < c.kv_heads) return;
+        x.head = 0;
         do ++x.b; while (x.b < t.batch && pre[x.b + 1] == pre[x.b]);
-        if (x.b < t.batch) x.t = Tiles(kv_len(t, x.b, status), a.window, a.sinks);
+        if (x.b < t.batch) x.t = Tiles(kv_len(t, x.b, status), a.window, a.sinks, kShift2);
     };
-    const int units_per_head = sc.units / c.kv_heads;
 
     // ---- the ring: this warp's tiles, filled S - 1 ahead ----
     unsigned char* ring = smem + (size_t)warp * (S * 2 * Sh::kTileBytes);
     const uint32_t ring_a = smem_addr(ring);
+    constexpr int kRows = 32 / Sh::kVecs;  // rows per copy instruction
+    const int cp_row = lane / Sh::kVecs, cp_v = lane % Sh::kVecs;
+    const bool in_row = cp_v * 16 < c.head_dim * Sh::kBytes;
+    const int64_t page_bytes = c.page_stride * Sh::kBytes, head_bytes = c.head_stride * Sh::kBytes, slot_bytes = c.slot_stride * Sh::kBytes;
+    const int64_t cp_at = cp_row * slot_bytes + cp_v * 16;
+    const bool paged_whole = c.page_size % T == 0;  // a tile lies in one page
     Cursor ld = cur;
-    int ld_page;  // the page of this lane's row (lane % 16) of the next tile, fetched one tile ahead
+    int ld_page = 0, ld_slot = 0;  // page and slot of this lane's row (lane % T) of the next tile, fetched one tile ahead
     auto fetch_page = [&]() {
-        const int p = ld.t.tile(ld.j) * kTile + (lane & 15);
-        ld_page = ld.b < t.batch && ld.t.visible(p) ? t.pages[(int64_t)ld.b * t.row_stride + p / c.page_size] : -1;
+        const int p = (ld.t.tile(ld.j) << kShift2) + (lane & (T - 1));
+        const int index = sc.page.div(p);
+        ld_slot = p - index * c.page_size;
+        ld_page = ld.b < t.batch && ld.t.visible(p) ? t.pages[(int64_t)ld.b * t.row_stride + index] : -1;
     };
     auto issue = [&](int stage) {
-        const int p = ld.t.tile(ld.j) * kTile + (lane & 15);
-        int64_t off = -1;
-        if (ld.t.visible(p)) {
-            if (ld_page >= 0 && ld_page < c.num_pages)
-                off = ((int64_t)ld_page * c.page_stride + (int64_t)(ld.u / units_per_head) * c.head_stride +
-                       (int64_t)(p % c.page_size) * c.slot_stride) * Sh::kBytes;
-            else
-                record_error(status, kErrKvTable, (uint32_t)(t.first + ld.b));
-        }
-        constexpr int kRows = 32 / Sh::kVecs > 0 ? 32 / Sh::kVecs : 1;  // rows per copy instruction
-        const int v = lane % Sh::kVecs;
-        const bool in_row = v * 16 < c.head_dim * Sh::kBytes;
         const uint32_t dst = ring_a + stage * (2 * Sh::kTileBytes);
+        const int p0 = ld.t.tile(ld.j) << kShift2;
+        const bool good = ld_page >= 0 && ld_page < c.num_pages;
+        const int64_t off = ld_page * page_bytes + ld.head * head_bytes + ld_slot * slot_bytes;
+        if (paged_whole && ld.t.whole(p0, T) && __all_sync(kFullMask, good)) {
+            // every row is there, one slot after the other from row 0's
+            const char *pk = c.k + cp_at, *pv = c.v + cp_at;
+            const int64_t base = __shfl_sync(kFullMask, off, 0);
+            pk += base;
+            pv += base;
+            const int size = in_row ? 16 : 0;
+            if (!in_row) {  // nothing is read there: any address in the pool
+                pk = c.k;
+                pv = c.v;
+            }
+            const int64_t step = in_row ? kRows * slot_bytes : 0;
 #pragma unroll
-        for (int i = 0; i < kTile / kRows; ++i) {
-            const int row = lane / Sh::kVecs + i * kRows;
-            const int64_t o = __shfl_sync(kFullMask, off, row);
+            for (int i = 0; i < T / kRows; ++i) {
+                const int row = cp_row + i * kRows;
+                cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, pk, size);
+                cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, pv, size);
+                pk += step;
+                pv += step;
+            }
+            return;
+        }
+        const bool see = ld.t.visible(p0 + (lane & (T - 1)));
+        if (see && !good) record_error(status, kErrKvTable, (uint32_t)(t.first + ld.b));
+        const int64_t mine = see && good ? off : -1;
+#pragma unroll
+        for (int i = 0; i < T / kRows; ++i) {
+            const int row = cp_row + i * kRows;
+            const int64_t o = __shfl_sync(kFullMask, mine, row);
             const bool ok = o >= 0 && in_row;  // otherwise the vector is filled with zeros
-            const int64_t at = ok ? o + v * 16 : 0;
-            cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, v) * 16, c.k + at, ok ? 16 : 0);
-            cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, v) * 16, c.v + at, ok ? 16 : 0);
+            const int64_t at = ok ? o + cp_v * 16 : 0;
+            cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, c.k + at, ok ? 16 : 0);
+            cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, c.v + at, ok ? 16 : 0);
         }
     };
     fetch_page();
@@ -298,8 +354,8 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     int head = 0, row0 = 0;    // key-value head, and the unit's first query head within it
 
     auto open_row = [&]() {
-        head = cur.u / units_per_head;
-        row0 = (cur.u % units_per_head) * 16;
+        head = cur.head;
+        row0 = cur.part * 16;
         began = cur.j == 0;
         const QT* q = static_cast<const QT*>(a.q) + (int64_t)cur.b * a.q_seq_stride;
         const int ra = row0 + g, rb = ra + 8;
@@ -462,60 +518,79 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
         const uint32_t kt = ring_a + stage * (2 * Sh::kTileBytes), vt = kt + Sh::kTileBytes;
         stage = stage + 1 == S ? 0 : stage + 1;
 
-        float x[2][4] = {};
+        float x[kPT][4] = {};
         if constexpr (!FP8) {
             const int row = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks) {
-                uint32_t kf[4], f[4];
-                ldmatrix4(kf, kt + row * Sh::kRowBytes + k_vec<FP8, DP>(row, 2 * ks + ((lane >> 3) & 1)) * 16);
+                uint32_t f[4];
                 q_frag(ks, f);
-                mma16816<MT>(x[0], f, kf[0], kf[1]);
-                mma16816<MT>(x[1], f, kf[2], kf[3]);
+#pragma unroll
+                for (int h = 0; h < kPT / 2; ++h) {
+                    uint32_t kf[4];
+                    ldmatrix4(kf, kt + (row + 16 * h) * Sh::kRowBytes + k_vec<FP8, DP>(row, 2 * ks + ((lane >> 3) & 1)) * 16);
+                    mma16816<MT>(x[2 * h], f, kf[0], kf[1]);
+                    mma16816<MT>(x[2 * h + 1], f, kf[2], kf[3]);
+                }
             }
         } else {
 #pragma unroll
             for (int v = 0; v < DP / 64; ++v) {
                 const int vec = q4 * (DP / 64) + v;
-                const uint4 ka = lds128(kt + g * Sh::kRowBytes + k_vec<FP8, DP>(g, vec) * 16);
-                const uint4 kb = lds128(kt + (g + 8) * Sh::kRowBytes + k_vec<FP8, DP>(g + 8, vec) * 16);
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                uint4 kw[kPT];
+#pragma unroll
+                for (int pt = 0; pt < kPT; ++pt) kw[pt] = lds128(kt + (g + 8 * pt) * Sh::kRowBytes + k_vec<FP8, DP>(g, vec) * 16);
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4) {
                     uint32_t f[4];
                     q_frag(v * 4 + i4, f);
-                    mma16816<MT>(x[0], f, e4m3x2_f16x2(wa[i4]), e4m3x2_f16x2(wa[i4] >> 16));
-                    mma16816<MT>(x[1], f, e4m3x2_f16x2(wb[i4]), e4m3x2_f16x2(wb[i4] >> 16));
+#pragma unroll
+                    for (int pt = 0; pt < kPT; ++pt) {
+                        const uint32_t w = i4 == 0 ? kw[pt].x : i4 == 1 ? kw[pt].y : i4 == 2 ? kw[pt].z : kw[pt].w;
+                        mma16816<MT>(x[pt], f, e4m3x2_f16x2(w), e4m3x2_f16x2(w >> 16));
+                    }
                 }
             }
         }
-        const int p0 = cur.t.tile(cur.j) * kTile + 2 * q4;
+        const int p0 = cur.t.tile(cur.j) << kShift2;
+        if (cur.t.whole(p0, T)) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+            for (int pt = 0; pt < kPT; ++pt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool see = cur.t.visible(p0 + nt * 8 + e);
-                x[nt][e] = see ? x[nt][e] * sl0 : -INFINITY;
-                x[nt][2 + e] = see ? x[nt][2 + e] * sl1 : -INFINITY;
-            }
+                for (int e = 0; e < 2; ++e) {
+                    x[pt][e] *= sl0;
+                    x[pt][2 + e] *= sl1;
+                }
+        } else {
+#pragma unroll
+            for (int pt = 0; pt < kPT; ++pt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool see = cur.t.visible(p0 + 2 * q4 + pt * 8 + e);
+                    x[pt][e] = see ? x[pt][e] * sl0 : -INFINITY;
+                    x[pt][2 + e] = see ? x[pt][2 + e] * sl1 : -INFINITY;
+                }
+        }
         if (sc.logits) {
             const int64_t tile = (int64_t)pre[cur.b] * c.kv_heads + (int64_t)head * cur.t.count + cur.j;
-            float* to = sc.logits + (tile * sc.group + row0 + g) * kTile + 2 * q4;
+            float* to = sc.logits + (tile * sc.group + row0 + g) * T + 2 * q4;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                if (row0 + g < sc.group) *reinterpret_cast<float2*>(to + nt * 8) = make_float2(x[nt][0], x[nt][1]);
-                if (row0 + g + 8 < sc.group) *reinterpret_cast<float2*>(to + 8 * kTile + nt * 8) = make_float2(x[nt][2], x[nt][3]);
+            for (int pt = 0; pt < kPT; ++pt) {
+                if (row0 + g < sc.group) *reinterpret_cast<float2*>(to + pt * 8) = make_float2(x[pt][0], x[pt][1]);
+                if (row0 + g + 8 < sc.group) *reinterpret_cast<float2*>(to + 8 * T + pt * 8) = make_float2(x[pt][2], x[pt][3]);
             }
         }
-        float top0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float top1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+        float top0 = m0, top1 = m1;
+#pragma unroll
+        for (int pt = 0; pt < kPT; ++pt) {
+            top0 = fmaxf(top0, fmaxf(x[pt][0], x[pt][1]));
+            top1 = fmaxf(top1, fmaxf(x[pt][2], x[pt][3]));
+        }
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) {
             top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, s));
             top1 = fmaxf(top1, __shfl_xor_sync(kFullMask, top1, s));
         }
-        top0 = fmaxf(top0, m0);
-        top1 = fmaxf(top1, m1);
         if (__any_sync(kFullMask, top0 != m0 || top1 != m1)) {
             const float f0 = top0 == m0 ? 1.0f : exp2_fast(m0 - top0), f1 = top1 == m1 ? 1.0f : exp2_fast(m1 - top1);
             m0 = top0;
@@ -532,70 +607,75 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
         }
         // a row that has seen nothing but -inf keeps reference 0, and P = 0
         const float ref0 = m0 == -INFINITY ? 0.0f : m0 - kShift, ref1 = m1 == -INFINITY ? 0.0f : m1 - kShift;
-        uint32_t ph[4], pl[4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const float a0 = exp2_fast(x[nt][0] - ref0), a1 = exp2_fast(x[nt][1] - ref0);
-            const float b0 = exp2_fast(x[nt][2] - ref1), b1 = exp2_fast(x[nt][3] - ref1);
-            l0 += a0 + a1;
-            l1 += b0 + b1;
-            ph[nt * 2] = pack2<MT>(a0, a1);
-            ph[nt * 2 + 1] = pack2<MT>(b0, b1);
-            if constexpr (kTwo) {
-                const float2 ra = open2<MT>(ph[nt * 2]), rb = open2<MT>(ph[nt * 2 + 1]);
-                pl[nt * 2] = pack2<MT>(a0 - ra.x, a1 - ra.y);
-                pl[nt * 2 + 1] = pack2<MT>(b0 - rb.x, b1 - rb.y);
-            }
-        }
-        if constexpr (!FP8) {
-            const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
+        for (int h = 0; h < kPT / 2; ++h) {  // 16 positions
+            uint32_t ph[4], pl[4];
 #pragma unroll
-            for (int nt = 0; nt < kNT; nt += 2) {
-                uint32_t vf[4];
-                ldmatrix4_t(vf, vt + row * Sh::kRowBytes + v_vec<FP8, DP>(row, nt + (lane >> 4)) * 16);
-                mma16816<MT>(o[nt], ph, vf[0], vf[1]);
-                mma16816<MT>(o[nt + 1], ph, vf[2], vf[3]);
+            for (int k = 0; k < 2; ++k) {
+                const float* y = x[2 * h + k];
+                const float a0 = exp2_fast(y[0] - ref0), a1 = exp2_fast(y[1] - ref0);
+                const float b0 = exp2_fast(y[2] - ref1), b1 = exp2_fast(y[3] - ref1);
+                l0 += a0 + a1;
+                l1 += b0 + b1;
+                ph[k * 2] = pack2<MT>(a0, a1);
+                ph[k * 2 + 1] = pack2<MT>(b0, b1);
                 if constexpr (kTwo) {
-                    mma16816<MT>(o[nt], pl, vf[0], vf[1]);
-                    mma16816<MT>(o[nt + 1], pl, vf[2], vf[3]);
+                    const float2 ra = open2<MT>(ph[k * 2]), rb = open2<MT>(ph[k * 2 + 1]);
+                    pl[k * 2] = pack2<MT>(a0 - ra.x, a1 - ra.y);
+                    pl[k * 2 + 1] = pack2<MT>(b0 - rb.x, b1 - rb.y);
                 }
             }
-        } else {
-            auto four = [&](int nt, uint32_t w0, uint32_t w1, uint32_t w8, uint32_t w9) {
-                // bytes of positions (2 q4, 2 q4 + 1) and (2 q4 + 8, + 9) side by side, for products nt .. nt + 3
-                const uint32_t a01 = __byte_perm(w0, w1, 0x5140), a23 = __byte_perm(w0, w1, 0x7362);
-                const uint32_t b01 = __byte_perm(w8, w9, 0x5140), b23 = __byte_perm(w8, w9, 0x7362);
-                const uint32_t va[4] = {a01, a01 >> 16, a23, a23 >> 16}, vb[4] = {b01, b01 >> 16, b23, b23 >> 16};
+            const uint32_t vh = vt + 16 * h * Sh::kRowBytes;
+            if constexpr (!FP8) {
+                const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t f0 = e4m3x2_f16x2(va[k]), f1 = e4m3x2_f16x2(vb[k]);
-                    mma16816<MT>(o[nt + k], ph, f0, f1);
-                    if constexpr (kTwo) mma16816<MT>(o[nt + k], pl, f0, f1);
+                for (int nt = 0; nt < kNT; nt += 2) {
+                    uint32_t vf[4];
+                    ldmatrix4_t(vf, vh + row * Sh::kRowBytes + v_vec<FP8, DP>(row, nt + (lane >> 4)) * 16);
+                    mma16816<MT>(o[nt], ph, vf[0], vf[1]);
+                    mma16816<MT>(o[nt + 1], ph, vf[2], vf[3]);
+                    if constexpr (kTwo) {
+                        mma16816<MT>(o[nt], pl, vf[0], vf[1]);
+                        mma16816<MT>(o[nt + 1], pl, vf[2], vf[3]);
+                    }
                 }
-            };
-            const int r0 = 2 * q4;
-            if constexpr (DP == 64) {
-                uint2 w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = r0 + (k & 1) + (k >> 1) * 8;
-                    w[k] = lds64(vt + row * Sh::kRowBytes + v_vec<FP8, DP>(row, g >> 1) * 16 + (g & 1) * 8);
-                }
-                four(0, w[0].x, w[1].x, w[2].x, w[3].x);
-                four(4, w[0].y, w[1].y, w[2].y, w[3].y);
             } else {
+                auto four = [&](int nt, uint32_t w0, uint32_t w1, uint32_t w8, uint32_t w9) {
+                    // bytes of positions (2 q4, 2 q4 + 1) and (2 q4 + 8, + 9) side by side, for products nt .. nt + 3
+                    const uint32_t a01 = __byte_perm(w0, w1, 0x5140), a23 = __byte_perm(w0, w1, 0x7362);
+                    const uint32_t b01 = __byte_perm(w8, w9, 0x5140), b23 = __byte_perm(w8, w9, 0x7362);
+                    const uint32_t va[4] = {a01, a01 >> 16, a23, a23 >> 16}, vb[4] = {b01, b01 >> 16, b23, b23 >> 16};
 #pragma unroll
-                for (int v = 0; v < DP / 128; ++v) {
-                    uint4 w[4];
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t f0 = e4m3x2_f16x2(va[k]), f1 = e4m3x2_f16x2(vb[k]);
+                        mma16816<MT>(o[nt + k], ph, f0, f1);
+                        if constexpr (kTwo) mma16816<MT>(o[nt + k], pl, f0, f1);
+                    }
+                };
+                const int r0 = 2 * q4;
+                if constexpr (DP == 64) {
+                    uint2 w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int row = r0 + (k & 1) + (k >> 1) * 8;
-                        w[k] = lds128(vt + row * Sh::kRowBytes + v_vec<FP8, DP>(row, g * (DP / 128) + v) * 16);
+                        w[k] = lds64(vh + row * Sh::kRowBytes + v_vec<FP8, DP>(row, g >> 1) * 16 + (g & 1) * 8);
                     }
-                    four(v * 16, w[0].x, w[1].x, w[2].x, w[3].x);
-                    four(v * 16 + 4, w[0].y, w[1].y, w[2].y, w[3].y);
-                    four(v * 16 + 8, w[0].z, w[1].z, w[2].z, w[3].z);
-                    four(v * 16 + 12, w[0].w, w[1].w, w[2].w, w[3].w);
+                    four(0, w[0].x, w[1].x, w[2].x, w[3].x);
+                    four(4, w[0].y, w[1].y, w[2].y, w[3].y);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < DP / 128; ++v) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = r0 + (k & 1) + (k >> 1) * 8;
+                            w[k] = lds128(vh + row * Sh::kRowBytes + v_vec<FP8, DP>(row, g * (DP / 128) + v) * 16);
+                        }
+                        four(v * 16, w[0].x, w[1].x, w[2].x, w[3].x);
+                        four(v * 16 + 4, w[0].y, w[1].y, w[2].y, w[3].y);
+                        four(v * 16 + 8, w[0].z, w[1].z, w[2].z, w[3].z);
+                        four(v * 16 + 12, w[0].w, w[1].w, w[2].w, w[3].w);
+                    }
                 }
             }
         }
@@ -613,124 +693,281 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
 
 // ---- the second launch: joins, empty rows, weights ----
 
-// The parts of unit u of a sequence: workers [w0, w1]; one worker: no parts.
+// The parts of one unit's rows: workers [w0, w0 + count); one worker: whole.
 struct Parts {
-    int w0, w1;
-    long long s0;
-    __device__ Parts(const Scratch& sc, const int* pre, int batch, int b, int u) {
-        const int count = pre[b + 1] - pre[b];
-        const long long total = (long long)pre[batch] * sc.units;
-        const int n = (int)min((long long)sc.workers, total);
-        s0 = (long long)pre[b] * sc.units + (long long)u * count;
-        w0 = share_of(s0, n, total);
-        w1 = share_of(s0 + count - 1, n, total);
+    int w0, count;
+    // `before` tiles precede the sequence in a unit's list, it has `tiles`, all sequences have `all`.
+    __device__ __forceinline__ Parts(const Scratch& sc, int before, int tiles, int all, int unit) {
+        const int total = all * sc.units;
+        const Shares shares(total, min(sc.workers, total));
+        const int s0 = before * sc.units + unit * tiles;
+        w0 = shares.holder(s0);
+        count = shares.holder(s0 + tiles - 1) - w0 + 1;
     }
     // The first part is its worker's last row, the others are their workers' first ones.
     __device__ __forceinline__ int slot(int i) const { return (w0 + i) * 2 + (i == 0 ? 1 : 0); }
-    __device__ __forceinline__ int count() const { return w1 - w0 + 1; }
 };
 
-// (R, l) of row `row` joined over the parts, by one warp.
-__device__ __forceinline__ float2 join_ml(const Scratch& sc, const Parts& p, int row, int lane) {
+__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.0f : exp2_fast(from - to); }
+
+// R + log2 l of row `row` joined over its parts, by one warp.
+__device__ __forceinline__ float join_lse2(const Scratch& sc, const Parts& p, int row, int lane) {
     float top = -INFINITY, l = 0.0f;
-    for (int i = lane; i < p.count(); i += 32) top = fmaxf(top, sc.ml[p.slot(i) * 16 + row].x);
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, s));
-    for (int i = lane; i < p.count(); i += 32) {
+    for (int i = lane; i < p.count; i += 32) {
         const float2 x = sc.ml[p.slot(i) * 16 + row];
-        l += x.x == -INFINITY ? 0.0f : x.y * exp2_fast(x.x - top);
+        const float up = fmaxf(top, x.x);
+        l = l * rescale(top, up) + x.y * rescale(x.x, up);
+        top = up;
     }
-    return make_float2(top, warp_sum<float>(l));
+    float all = top;
+    for (int s = 16; s > 0; s >>= 1) all = fmaxf(all, __shfl_xor_sync(kFullMask, all, s));
+    l = warp_sum<float>(l * rescale(top, all));
+    return l == 0.0f ? -INFINITY : all + log2f(l);
 }
 
-template <typename QT, int DP>
-__global__ void __launch_bounds__(kFinishThreads) k_kv_finish(KvPages c, KvTable t, KvAttention a, Scratch sc, int chunks,
+// One warp's share of a row's join: the parts team, team + teams, ..., with
+// every load independent of the others.
+template <int DP> struct RowSum {
+    static constexpr int kVec = (DP + 127) / 128;
+    float4 x[kVec];
+    float top, l;
+    __device__ __forceinline__ void add(const Scratch& sc, const Parts& p, int row, int team, int teams, int lane) {
+        top = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        constexpr int kAhead = 4;
+        for (int i0 = team; i0 < p.count; i0 += teams * kAhead) {
+            float2 ml[kAhead];
+            float4 y[kAhead][kVec];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int i = i0 + q * teams;
+                ml[q] = make_float2(-INFINITY, 0.0f);
+                if (i < p.count) ml[q] = sc.ml[p.slot(i) * 16 + row];
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    y[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < p.count && lane + k * 32 < DP / 4)
+                        y[q][k] = reinterpret_cast<const float4*>(sc.o + ((int64_t)p.slot(i) * sc.rows + row) * DP)[lane + k * 32];
+                }
+            }
+            float up = top;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) up = fmaxf(up, ml[q].x);
+            const float f = rescale(top, up);
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                x[k].x *= f;
+                x[k].y *= f;
+                x[k].z *= f;
+                x[k].w *= f;
+            }
+            top = up;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const float e = rescale(ml[q].x, up);
+                l += e * ml[q].y;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    x[k].x += e * y[q][k].x;
+                    x[k].y += e * y[q][k].y;
+                    x[k].z += e * y[q][k].z;
+                    x[k].w += e * y[q][k].w;
+                }
+            }
+        }
+    }
+};
+
+constexpr int kTeamParts = 16;  // rows of more parts than this are joined by a whole CTA
+
+// The second launch: `join_blocks` CTAs of `join_rows` rows each (1 or one per
+// warp) finish the rows that were cut and those without a visible position;
+// the other CTAs share the positions' weights, in equal runs of tiles.
+template <typename QT, int DP, int V>
+__global__ void __launch_bounds__(kFinishThreads) k_kv_finish(KvPages c, KvTable t, KvAttention a, Scratch sc, int join_blocks, int join_rows,
                                                              uint32_t* status) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float s_lse[kMaxGroup];
     __shared__ float4 s_o[kFinishWarps][DP / 4];
+    __shared__ float2 s_ml[kFinishWarps];
+    __shared__ int s_pre[kMaxBatch + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int units_per_head = sc.units / c.kv_heads;
-    const int joins = t.batch * a.q_heads;
-    if ((int)blockIdx.x < joins) {
-        const int b = blockIdx.x / a.q_heads, j = blockIdx.x % a.q_heads;
-        const int h = j / sc.group, r = j % sc.group;
-        QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
-        if (sc.pre[b + 1] == sc.pre[b]) {  // no visible position
-            for (int d = tid; d < c.head_dim; d += kFinishThreads) out[d] = from_f32<QT>(0.0f);
-            if (tid == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + j] = -INFINITY;
-            return;
-        }
-        const Parts p(sc, sc.pre, t.batch, b, h * units_per_head + r / 16);
-        if (p.count() == 1) return;
-        const int row = r % 16;
-        const float2 ml = join_ml(sc, p, row, lane);
-        float4 acc[(DP + 127) / 128] = {};
-        for (int i = warp; i < p.count(); i += kFinishWarps) {
-            const int slot = p.slot(i);
-            const float ref = sc.ml[slot * 16 + row].x;
-            const float f = ref == -INFINITY ? 0.0f : exp2_fast(ref - ml.x);
-            const float4* part = reinterpret_cast<const float4*>(sc.o + ((int64_t)slot * sc.rows + row) * DP);
+    const int parts = sc.units / c.kv_heads;
+    if ((int)blockIdx.x < join_blocks) {
+        const int rows = t.batch * a.q_heads, all = sc.pre[t.batch];
+        auto unit = [&](int j) { return j / sc.group * parts + j % sc.group / 16; };
+        // Adds up the sums of warps [w, w + n) and writes dimensions d0, d0 + step, ... of row r.
+        auto store = [&](int r, int w, int n, int d0, int step) {
+            const int b = r / a.q_heads, j = r % a.q_heads;
+            float top = -INFINITY, l = 0.0f;
+            for (int i = w; i < w + n; ++i) top = fmaxf(top, s_ml[i].x);
+            for (int i = w; i < w + n; ++i) l += s_ml[i].y * rescale(s_ml[i].x, top);
+            const float vs = c.v_scale ? c.v_scale[j / sc.group] : 1.0f;
+            const float inv = l == 0.0f ? 0.0f : vs / l;
+            QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
+            for (int d = d0; d < c.head_dim; d += step) {
+                float x = 0.0f;
+                for (int i = w; i < w + n; ++i) x += reinterpret_cast<const float*>(s_o[i])[d] * rescale(s_ml[i].x, top);
+                out[d] = from_f32<QT>(l == 0.0f ? 0.0f : x * inv);
+            }
+            if (d0 == 0 && a.lse) a.lse[r] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+        };
+        auto keep = [&](const RowSum<DP>& sum) {
 #pragma unroll
-            for (int k = 0; k < (DP + 127) / 128; ++k) {
-                if (lane + k * 32 >= DP / 4) continue;
-                const float4 x = part[lane + k * 32];
-                acc[k].x += f * x.x;
-                acc[k].y += f * x.y;
-                acc[k].z += f * x.z;
-                acc[k].w += f * x.w;
+            for (int k = 0; k < RowSum<DP>::kVec; ++k)
+                if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = sum.x[k];
+            if (lane == 0) s_ml[warp] = make_float2(sum.top, sum.l);
+        };
+        // Each warp looks at its row; long joins are left to the whole CTA.
+        const int r = blockIdx.x * join_rows + (join_rows == 1 ? 0 : warp);
+        bool wide = false;
+        if (r < rows && (join_rows > 1 || warp == 0)) {
+            const int b = r / a.q_heads, j = r % a.q_heads, before = sc.pre[b], tiles = sc.pre[b + 1] - before;
+            if (tiles == 0) {  // no visible position
+                QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
+                for (int d = lane; d < c.head_dim; d += 32) out[d] = from_f32<QT>(0.0f);
+                if (lane == 0 && a.lse) a.lse[r] = -INFINITY;
+            } else {
+                const Parts p(sc, before, tiles, all, unit(j));
+                wide = p.count > (join_rows == 1 ? 1 : kTeamParts);
+                if (!wide && p.count > 1) {
+                    RowSum<DP> sum;
+                    sum.add(sc, p, j % sc.group % 16, 0, 1, lane);
+                    keep(sum);
+                    __syncwarp();
+                    store(r, warp, 1, lane, 32);
+                }
             }
         }
-#pragma unroll
-        for (int k = 0; k < (DP + 127) / 128; ++k)
-            if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = acc[k];
-        __syncthreads();
-        const float vs = c.v_scale ? c.v_scale[h] : 1.0f;
-        const float inv = ml.y == 0.0f ? 0.0f : vs / ml.y;
-        for (int d = tid; d < c.head_dim; d += kFinishThreads) {
-            float x = 0.0f;
-            for (int w = 0; w < kFinishWarps; ++w) x += reinterpret_cast<const float*>(s_o[w])[d];
-            out[d] = from_f32<QT>(ml.y == 0.0f ? 0.0f : x * inv);
+        for (int k = 0; k < join_rows; ++k) {
+            if (!__syncthreads_or(wide && warp == k)) continue;
+            const int rk = blockIdx.x * join_rows + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
+            RowSum<DP> sum;
+            sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j)), j % sc.group % 16, warp, kFinishWarps, lane);
+            keep(sum);
+            __syncthreads();
+            store(rk, 0, kFinishWarps, tid, kFinishThreads);
         }
-        if (tid == 0 && a.lse)
-            a.lse[(int64_t)b * a.q_heads + j] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
         return;
     }
-    // Weights of kWeightChunk positions of one (sequence, key-value head).
-    const int k = blockIdx.x - joins;
-    const int chunk = k % chunks, bh = k / chunks;
-    const int b = bh / c.kv_heads, h = bh % c.kv_heads;
-    const Tiles tl(kv_len(t, b, status), a.window, a.sinks);
-    if (chunk * kWeightChunk >= tl.len) return;
-    for (int r = warp; r < sc.group; r += kFinishWarps) {
-        const Parts p(sc, sc.pre, t.batch, b, h * units_per_head + r / 16);
-        float lse;
-        if (p.count() == 1) {
-            lse = sc.lse2[(int64_t)b * a.q_heads + h * sc.group + r];
-        } else {
-            const float2 ml = join_ml(sc, p, r % 16, lane);
-            lse = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
-        }
-        if (lane == 0) s_lse[r] = lse;
-    }
+
+    // Weights.  Accumulated in place, only visible positions change.
+    const bool only_visible = sc.pre_all == sc.pre;
+    for (int i = tid; i <= t.batch; i += kFinishThreads) s_pre[i] = sc.pre_all[i];
     __syncthreads();
-    const int64_t tile0 = (int64_t)sc.pre[b] * c.kv_heads + (int64_t)h * tl.count;
-    for (int p = chunk * kWeightChunk + tid; p < min(tl.len, (chunk + 1) * kWeightChunk); p += kFinishThreads) {
-        const bool see = tl.visible(p);
-        if (!see && a.weight_in == a.weight_out) continue;  // accumulated in place: nothing to add
-        const int page = kv_page(t, c.num_pages, b, p / c.page_size, status);
-        if (page < 0) continue;
-        float w = 0.0f;
-        if (see) {
-            const int tile = p / kTile;
-            const int j = tile < tl.nsink ? tile : tl.nsink + tile - tl.first;
-            const float* x = sc.logits + (tile0 + j) * sc.group * kTile + p % kTile;
-            for (int r = 0; r < sc.group; ++r) {
-                const float z = s_lse[r];
-                w += z == -INFINITY ? 0.0f : exp2_fast(x[r * kTile] - z);
-            }
+    const int total = s_pre[t.batch] * c.kv_heads;
+    const int blocks = min((int)gridDim.x - join_blocks, (total + kWeightTiles - 1) / kWeightTiles);
+    const int me = blockIdx.x - join_blocks;
+    if (me >= blocks) return;
+    const Shares shares(total, blocks);
+    int at = shares.begin(me);
+    const int end = shares.begin(me + 1), T = 1 << sc.shift;
+    int b = find_sequence(s_pre, t.batch, c.kv_heads, at);
+    while (at < end) {
+        const int tiles = s_pre[b + 1] - s_pre[b];
+        if (tiles == 0) {
+            ++b;
+            continue;
         }
-        const int64_t at = ((int64_t)page * c.kv_heads + h) * c.page_size + p % c.page_size;
-        a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.0f) + w;
+        const int in_b = at - s_pre[b] * c.kv_heads, h = in_b / tiles, j0 = in_b - h * tiles;
+        const int j1 = min(tiles, j0 + (end - at));
+        const Tiles tl(kv_len(t, b, status), a.window, a.sinks, sc.shift);
+        const int before = only_visible ? s_pre[b] : sc.pre[b], all = only_visible ? s_pre[t.batch] : sc.pre[t.batch];
+        const float* scores = sc.logits + ((int64_t)before * c.kv_heads + (int64_t)h * tl.count) * sc.group * T;
+
+        // V consecutive positions: their place in the pool, old weights and
+        // the first rows' scores.  Loaded before the sums of the rows are
+        // joined, which takes as long as the loads.
+        constexpr int kRowsAhead = 4;
+        int p = 0;
+        int64_t to = -1;
+        const float* x = nullptr;
+        float old[V], y[kRowsAhead][V];
+        auto load = [&](int i) {
+            to = -1;
+            const int j = j0 + (i >> sc.shift), in = i & (T - 1);
+            const int tile = only_visible ? tl.tile(j) : j;
+            p = (tile << sc.shift) + in;
+            if (p >= tl.len) return;
+            const int index = sc.page.div(p);
+            const int page = kv_page(t, c.num_pages, b, index, status);
+            const bool stored = tile < tl.nsink || tile >= tl.first;  // the tile has scores
+            x = stored ? scores + (int64_t)(tile < tl.nsink ? tile : tl.nsink + tile - tl.first) * sc.group * T + in : nullptr;
+#pragma unroll
+            for (int q = 0; q < kRowsAhead; ++q) {
+                if constexpr (V == 4) {
+                    float4 z = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    if (stored && q < sc.group) z = __ldcs(reinterpret_cast<const float4*>(x + q * T));
+                    y[q][0] = z.x; y[q][1] = z.y; y[q][2] = z.z; y[q][3] = z.w;
+                } else {
+                    y[q][0] = stored && q < sc.group ? __ldcs(x + q * T) : -INFINITY;
+                }
+            }
+            if (page < 0) return;
+            to = ((int64_t)page * c.kv_heads + h) * c.page_size + (p - index * c.page_size);
+            if constexpr (V == 4) {  // positions of one page, 16-byte aligned
+                const float4 z = a.weight_in ? *reinterpret_cast<const float4*>(a.weight_in + to) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                old[0] = z.x; old[1] = z.y; old[2] = z.z; old[3] = z.w;
+            } else {
+                old[0] = a.weight_in ? a.weight_in[to] : 0.0f;
+            }
+        };
+        auto finish = [&]() {
+            if (to < 0) return;
+            float w[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kRowsAhead; ++q)
+                if (q < sc.group)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) w[e] += exp2_fast(y[q][e] - s_lse[q]);
+            if (x) {
+#pragma unroll 4
+                for (int r = kRowsAhead; r < sc.group; ++r) {
+                    if constexpr (V == 4) {
+                        const float4 z = __ldcs(reinterpret_cast<const float4*>(x + r * T));
+                        w[0] += exp2_fast(z.x - s_lse[r]);
+                        w[1] += exp2_fast(z.y - s_lse[r]);
+                        w[2] += exp2_fast(z.z - s_lse[r]);
+                        w[3] += exp2_fast(z.w - s_lse[r]);
+                    } else {
+                        w[0] += exp2_fast(__ldcs(x + r * T) - s_lse[r]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (!tl.visible(p + e)) w[e] = 0.0f;  // also where a NaN row makes 2^(-inf - NaN)
+            if constexpr (V == 4) {
+                if (p + 3 < tl.len) {
+                    *reinterpret_cast<float4*>(a.weight_out + to) = make_float4(old[0] + w[0], old[1] + w[1], old[2] + w[2], old[3] + w[3]);
+                    return;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (p + e < tl.len) a.weight_out[to + e] = old[e] + w[e];
+        };
+
+        const int count = (j1 - j0) << sc.shift;
+        if (tid * V < count) load(tid * V);
+        for (int r = warp; r < sc.group; r += kFinishWarps) {
+            const Parts p(sc, before, tl.count, all, h * parts + r / 16);
+            const float lse = p.count == 1 ? sc.lse2[(int64_t)b * a.q_heads + h * sc.group + r] : join_lse2(sc, p, r % 16, lane);
+            if (lane == 0) s_lse[r] = lse == -INFINITY ? INFINITY : lse;  // a row without weights: 2^(X - inf) = 0
+        }
+        __syncthreads();
+        for (int i = tid * V; i < count; i += kFinishThreads * V) {
+            if (i != tid * V) load(i);
+            finish();
+        }
+        __syncthreads();
+        at += j1 - j0;
+        if (j1 == tiles && h + 1 == c.kv_heads) ++b;
     }
 }
 
@@ -744,23 +981,25 @@ struct Plan {
     size_t at_lse2, at_ml, at_o, at_logits, bytes;
 };
 
-Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int warps, int dp, int sms) {
+Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int warps, int dp, int tile, int sms) {
     Plan p{};
     p.dp = dp;
     p.warps = warps;
     p.sc.group = a.q_heads / c.kv_heads;
     p.sc.units = c.kv_heads * ((p.sc.group + 15) / 16);
     p.sc.rows = p.sc.group < 16 ? p.sc.group : 16;
-    const size_t tiles = ((size_t)t.max_len + kTile - 1) / kTile;  // of one sequence and unit, at most
-    const size_t seq_logits = a.weight_out ? tiles * a.q_heads * kTile * 4 : 0;
+    const size_t tiles = ((size_t)t.max_len + tile - 1) / tile;  // of one sequence and unit, at most
+    const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
     size_t batch = (size_t)t.batch < kMaxBatch ? t.batch : kMaxBatch;
     if (seq_logits * batch > kMaxLogits) batch = kMaxLogits / seq_logits;
-    while (batch > 1 && batch * tiles > 0x7fffffff) batch /= 2;
+    while (batch > 1 && batch * tiles * p.sc.units > 0x7fffffff) batch /= 2;  // lists are counted in 32 bits
     p.batch = batch < 1 ? 1 : (int)batch;
     const size_t most = (size_t)p.batch * tiles * p.sc.units;
     p.grid = most < (size_t)sms ? (most < 1 ? 1 : (int)most) : sms;
     p.sc.workers = p.grid * warps;
-    p.at_lse2 = round256((kMaxBatch + 1) * 4);
+    p.sc.shift = tile == 16 ? 4 : 5;
+    p.sc.page = FastDiv(c.page_size);
+    p.at_lse2 = 2 * round256((kMaxBatch + 1) * 4);
     p.at_ml = p.at_lse2 + round256((size_t)p.batch * a.q_heads * 4);
     p.at_o = p.at_ml + round256((size_t)p.sc.workers * 2 * 16 * 8);
     p.at_logits = p.at_o + round256((size_t)p.sc.workers * 2 * p.sc.rows * dp * 4);
@@ -768,21 +1007,23 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int war
     return p;
 }
 
-template <typename QT, bool FP8, int DP, int NW, int S>
+template <typename QT, bool FP8, int DP, int T, int NW, int S>
 cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
-    auto* kern = k_kv_attend<QT, FP8, DP, NW, S>;
-    constexpr size_t smem = Shape<QT, FP8, DP, NW, S>::kSmem;
+    auto* kern = k_kv_attend<QT, FP8, DP, T, NW, S>;
+    constexpr size_t smem = Shape<FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
     KernelSetup su;
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
     if (e != cudaSuccess) return e;
-    Plan p = make_plan(c, t, a, NW, DP, su.sms);
+    Plan p = make_plan(c, t, a, NW, DP, T, su.sms);
     if (scratch == nullptr) {
         *bytes = p.bytes;
         return cudaSuccess;
     }
     char* base = static_cast<char*>(scratch);
     p.sc.pre = reinterpret_cast<int*>(base);
+    p.sc.pre_all = p.sc.pre;
+    if (a.window > 0 && a.weight_out && a.weight_in != a.weight_out) p.sc.pre_all = reinterpret_cast<int*>(base + p.at_lse2 / 2);
     p.sc.lse2 = reinterpret_cast<float*>(base + p.at_lse2);
     p.sc.ml = reinterpret_cast<float2*>(base + p.at_ml);
     p.sc.o = reinterpret_cast<float*>(base + p.at_o);
@@ -800,10 +1041,22 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         kern<<<p.grid, NW * 32, smem, s>>>(c, u, v, p.sc, status);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int chunks = (t.max_len + kWeightChunk - 1) / kWeightChunk;
-        const size_t blocks = (size_t)u.batch * a.q_heads + (a.weight_out ? (size_t)u.batch * c.kv_heads * chunks : 0);
+        // One row per CTA until there are more rows than resident warps would
+        // leave idle; then one per warp.
+        const int rows = u.batch * a.q_heads;
+        const int join_rows = rows >= su.sms * kFinishWarps ? kFinishWarps : 1;
+        const int join_blocks = (rows + join_rows - 1) / join_rows;
+        size_t weight_blocks = 0;
+        bool vec4 = false;
+        if (a.weight_out) {
+            const size_t tiles = ((size_t)t.max_len + T - 1) / T * u.batch * c.kv_heads;
+            weight_blocks = (tiles + kWeightTiles - 1) / kWeightTiles;
+            const size_t most = (size_t)su.sms * 8;  // resident at 256 threads
+            weight_blocks = weight_blocks < most ? weight_blocks : most;
+            vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;
+        }
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.gridDim = dim3((unsigned)(join_blocks + weight_blocks));
         cfg.blockDim = dim3(kFinishThreads);
         cfg.stream = s;
         cudaLaunchAttribute at;
@@ -811,19 +1064,20 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         at.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k_kv_finish<QT, DP>, c, u, v, p.sc, chunks, status);
+        e = cudaLaunchKernelEx(&cfg, vec4 ? k_kv_finish<QT, DP, 4> : k_kv_finish<QT, DP, 1>, c, u, v, p.sc, join_blocks, join_rows, status);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-// Warps and stages by tile size: the ring takes about 192 KB of the SM, and
-// the warps as many as their registers allow.
+// Tile, warps and stages by row size: the ring takes about 192 KB of the SM,
+// and the warps as many as their registers allow.  8-bit rows take tiles of 32
+// positions, which spreads a tile's fixed instructions over as many bytes.
 template <typename QT, bool FP8>
 cudaError_t run_dim(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
-    if (c.head_dim <= 64) return run<QT, FP8, 64, FP8 ? 16 : 12, FP8 ? 6 : 4>(c, t, a, scratch, bytes, status, s);
-    if (c.head_dim <= 128) return run<QT, FP8, 128, FP8 ? 12 : 8, FP8 ? 4 : 3>(c, t, a, scratch, bytes, status, s);
-    return run<QT, FP8, 256, FP8 ? 7 : 4, 3>(c, t, a, scratch, bytes, status, s);
+    if (c.head_dim <= 64) return run<QT, FP8, 64, 32, FP8 ? 12 : 8, FP8 ? 4 : 3>(c, t, a, scratch, bytes, status, s);
+    if (c.head_dim <= 128) return run<QT, FP8, 128, FP8 ? 32 : 16, 8, 3>(c, t, a, scratch, bytes, status, s);
+    return run<QT, FP8, 256, 16, FP8 ? 7 : 4, 3>(c, t, a, scratch, bytes, status, s);
 }
 
 cudaError_t run_any(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {

@@ -192,6 +192,13 @@ def test_attend_infinities_and_nan_spread_as_in_the_formula(ss):
     ss.ss_kv_attend(pages, table, q, out2, window=20)
     ok(ss)
     assert bool(torch.isfinite(out2[[0, 1, 3]]).all())
+    # a NaN inside the window spreads to the visible weights only
+    c.k[at(1, 25)] = math.nan
+    w = torch.zeros_like(c.weight)
+    ss.ss_kv_attend(pages, table, q, out2, window=20, weight_out=w)
+    ok(ss)
+    assert all(math.isnan(float(w[at(1, p)])) == (p >= 10) for p in range(30))
+    assert all(float(w[at(1, p)]) == 0.0 for p in range(10))
 
 
 def test_attend_is_the_same_on_every_run_and_stream(ss):
