@@ -1,6 +1,6 @@
 // kv_attend.cu -- attention of one new token per sequence over a paged
 // key-value cache (streamscan.h, ss_kv_attend), split over the cache's length
-// and joined, in two launches.
+// and joined, in two launches, and a third where weights are kept.
 //
 // Mathematics.  For one key-value head, its `group` query heads are the rows
 // of a 16-row matrix Q.  Over a tile of 16 positions, X = (Q K^T) scale log2 e
@@ -24,7 +24,7 @@
 // that lie within one warp's share are written at once; a share's first and
 // last row may be parts, which go to scratch, and the second launch joins
 // them.  Where weights are kept, the first launch leaves X (fp32) in scratch
-// and the second turns it into weights, since they need the joined sums.
+// and the third turns it into weights, since they need the joined sums.
 #include "kv.cuh"
 
 namespace ss {
@@ -32,10 +32,9 @@ namespace ss {
 namespace {
 
 constexpr int kMaxBatch = 512;  // sequences per launch: their tile counts' prefix sums are in shared memory
-constexpr int kFinishThreads = 256;
-constexpr int kFinishWarps = kFinishThreads / 32;
-constexpr int kWeightTiles = 16;  // tiles that a CTA of the weights' part takes at least
-constexpr int kMaxGroup = 128;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kWeightThreads = 256;
 constexpr size_t kMaxLogits = (size_t)2 << 30;  // bytes of scores one launch may leave in scratch
 
 // Which positions of a sequence are visible, and in which tiles they lie: the
@@ -61,7 +60,7 @@ struct Tiles {
 struct Scratch {
     int* pre;       // batch + 1: tiles of the sequences before, per unit
     int* pre_all;   // the same of all positions, where those that are not visible get a weight too (else pre)
-    float* lse2;    // batch x q_heads: R + log2 l of the rows the first launch finished
+    float* lse2;    // batch x q_heads: R + log2 l of every row, for the weights
     float2* ml;     // workers x 2 x 16: (R, l) of a part
     float* o;       // workers x 2 x rows x DP: its O
     float* logits;  // per (sequence, key-value head) tile: group x 16 scores, log2 units; or null
@@ -189,6 +188,14 @@ template <bool FP8, int DP> __device__ __forceinline__ int v_vec(int row, int v)
     if (DP == 64) return v ^ ((row >> 1) & 3);
     if (DP == 128) return v ^ (((row >> 1) & 3) << 1);
     return v ^ ((row >> 1) & 1) ^ (((row >> 2) & 1) << 2);
+}
+
+// The sum of row `at` (sequence * q_heads + head): R and l.  A row without
+// weights leaves +inf for the weights' pass, where 2^(X - inf) = 0.
+__device__ __forceinline__ void store_lse(const Scratch& sc, const KvAttention& a, int64_t at, float ref, float l) {
+    const float x = ref + log2f(l);
+    sc.lse2[at] = l == 0.0f ? INFINITY : x;
+    if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : x * 0.6931471805599453f;
 }
 
 // A place in the list of tiles: sequence, key-value head, 16 query heads of
@@ -483,13 +490,9 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
                 if (in[half] && d < c.head_dim) *reinterpret_cast<uint32_t*>(po[half] + d) = pack2<QT>(x * f[half], y * f[half]);
             });
             if (q4 == 0) {
-                const float z[2] = {la == 0.0f ? -INFINITY : m0 - kShift + log2f(la), lb == 0.0f ? -INFINITY : m1 - kShift + log2f(lb)};
-                for (int half = 0; half < 2; ++half) {
-                    const int64_t at = (int64_t)cur.b * a.q_heads + head * sc.group + (half ? rb : ra);
-                    if (!in[half]) continue;
-                    sc.lse2[at] = z[half];
-                    if (a.lse) a.lse[at] = z[half] * 0.6931471805599453f;
-                }
+                const int64_t at = (int64_t)cur.b * a.q_heads + head * sc.group;
+                if (in[0]) store_lse(sc, a, at + ra, m0 - kShift, la);
+                if (in[1]) store_lse(sc, a, at + rb, m1 - kShift, lb);
             }
             return;
         }
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     cp_wait<0>();
 }
 
-// ---- the second launch: joins, empty rows, weights ----
+// ---- the second and third launch: joins, empty rows, weights ----
 
 // The parts of one unit's rows: workers [w0, w0 + count); one worker: whole.
 struct Parts {
@@ -709,21 +712,6 @@ struct Parts {
 };
 
 __device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.0f : exp2_fast(from - to); }
-
-// R + log2 l of row `row` joined over its parts, by one warp.
-__device__ __forceinline__ float join_lse2(const Scratch& sc, const Parts& p, int row, int lane) {
-    float top = -INFINITY, l = 0.0f;
-    for (int i = lane; i < p.count; i += 32) {
-        const float2 x = sc.ml[p.slot(i) * 16 + row];
-        const float up = fmaxf(top, x.x);
-        l = l * rescale(top, up) + x.y * rescale(x.x, up);
-        top = up;
-    }
-    float all = top;
-    for (int s = 16; s > 0; s >>= 1) all = fmaxf(all, __shfl_xor_sync(kFullMask, all, s));
-    l = warp_sum<float>(l * rescale(top, all));
-    return l == 0.0f ? -INFINITY : all + log2f(l);
-}
 
 // One warp's share of a row's join: the parts team, team + teams, ..., with
 // every load independent of the others.
@@ -783,191 +771,142 @@ template <int DP> struct RowSum {
 
 constexpr int kTeamParts = 16;  // rows of more parts than this are joined by a whole CTA
 
-// The second launch: `join_blocks` CTAs of `join_rows` rows each (1 or one per
-// warp) finish the rows that were cut and those without a visible position;
-// the other CTAs share the positions' weights, in equal runs of tiles.
-template <typename QT, int DP, int V>
-__global__ void __launch_bounds__(kFinishThreads) k_kv_finish(KvPages c, KvTable t, KvAttention a, Scratch sc, int join_blocks, int join_rows,
-                                                             uint32_t* status) {
-    __shared__ float s_lse[kMaxGroup];
-    __shared__ float4 s_o[kFinishWarps][DP / 4];
-    __shared__ float2 s_ml[kFinishWarps];
-    __shared__ int s_pre[kMaxBatch + 1];
+// The second launch finishes the rows that were cut and those without a
+// visible position: `per` rows a CTA, 1 or one per warp.
+template <typename QT, int DP>
+__global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, KvAttention a, Scratch sc, int per) {
+    __shared__ float4 s_o[kJoinWarps][DP / 4];
+    __shared__ float2 s_ml[kJoinWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int parts = sc.units / c.kv_heads;
-    if ((int)blockIdx.x < join_blocks) {
-        const int rows = t.batch * a.q_heads, all = sc.pre[t.batch];
-        auto unit = [&](int j) { return j / sc.group * parts + j % sc.group / 16; };
-        // Adds up the sums of warps [w, w + n) and writes dimensions d0, d0 + step, ... of row r.
-        auto store = [&](int r, int w, int n, int d0, int step) {
-            const int b = r / a.q_heads, j = r % a.q_heads;
-            float top = -INFINITY, l = 0.0f;
-            for (int i = w; i < w + n; ++i) top = fmaxf(top, s_ml[i].x);
-            for (int i = w; i < w + n; ++i) l += s_ml[i].y * rescale(s_ml[i].x, top);
-            const float vs = c.v_scale ? c.v_scale[j / sc.group] : 1.0f;
-            const float inv = l == 0.0f ? 0.0f : vs / l;
+    const int units_per_head = sc.units / c.kv_heads;
+    const int rows = t.batch * a.q_heads, all = sc.pre[t.batch];
+    auto unit = [&](int j) { return j / sc.group * units_per_head + j % sc.group / 16; };
+    // Adds up the sums of warps [w, w + n) and writes dimensions d0, d0 + step, ... of row r.
+    auto store = [&](int r, int w, int n, int d0, int step) {
+        const int b = r / a.q_heads, j = r % a.q_heads;
+        float top = -INFINITY, l = 0.0f;
+        for (int i = w; i < w + n; ++i) top = fmaxf(top, s_ml[i].x);
+        for (int i = w; i < w + n; ++i) l += s_ml[i].y * rescale(s_ml[i].x, top);
+        const float vs = c.v_scale ? c.v_scale[j / sc.group] : 1.0f;
+        const float inv = l == 0.0f ? 0.0f : vs / l;
+        QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
+        for (int d = d0; d < c.head_dim; d += step) {
+            float x = 0.0f;
+            for (int i = w; i < w + n; ++i) x += reinterpret_cast<const float*>(s_o[i])[d] * rescale(s_ml[i].x, top);
+            out[d] = from_f32<QT>(l == 0.0f ? 0.0f : x * inv);
+        }
+        if (d0 == 0) store_lse(sc, a, r, top, l);
+    };
+    auto keep = [&](const RowSum<DP>& sum) {
+#pragma unroll
+        for (int k = 0; k < RowSum<DP>::kVec; ++k)
+            if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = sum.x[k];
+        if (lane == 0) s_ml[warp] = make_float2(sum.top, sum.l);
+    };
+    // Each warp looks at its row; long joins are left to the whole CTA.
+    const int r = blockIdx.x * per + (per == 1 ? 0 : warp);
+    bool wide = false;
+    if (r < rows && (per > 1 || warp == 0)) {
+        const int b = r / a.q_heads, j = r % a.q_heads, before = sc.pre[b], tiles = sc.pre[b + 1] - before;
+        if (tiles == 0) {  // no visible position
             QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
-            for (int d = d0; d < c.head_dim; d += step) {
-                float x = 0.0f;
-                for (int i = w; i < w + n; ++i) x += reinterpret_cast<const float*>(s_o[i])[d] * rescale(s_ml[i].x, top);
-                out[d] = from_f32<QT>(l == 0.0f ? 0.0f : x * inv);
-            }
-            if (d0 == 0 && a.lse) a.lse[r] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
-        };
-        auto keep = [&](const RowSum<DP>& sum) {
-#pragma unroll
-            for (int k = 0; k < RowSum<DP>::kVec; ++k)
-                if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = sum.x[k];
-            if (lane == 0) s_ml[warp] = make_float2(sum.top, sum.l);
-        };
-        // Each warp looks at its row; long joins are left to the whole CTA.
-        const int r = blockIdx.x * join_rows + (join_rows == 1 ? 0 : warp);
-        bool wide = false;
-        if (r < rows && (join_rows > 1 || warp == 0)) {
-            const int b = r / a.q_heads, j = r % a.q_heads, before = sc.pre[b], tiles = sc.pre[b + 1] - before;
-            if (tiles == 0) {  // no visible position
-                QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
-                for (int d = lane; d < c.head_dim; d += 32) out[d] = from_f32<QT>(0.0f);
-                if (lane == 0 && a.lse) a.lse[r] = -INFINITY;
-            } else {
-                const Parts p(sc, before, tiles, all, unit(j));
-                wide = p.count > (join_rows == 1 ? 1 : kTeamParts);
-                if (!wide && p.count > 1) {
-                    RowSum<DP> sum;
-                    sum.add(sc, p, j % sc.group % 16, 0, 1, lane);
-                    keep(sum);
-                    __syncwarp();
-                    store(r, warp, 1, lane, 32);
-                }
+            for (int d = lane; d < c.head_dim; d += 32) out[d] = from_f32<QT>(0.0f);
+            if (lane == 0 && a.lse) a.lse[r] = -INFINITY;
+        } else {
+            const Parts p(sc, before, tiles, all, unit(j));
+            wide = p.count > (per == 1 ? 1 : kTeamParts);
+            if (!wide && p.count > 1) {
+                RowSum<DP> sum;
+                sum.add(sc, p, j % sc.group % 16, 0, 1, lane);
+                keep(sum);
+                __syncwarp();
+                store(r, warp, 1, lane, 32);
             }
         }
-        for (int k = 0; k < join_rows; ++k) {
-            if (!__syncthreads_or(wide && warp == k)) continue;
-            const int rk = blockIdx.x * join_rows + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
-            RowSum<DP> sum;
-            sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j)), j % sc.group % 16, warp, kFinishWarps, lane);
-            keep(sum);
-            __syncthreads();
-            store(rk, 0, kFinishWarps, tid, kFinishThreads);
-        }
-        return;
     }
+    if (!__syncthreads_or(wide)) return;
+    for (int k = 0; k < per; ++k) {
+        if (!__syncthreads_or(wide && warp == k)) continue;
+        const int rk = blockIdx.x * per + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
+        RowSum<DP> sum;
+        sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j)), j % sc.group % 16, warp, kJoinWarps, lane);
+        keep(sum);
+        __syncthreads();
+        store(rk, 0, kJoinWarps, tid, kJoinThreads);
+    }
+}
 
-    // Weights.  Accumulated in place, only visible positions change.
-    const bool only_visible = sc.pre_all == sc.pre;
-    for (int i = tid; i <= t.batch; i += kFinishThreads) s_pre[i] = sc.pre_all[i];
+// The third launch, where weights are kept: every thread takes V consecutive
+// positions of one tile, and every tile finds its sequence and head by itself,
+// so that short sequences cost no more than long ones.  Accumulated in place,
+// only visible positions change.
+template <int V>
+__global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
+    __shared__ int s_pre[kMaxBatch + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i <= t.batch; i += kWeightThreads) s_pre[i] = sc.pre_all[i];
     __syncthreads();
-    const int total = s_pre[t.batch] * c.kv_heads;
-    const int blocks = min((int)gridDim.x - join_blocks, (total + kWeightTiles - 1) / kWeightTiles);
-    const int me = blockIdx.x - join_blocks;
-    if (me >= blocks) return;
-    const Shares shares(total, blocks);
-    int at = shares.begin(me);
-    const int end = shares.begin(me + 1), T = 1 << sc.shift;
-    int b = find_sequence(s_pre, t.batch, c.kv_heads, at);
-    while (at < end) {
+    const bool only_visible = sc.pre_all == sc.pre;
+    const int T = 1 << sc.shift, total = s_pre[t.batch] * c.kv_heads;
+    const int per_tile = T / V;
+    const int64_t end = (int64_t)total * per_tile;
+    for (int64_t at = (int64_t)blockIdx.x * kWeightThreads + threadIdx.x; at < end; at += (int64_t)gridDim.x * kWeightThreads) {
+        const int tile_at = (int)(at / per_tile), in = (int)(at % per_tile) * V;
+        const int b = find_sequence(s_pre, t.batch, c.kv_heads, tile_at);
         const int tiles = s_pre[b + 1] - s_pre[b];
-        if (tiles == 0) {
-            ++b;
-            continue;
-        }
-        const int in_b = at - s_pre[b] * c.kv_heads, h = in_b / tiles, j0 = in_b - h * tiles;
-        const int j1 = min(tiles, j0 + (end - at));
+        const int in_b = tile_at - s_pre[b] * c.kv_heads, h = in_b / tiles, j = in_b - h * tiles;
         const Tiles tl(kv_len(t, b, status), a.window, a.sinks, sc.shift);
-        const int before = only_visible ? s_pre[b] : sc.pre[b], all = only_visible ? s_pre[t.batch] : sc.pre[t.batch];
-        const float* scores = sc.logits + ((int64_t)before * c.kv_heads + (int64_t)h * tl.count) * sc.group * T;
-
-        // V consecutive positions: their place in the pool, old weights and
-        // the first rows' scores.  Loaded before the sums of the rows are
-        // joined, which takes as long as the loads.
-        constexpr int kRowsAhead = 4;
-        int p = 0;
-        int64_t to = -1;
-        const float* x = nullptr;
-        float old[V], y[kRowsAhead][V];
-        auto load = [&](int i) {
-            to = -1;
-            const int j = j0 + (i >> sc.shift), in = i & (T - 1);
-            const int tile = only_visible ? tl.tile(j) : j;
-            p = (tile << sc.shift) + in;
-            if (p >= tl.len) return;
-            const int index = sc.page.div(p);
-            const int page = kv_page(t, c.num_pages, b, index, status);
-            const bool stored = tile < tl.nsink || tile >= tl.first;  // the tile has scores
-            x = stored ? scores + (int64_t)(tile < tl.nsink ? tile : tl.nsink + tile - tl.first) * sc.group * T + in : nullptr;
+        const int tile = only_visible ? tl.tile(j) : j;
+        const int p = (tile << sc.shift) + in;
+        if (p >= tl.len) continue;
+        const int index = sc.page.div(p);
+        const int page = kv_page(t, c.num_pages, b, index, status);
+        if (page < 0) continue;
+        const int64_t to = ((int64_t)page * c.kv_heads + h) * c.page_size + (p - index * c.page_size);
+        float w[V], old[V];
 #pragma unroll
-            for (int q = 0; q < kRowsAhead; ++q) {
-                if constexpr (V == 4) {
-                    float4 z = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    if (stored && q < sc.group) z = __ldcs(reinterpret_cast<const float4*>(x + q * T));
-                    y[q][0] = z.x; y[q][1] = z.y; y[q][2] = z.z; y[q][3] = z.w;
-                } else {
-                    y[q][0] = stored && q < sc.group ? __ldcs(x + q * T) : -INFINITY;
-                }
-            }
-            if (page < 0) return;
-            to = ((int64_t)page * c.kv_heads + h) * c.page_size + (p - index * c.page_size);
-            if constexpr (V == 4) {  // positions of one page, 16-byte aligned
-                const float4 z = a.weight_in ? *reinterpret_cast<const float4*>(a.weight_in + to) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int e = 0; e < V; ++e) w[e] = old[e] = 0.0f;
+        if constexpr (V == 4) {  // positions of one page, 16-byte aligned
+            if (a.weight_in) {
+                const float4 z = *reinterpret_cast<const float4*>(a.weight_in + to);
                 old[0] = z.x; old[1] = z.y; old[2] = z.z; old[3] = z.w;
-            } else {
-                old[0] = a.weight_in ? a.weight_in[to] : 0.0f;
             }
-        };
-        auto finish = [&]() {
-            if (to < 0) return;
-            float w[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kRowsAhead; ++q)
-                if (q < sc.group)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) w[e] += exp2_fast(y[q][e] - s_lse[q]);
-            if (x) {
+        } else {
+            if (a.weight_in) old[0] = a.weight_in[to];
+        }
+        if (tile < tl.nsink || tile >= tl.first) {  // the tile has scores
+            const int before = only_visible ? s_pre[b] : sc.pre[b];
+            const int64_t jv = (int64_t)before * c.kv_heads + (int64_t)h * tl.count + (tile < tl.nsink ? tile : tl.nsink + tile - tl.first);
+            const float* x = sc.logits + jv * sc.group * T + in;
+            const float* lse = sc.lse2 + (int64_t)b * a.q_heads + h * sc.group;
 #pragma unroll 4
-                for (int r = kRowsAhead; r < sc.group; ++r) {
-                    if constexpr (V == 4) {
-                        const float4 z = __ldcs(reinterpret_cast<const float4*>(x + r * T));
-                        w[0] += exp2_fast(z.x - s_lse[r]);
-                        w[1] += exp2_fast(z.y - s_lse[r]);
-                        w[2] += exp2_fast(z.z - s_lse[r]);
-                        w[3] += exp2_fast(z.w - s_lse[r]);
-                    } else {
-                        w[0] += exp2_fast(__ldcs(x + r * T) - s_lse[r]);
-                    }
+            for (int r = 0; r < sc.group; ++r) {
+                const float z = lse[r];
+                if constexpr (V == 4) {
+                    const float4 y = __ldcs(reinterpret_cast<const float4*>(x + r * T));
+                    w[0] += exp2_fast(y.x - z);
+                    w[1] += exp2_fast(y.y - z);
+                    w[2] += exp2_fast(y.z - z);
+                    w[3] += exp2_fast(y.w - z);
+                } else {
+                    w[0] += exp2_fast(__ldcs(x + r * T) - z);
                 }
             }
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (!tl.visible(p + e)) w[e] = 0.0f;  // also where a NaN row makes 2^(-inf - NaN)
-            if constexpr (V == 4) {
-                if (p + 3 < tl.len) {
-                    *reinterpret_cast<float4*>(a.weight_out + to) = make_float4(old[0] + w[0], old[1] + w[1], old[2] + w[2], old[3] + w[3]);
-                    return;
-                }
+        }
+        if constexpr (V == 4) {
+            if (p + 3 < tl.len) {
+                *reinterpret_cast<float4*>(a.weight_out + to) = make_float4(old[0] + w[0], old[1] + w[1], old[2] + w[2], old[3] + w[3]);
+                continue;
             }
+        }
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (p + e < tl.len) a.weight_out[to + e] = old[e] + w[e];
-        };
-
-        const int count = (j1 - j0) << sc.shift;
-        if (tid * V < count) load(tid * V);
-        for (int r = warp; r < sc.group; r += kFinishWarps) {
-            const Parts p(sc, before, tl.count, all, h * parts + r / 16);
-            const float lse = p.count == 1 ? sc.lse2[(int64_t)b * a.q_heads + h * sc.group + r] : join_lse2(sc, p, r % 16, lane);
-            if (lane == 0) s_lse[r] = lse == -INFINITY ? INFINITY : lse;  // a row without weights: 2^(X - inf) = 0
-        }
-        __syncthreads();
-        for (int i = tid * V; i < count; i += kFinishThreads * V) {
-            if (i != tid * V) load(i);
-            finish();
-        }
-        __syncthreads();
-        at += j1 - j0;
-        if (j1 == tiles && h + 1 == c.kv_heads) ++b;
+        for (int e = 0; e < V; ++e)
+            if (p + e < tl.len) a.weight_out[to + e] = old[e] + w[e];
     }
 }
 
@@ -1041,30 +980,27 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         kern<<<p.grid, NW * 32, smem, s>>>(c, u, v, p.sc, status);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        // One row per CTA until there are more rows than resident warps would
-        // leave idle; then one per warp.
-        const int rows = u.batch * a.q_heads;
-        const int join_rows = rows >= su.sms * kFinishWarps ? kFinishWarps : 1;
-        const int join_blocks = (rows + join_rows - 1) / join_rows;
-        size_t weight_blocks = 0;
-        bool vec4 = false;
-        if (a.weight_out) {
-            const size_t tiles = ((size_t)t.max_len + T - 1) / T * u.batch * c.kv_heads;
-            weight_blocks = (tiles + kWeightTiles - 1) / kWeightTiles;
-            const size_t most = (size_t)su.sms * 8;  // resident at 256 threads
-            weight_blocks = weight_blocks < most ? weight_blocks : most;
-            vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(join_blocks + weight_blocks));
-        cfg.blockDim = dim3(kFinishThreads);
-        cfg.stream = s;
+        // One row per CTA until there are more rows than an SM's worth of warps
+        // on every SM; then one per warp.
+        const int rows = u.batch * a.q_heads, per = rows >= su.sms * kJoinWarps ? kJoinWarps : 1;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.stream = s;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, vec4 ? k_kv_finish<QT, DP, 4> : k_kv_finish<QT, DP, 1>, c, u, v, p.sc, join_blocks, join_rows, status);
+        e = cudaLaunchKernelEx(&cfg, k_kv_join<QT, DP>, c, u, v, p.sc, per);
+        if (e != cudaSuccess) return e;
+        if (a.weight_out == nullptr) continue;
+        const bool vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;
+        const size_t tiles = ((size_t)t.max_len + T - 1) / T * u.batch * c.kv_heads;
+        const size_t blocks = (tiles * (vec4 ? T / 4 : T) + kWeightThreads - 1) / kWeightThreads, most = (size_t)su.sms * 8;
+        cfg.gridDim = dim3((unsigned)(blocks < most ? blocks < 1 ? 1 : blocks : most));
+        cfg.blockDim = dim3(kWeightThreads);
+        e = cudaLaunchKernelEx(&cfg, vec4 ? k_kv_weights<4> : k_kv_weights<1>, c, u, v, p.sc, status);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
