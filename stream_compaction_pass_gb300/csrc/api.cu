@@ -484,7 +484,7 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     st = get_workspace((cudaStream_t)stream, &w);
     if (st != SS_OK) return st;
     cudaError_t e = ss::launch_kv_append(c, t, static_cast<ss::KvElem>(type), k_new, v_new, token_stride, head_stride,
-                                         offsets, (int64_t)tokens, ws_status(w), (cudaStream_t)stream);
+                                         offsets, (int64_t)tokens, device_sms(w->device), ws_status(w), (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "append launch");
 } catch (...) {
     return SS_ERR_NO_MEMORY;
@@ -577,7 +577,8 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
         if (st != SS_OK) return st;
         kept = static_cast<int32_t*>(w->kv);
     }
-    cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, ws_status(w), (cudaStream_t)stream);
+    cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, device_sms(w->device), ws_status(w),
+                                        (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "eviction launch");
 } catch (...) {
     return SS_ERR_NO_MEMORY;

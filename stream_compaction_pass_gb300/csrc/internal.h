@@ -202,13 +202,13 @@ struct KvAttention {
 };
 cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, const void* k_new, const void* v_new,
                              int64_t token_stride, int64_t head_stride, const int32_t* offsets, int64_t tokens,
-                             uint32_t* status, cudaStream_t s);
+                             int sms, uint32_t* status, cudaStream_t s);
 // Device scratch of one attention call, in bytes.
 cudaError_t kv_attend_scratch(const KvPages& c, const KvTable& t, const KvAttention& a, size_t* bytes);
 cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, uint32_t* status,
                              cudaStream_t s);
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
-                            int sinks, int recent, int32_t* kept, uint32_t* status, cudaStream_t s);
+                            int sinks, int recent, int32_t* kept, int sms, uint32_t* status, cudaStream_t s);
 
 // Ablations (reduce-then-scan, three kernels).  `totals` holds one value
 // per 4096-element tile.  tile_scan: 0 = register/shuffle tile scan,

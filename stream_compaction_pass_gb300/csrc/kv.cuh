@@ -26,6 +26,16 @@ struct FastDiv {
     __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
 };
 
+// Rows of a CTA that first looks up its rows' places, a thread a row, and then
+// moves their vectors, `round` rows at a time: more rounds share the look-up,
+// as long as every SM still has 8 CTAs of them, up to `most` rows.
+inline int kv_rows_per_cta(int round, int most, int64_t rows, int sms) {
+    round = round < 1 ? 1 : round > most ? most : round;
+    int64_t rounds = rows / ((int64_t)round * sms * 8);
+    rounds = rounds < 1 ? 1 : rounds > most / round ? most / round : rounds;
+    return round * (int)rounds;
+}
+
 // The length of sequence b as every kernel reads it: clamped to what the
 // table can hold, and reported where it had to be.
 __device__ __forceinline__ int kv_len(const KvTable& t, int b, uint32_t* status) {

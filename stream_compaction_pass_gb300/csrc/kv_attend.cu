@@ -32,7 +32,7 @@ namespace ss {
 namespace {
 
 constexpr int kMaxBatch = 512;  // sequences per launch: their tile counts' prefix sums are in shared memory
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
 constexpr size_t kMaxLogits = (size_t)2 << 30;  // bytes of scores one launch may leave in scratch
@@ -97,8 +97,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -292,6 +292,8 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     const int64_t page_bytes = c.page_stride * Sh::kBytes, head_bytes = c.head_stride * Sh::kBytes, slot_bytes = c.slot_stride * Sh::kBytes;
     const int64_t cp_at = cp_row * slot_bytes + cp_v * 16;
     const bool paged_whole = c.page_size % T == 0;  // a tile lies in one page
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     Cursor ld = cur;
     int ld_page = 0, ld_slot = 0;  // page and slot of this lane's row (lane % T) of the next tile, fetched one tile ahead
     auto fetch_page = [&]() {
@@ -320,8 +322,8 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
 #pragma unroll
             for (int i = 0; i < T / kRows; ++i) {
                 const int row = cp_row + i * kRows;
-                cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, pk, size);
-                cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, pv, size);
+                cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, pk, size, policy);
+                cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, pv, size, policy);
                 pk += step;
                 pv += step;
             }
@@ -336,8 +338,8 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
             const int64_t o = __shfl_sync(kFullMask, mine, row);
             const bool ok = o >= 0 && in_row;  // otherwise the vector is filled with zeros
             const int64_t at = ok ? o + cp_v * 16 : 0;
-            cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, c.k + at, ok ? 16 : 0);
-            cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, c.v + at, ok ? 16 : 0);
+            cp_async16(dst + row * Sh::kRowBytes + k_vec<FP8, DP>(row, cp_v) * 16, c.k + at, ok ? 16 : 0, policy);
+            cp_async16(dst + Sh::kTileBytes + row * Sh::kRowBytes + v_vec<FP8, DP>(row, cp_v) * 16, c.v + at, ok ? 16 : 0, policy);
         }
     };
     fetch_page();
@@ -724,7 +726,7 @@ template <int DP> struct RowSum {
         l = 0.0f;
 #pragma unroll
         for (int k = 0; k < kVec; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        constexpr int kAhead = 4;
+        constexpr int kAhead = DP == 256 ? 4 : 8;
         for (int i0 = team; i0 < p.count; i0 += teams * kAhead) {
             float2 ml[kAhead];
             float4 y[kAhead][kVec];
@@ -980,9 +982,10 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         kern<<<p.grid, NW * 32, smem, s>>>(c, u, v, p.sc, status);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        // One row per CTA until there are more rows than an SM's worth of warps
-        // on every SM; then one per warp.
-        const int rows = u.batch * a.q_heads, per = rows >= su.sms * kJoinWarps ? kJoinWarps : 1;
+        // One row per warp, except where rows are few, or have so many parts on
+        // average that a whole CTA joins each.
+        const int rows = u.batch * a.q_heads;
+        const int per = rows <= 2 * su.sms || p.sc.workers > kTeamParts * u.batch * p.sc.units ? 1 : kJoinWarps;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at.val.programmaticStreamSerializationAllowed = 1;
