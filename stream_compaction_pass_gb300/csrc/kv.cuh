@@ -69,11 +69,9 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return
 // weight has the smaller key, -0 and +0 the same one, NaN the last.  Key 0 is
 // no number's: it stands for the positions that stay whatever their weight.
 __device__ __forceinline__ uint32_t evict_key(float w) {
-    if (w != w) return 0xffffffffu;
-    uint32_t u = __float_as_uint(w);
-    if (u == 0x80000000u) u = 0;
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);  // ascending in the weight
-    return ~u;
+    const int u = __float_as_int(w + 0.0f);  // -0 + 0 = +0
+    const uint32_t k = (uint32_t)u ^ ((uint32_t)(~u >> 31) & 0x7fffffffu);
+    return w != w ? 0xffffffffu : k;
 }
 
 }  // namespace ss

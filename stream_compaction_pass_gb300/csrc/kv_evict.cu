@@ -13,9 +13,7 @@
 // by memory.  The selection reads 4 bytes a position; it is bound by latency
 // (three passes, each with a histogram, a scan and a barrier).  A row is one
 // CTA's; where there are few rows it is split over a cluster of up to 8 CTAs,
-// which add up their histograms through distributed shared memory.  The keys
-// of a share stay in shared memory where they fit; longer ones are read again
-// in every pass, from L2.
+// which add up their histograms through distributed shared memory.
 #include <cooperative_groups.h>
 
 #include "kv.cuh"
@@ -28,7 +26,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStaged = 48 * 1024;  // keys a CTA can hold in shared memory
+constexpr int kStagedShare = 16384;            // the longest share whose keys are kept in shared memory
+constexpr int kMaskedShare = 512 * 1024;       // the longest share whose classes are
+static_assert((int64_t)kMaskedShare * kMaxCluster == kKvMaxEvict, "the longest sequence is what a cluster can hold");
 
 template <int N> struct SelectShared {
     uint32_t hist[3][kBins];  // one per pass: nobody clears what another CTA still reads
@@ -44,16 +44,22 @@ struct Choice {
 };
 
 // One cluster per (sequence, head); its CTAs take consecutive shares of the
-// positions, each a multiple of 4 long.  STAGED: the keys of a share fit in
-// shared memory (otherwise every pass reads the weights again).  V: weights
-// are read in fours, which lie in one page and are 16-byte aligned.
-// N threads.
+// positions, each a multiple of 4 long.  N threads.  V: weights are read in
+// fours, which lie in one page and are 16-byte aligned.
+//
+// Every position is classed by what is known of its key: below T, possibly T,
+// above.  STAGED: the keys of a share are read once and stay in shared memory,
+// 4 bytes a position, and so do their classes implicitly.  Otherwise a share
+// keeps 2 bits a position (a byte for four: low half below T, high half
+// possibly T), the first two passes read every weight, and the later ones
+// only those of fours that may still hold T.
 template <int N, bool STAGED, int V>
 __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* __restrict__ kept,
-                                                             int32_t* __restrict__ new_lens, uint32_t* status) {
+                                                 int32_t* __restrict__ new_lens, uint32_t* status) {
     constexpr int kWarps = N / 32, kPer = kBins / N;  // bins a thread adds up
     __shared__ SelectShared<N> sh;
-    extern __shared__ __align__(16) uint32_t s_keys[];
+    extern __shared__ __align__(16) unsigned char s_share[];
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_share);  // STAGED
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -73,78 +79,97 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
         if (ranks == 1) __syncthreads(); else cluster.sync();
     };
 
-    // Four keys of the share from position i on (a multiple of 4); past the
-    // share's end they are meaningless.  A page out of range reads page 0 and
-    // ranks last, so that loads wait for no branch; it is reported at the end.
+    // Four keys of the share from position i < count on (a multiple of 4);
+    // those past the share's end are the last of all.  A page out of range
+    // reads page 0 and ranks last, so that no load waits for a branch; it is
+    // reported at the end.
     bool bad = false;
+    const int32_t* pages = t.pages + (int64_t)b * t.row_stride;
+    const float* weight = c.weight + (int64_t)h * c.page_size;
+    const int64_t per_page = (int64_t)c.kv_heads * c.page_size;
     auto place = [&](int p, bool& good) {
-        const int index = ch.page.div(p), page = __ldg(t.pages + (int64_t)b * t.row_stride + index);
-        good = page >= 0 && page < c.num_pages;
-        return ((int64_t)(good ? page : 0) * c.kv_heads + h) * c.page_size + (p - index * c.page_size);
+        const int index = ch.page.div(p), page = __ldg(pages + index);
+        good = (uint32_t)page < (uint32_t)c.num_pages;
+        return weight + ((good ? page : 0) * per_page + (p - index * c.page_size));
     };
     auto read4 = [&](int i, uint32_t (&k)[4]) {
-        const int p = begin + min(i, (count - 1) / 4 * 4);  // in range whatever i is
+        const int p = begin + i;
         float w[4];
         bool good[4];
         if constexpr (V == 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(c.weight + place(p, good[0])));
+            const float4 x = __ldg(reinterpret_cast<const float4*>(place(p, good[0])));
             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
             good[1] = good[2] = good[3] = good[0];
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = __ldg(c.weight + place(min(p + e, len - 1), good[e]));
+            for (int e = 0; e < 4; ++e) w[e] = __ldg(place(min(p + e, len - 1), good[e]));
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = evict_key(w[e]);
+        if (p >= ch.sinks && p + 4 <= len - ch.recent && i + 4 <= count && good[0] && good[1] && good[2] && good[3]) return;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            k[e] = p + e < ch.sinks || p + e >= len - ch.recent ? 0u : good[e] ? evict_key(w[e]) : 0xffffffffu;
             bad |= !good[e];
+            if (!good[e] || i + e >= count) k[e] = 0xffffffffu;
+            else if (p + e < ch.sinks || p + e >= len - ch.recent) k[e] = 0u;
         }
     };
-    auto keys4 = [&](int i, uint32_t (&k)[4]) {
-        if constexpr (STAGED) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
-            k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
-        } else {
-            read4(i, k);
-        }
+    // Calls f(position) for this thread's fours, several at a time.
+    constexpr int kAhead = 4;
+    auto each_four = [&](auto&& f) {
+        for (int i0 = tid * 4; i0 < count; i0 += N * 4 * kAhead) f(i0);
     };
-    // Visits the share's keys as (position, key), several loads at a time.
-    auto each_key = [&](auto&& read, auto&& f) {
-        constexpr int kAhead = 4;
-        for (int i0 = tid * 4; i0 < count; i0 += N * 4 * kAhead) {
-            uint32_t k[kAhead][4];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (a == 0 || i0 + a * N * 4 < count) read(i0 + a * N * 4, k[a]);
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (i0 + a * N * 4 < count) f(i0 + a * N * 4, k[a]);
-        }
-    };
+    auto in_share = [&](int i0, int a) { return a == 0 || i0 + a * N * 4 < count; };
 
     for (int i = tid; i < 3 * kBins; i += N) (&sh.hist[0][0])[i] = 0;
     __syncthreads();
-    // First pass: the keys enter shared memory and their top digit is counted.
-    each_key(read4, [&](int i, const uint32_t (&k)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (i + e < count) atomicAdd(&sh.hist[0][k[e] >> 21], 1u);
-        if constexpr (STAGED) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
-    });
-
     uint32_t prefix = 0, want = (uint32_t)m;  // T's digits so far; which of the keys sharing them is T, from 1
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t bins = pass == 2 ? 1024u : 2048u;
-        if (pass > 0) {
-            const int above = pass == 1 ? 21 : 10;
-            each_key(keys4, [&](int i, const uint32_t (&k)[4]) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;  // of this pass's digit
+        const int above = pass == 1 ? 21 : 10;                   // of the digits known
+        const uint32_t digits = pass == 2 ? 1023u : 2047u;
+        each_four([&](int i0) {
+            uint32_t k[kAhead][4];
+            unsigned char cls[kAhead];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (k[e] >> above == prefix >> above && i + e < count) atomicAdd(&sh.hist[pass][(k[e] >> shift) & (bins - 1)], 1u);
-            });
-        }
+            for (int a = 0; a < kAhead; ++a) {
+                if (!in_share(i0, a)) continue;
+                const int i = i0 + a * N * 4;
+                cls[a] = 0xf0;
+                if (!STAGED && pass == 2) cls[a] = s_share[i / 4];
+                if (STAGED && pass > 0) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
+                    k[a][0] = x.x; k[a][1] = x.y; k[a][2] = x.z; k[a][3] = x.w;
+                } else if (cls[a] & 0xf0) {
+                    read4(i, k[a]);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                if (!in_share(i0, a)) continue;
+                const int i = i0 + a * N * 4;
+                if (STAGED && pass == 0) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[a][0], k[a][1], k[a][2], k[a][3]);
+                if (!(cls[a] & 0xf0)) continue;
+                uint32_t now = cls[a] & 0x0fu;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool maybe = (STAGED || pass < 2) ? (pass > 0 || i + e < count) : (cls[a] >> (4 + e)) & 1;
+                    if (pass == 0) {
+                        if (maybe) atomicAdd(&sh.hist[0][k[a][e] >> 21], 1u);
+                        continue;
+                    }
+                    const uint32_t known = k[a][e] >> above;
+                    if (maybe && known == prefix >> above && i + e < count) {
+                        atomicAdd(&sh.hist[pass][(k[a][e] >> shift) & digits], 1u);
+                        now |= 0x10u << e;
+                    } else if (maybe && known < prefix >> above) {
+                        now |= 1u << e;
+                    }
+                }
+                if (!STAGED && pass > 0) s_share[i / 4] = (unsigned char)now;
+            }
+        });
         meet();
         // Every thread sums kPer consecutive bins over the cluster; a scan over the block finds the bin of the want-th key.
         uint32_t s[kPer] = {}, mine = 0;
@@ -186,22 +211,28 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     // low half and equal to T in the high half.
     const int part = ((count + kWarps - 1) / kWarps + 127) / 128 * 128;
     const int from = min(warp * part, count), to = min(from + part, count);
-    auto classify = [&](int i, uint32_t (&k)[4], uint32_t (&is)[4]) {
-        keys4(i, k);
-        uint32_t sum = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            is[e] = i + e >= to ? 0u : k[e] < prefix ? 1u : k[e] == prefix ? 0x10000u : 0u;
-            sum += is[e];
+    auto classes = [&](int i) -> uint32_t {  // of the four from i on, final
+        uint32_t k[4], cls = 0xf0u;
+        if constexpr (STAGED) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
+            k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
+        } else {
+            cls = s_share[i / 4];
+            if (!(cls & 0xf0u)) return cls;
+            read4(i, k);
         }
-        return sum;
+        uint32_t now = cls & 0x0fu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((cls >> (4 + e) & 1u) && i + e < to) now |= k[e] < prefix ? 1u << e : k[e] == prefix ? 0x10u << e : 0u;
+        return now;
     };
     uint32_t lt = 0, eq = 0;
     for (int i = from + lane * 4; i < to; i += 128) {
-        uint32_t k[4], is[4];
-        const uint32_t sum = classify(i, k, is);
-        lt += sum & 0xffffu;
-        eq += sum >> 16;
+        const uint32_t cls = classes(i);
+        if constexpr (!STAGED) s_share[i / 4] = (unsigned char)cls;
+        lt += __popc(cls & 0x0fu);
+        eq += __popc(cls & 0xf0u);
     }
     lt = warp_sum<uint32_t>(lt);
     eq = warp_sum<uint32_t>(eq);
@@ -232,17 +263,19 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     }
     for (int i0 = from; i0 < to; i0 += 128) {
         const int i = i0 + lane * 4;
-        uint32_t k[4], is[4], sum = 0;
-        is[0] = is[1] = is[2] = is[3] = 0;
-        if (i < to) sum = classify(i, k, is);
+        uint32_t cls = 0;
+        if (i < to) {
+            if constexpr (STAGED) cls = classes(i); else cls = s_share[i / 4];
+        }
+        const uint32_t sum = __popc(cls & 0x0fu) | __popc(cls & 0xf0u) << 16;
         const uint32_t incl = warp_inclusive_scan<uint32_t>(sum, lane);
         uint32_t my_lt = lt + ((incl - sum) & 0xffffu), my_eq = eq + ((incl - sum) >> 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t at = my_lt + min(my_eq, want);
-            if ((is[e] == 1u || (is[e] && my_eq < want)) && at < (uint32_t)m) out[at] = begin + i + e;
-            my_lt += is[e] & 0xffffu;
-            my_eq += is[e] >> 16;
+            const uint32_t is_lt = cls >> e & 1u, is_eq = cls >> (4 + e) & 1u, at = my_lt + min(my_eq, want);
+            if ((is_lt || (is_eq && my_eq < want)) && at < (uint32_t)m) out[at] = begin + i + e;
+            my_lt += is_lt;
+            my_eq += is_eq;
         }
         const uint32_t all = __shfl_sync(kFullMask, incl, 31);
         lt += all & 0xffffu;
@@ -319,23 +352,22 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     // One CTA per row where there are rows for half the SMs; otherwise a row is
     // split, into shares of 2048 positions or more, while the CTAs fit the SMs.
     int ranks = 1;
-    while (ranks < kMaxCluster && (int64_t)rows * ranks * 2 <= sms && t.max_len / (ranks * 2) >= 2048) ranks *= 2;
+    auto split = [&](int r) { return (int64_t)rows * r * 2 <= sms && t.max_len / (r * 2) >= 2048; };
+    while (ranks < kMaxCluster && (split(ranks) || t.max_len / ranks > kMaskedShare - 4)) ranks *= 2;
     const int share = ((t.max_len + ranks - 1) / ranks + 3) / 4 * 4;
-    const bool staged = share <= kMaxStaged;
+    const bool staged = share <= kStagedShare;
     const bool vec4 = c.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(c.weight) & 15u) == 0;
-    const bool large = share > 16384;  // 32 keys a thread at 512 threads: twice the threads from here on
-    auto* kern = large ? (staged ? (vec4 ? k_kv_select<1024, true, 4> : k_kv_select<1024, true, 1>) : (vec4 ? k_kv_select<1024, false, 4> : k_kv_select<1024, false, 1>))
-                       : (vec4 ? k_kv_select<512, true, 4> : k_kv_select<512, true, 1>);
-    const int threads = large ? 1024 : 512;
+    auto* kern = staged ? (vec4 ? k_kv_select<512, true, 4> : k_kv_select<512, true, 1>) : (vec4 ? k_kv_select<1024, false, 4> : k_kv_select<1024, false, 1>);
+    const int threads = staged ? 512 : 1024, bytes_most = staged ? kStagedShare * 4 : kMaskedShare / 4;
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), threads, staged ? (size_t)kMaxStaged * 4 : 0, &su);
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), threads, (size_t)bytes_most, &su);
     if (e != cudaSuccess) return e;
 
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * ranks);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = staged ? (size_t)share * 4 : 0;
+    cfg.dynamicSmemBytes = staged ? (size_t)share * 4 : (size_t)share / 4;
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ranks;
