@@ -461,23 +461,31 @@ def ss_temp_status(temp, stream=None):
     return st, tile.value
 
 
+_elems = {}  # torch dtype -> the library's element type
+
+
 def _elem(t) -> int:
     """The library's element type of a torch tensor."""
-    name = str(t.dtype)
-    kinds = {"torch.bfloat16": SS_BF16, "torch.float16": SS_F16, "torch.float8_e4m3fn": SS_E4M3}
-    if name not in kinds:
-        raise TypeError(f"{name} is not a type of the key-value cache calls (bfloat16, float16, float8_e4m3fn)")
-    return kinds[name]
+    if not _elems:
+        import torch
+        _elems.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float8_e4m3fn: SS_E4M3})
+    kind = _elems.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{t.dtype} is not a type of the key-value cache calls (bfloat16, float16, float8_e4m3fn)")
+    return kind
 
 
 def _like(name: str, t, shape, dtype: str):
     """Checks an optional tensor argument's shape, type and (for contiguous
     arguments) layout; the C ABI sees only addresses."""
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or str(t.dtype) != "torch." + dtype or not t.is_contiguous():
+    if t is not None and (t.shape != shape or t.dtype is not _dtype(dtype) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                          f"{str(t.dtype)[6:]} {tuple(t.shape)}")
+
+
+def _dtype(name: str):
+    import torch
+    return getattr(torch, name)
 
 
 class KVPages:
@@ -501,7 +509,7 @@ class KVPages:
         _like("k_scale", k_scale, (heads,), "float32")
         _like("v_scale", v_scale, (heads,), "float32")
         self.k, self.v, self.weight, self.k_scale, self.v_scale = k, v, weight, k_scale, v_scale
-        self.kv_heads, self.head_dim = heads, dim
+        self.kv_heads, self.head_dim, self.weight_shape = heads, dim, k.shape[:3]
         self._c = _KvPages(_elem(k), heads, dim, page, pages, _addr(k), _addr(v), k.stride(0), k.stride(1),
                            k.stride(2), _addr(k_scale), _addr(v_scale), _addr(weight))
         self._ref = ctypes.addressof(self._c)
@@ -540,11 +548,13 @@ def ss_kv_append(cache: KVPages, seqs: KVTable, k_new, v_new, offsets=None, stre
     int32 (batch + 1,), or None for one token per sequence."""
     if k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.dtype != v_new.dtype or k_new.stride() != v_new.stride():
         raise ValueError("k_new and v_new must be 3-dimensional, of one shape, type and strides")
-    if tuple(k_new.shape[1:]) != (cache.kv_heads, cache.head_dim) or k_new.stride(2) != 1:
+    tokens, heads, dim = k_new.shape
+    token_stride, head_stride, unit = k_new.stride()
+    if heads != cache.kv_heads or dim != cache.head_dim or unit != 1:
         raise ValueError(f"k_new must be (tokens, {cache.kv_heads}, {cache.head_dim}) with a contiguous last dimension")
     _like("offsets", offsets, (seqs.batch + 1,), "int32")
-    _check(lib().ss_kv_append(cache._ref, seqs._ref, _elem(k_new), k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
-                              k_new.stride(1), _addr(offsets), k_new.shape[0], _stream(stream, k_new)), "ss_kv_append")
+    _check(lib().ss_kv_append(cache._ref, seqs._ref, _elem(k_new), k_new.data_ptr(), v_new.data_ptr(), token_stride,
+                              head_stride, _addr(offsets), tokens, _stream(stream, k_new)), "ss_kv_append")
 
 
 def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int = 0, sinks: int = 0, lse=None,
@@ -553,18 +563,20 @@ def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int 
     into out; scale defaults to head_dim ** -0.5.  lse: float32 (batch,
     q_heads).  weight_out, weight_in: float32 tensors of the pool's weight
     shape (weight_out = weight_in = cache.weight accumulates in place)."""
-    if q.dim() != 3 or q.shape != out.shape or q.dtype != out.dtype or q.stride(2) != 1 or out.stride(2) != 1:
-        raise ValueError("q and out must be 3-dimensional, of one shape and type, with a contiguous last dimension")
-    if q.shape[0] != seqs.batch or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be ({seqs.batch}, q_heads, {cache.head_dim})")
-    _like("lse", lse, q.shape[:2], "float32")
+    if q.dim() != 3 or q.shape != out.shape or q.dtype != out.dtype:
+        raise ValueError("q and out must be 3-dimensional, of one shape and type")
+    batch, heads, dim = q.shape
+    q_seq, q_head, q_unit = q.stride()
+    out_seq, out_head, out_unit = out.stride()
+    if batch != seqs.batch or dim != cache.head_dim or q_unit != 1 or out_unit != 1:
+        raise ValueError(f"q and out must be ({seqs.batch}, q_heads, {cache.head_dim}) with a contiguous last dimension")
+    _like("lse", lse, (batch, heads), "float32")
     if weight_in is not None or weight_out is not None:
-        shape = tuple(cache.k.shape[:3])
-        _like("weight_in", weight_in, shape, "float32")
-        _like("weight_out", weight_out, shape, "float32")
-    a = _KvAttention(_elem(q), q.shape[1], q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0),
-                     out.stride(1), cache.head_dim ** -0.5 if scale is None else scale, window, sinks, _addr(lse),
-                     _addr(weight_in), _addr(weight_out))
+        _like("weight_in", weight_in, cache.weight_shape, "float32")
+        _like("weight_out", weight_out, cache.weight_shape, "float32")
+    a = _KvAttention(_elem(q), heads, q.data_ptr(), q_seq, q_head, out.data_ptr(), out_seq, out_head,
+                     dim ** -0.5 if scale is None else scale, window, sinks, _addr(lse), _addr(weight_in),
+                     _addr(weight_out))
     _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a), _stream(stream, q)), "ss_kv_attend")
 
 

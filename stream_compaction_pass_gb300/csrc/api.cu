@@ -565,7 +565,7 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     if (t.batch == 0) return SS_OK;
     if (overlaps(t.lens, (size_t)t.batch * 4, dt.lens, (size_t)t.batch * 4))
         return fail(SS_ERR_INVALID_ARG, "the lengths of src_seqs and dst_seqs overlap");
-    if (t.max_len > ss::kKvMaxEvict) return fail(SS_ERR_INVALID_ARG, "max_len must be at most 2^22 for an eviction");
+    if (t.max_len > ss::kKvMaxEvict) return fail(SS_ERR_INVALID_ARG, "max_len must be at most 2^21 for an eviction");
     if ((int64_t)t.batch * c.kv_heads * (std::min(keep, t.max_len) / 16 + 1) > 0x7fffffff)
         return fail(SS_ERR_INVALID_ARG, "batch * kv_heads * kept positions is too large for one call");
     if (std::min(keep, t.max_len) > (int64_t)dt.max_pages * d.page_size)

@@ -207,7 +207,7 @@ cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, co
 cudaError_t kv_attend_scratch(const KvPages& c, const KvTable& t, const KvAttention& a, size_t* bytes);
 cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, uint32_t* status,
                              cudaStream_t s);
-constexpr int kKvMaxEvict = 1 << 22;  // the longest sequence an eviction takes
+constexpr int kKvMaxEvict = 1 << 21;  // the longest sequence an eviction takes
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
                             int sinks, int recent, int32_t* kept, int sms, uint32_t* status, cudaStream_t s);
 

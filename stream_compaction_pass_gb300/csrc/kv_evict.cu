@@ -27,39 +27,55 @@ namespace cg = cooperative_groups;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kStagedShare = 16384;            // the longest share whose keys are kept in shared memory
-constexpr int kMaskedShare = 512 * 1024;       // the longest share whose classes are
-static_assert((int64_t)kMaskedShare * kMaxCluster == kKvMaxEvict, "the longest sequence is what a cluster can hold");
+constexpr int kClassedShare = 256 * 1024;      // the longest share whose classes are
+constexpr int kBlock = 1024;                   // positions a warp compacts at a time
+constexpr int kListed = 16384;                 // candidates a long share keeps, 8 bytes each
+static_assert((int64_t)kClassedShare * kMaxCluster == kKvMaxEvict, "the longest sequence is what a cluster can hold");
 
 template <int N> struct SelectShared {
     uint32_t hist[3][kBins];  // one per pass: nobody clears what another CTA still reads
     uint32_t counts[2];       // this CTA's keys below T, and equal to it
     uint32_t warp_lt[N / 32], warp_eq[N / 32];
-    uint32_t digit, before;
+    uint32_t digit, before, listed;
 };
 
 // What the selection is asked for.
 struct Choice {
     int keep, sinks, recent;
-    FastDiv page;  // by src's page_size
+    int most_share;  // the longest share that the launch provides for, a multiple of 4
+    FastDiv page;    // by src's page_size
 };
+
+// Shared memory of the selection before its classes, and in all.
+__host__ __device__ constexpr int select_front(int threads, bool staged, int share) {
+    const int blocks = threads / 32 * kBlock * 4, first = staged ? share * 4 : kListed * 8;
+    return first > blocks ? first : blocks;
+}
+constexpr int select_bytes(int threads, bool staged, int share) { return select_front(threads, staged, share) + (share / 4 + 15) / 16 * 16; }
 
 // One cluster per (sequence, head); its CTAs take consecutive shares of the
 // positions, each a multiple of 4 long.  N threads.  V: weights are read in
 // fours, which lie in one page and are 16-byte aligned.
 //
-// Every position is classed by what is known of its key: below T, possibly T,
-// above.  STAGED: the keys of a share are read once and stay in shared memory,
-// 4 bytes a position, and so do their classes implicitly.  Otherwise a share
-// keeps 2 bits a position (a byte for four: low half below T, high half
-// possibly T), the first two passes read every weight, and the later ones
-// only those of fours that may still hold T.
+// A position is classed by what is known of its key: below T, possibly T,
+// above; 2 bits, a byte for four positions (low half below T, high half
+// possibly T).  STAGED: the keys of a share are read once and stay in shared
+// memory, and the classes follow when T is known.  Otherwise two passes read
+// every weight; the second one knows T's top digit, classes every position and
+// lists those that share it with their keys.  The rest is done on the list,
+// or, where that overflows (many equal weights), by reading the weights of
+// the fours that may still hold T again.
 template <int N, bool STAGED, int V>
 __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* __restrict__ kept,
                                                  int32_t* __restrict__ new_lens, uint32_t* status) {
     constexpr int kWarps = N / 32, kPer = kBins / N;  // bins a thread adds up
     __shared__ SelectShared<N> sh;
     extern __shared__ __align__(16) unsigned char s_share[];
-    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_share);  // STAGED
+    // Keys (STAGED) or the list, later the warps' compaction blocks; then the classes.
+    uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_share);
+    uint2* s_list = reinterpret_cast<uint2*>(s_share);
+    int32_t* s_block = reinterpret_cast<int32_t*>(s_share) + (threadIdx.x >> 5) * kBlock;
+    unsigned char* s_class = s_share + select_front(N, STAGED, ch.most_share);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -115,13 +131,14 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
         }
     };
     // Calls f(position) for this thread's fours, several at a time.
-    constexpr int kAhead = 4;
+    constexpr int kAhead = STAGED ? 4 : 2;
     auto each_four = [&](auto&& f) {
         for (int i0 = tid * 4; i0 < count; i0 += N * 4 * kAhead) f(i0);
     };
     auto in_share = [&](int i0, int a) { return a == 0 || i0 + a * N * 4 < count; };
 
     for (int i = tid; i < 3 * kBins; i += N) (&sh.hist[0][0])[i] = 0;
+    if (tid == 0) sh.listed = 0;
     __syncthreads();
     uint32_t prefix = 0, want = (uint32_t)m;  // T's digits so far; which of the keys sharing them is T, from 1
 #pragma unroll
@@ -129,47 +146,64 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;  // of this pass's digit
         const int above = pass == 1 ? 21 : 10;                   // of the digits known
         const uint32_t digits = pass == 2 ? 1023u : 2047u;
-        each_four([&](int i0) {
-            uint32_t k[kAhead][4];
-            unsigned char cls[kAhead];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (!in_share(i0, a)) continue;
-                const int i = i0 + a * N * 4;
-                cls[a] = 0xf0;
-                if (!STAGED && pass == 2) cls[a] = s_share[i / 4];
-                if (STAGED && pass > 0) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
-                    k[a][0] = x.x; k[a][1] = x.y; k[a][2] = x.z; k[a][3] = x.w;
-                } else if (cls[a] & 0xf0) {
-                    read4(i, k[a]);
-                }
+        const bool on_list = !STAGED && pass == 2 && sh.listed <= kListed;
+        if (on_list) {
+            for (int i = tid; i < (int)sh.listed; i += N) {
+                const uint32_t k = s_list[i].y;
+                if (k >> above == prefix >> above) atomicAdd(&sh.hist[2][k & digits], 1u);
             }
+        } else {
+            each_four([&](int i0) {
+                uint32_t k[kAhead][4];
+                unsigned char cls[kAhead];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (!in_share(i0, a)) continue;
-                const int i = i0 + a * N * 4;
-                if (STAGED && pass == 0) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[a][0], k[a][1], k[a][2], k[a][3]);
-                if (!(cls[a] & 0xf0)) continue;
-                uint32_t now = cls[a] & 0x0fu;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool maybe = (STAGED || pass < 2) ? (pass > 0 || i + e < count) : (cls[a] >> (4 + e)) & 1;
-                    if (pass == 0) {
-                        if (maybe) atomicAdd(&sh.hist[0][k[a][e] >> 21], 1u);
-                        continue;
-                    }
-                    const uint32_t known = k[a][e] >> above;
-                    if (maybe && known == prefix >> above && i + e < count) {
-                        atomicAdd(&sh.hist[pass][(k[a][e] >> shift) & digits], 1u);
-                        now |= 0x10u << e;
-                    } else if (maybe && known < prefix >> above) {
-                        now |= 1u << e;
+                for (int a = 0; a < kAhead; ++a) {
+                    if (!in_share(i0, a)) continue;
+                    const int i = i0 + a * N * 4;
+                    cls[a] = 0xf0;
+                    if (!STAGED && pass == 2) cls[a] = s_class[i / 4];
+                    if (STAGED && pass > 0) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
+                        k[a][0] = x.x; k[a][1] = x.y; k[a][2] = x.z; k[a][3] = x.w;
+                    } else if (cls[a] & 0xf0) {
+                        read4(i, k[a]);
                     }
                 }
-                if (!STAGED && pass > 0) s_share[i / 4] = (unsigned char)now;
-            }
-        });
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    if (!in_share(i0, a)) continue;
+                    const int i = i0 + a * N * 4;
+                    if (STAGED && pass == 0) *reinterpret_cast<uint4*>(s_keys + i) = make_uint4(k[a][0], k[a][1], k[a][2], k[a][3]);
+                    if (!(cls[a] & 0xf0)) continue;
+                    uint32_t now = cls[a] & 0x0fu;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (pass == 0) {
+                            if (i + e < count) atomicAdd(&sh.hist[0][k[a][e] >> 21], 1u);
+                            continue;
+                        }
+                        const uint32_t known = k[a][e] >> above;
+                        if (known > prefix >> above || i + e >= count || !(cls[a] >> (4 + e) & 1)) continue;
+                        if (known == prefix >> above) {
+                            atomicAdd(&sh.hist[pass][(k[a][e] >> shift) & digits], 1u);
+                            now |= 0x10u << e;
+                        } else {
+                            now |= 1u << e;
+                        }
+                    }
+                    if (!STAGED && pass > 0) s_class[i / 4] = (unsigned char)now;
+                    if (!STAGED && pass == 1 && (now & 0xf0u)) {
+                        uint32_t at = atomicAdd(&sh.listed, (uint32_t)__popc(now & 0xf0u));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (now >> (4 + e) & 1u) {
+                                if (at < (uint32_t)kListed) s_list[at] = make_uint2(i + e, k[a][e]);
+                                ++at;
+                            }
+                    }
+                }
+            });
+        }
         meet();
         // Every thread sums kPer consecutive bins over the cluster; a scan over the block finds the bin of the want-th key.
         uint32_t s[kPer] = {}, mine = 0;
@@ -206,9 +240,16 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     }
 
     // T = prefix, and the first `want` of the positions that hold it stay.
-    // Each warp takes a consecutive part of the share, 128 positions at a
-    // time, four to a lane; the 128 counts share a word, keys below T in the
-    // low half and equal to T in the high half.
+    const bool listed = !STAGED && sh.listed <= kListed;
+    if (listed) {
+        for (int i = tid; i < (int)sh.listed; i += N) {
+            const uint2 x = s_list[i];
+            const uint32_t may = 0x10u << (x.x & 3u), below = 1u << (x.x & 3u), byte = (x.x >> 2 & 3u) * 8;
+            if (x.y != prefix) atomicXor(reinterpret_cast<uint32_t*>(s_class) + (x.x >> 4), (x.y < prefix ? may | below : may) << byte);
+        }
+        __syncthreads();
+    }
+    // Each warp takes a consecutive part of the share.
     const int part = ((count + kWarps - 1) / kWarps + 127) / 128 * 128;
     const int from = min(warp * part, count), to = min(from + part, count);
     auto classes = [&](int i) -> uint32_t {  // of the four from i on, final
@@ -217,8 +258,8 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
             const uint4 x = *reinterpret_cast<const uint4*>(s_keys + i);
             k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
         } else {
-            cls = s_share[i / 4];
-            if (!(cls & 0xf0u)) return cls;
+            cls = s_class[i / 4];
+            if (listed || !(cls & 0xf0u)) return cls;
             read4(i, k);
         }
         uint32_t now = cls & 0x0fu;
@@ -230,7 +271,7 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     uint32_t lt = 0, eq = 0;
     for (int i = from + lane * 4; i < to; i += 128) {
         const uint32_t cls = classes(i);
-        if constexpr (!STAGED) s_share[i / 4] = (unsigned char)cls;
+        s_class[i / 4] = (unsigned char)cls;
         lt += __popc(cls & 0x0fu);
         eq += __popc(cls & 0xf0u);
     }
@@ -261,25 +302,38 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
         lt += sh.warp_lt[w];
         eq += sh.warp_eq[w];
     }
-    for (int i0 = from; i0 < to; i0 += 128) {
-        const int i = i0 + lane * 4;
-        uint32_t cls = 0;
+    // kBlock positions at a time, 32 to a lane, compacted in shared memory and
+    // written from there in order; the block's counts share a word.
+    for (int i0 = from; i0 < to; i0 += kBlock) {
+        const int i = i0 + lane * 32;
+        uint32_t is_lt = 0, is_eq = 0;
         if (i < to) {
-            if constexpr (STAGED) cls = classes(i); else cls = s_share[i / 4];
+            const uint2 x = *reinterpret_cast<const uint2*>(s_class + i / 4);
+            auto half = [](uint32_t w) {  // the low halves of four bytes, side by side
+                w &= 0x0f0f0f0fu;
+                w = (w | w >> 4) & 0x00ff00ffu;
+                return (w | w >> 8) & 0xffffu;
+            };
+            const uint32_t here = to - i >= 32 ? 0xffffffffu : (1u << (to - i)) - 1u;
+            is_lt = (half(x.x) | half(x.y) << 16) & here;
+            is_eq = (half(x.x >> 4) | half(x.y >> 4) << 16) & here;
         }
-        const uint32_t sum = __popc(cls & 0x0fu) | __popc(cls & 0xf0u) << 16;
+        const uint32_t sum = __popc(is_lt) | __popc(is_eq) << 16;
         const uint32_t incl = warp_inclusive_scan<uint32_t>(sum, lane);
-        uint32_t my_lt = lt + ((incl - sum) & 0xffffu), my_eq = eq + ((incl - sum) >> 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t is_lt = cls >> e & 1u, is_eq = cls >> (4 + e) & 1u, at = my_lt + min(my_eq, want);
-            if ((is_lt || (is_eq && my_eq < want)) && at < (uint32_t)m) out[at] = begin + i + e;
-            my_lt += is_lt;
-            my_eq += is_eq;
-        }
+        const uint32_t my_lt = lt + ((incl - sum) & 0xffffu), my_eq = eq + ((incl - sum) >> 16);
+        const uint32_t base = lt + min(eq, want);
+        const int ties = my_eq < want ? (int)min(want - my_eq, sum >> 16) : 0;  // of this lane's that stay
+        for (int drop = (int)(sum >> 16) - ties; drop > 0; --drop) is_eq &= ~(0x80000000u >> __clz(is_eq));
+        uint32_t at = my_lt + min(my_eq, want) - base;
+        for (uint32_t keep = is_lt | is_eq; keep; keep &= keep - 1) s_block[at++] = begin + i + __ffs(keep) - 1;
         const uint32_t all = __shfl_sync(kFullMask, incl, 31);
         lt += all & 0xffffu;
         eq += all >> 16;
+        const uint32_t stay = lt + min(eq, want) - base;
+        __syncwarp();
+        for (uint32_t j = lane; j < stay; j += 32)
+            if (base + j < (uint32_t)m) out[base + j] = s_block[j];
+        __syncwarp();
     }
     if (bad) record_error(status, kErrKvTable, (uint32_t)(t.first + b));
     if (ranks > 1) cluster.sync();  // no CTA leaves while another may read its shared memory
@@ -353,12 +407,12 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     // split, into shares of 2048 positions or more, while the CTAs fit the SMs.
     int ranks = 1;
     auto split = [&](int r) { return (int64_t)rows * r * 2 <= sms && t.max_len / (r * 2) >= 2048; };
-    while (ranks < kMaxCluster && (split(ranks) || t.max_len / ranks > kMaskedShare - 4)) ranks *= 2;
+    while (ranks < kMaxCluster && (split(ranks) || t.max_len / ranks > kClassedShare - 4)) ranks *= 2;
     const int share = ((t.max_len + ranks - 1) / ranks + 3) / 4 * 4;
     const bool staged = share <= kStagedShare;
     const bool vec4 = c.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(c.weight) & 15u) == 0;
     auto* kern = staged ? (vec4 ? k_kv_select<512, true, 4> : k_kv_select<512, true, 1>) : (vec4 ? k_kv_select<1024, false, 4> : k_kv_select<1024, false, 1>);
-    const int threads = staged ? 512 : 1024, bytes_most = staged ? kStagedShare * 4 : kMaskedShare / 4;
+    const int threads = staged ? 512 : 1024, bytes_most = select_bytes(threads, staged, staged ? kStagedShare : kClassedShare);
     KernelSetup su;
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), threads, (size_t)bytes_most, &su);
     if (e != cudaSuccess) return e;
@@ -367,14 +421,14 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * ranks);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = staged ? (size_t)share * 4 : (size_t)share / 4;
+    cfg.dynamicSmemBytes = (size_t)select_bytes(threads, staged, share);
     cfg.stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ranks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, c, t, Choice{keep, sinks, recent, FastDiv(c.page_size)}, kept, dt.lens, status);
+    e = cudaLaunchKernelEx(&cfg, kern, c, t, Choice{keep, sinks, recent, share, FastDiv(c.page_size)}, kept, dt.lens, status);
     if (e != cudaSuccess) return e;
 
     const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
