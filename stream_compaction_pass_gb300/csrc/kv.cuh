@@ -12,6 +12,32 @@
 
 namespace ss {
 
+// Every kernel of this family is launched so that it may start before the
+// kernel ahead of it on the stream has ended (programmatic dependent launch),
+// and waits for that end here, first of all: only its launch overlaps.
+__device__ __forceinline__ void begin_dependent() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), size_t grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Division of numbers below 2^31 by a fixed one, by a multiplication: with
 // 2^l >= d and m = floor(2^32 (2^l - d) / d) + 1, n / d = (n m / 2^32 + n) / 2^l
 // (Granlund and Montgomery, "Division by invariant integers using multiplication").

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kAppendThreads, QUANT ? 4 : 6) k_kv_append(KvP
     constexpr int kBytes = QUANT ? 1 : 2;
     __shared__ int64_t s_src[kAppendThreads], s_dst[kAppendThreads];  // byte offsets, dst -1: not written
     __shared__ float2 s_scale[2][kAppendThreads];  // k's and v's scale and its inverse
+    begin_dependent();
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * per;
     if (tid < per && row0 + tid < rows) {
@@ -155,10 +156,9 @@ cudaError_t run(const KvPages& c, const KvTable& t, const void* k_new, const voi
     const int64_t rows = tokens * c.kv_heads;
     const int vecs = c.head_dim * (QUANT ? 1 : 2) / 16;
     const int per = kv_rows_per_cta(kAppendThreads * kAppendVecs<QUANT> / (2 * vecs), kAppendThreads, rows, sms);
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
-    k_kv_append<T, QUANT><<<grid, kAppendThreads, 0, s>>>(c, t, static_cast<const T*>(k_new), static_cast<const T*>(v_new), token_stride,
-                                                          head_stride, offsets, rows, per, vecs, FastDiv(vecs), FastDiv(c.page_size), status);
-    return cudaGetLastError();
+    return launch_dependent(k_kv_append<T, QUANT>, (rows + per - 1) / per, kAppendThreads, 0, 1, s, c, t, static_cast<const T*>(k_new),
+                            static_cast<const T*>(v_new), token_stride, head_stride, offsets, rows, per, vecs, FastDiv(vecs),
+                            FastDiv(c.page_size), status);
 }
 
 }  // namespace

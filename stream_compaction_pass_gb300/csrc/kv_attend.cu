@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, q4 = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();
 
     // Prefix sums of the sequences' tile counts.
     int* pre = reinterpret_cast<int*>(smem + (size_t)NW * (S * 2 * Sh::kTileBytes + Sh::kQBytes));
@@ -779,8 +779,7 @@ template <typename QT, int DP>
 __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, KvAttention a, Scratch sc, int per) {
     __shared__ float4 s_o[kJoinWarps][DP / 4];
     __shared__ float2 s_ml[kJoinWarps];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units_per_head = sc.units / c.kv_heads;
     const int rows = t.batch * a.q_heads, all = sc.pre[t.batch];
@@ -847,7 +846,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
 template <int V>
 __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
     __shared__ int s_pre[kMaxBatch + 1];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     for (int i = threadIdx.x; i <= t.batch; i += kWeightThreads) s_pre[i] = sc.pre_all[i];
     __syncthreads();
     const bool only_visible = sc.pre_all == sc.pre;
@@ -979,31 +978,19 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         v.q = static_cast<const QT*>(a.q) + (int64_t)b0 * a.q_seq_stride;
         v.out = static_cast<QT*>(a.out) + (int64_t)b0 * a.out_seq_stride;
         if (a.lse) v.lse = a.lse + (int64_t)b0 * a.q_heads;
-        kern<<<p.grid, NW * 32, smem, s>>>(c, u, v, p.sc, status);
-        e = cudaGetLastError();
+        e = launch_dependent(kern, p.grid, NW * 32, smem, 1, s, c, u, v, p.sc, status);
         if (e != cudaSuccess) return e;
         // One row per warp, except where rows are few, or have so many parts on
         // average that a whole CTA joins each.
         const int rows = u.batch * a.q_heads;
         const int per = rows <= 2 * su.sms || p.sc.workers > kTeamParts * u.batch * p.sc.units ? 1 : kJoinWarps;
-        cudaLaunchAttribute at;
-        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
-        cfg.blockDim = dim3(kJoinThreads);
-        cfg.stream = s;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k_kv_join<QT, DP>, c, u, v, p.sc, per);
+        e = launch_dependent(k_kv_join<QT, DP>, (rows + per - 1) / per, kJoinThreads, 0, 1, s, c, u, v, p.sc, per);
         if (e != cudaSuccess) return e;
         if (a.weight_out == nullptr) continue;
         const bool vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;
         const size_t tiles = ((size_t)t.max_len + T - 1) / T * u.batch * c.kv_heads;
         const size_t blocks = (tiles * (vec4 ? T / 4 : T) + kWeightThreads - 1) / kWeightThreads, most = (size_t)su.sms * 8;
-        cfg.gridDim = dim3((unsigned)(blocks < most ? blocks < 1 ? 1 : blocks : most));
-        cfg.blockDim = dim3(kWeightThreads);
-        e = cudaLaunchKernelEx(&cfg, vec4 ? k_kv_weights<4> : k_kv_weights<1>, c, u, v, p.sc, status);
+        e = launch_dependent(vec4 ? k_kv_weights<4> : k_kv_weights<1>, blocks < most ? blocks < 1 ? 1 : blocks : most, kWeightThreads, 0, 1, s, c, u, v, p.sc, status);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     uint2* s_list = reinterpret_cast<uint2*>(s_share);
     int32_t* s_block = reinterpret_cast<int32_t*>(s_share) + (threadIdx.x >> 5) * kBlock;
     unsigned char* s_class = s_share + select_front(N, STAGED, ch.most_share);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = blockIdx.x / ranks, b = row / c.kv_heads, h = row % c.kv_heads;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, 
                                                          const int32_t* __restrict__ kept, uint32_t* status) {
     const int keep = mv.keep, rows = mv.rows, vecs = mv.vecs;
     __shared__ int64_t s_src[kMoveThreads], s_dst[kMoveThreads];  // byte offsets, or -1
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     const int tid = threadIdx.x;
     const int row = blockIdx.x / mv.groups, j0 = (blockIdx.x - row * mv.groups) * rows;
     const int b = row / c.kv_heads, h = row % c.kv_heads;
@@ -417,18 +417,8 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), threads, (size_t)bytes_most, &su);
     if (e != cudaSuccess) return e;
 
-    cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows * ranks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = (size_t)select_bytes(threads, staged, share);
-    cfg.stream = s;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ranks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, c, t, Choice{keep, sinks, recent, share, FastDiv(c.page_size)}, kept, dt.lens, status);
+    e = launch_dependent(kern, (size_t)rows * ranks, threads, (size_t)select_bytes(threads, staged, share), ranks, s, c, t,
+                         Choice{keep, sinks, recent, share, FastDiv(c.page_size)}, kept, dt.lens, status);
     if (e != cudaSuccess) return e;
 
     const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
@@ -436,16 +426,8 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     const int per = kv_rows_per_cta(kMoveThreads * kMoveLoads / (2 * vecs), kMoveThreads, (int64_t)rows * most, sms);
     const int groups = (most + per - 1) / per;
     if (groups == 0) return cudaSuccess;
-    cfg = {};
-    cfg.gridDim = dim3(rows * (unsigned)groups);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = s;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     const Move mv{keep, per, groups, vecs, bytes, FastDiv(c.page_size), FastDiv(d.page_size), FastDiv(vecs)};
-    return cudaLaunchKernelEx(&cfg, k_kv_move, c, t, d, dt, mv, (const int32_t*)kept, status);
+    return launch_dependent(k_kv_move, (size_t)rows * groups, kMoveThreads, 0, 1, s, c, t, d, dt, mv, kept, status);
 }
 
 }  // namespace ss
