@@ -412,26 +412,25 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // The public description as the kernels take it; `name` says which argument
 // an error is about.
 ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
-    const std::string who(name);
-    if (p == nullptr) return fail(SS_ERR_INVALID_ARG, who + " is null");
+    if (p == nullptr) return fail(SS_ERR_INVALID_ARG, std::string(name) + " is null");
     if (p->type != SS_BF16 && p->type != SS_F16 && p->type != SS_E4M3)
-        return fail(SS_ERR_UNSUPPORTED, who + ": unknown element type");
+        return fail(SS_ERR_UNSUPPORTED, std::string(name) + ": unknown element type");
     const int64_t size = p->type == SS_E4M3 ? 1 : 2;
     if (p->kv_heads < 1 || p->page_size < 1 || p->num_pages < 1)
-        return fail(SS_ERR_INVALID_ARG, who + ": kv_heads, page_size and num_pages must be positive");
-    if (p->num_pages > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, who + ": num_pages must be below 2^31");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": kv_heads, page_size and num_pages must be positive");
+    if (p->num_pages > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": num_pages must be below 2^31");
     if (p->head_dim < 1 || p->head_dim > 256 || p->head_dim * size % 16 != 0)
-        return fail(SS_ERR_INVALID_ARG, who + ": head_dim must be at most 256 and a whole number of 16-byte vectors");
-    if (!p->k || !p->v) return fail(SS_ERR_INVALID_ARG, who + ": null k or v");
-    if (!aligned16(p->k) || !aligned16(p->v)) return fail(SS_ERR_INVALID_ARG, who + ": k and v must be 16-byte aligned");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": head_dim must be at most 256 and a whole number of 16-byte vectors");
+    if (!p->k || !p->v) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": null k or v");
+    if (!aligned16(p->k) || !aligned16(p->v)) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": k and v must be 16-byte aligned");
     if (p->page_stride * size % 16 || p->head_stride * size % 16 || p->slot_stride * size % 16)
-        return fail(SS_ERR_INVALID_ARG, who + ": strides must be multiples of 16 bytes");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be multiples of 16 bytes");
     if (p->page_stride < 0 || p->head_stride < 0 || p->slot_stride < 0)
-        return fail(SS_ERR_INVALID_ARG, who + ": strides must not be negative");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must not be negative");
     if (p->type != SS_E4M3 && (p->k_scale || p->v_scale))
-        return fail(SS_ERR_INVALID_ARG, who + ": scales belong to an SS_E4M3 cache");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales belong to an SS_E4M3 cache");
     if (!aligned4(p->k_scale) || !aligned4(p->v_scale) || !aligned4(p->weight))
-        return fail(SS_ERR_INVALID_ARG, who + ": scales and weight must be 4-byte aligned");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales and weight must be 4-byte aligned");
     *out = ss::KvPages{static_cast<ss::KvElem>(p->type), p->kv_heads, p->head_dim, p->page_size, p->num_pages,
                        static_cast<char*>(p->k), static_cast<char*>(p->v), p->page_stride, p->head_stride,
                        p->slot_stride, p->k_scale, p->v_scale, p->weight};
@@ -439,17 +438,16 @@ ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
 }
 
 ss_status kv_table(const ss_kv_table* t, const ss::KvPages& c, const char* name, ss::KvTable* out) {
-    const std::string who(name);
-    if (t == nullptr) return fail(SS_ERR_INVALID_ARG, who + " is null");
+    if (t == nullptr) return fail(SS_ERR_INVALID_ARG, std::string(name) + " is null");
     if (t->batch < 0 || t->max_pages < 0 || t->max_len < 0 || t->row_stride < 0)
-        return fail(SS_ERR_INVALID_ARG, who + ": negative batch, max_pages, max_len or row_stride");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": negative batch, max_pages, max_len or row_stride");
     if (t->batch > 0 && (!t->lens || (t->max_pages > 0 && !t->pages)))
-        return fail(SS_ERR_INVALID_ARG, who + ": null pages or lens");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": null pages or lens");
     if (!aligned4(t->pages) || !aligned4(t->lens))
-        return fail(SS_ERR_INVALID_ARG, who + ": pages and lens must be 4-byte aligned");
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": pages and lens must be 4-byte aligned");
     int64_t held = (int64_t)t->max_pages * c.page_size;
     if (t->max_len > 0 && t->max_len < held) held = t->max_len;
-    if (held > 0x7fffffff - 4096) return fail(SS_ERR_INVALID_ARG, who + ": max_len must be below 2^31 - 4096");
+    if (held > 0x7fffffff - 4096) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": max_len must be below 2^31 - 4096");
     *out = ss::KvTable{t->pages, t->row_stride, t->max_pages, t->batch, t->lens, (int)held, 0};
     return SS_OK;
 }

@@ -31,7 +31,9 @@ namespace ss {
 
 namespace {
 
-constexpr int kMaxBatch = 512;  // sequences per launch: their tile counts' prefix sums are in shared memory
+// Sequences per launch: their tile counts' prefix sums are in shared memory,
+// beside a ring that leaves little of it at head_dim 256.
+template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
@@ -217,7 +219,7 @@ struct Shape {
     static constexpr int kTileBytes = T * kRowBytes;        // of k, and of v
     static constexpr bool kQShared = DP == 256;             // Q's fragments in shared memory: registers are short
     static constexpr int kQBytes = kQShared ? DP / 16 * 32 * 16 : 0;
-    static constexpr size_t kSmem = (size_t)NW * (S * 2 * kTileBytes + kQBytes) + (kMaxBatch + 1) * 4;
+    static constexpr size_t kSmem = (size_t)NW * (S * 2 * kTileBytes + kQBytes) + (kMaxBatch<DP> + 1) * 4;
 };
 
 template <typename QT, bool FP8, int DP, int T, int NW, int S>
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
 // only visible positions change.
 template <int V>
 __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
-    __shared__ int s_pre[kMaxBatch + 1];
+    __shared__ int s_pre[kMaxBatch<0> + 1];
     begin_dependent();
     for (int i = threadIdx.x; i <= t.batch; i += kWeightThreads) s_pre[i] = sc.pre_all[i];
     __syncthreads();
@@ -921,7 +923,7 @@ struct Plan {
     size_t at_lse2, at_ml, at_o, at_logits, bytes;
 };
 
-Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int warps, int dp, int tile, int sms) {
+Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int most_batch, int warps, int dp, int tile, int sms) {
     Plan p{};
     p.dp = dp;
     p.warps = warps;
@@ -930,7 +932,7 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int war
     p.sc.rows = p.sc.group < 16 ? p.sc.group : 16;
     const size_t tiles = ((size_t)t.max_len + tile - 1) / tile;  // of one sequence and unit, at most
     const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
-    size_t batch = (size_t)t.batch < kMaxBatch ? t.batch : kMaxBatch;
+    size_t batch = t.batch < most_batch ? t.batch : most_batch;
     if (seq_logits * batch > kMaxLogits) batch = kMaxLogits / seq_logits;
     while (batch > 1 && batch * tiles * p.sc.units > 0x7fffffff) batch /= 2;  // lists are counted in 32 bits
     p.batch = batch < 1 ? 1 : (int)batch;
@@ -939,7 +941,7 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int war
     p.sc.workers = p.grid * warps;
     p.sc.shift = tile == 16 ? 4 : 5;
     p.sc.page = FastDiv(c.page_size);
-    p.at_lse2 = 2 * round256((kMaxBatch + 1) * 4);
+    p.at_lse2 = 2 * round256(((size_t)p.batch + 1) * 4);
     p.at_ml = p.at_lse2 + round256((size_t)p.batch * a.q_heads * 4);
     p.at_o = p.at_ml + round256((size_t)p.sc.workers * 2 * 16 * 8);
     p.at_logits = p.at_o + round256((size_t)p.sc.workers * 2 * p.sc.rows * dp * 4);
@@ -955,7 +957,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
     KernelSetup su;
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
     if (e != cudaSuccess) return e;
-    Plan p = make_plan(c, t, a, NW, DP, T, su.sms);
+    Plan p = make_plan(c, t, a, kMaxBatch<DP>, NW, DP, T, su.sms);
     if (scratch == nullptr) {
         *bytes = p.bytes;
         return cudaSuccess;
