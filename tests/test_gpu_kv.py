@@ -523,3 +523,85 @@ def test_a_sequence_lives_through_append_attend_and_evict(ss):
     assert held.any()
     weights = np.where(held, c.weight.cpu().numpy(), 0).astype(np.float32)
     run_evict(ss, c, weights, 70, 4, 20)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float8_e4m3fn"])
+def test_example_decodes_within_a_budget(dtype):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.run(batch=3, heads=2, group=4, dim=64, prompt=90, steps=60, budget=64, slack=16, sinks=2, recent=16, dtype=dtype, check=True)
+    assert got["evictions"] >= 3 and max(got["lens"]) <= 80
+    # out is rounded to bf16 (2^-8 of the value), weights under an 8-bit cache to fp16 (2^-11)
+    assert got["worst"] <= 2.0 ** -8 + 2.0 ** -10
+
+
+# ---- further sizes ----
+
+@pytest.mark.parametrize("kind,dims", [("bf16", [8, 24, 72, 120, 136, 200, 248]), ("e4m3", [32, 48, 112, 144, 240])])
+def test_attend_odd_dims(ss, kind, dims):
+    for dim in dims:
+        check_attend(ss, Cache([45, 3, 200], heads=2, dim=dim, page=16, kind=kind, seed=dim), 3, "bf16")
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 128), ("e4m3", 128), ("f16", 64)])
+def test_attend_one_shared_head(ss, kind, group):
+    check_attend(ss, Cache([150, 0, 31, 2000], heads=1, dim=64, page=32, kind=kind, seed=group), group, "f16" if kind == "f16" else "bf16")
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_attend_more_sequences_than_one_launch_takes(ss, dim):
+    rng = np.random.default_rng(dim)
+    n = 600 if dim == 256 else 4200
+    check_attend(ss, Cache(rng.integers(0, 20, n).tolist(), heads=1, dim=dim, page=16, seed=dim), 1, "bf16")
+
+
+def test_attend_scratch_of_larger_calls_does_not_leak(ss):
+    """The scratch of a large call does not leak into smaller ones."""
+    check_attend(ss, Cache([9000, 5000], heads=2, dim=128, page=16, seed=41), 4, "bf16")
+    for n in (1, 17, 400):
+        check_attend(ss, Cache([n], heads=1, dim=128, page=16, seed=n), 2, "bf16")
+        check_attend(ss, Cache([n, 0, n], heads=1, dim=128, page=16, seed=n), 2, "bf16", window=10, sinks=3, weights="apart")
+
+
+def test_append_scales_of_every_size(ss):
+    """Quotients next to ties and scales outside the reciprocal's range."""
+    import torch
+    gen = torch.Generator().manual_seed(51)
+    heads, dim, n = 64, 128, 64
+    for low, high in ((-3.0, 3.0), (-59.0, 59.0), (-120.0, 120.0)):
+        c = Cache([n], heads=heads, dim=dim, page=16, kind="e4m3", seed=52)
+        c.ks, c.vs = (torch.exp2(torch.rand(heads, generator=gen) * (high - low) + low) for _ in range(2))
+        x = torch.randn(n, 2, heads, dim, generator=gen)
+        ties = (torch.randint(16, 32, x.shape, generator=gen) * 2 + 1) * torch.exp2(torch.randint(-12, 4, x.shape, generator=gen).float())
+        x = torch.where(torch.rand(x.shape, generator=gen) < 0.5, x * 20, ties) * c.ks[None, None, :, None]
+        x = x.to(torch.bfloat16).clamp(-3e38, 3e38)
+        pages, table = c.ss(ss)
+        ss.ss_kv_append(pages, table, x[:, 0].contiguous().cuda(), x[:, 1].contiguous().cuda(),
+                        offsets=torch.tensor([0, n], dtype=torch.int32).cuda())
+        ok(ss)
+        for i, (pool, scale) in enumerate(((c.k, c.ks), (c.v, c.vs))):
+            with np.errstate(over="ignore", under="ignore"):
+                want = e4m3_reference(x[:, i].float().numpy() / scale.numpy()[:, None])
+            p = np.arange(n)
+            got = pool.float().cpu().numpy()[c.table_host[0, p // 16], :, p % 16]
+            assert np.array_equal(got, want.astype(np.float32))
+
+
+@pytest.mark.parametrize("n,levels", [(40000, 1), (40000, 2), (70000, 5)])
+def test_evict_long_rows_of_equal_weights(ss, n, levels):
+    """More candidates than a row can list."""
+    c = Cache([n, n - 1], heads=1, dim=16, page=64, seed=n, kind="e4m3")
+    run_evict(ss, c, random_weights(c, levels, 0.3, levels), n // 3, 4, 500)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 80, 200])
+def test_evict_rows_alone_and_together(ss, rows):
+    """Few rows are split over clusters, many are a CTA each."""
+    rng = np.random.default_rng(rows)
+    c = Cache(rng.integers(17000, 21000, rows).tolist() if rows <= 3 else rng.integers(3000, 5000, rows).tolist(), heads=1, dim=16, page=32,
+              seed=rows, kind="e4m3")
+    run_evict(ss, c, random_weights(c, rows), 2500, 4, 700)
