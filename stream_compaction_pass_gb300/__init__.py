@@ -473,31 +473,37 @@ def ss_temp_status(temp, stream=None):
     return st, tile.value
 
 
-_elems = {}  # torch dtype -> the library's element type
+_elems = {}   # torch dtype -> the library's element type
+_dtypes = {}  # name -> torch dtype
+
+
+def _load_dtypes() -> None:
+    import torch
+    _elems.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float8_e4m3fn: SS_E4M3})
+    _dtypes.update({"float32": torch.float32, "int32": torch.int32})
 
 
 def _elem(t) -> int:
     """The library's element type of a torch tensor."""
     if not _elems:
-        import torch
-        _elems.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float8_e4m3fn: SS_E4M3})
+        _load_dtypes()
     kind = _elems.get(t.dtype)
     if kind is None:
         raise TypeError(f"{t.dtype} is not a type of the key-value cache calls (bfloat16, float16, float8_e4m3fn)")
     return kind
 
 
-def _like(name: str, t, shape, dtype: str):
-    """Checks an optional tensor argument's shape, type and (for contiguous
-    arguments) layout; the C ABI sees only addresses."""
-    if t is not None and (t.shape != shape or t.dtype is not _dtype(dtype) or not t.is_contiguous()):
+def _like(name: str, t, shape, dtype: str) -> int:
+    """The address of an optional contiguous tensor argument (0 for None), its
+    shape and type checked; the C ABI sees only addresses."""
+    if t is None:
+        return 0
+    if not _dtypes:
+        _load_dtypes()
+    if t.shape != shape or t.dtype is not _dtypes[dtype] or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                          f"{str(t.dtype)[6:]} {tuple(t.shape)}")
-
-
-def _dtype(name: str):
-    import torch
-    return getattr(torch, name)
+    return t.data_ptr()
 
 
 class KVPages:
@@ -517,13 +523,12 @@ class KVPages:
         if k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must have the same strides and a contiguous last dimension")
         pages, heads, page, dim = k.shape
-        _like("weight", weight, (pages, heads, page), "float32")
-        _like("k_scale", k_scale, (heads,), "float32")
-        _like("v_scale", v_scale, (heads,), "float32")
+        d_weight = _like("weight", weight, (pages, heads, page), "float32")
+        d_scales = [_like(name, x, (heads,), "float32") for name, x in (("k_scale", k_scale), ("v_scale", v_scale))]
         self.k, self.v, self.weight, self.k_scale, self.v_scale = k, v, weight, k_scale, v_scale
         self.kv_heads, self.head_dim, self.weight_shape = heads, dim, k.shape[:3]
         self._c = _KvPages(_elem(k), heads, dim, page, pages, _addr(k), _addr(v), k.stride(0), k.stride(1),
-                           k.stride(2), _addr(k_scale), _addr(v_scale), _addr(weight))
+                           k.stride(2), *d_scales, d_weight)
         self._ref = ctypes.addressof(self._c)
 
 
@@ -564,9 +569,9 @@ def ss_kv_append(cache: KVPages, seqs: KVTable, k_new, v_new, offsets=None, stre
     token_stride, head_stride, unit = k_new.stride()
     if heads != cache.kv_heads or dim != cache.head_dim or unit != 1:
         raise ValueError(f"k_new must be (tokens, {cache.kv_heads}, {cache.head_dim}) with a contiguous last dimension")
-    _like("offsets", offsets, (seqs.batch + 1,), "int32")
+    d_offsets = _like("offsets", offsets, (seqs.batch + 1,), "int32")
     _check(lib().ss_kv_append(cache._ref, seqs._ref, _elem(k_new), k_new.data_ptr(), v_new.data_ptr(), token_stride,
-                              head_stride, _addr(offsets), tokens, _stream(stream, k_new)), "ss_kv_append")
+                              head_stride, d_offsets, tokens, _stream(stream, k_new)), "ss_kv_append")
 
 
 def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int = 0, sinks: int = 0, lse=None,
@@ -582,13 +587,11 @@ def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int 
     out_seq, out_head, out_unit = out.stride()
     if batch != seqs.batch or dim != cache.head_dim or q_unit != 1 or out_unit != 1:
         raise ValueError(f"q and out must be ({seqs.batch}, q_heads, {cache.head_dim}) with a contiguous last dimension")
-    _like("lse", lse, (batch, heads), "float32")
-    if weight_in is not None or weight_out is not None:
-        _like("weight_in", weight_in, cache.weight_shape, "float32")
-        _like("weight_out", weight_out, cache.weight_shape, "float32")
+    d_lse = _like("lse", lse, (batch, heads), "float32")
+    d_in, d_out = (_like("weight_in", weight_in, cache.weight_shape, "float32"),
+                   _like("weight_out", weight_out, cache.weight_shape, "float32"))
     a = _KvAttention(_elem(q), heads, q.data_ptr(), q_seq, q_head, out.data_ptr(), out_seq, out_head,
-                     dim ** -0.5 if scale is None else scale, window, sinks, _addr(lse), _addr(weight_in),
-                     _addr(weight_out))
+                     dim ** -0.5 if scale is None else scale, window, sinks, d_lse, d_in, d_out)
     _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a), _stream(stream, q)), "ss_kv_attend")
 
 
@@ -596,6 +599,6 @@ def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable
                 recent: int = 0, kept=None, stream=None) -> None:
     """Moves the kept rows of every sequence and head into dst's pages and
     their number into dst_seqs.lens; kept: int32 (batch, kv_heads, keep)."""
-    _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32")
-    _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, _addr(kept),
+    d_kept = _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32")
+    _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, d_kept,
                              _stream(stream, src.k)), "ss_kv_evict")
