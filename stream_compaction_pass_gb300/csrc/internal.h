@@ -35,6 +35,10 @@ struct KernelSetup {
 };
 cudaError_t kernel_setup(const void* kern, int threads, size_t max_smem, KernelSetup* out);
 
+// How many clusters of `ranks` CTAs the current device holds at a time (1: CTAs).
+// The set-up above is done too; kept per (kernel, device, ranks).
+cudaError_t cluster_limit(const void* kern, int threads, size_t smem, int ranks, int* clusters);
+
 // A single-pass scan configuration: which kernel, its tile geometry and
 // its look-back window.
 struct ScanConfig {

@@ -25,6 +25,8 @@
 // last row may be parts, which go to scratch, and the second launch joins
 // them.  Where weights are kept, the first launch leaves X (fp32) in scratch
 // and the third turns it into weights, since they need the joined sums.
+#include <cooperative_groups.h>
+
 #include "kv_rows.cuh"
 
 namespace ss {
@@ -34,6 +36,13 @@ namespace {
 // Sequences per launch: their tile counts' prefix sums are in shared memory,
 // beside a ring that leaves little of it at head_dim 256.
 template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
+namespace cg = cooperative_groups;
+
+// Tiles of a warp up to which a call whose units fit the GPU takes the form of
+// one launch.  Measured on 8 heads of 128, one sequence: 517 positions 5.2
+// against 9.7 us, 16000 (10 tiles) 17.2 / 22.3 and with weights 24.3 / 25.2,
+// 32000 (21 tiles) 27.7 / 31.1 and with weights 40.4 / 35.1.
+constexpr int kSmallTiles = 24, kSmallTilesWeights = 12;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
@@ -48,6 +57,7 @@ struct Scratch {
     float* logits;  // per (sequence, key-value head) tile: group x 16 scores, log2 units; or null
     int group, units, rows, workers;  // units per sequence, of `heads` query heads; rows = min(group, heads)
     int heads;
+    int ranks, max_tiles;             // small calls: CTAs of a unit's cluster, tiles of the longest sequence
     int shift;                        // tiles have 2^shift positions
     FastDiv page;                     // by page_size
 };
@@ -100,6 +110,24 @@ __device__ __forceinline__ void store_lse(const Scratch& sc, const KvAttention& 
     if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : x * 0.6931471805599453f;
 }
 
+// Outputs of a row without a visible position.
+template <typename QT> __device__ __forceinline__ void empty_row(const KvAttention& a, int b, int j, int dim, int first, int step) {
+    QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
+    for (int d = first; d < dim; d += step) out[d] = from_f32<QT>(0.0f);
+    if (first == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + j] = -INFINITY;
+}
+
+__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.0f : exp2_fast(from - to); }
+
+// A part's O and l, by their factor; a part of nothing but -inf (factor 0) has no O.
+__device__ __forceinline__ void add_part(float4& x, float& l, const float4& y, float l_part, float factor) {
+    l += l_part * factor;
+    x.x += y.x * factor;
+    x.y += y.y * factor;
+    x.z += y.z * factor;
+    x.w += y.w * factor;
+}
+
 // A place in the list of tiles: sequence, key-value head, 16 query heads of
 // its group, tile.
 struct Cursor {
@@ -121,7 +149,11 @@ struct Shape {
     static constexpr size_t kSmem = (size_t)NW * (kRing + Rows::kQBytes) + (kMaxBatch<DP> + 1) * 4;
 };
 
-template <typename Rows, bool FP8, int DP, int T, int NW, int S>
+// SMALL: a call of few rows, a cluster of CTAs each.  The warps of a cluster
+// share one unit's tiles; the parts are joined through shared memory, first of
+// the CTA and then of the cluster, and the same warps add their tiles' weights:
+// one launch in all.
+template <typename Rows, bool FP8, int DP, int T, int NW, int S, bool SMALL>
 __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
     using Sh = Shape<Rows, FP8, DP, T, NW, S>;
     constexpr int kShift2 = T == 16 ? 4 : 5;
@@ -129,31 +161,49 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     begin_dependent();
 
-    // Prefix sums of the sequences' tile counts.
-    int* pre = reinterpret_cast<int*>(smem + (size_t)NW * (Sh::kRing + Rows::kQBytes));
-    for (int i = tid; i < t.batch; i += NW * 32) pre[i + 1] = Tiles(kv_len(t, i, status), a.window, a.sinks, kShift2).count;
-    __syncthreads();
-    if (warp == 0) prefix_sums(pre, t.batch, lane);
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= t.batch; i += NW * 32) sc.pre[i] = pre[i];
-    if (blockIdx.x == 0 && warp == 0 && sc.pre_all != sc.pre) {
-        for (int i = lane; i < t.batch; i += 32) sc.pre_all[i + 1] = (kv_len(t, i, status) + T - 1) >> kShift2;
-        __syncwarp();
-        prefix_sums(sc.pre_all, t.batch, lane);
-    }
-
-    const int total = pre[t.batch] * sc.units;
-    const int workers = min((int)gridDim.x * NW, total);
-    const int me = warp * gridDim.x + blockIdx.x;  // the first workers are on different SMs
-    if (me >= workers) return;
-    const Shares shares(total, workers);
-    const int t0 = shares.begin(me), n = shares.begin(me + 1) - t0;
-    const int parts = sc.units / c.kv_heads;
-
-    // The sequence, unit and tile at t0.
     Cursor cur;
-    {
+    int n, me = 0;
+    const int parts = sc.units / c.kv_heads;
+    int* pre = reinterpret_cast<int*>(smem + (size_t)NW * (Sh::kRing + Rows::kQBytes));
+    if constexpr (SMALL) {
+        const int row = blockIdx.x / sc.ranks, unit_no = row % sc.units;
+        cur.b = row / sc.units;
+        cur.t = Tiles(kv_len(t, cur.b, status), a.window, a.sinks, kShift2);
+        cur.head = unit_no / parts;
+        cur.part = unit_no % parts;
+        if (cur.t.count == 0) {  // no visible position: the same for the whole cluster
+            const int j0 = cur.head * sc.group + cur.part * Rows::kHeads, rows = min(Rows::kHeads, sc.group - cur.part * Rows::kHeads);
+            for (int r = blockIdx.x % sc.ranks; r < rows; r += sc.ranks) empty_row<typename Rows::Query>(a, cur.b, j0 + r, c.head_dim, tid, NW * 32);
+            return;
+        }
+        const int workers = min(sc.ranks * NW, cur.t.count);
+        me = warp * sc.ranks + blockIdx.x % sc.ranks;
+        const Shares shares(cur.t.count, workers);
+        cur.j = me < workers ? shares.begin(me) : 0;
+        n = me < workers ? shares.begin(me + 1) - cur.j : 0;
+    } else {
+        // Prefix sums of the sequences' tile counts.
+        for (int i = tid; i < t.batch; i += NW * 32) pre[i + 1] = Tiles(kv_len(t, i, status), a.window, a.sinks, kShift2).count;
+        __syncthreads();
+        if (warp == 0) prefix_sums(pre, t.batch, lane);
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int i = tid; i <= t.batch; i += NW * 32) sc.pre[i] = pre[i];
+        if (blockIdx.x == 0 && warp == 0 && sc.pre_all != sc.pre) {
+            for (int i = lane; i < t.batch; i += 32) sc.pre_all[i + 1] = (kv_len(t, i, status) + T - 1) >> kShift2;
+            __syncwarp();
+            prefix_sums(sc.pre_all, t.batch, lane);
+        }
+
+        const int total = pre[t.batch] * sc.units;
+        const int workers = min((int)gridDim.x * NW, total);
+        me = warp * gridDim.x + blockIdx.x;  // the first workers are on different SMs
+        if (me >= workers) return;
+        const Shares shares(total, workers);
+        const int t0 = shares.begin(me);
+        n = shares.begin(me + 1) - t0;
+
+        // The sequence, unit and tile at t0.
         cur.b = find_sequence(pre, t.batch, sc.units, t0);
         cur.t = Tiles(kv_len(t, cur.b, status), a.window, a.sinks, kShift2);
         const int r = t0 - pre[cur.b] * sc.units, u = r / cur.t.count;
@@ -162,7 +212,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
         cur.part = u - cur.head * parts;
     }
     auto advance = [&](Cursor& x) {
-        if (++x.j < x.t.count) return;
+        if (++x.j < x.t.count || SMALL) return;
         x.j = 0;
         if (++x.part < parts) return;
         x.part = 0;
@@ -264,7 +314,13 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
         rows.each_sum(unit, lane, [&](int r, float ref, float l) { sc.ml[slot * 16 + r] = make_float2(ref, l); });
     };
 
+    auto tile_number = [&](const Cursor& x) -> int64_t {  // where its scores are
+        if constexpr (SMALL) return ((int64_t)x.b * c.kv_heads + x.head) * sc.max_tiles + x.j;
+        return (int64_t)pre[x.b] * c.kv_heads + (int64_t)x.head * x.t.count + x.j;
+    };
+
     open_row();
+    [[maybe_unused]] const int first = cur.j;
     int stage = 0;
     for (int i = 0; i < n; ++i) {
         cp_wait<S - 2>();
@@ -278,21 +334,99 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
         const uint32_t kt = ring_a + stage * (2 * Sh::kTileBytes);
         stage = stage + 1 == S ? 0 : stage + 1;
         float* scores = nullptr;
-        if (sc.logits) {
-            const int64_t tile = (int64_t)pre[cur.b] * c.kv_heads + (int64_t)cur.head * cur.t.count + cur.j;
-            scores = sc.logits + (tile * sc.group + unit.row0) * T;
-        }
+        if (sc.logits) scores = sc.logits + (tile_number(cur) * sc.group + unit.row0) * T;
         rows.tile(kt, kt + Sh::kTileBytes, queries, cur.t, cur.t.tile(cur.j) << kShift2, scores, unit, lane);
-        if (cur.j + 1 == cur.t.count) {
+        if (!SMALL && cur.j + 1 == cur.t.count) {
             close_row(true);
             advance(cur);
             if (i + 1 < n) open_row();
         } else {
             advance(cur);
-            if (i + 1 == n) close_row(false);
+            if (!SMALL && i + 1 == n) close_row(false);
         }
     }
     cp_wait<0>();
+
+    if constexpr (SMALL) {
+        // Parts of the warps, then of the CTA, over the rings' shared memory.
+        cg::cluster_group cluster = cg::this_cluster();
+        const int nrows = min(Rows::kHeads, sc.group - unit.row0), rank = blockIdx.x % sc.ranks;
+        float* w_o = reinterpret_cast<float*>(smem);             // NW x rows x DP
+        float* c_o = w_o + NW * Rows::kHeads * DP;               // rows x DP
+        float2* w_ml = reinterpret_cast<float2*>(c_o + Rows::kHeads * DP);  // NW x rows
+        float2* c_ml = w_ml + NW * Rows::kHeads;                 // rows
+        float* s_lse = reinterpret_cast<float*>(c_ml + Rows::kHeads);
+        static_assert((size_t)(NW + 1) * Rows::kHeads * (DP * 4 + 8) + Rows::kHeads * 4 <= (size_t)NW * Sh::kRing, "the parts fit in the rings");
+        rows.gather();
+        __syncthreads();
+        rows.store_part(w_o + warp * Rows::kHeads * DP, unit, lane);
+        rows.each_sum(unit, lane, [&](int r, float ref, float l) { w_ml[warp * Rows::kHeads + r] = make_float2(ref, l); });
+        __syncthreads();
+        for (int i = tid; i < nrows * (DP / 4); i += NW * 32) {
+            const int r = i / (DP / 4), d = i % (DP / 4);
+            float top = -INFINITY, l = 0.0f;
+            for (int w = 0; w < NW; ++w) top = fmaxf(top, w_ml[w * Rows::kHeads + r].x);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int w = 0; w < NW; ++w) {
+                const float2 ml = w_ml[w * Rows::kHeads + r];
+                add_part(x, l, reinterpret_cast<const float4*>(w_o + (w * Rows::kHeads + r) * DP)[d], ml.y, rescale(ml.x, top));
+            }
+            reinterpret_cast<float4*>(c_o + r * DP)[d] = x;
+            if (d == 0) c_ml[r] = make_float2(top, l);
+        }
+        cluster.sync();
+        const float vs = FP8 && c.v_scale ? c.v_scale[unit.head] : 1.0f;
+        const int64_t row0 = (int64_t)unit.b * a.q_heads + unit.head * sc.group + unit.row0;
+        for (int i = rank * (NW * 32) + tid; i < nrows * (DP / 4); i += sc.ranks * (NW * 32)) {
+            const int r = i / (DP / 4), d = i % (DP / 4);
+            float top = -INFINITY, l = 0.0f;
+            for (int k = 0; k < sc.ranks; ++k) top = fmaxf(top, cluster.map_shared_rank(c_ml, k)[r].x);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < sc.ranks; ++k) {
+                const float2 ml = cluster.map_shared_rank(c_ml, k)[r];
+                add_part(x, l, reinterpret_cast<const float4*>(cluster.map_shared_rank(c_o, k) + r * DP)[d], ml.y, rescale(ml.x, top));
+            }
+            using QT = typename Rows::Query;
+            const float inv = l == 0.0f ? 0.0f : vs / l;
+            if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            QT* out = static_cast<QT*>(a.out) + (int64_t)unit.b * a.out_seq_stride + (int64_t)(unit.head * sc.group + unit.row0 + r) * a.out_head_stride;
+            if (4 * d < c.head_dim) *reinterpret_cast<uint2*>(out + 4 * d) = make_uint2(pack2<QT>(x.x * inv, x.y * inv), pack2<QT>(x.z * inv, x.w * inv));
+            if (d == 0 && a.lse) a.lse[row0 + r] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+        }
+        if (a.weight_out) {
+            if (tid < nrows) {
+                float top = -INFINITY, l = 0.0f;
+                for (int k = 0; k < sc.ranks; ++k) top = fmaxf(top, cluster.map_shared_rank(c_ml, k)[tid].x);
+                for (int k = 0; k < sc.ranks; ++k) {
+                    const float2 ml = cluster.map_shared_rank(c_ml, k)[tid];
+                    l += ml.y * rescale(ml.x, top);
+                }
+                s_lse[tid] = l == 0.0f ? INFINITY : top + log2f(l);
+            }
+            __syncthreads();
+            auto add = [&](int p, float w) {
+                const int index = sc.page.div(p), page = kv_page(t, c.num_pages, unit.b, index, status);
+                if (page < 0) return;
+                const int64_t at = ((int64_t)page * c.kv_heads + unit.head) * c.page_size + (p - index * c.page_size);
+                a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.0f) + w;
+            };
+            // the scores of this warp's own tiles
+            for (int i = lane; i < n * T; i += 32) {
+                const int j = first + i / T, p = (cur.t.tile(j) << kShift2) + i % T;
+                if (!cur.t.visible(p)) continue;
+                Cursor x = cur;
+                x.j = j;
+                const float* score = sc.logits + tile_number(x) * sc.group * T + i % T;
+                float w = 0.0f;
+                for (int r = 0; r < nrows; ++r) w += exp2_fast(score[r * T] - s_lse[r]);
+                add(p, w);
+            }
+            if (a.weight_in != a.weight_out && a.window > 0)
+                for (int p = rank * (NW * 32) + tid; p < cur.t.len; p += sc.ranks * (NW * 32))
+                    if (!cur.t.visible(p)) add(p, 0.0f);
+        }
+        cluster.sync();  // no CTA leaves while another may read its shared memory
+    }
 }
 
 // ---- the second and third launch: joins, empty rows, weights ----
@@ -311,8 +445,6 @@ struct Parts {
     // The first part is its worker's last row, the others are their workers' first ones.
     __device__ __forceinline__ int slot(int i) const { return (w0 + i) * 2 + (i == 0 ? 1 : 0); }
 };
-
-__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.0f : exp2_fast(from - to); }
 
 // One warp's share of a row's join: the parts team, team + teams, ..., with
 // every load independent of the others.
@@ -370,19 +502,24 @@ template <int DP> struct RowSum {
     }
 };
 
-constexpr int kTeamParts = 16;  // rows of more parts than this are joined by a whole CTA
-
 // The second launch finishes the rows that were cut and those without a
-// visible position: `per` rows a CTA, 1 or one per warp.
-template <typename QT, int DP>
-__global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, KvAttention a, Scratch sc, int per) {
+// visible position: a team of TEAM warps (1, 4 or all 16) a row.
+template <typename QT, int DP, int TEAM>
+__global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, KvAttention a, Scratch sc) {
     __shared__ float4 s_o[kJoinWarps][DP / 4];
     __shared__ float2 s_ml[kJoinWarps];
     begin_dependent();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units_per_head = sc.units / c.kv_heads;
     const int rows = t.batch * a.q_heads, all = sc.pre[t.batch];
+    constexpr int kPer = kJoinWarps / TEAM;
     auto unit = [&](int j) { return j / sc.group * units_per_head + j % sc.group / sc.heads; };
+    auto keep = [&](const RowSum<DP>& sum) {
+#pragma unroll
+        for (int k = 0; k < RowSum<DP>::kVec; ++k)
+            if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = sum.x[k];
+        if (lane == 0) s_ml[warp] = make_float2(sum.top, sum.l);
+    };
     // Adds up the sums of warps [w, w + n) and writes dimensions d0, d0 + step, ... of row r.
     auto store = [&](int r, int w, int n, int d0, int step) {
         const int b = r / a.q_heads, j = r % a.q_heads;
@@ -399,37 +536,35 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
         }
         if (d0 == 0) store_lse(sc, a, r, top, l);
     };
-    auto keep = [&](const RowSum<DP>& sum) {
-#pragma unroll
-        for (int k = 0; k < RowSum<DP>::kVec; ++k)
-            if (lane + k * 32 < DP / 4) s_o[warp][lane + k * 32] = sum.x[k];
-        if (lane == 0) s_ml[warp] = make_float2(sum.top, sum.l);
-    };
-    // Each warp looks at its row; long joins are left to the whole CTA.
-    const int r = blockIdx.x * per + (per == 1 ? 0 : warp);
-    bool wide = false;
-    if (r < rows && (per > 1 || warp == 0)) {
+    // Each team looks at its row; a row of many more parts than others is left
+    // to the whole CTA.
+    const int mine = warp / TEAM, member = warp % TEAM, r = blockIdx.x * kPer + mine;
+    bool joined = false, wide = false;
+    if (r < rows) {
         const int b = r / a.q_heads, j = r % a.q_heads, before = sc.pre[b], tiles = sc.pre[b + 1] - before;
-        if (tiles == 0) {  // no visible position
-            QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
-            for (int d = lane; d < c.head_dim; d += 32) out[d] = from_f32<QT>(0.0f);
-            if (lane == 0 && a.lse) a.lse[r] = -INFINITY;
+        if (tiles == 0) {
+            empty_row<QT>(a, b, j, c.head_dim, member * 32 + lane, TEAM * 32);
         } else {
             const Parts p(sc, before, tiles, all, unit(j));
-            wide = p.count > (per == 1 ? 1 : kTeamParts);
-            if (!wide && p.count > 1) {
+            wide = TEAM < kJoinWarps && p.count > 32 * TEAM;
+            joined = p.count > 1 && !wide;
+            if (joined) {
                 RowSum<DP> sum;
-                sum.add(sc, p, j % sc.group % sc.heads, 0, 1, lane);
+                sum.add(sc, p, j % sc.group % sc.heads, member, TEAM, lane);
                 keep(sum);
-                __syncwarp();
-                store(r, warp, 1, lane, 32);
             }
         }
     }
-    if (!__syncthreads_or(wide)) return;
-    for (int k = 0; k < per; ++k) {
-        if (!__syncthreads_or(wide && warp == k)) continue;
-        const int rk = blockIdx.x * per + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
+    if constexpr (TEAM == 1) {
+        __syncwarp();
+        if (joined) store(r, warp, 1, lane, 32);
+    }
+    const bool any = __syncthreads_or(wide);
+    if (TEAM > 1 && joined) store(r, mine * TEAM, TEAM, member * 32 + lane, TEAM * 32);
+    if (!any) return;
+    for (int k = 0; k < kPer; ++k) {
+        if (!__syncthreads_or(wide && mine == k)) continue;
+        const int rk = blockIdx.x * kPer + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
         RowSum<DP> sum;
         sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j)), j % sc.group % sc.heads, warp, kJoinWarps, lane);
         keep(sum);
@@ -547,14 +682,63 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     return p;
 }
 
+// Whether a call is small: a cluster of up to 8 CTAs for every unit (group <= 8:
+// one per key-value head) fits the GPU at a time, with few tiles a warp.  ranks
+// 0: it is not.
+struct SmallPlan {
+    int ranks;
+    Scratch sc;
+    size_t bytes;
+};
+
+cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const KvTable& t, const KvAttention& a, int warps, int tile,
+                       SmallPlan* out) {
+    SmallPlan p{};
+    *out = p;
+    const int tiles = (t.max_len + tile - 1) / tile;
+    const int64_t units = (int64_t)t.batch * c.kv_heads;
+    int ranks = 1;
+    while (ranks < 8 && ranks * warps < tiles) ranks *= 2;
+    for (; ranks > 0; ranks /= 2) {
+        int most = 0;
+        const cudaError_t e = cluster_limit(kern, warps * 32, smem, ranks, &most);
+        if (e != cudaSuccess) return e;
+        if (units <= most) break;
+    }
+    if (ranks == 0 || tiles > (a.weight_out ? kSmallTilesWeights : kSmallTiles) * ranks * warps) return cudaSuccess;
+    p.ranks = p.sc.ranks = ranks;
+    p.sc.group = a.q_heads / c.kv_heads;
+    p.sc.units = c.kv_heads;
+    p.sc.heads = 8;
+    p.sc.max_tiles = tiles;
+    p.sc.page = FastDiv(c.page_size);
+    p.bytes = round256(a.weight_out ? (size_t)units * tiles * p.sc.group * tile * 4 : 1);
+    *out = p;
+    return cudaSuccess;
+}
+
 template <typename QT, typename Rows, bool FP8, int DP, int T, int NW, int S>
 cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
-    auto* kern = k_kv_attend<Rows, FP8, DP, T, NW, S>;
+    auto* kern = k_kv_attend<Rows, FP8, DP, T, NW, S, false>;
     constexpr size_t smem = Shape<Rows, FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
     KernelSetup su;
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
     if (e != cudaSuccess) return e;
+    if constexpr (Rows::kHeads == 8) {
+        auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
+        SmallPlan small;
+        e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, NW, T, &small);
+        if (e != cudaSuccess) return e;
+        if (small.ranks > 0) {
+            if (scratch == nullptr) {
+                *bytes = small.bytes;
+                return cudaSuccess;
+            }
+            small.sc.logits = a.weight_out ? static_cast<float*>(scratch) : nullptr;
+            return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
+        }
+    }
     Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, su.sms);
     if (scratch == nullptr) {
         *bytes = p.bytes;
@@ -580,11 +764,12 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         if (a.lse) v.lse = a.lse + (int64_t)b0 * a.q_heads;
         e = launch_dependent(kern, p.grid, NW * 32, smem, 1, s, c, u, v, p.sc, status);
         if (e != cudaSuccess) return e;
-        // One row per warp, except where rows are few, or have so many parts on
-        // average that a whole CTA joins each.
-        const int rows = u.batch * a.q_heads;
-        const int per = rows <= 2 * su.sms || p.sc.workers > kTeamParts * u.batch * p.sc.units ? 1 : kJoinWarps;
-        e = launch_dependent(k_kv_join<QT, DP>, (rows + per - 1) / per, kJoinThreads, 0, 1, s, c, u, v, p.sc, per);
+        // Warps a row by the parts that rows have on average: most rows of more
+        // units than workers are whole.
+        const int rows = u.batch * a.q_heads, units = u.batch * p.sc.units;
+        const int team = units * 8 >= p.sc.workers ? 1 : units * 32 >= p.sc.workers ? 4 : kJoinWarps, per = kJoinWarps / team;
+        auto* join = team == 1 ? k_kv_join<QT, DP, 1> : team == 4 ? k_kv_join<QT, DP, 4> : k_kv_join<QT, DP, kJoinWarps>;
+        e = launch_dependent(join, (rows + per - 1) / per, kJoinThreads, 0, 1, s, c, u, v, p.sc);
         if (e != cudaSuccess) return e;
         if (a.weight_out == nullptr) continue;
         const bool vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;

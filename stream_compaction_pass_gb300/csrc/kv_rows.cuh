@@ -216,6 +216,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     using Base = RowsBase<QT, FP8, DP, T>;
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
+    using Query = QT;
     static constexpr int kHeads = 16, kNT = DP / 8, kPT = T / 8;
     static constexpr bool kQShared = DP == 256;  // Q's fragments in shared memory: registers are short
     static constexpr int kQBytes = kQShared ? kKS * 32 * 16 : 0;
@@ -479,6 +480,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
     using Base = RowsBase<QT, FP8, DP, T>;
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
+    using Query = QT;
     static constexpr int kHeads = 8, kMT = DP / 16, kHB = T / 16;
     static constexpr int kQBytes = 0;
 

@@ -15,6 +15,14 @@ namespace ss {
 namespace {
 std::mutex g_setup_mu;
 std::map<std::pair<const void*, int>, KernelSetup> g_setup;
+struct ClusterKey {
+    const void* kern;
+    int dev, ranks;
+    bool operator<(const ClusterKey& o) const {
+        return kern != o.kern ? kern < o.kern : dev != o.dev ? dev < o.dev : ranks < o.ranks;
+    }
+};
+std::map<ClusterKey, int> g_clusters;
 }  // namespace
 
 cudaError_t kernel_setup(const void* kern, int threads, size_t max_smem, KernelSetup* out) {
@@ -42,6 +50,37 @@ cudaError_t kernel_setup(const void* kern, int threads, size_t max_smem, KernelS
     k.blocks_per_sm = b > 0 ? b : 1;
     g_setup[key] = k;
     *out = k;
+    return cudaSuccess;
+}
+
+cudaError_t cluster_limit(const void* kern, int threads, size_t smem, int ranks, int* clusters) {
+    KernelSetup su;
+    cudaError_t e = kernel_setup(kern, threads, smem, &su);
+    if (e != cudaSuccess) return e;
+    ClusterKey key{kern, 0, ranks};
+    e = cudaGetDevice(&key.dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    auto it = g_clusters.find(key);
+    if (it == g_clusters.end()) {
+        int n = su.sms * su.blocks_per_sm;
+        if (ranks > 1) {
+            cudaLaunchAttribute at;
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = (unsigned)ranks;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(ranks * su.sms));
+            cfg.blockDim = dim3((unsigned)threads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        it = g_clusters.emplace(key, n).first;
+    }
+    *clusters = it->second;
     return cudaSuccess;
 }
 
