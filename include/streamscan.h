@@ -262,9 +262,8 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *
  * Shared rules:
  *   - head_dim is at most 256 and head_dim * element size a multiple of 16
- *     bytes, as are the strides; k, v and the rows of new tokens, q and out
- *     are 16-byte aligned (evict and append take up to 2^20 kv_heads *
- *     batch rows; attend 2^31 of any product that it forms).
+ *     bytes, as are the strides; k, v, the rows of new tokens, q and out are
+ *     16-byte aligned.
  *   - Lengths and page numbers are device data, checked on the device: a
  *     length below 0 or above max_len (or max_pages * page_size) is clamped,
  *     a page number outside [0, num_pages) is not followed, and either is
@@ -272,6 +271,10 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *     sequence in *failing_tile; the outputs of that sequence are then
  *     undefined, and nothing outside the arrays is touched.
  *   - batch == 0 is a no-op.  Results do not change from run to run.
+ *   - attend, and evict without `kept`, keep scratch in the stream's
+ *     workspace, sized by batch, heads and max_len (with weights 4 bytes a
+ *     score, at most 2 GB); as for the other calls, make one call of the
+ *     largest size before capturing a stream into a graph.
  */
 typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2 } ss_elem;
 
@@ -311,7 +314,8 @@ typedef struct ss_kv_table {
  * clamped to [-448, 448] and rounded to the nearest e4m3, ties to even; NaN
  * stays NaN.  The new slots' weights become 0 (where weight is not NULL).
  *   offsets  device, batch + 1 int32, offsets[0] = 0, non-decreasing, or NULL.
- *   tokens   offsets[batch]; batch where offsets is NULL.
+ *   tokens   offsets[batch]; batch where offsets is NULL.  tokens *
+ *            kv_heads < 2^31.
  * No two sequences may share a page that is appended to.
  */
 ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_elem type, const void *k_new,
@@ -337,7 +341,8 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *   weight_out  device, the layout of ss_kv_pages.weight, or NULL: no weights.
  *   weight_in   the same layout, or NULL (zeros).  weight_in == weight_out
  *               accumulates in place; a partial overlap is not allowed.
- * Scores, softmax and sums are fp32; out is rounded once.
+ * Scores, softmax and sums are fp32; out is rounded once.  At most 128 query
+ * heads per key-value head, and (max_len / 16 + 1) * q_heads < 2^31.
  */
 typedef struct ss_kv_attention {
     ss_elem type;
@@ -372,7 +377,8 @@ ss_status ss_kv_attend(const ss_kv_pages *cache, const ss_kv_table *seqs, const 
  * any sequence of src reads; source pages may be shared.
  *   kept  device, batch x kv_heads x keep int32, or NULL: the source position
  *         of each kept row, -1 from m on.
- *   0 <= sinks, 0 <= recent, sinks + recent <= keep, 1 <= keep.
+ *   0 <= sinks, 0 <= recent, sinks + recent <= keep, 1 <= keep; max_len <=
+ *   2^21, batch * kv_heads <= 2^20.
  */
 ss_status ss_kv_evict(const ss_kv_pages *src, const ss_kv_table *src_seqs, const ss_kv_pages *dst,
                       const ss_kv_table *dst_seqs, int32_t keep, int32_t sinks, int32_t recent, int32_t *kept,

@@ -3,7 +3,9 @@
 // head.  Bound by memory: each row is read once and written once.  A CTA takes
 // a few (token, head) rows: one thread a row finds its page and slot, then all
 // threads move 16-byte vectors of the result, every load issued before the
-// first store.
+// first store.  108 thousand tokens of 8 heads of 128, bf16 to e4m3: 62 us, 0.84
+// of the copy rate (96 with a look-up for every 64 rows, 102 with IEEE
+// divisions, which made it instruction-bound); 64 tokens 2.5 us.
 #include "kv.cuh"
 
 namespace ss {

