@@ -427,6 +427,9 @@ ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be multiples of 16 bytes");
     if (p->page_stride < 0 || p->head_stride < 0 || p->slot_stride < 0)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must not be negative");
+    if (p->page_stride > (1ll << 60) / p->num_pages || p->head_stride > (1ll << 60) / p->kv_heads ||
+        p->slot_stride > (1ll << 60) / p->page_size)
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides reach past 2^60 elements");
     if (p->type != SS_E4M3 && (p->k_scale || p->v_scale))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales belong to an SS_E4M3 cache");
     if (!aligned4(p->k_scale) || !aligned4(p->v_scale) || !aligned4(p->weight))
@@ -434,6 +437,15 @@ ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
     *out = ss::KvPages{static_cast<ss::KvElem>(p->type), p->kv_heads, p->head_dim, p->page_size, p->num_pages,
                        static_cast<char*>(p->k), static_cast<char*>(p->v), p->page_stride, p->head_stride,
                        p->slot_stride, p->k_scale, p->v_scale, p->weight};
+    return SS_OK;
+}
+
+// Rows that are written must not be one another's: each stride of more than
+// one row reaches past a row.
+ss_status kv_writable(const ss::KvPages& c, const char* name) {
+    if ((c.page_size > 1 && c.slot_stride < c.head_dim) || (c.kv_heads > 1 && c.head_stride < c.head_dim) ||
+        (c.num_pages > 1 && c.page_stride < c.head_dim))
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
     return SS_OK;
 }
 
@@ -465,6 +477,8 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     if (st != SS_OK) return st;
     st = kv_table(seqs, c, "seqs", &t);
     if (st != SS_OK) return st;
+    st = kv_writable(c, "cache");
+    if (st != SS_OK) return st;
     if (type != SS_BF16 && type != SS_F16) return fail(SS_ERR_UNSUPPORTED, "new tokens must be SS_BF16 or SS_F16");
     if (cache->type != SS_E4M3 && cache->type != type)
         return fail(SS_ERR_INVALID_ARG, "new tokens must have the cache's type, or the cache be SS_E4M3");
@@ -475,16 +489,16 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     if (tokens == 0 || t.batch == 0) return SS_OK;
     if (!k_new || !v_new) return fail(SS_ERR_INVALID_ARG, "null k_new or v_new");
     if (!aligned16(k_new) || !aligned16(v_new)) return fail(SS_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
-    if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8)
-        return fail(SS_ERR_INVALID_ARG, "token_stride and head_stride must be non-negative multiples of 16 bytes");
-    if (c.head_dim % 8) return fail(SS_ERR_INVALID_ARG, "head_dim must be a multiple of 8");
+    if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 || token_stride > 1ll << 40 || head_stride > 1ll << 40)
+        return fail(SS_ERR_INVALID_ARG, "token_stride and head_stride must be non-negative multiples of 16 bytes, at most 2^40 elements");
     Workspace* w = nullptr;
     st = get_workspace((cudaStream_t)stream, &w);
     if (st != SS_OK) return st;
     cudaError_t e = ss::launch_kv_append(c, t, static_cast<ss::KvElem>(type), k_new, v_new, token_stride, head_stride,
                                          offsets, (int64_t)tokens, device_sms(w->device), ws_status(w), (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "append launch");
-} catch (...) {
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
     return SS_ERR_NO_MEMORY;
 }
 
@@ -518,7 +532,10 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     if (!aligned16(a.q) || !aligned16(a.out)) return fail(SS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
     const int64_t strides[] = {a.q_seq_stride, a.q_head_stride, a.out_seq_stride, a.out_head_stride};
     for (int64_t x : strides)
-        if (x < 0 || x % 8) return fail(SS_ERR_INVALID_ARG, "strides of q and out must be non-negative multiples of 16 bytes");
+        if (x < 0 || x % 8 || x > 1ll << 40)
+            return fail(SS_ERR_INVALID_ARG, "strides of q and out must be non-negative multiples of 16 bytes, at most 2^40 elements");
+    if ((t.batch > 1 && a.out_seq_stride < c.head_dim) || (a.q_heads > 1 && a.out_head_stride < c.head_dim))
+        return fail(SS_ERR_INVALID_ARG, "rows of out overlap");
     const size_t qb = (size_t)((t.batch - 1) * strides[0] + (a.q_heads - 1) * strides[1] + c.head_dim) * 2;
     const size_t ob = (size_t)((t.batch - 1) * strides[2] + (a.q_heads - 1) * strides[3] + c.head_dim) * 2;
     if (overlaps(a.q, qb, a.out, ob)) return fail(SS_ERR_INVALID_ARG, "q and out overlap");
@@ -535,7 +552,8 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     if (st != SS_OK) return st;
     e = ss::launch_kv_attend(c, t, k, w->kv, ws_status(w), (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "attention launch");
-} catch (...) {
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
     return SS_ERR_NO_MEMORY;
 }
 
@@ -551,6 +569,8 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     st = kv_pages(dst, "dst", &d);
     if (st != SS_OK) return st;
     st = kv_table(dst_seqs, d, "dst_seqs", &dt);
+    if (st != SS_OK) return st;
+    st = kv_writable(d, "dst");
     if (st != SS_OK) return st;
     if (c.type != d.type || c.kv_heads != d.kv_heads || c.head_dim != d.head_dim)
         return fail(SS_ERR_INVALID_ARG, "dst must have src's type, kv_heads and head_dim");
@@ -571,7 +591,8 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     Workspace* w = nullptr;
     st = get_workspace((cudaStream_t)stream, &w);
     if (st != SS_OK) return st;
-    if (kept == nullptr) {
+    if (kept == nullptr) {  // no longer than the sequences can be
+        keep = std::min(keep, std::max(t.max_len, 1));
         st = ensure_kv(w, (size_t)t.batch * c.kv_heads * keep * 4);
         if (st != SS_OK) return st;
         kept = static_cast<int32_t*>(w->kv);
@@ -579,7 +600,8 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, device_sms(w->device), ws_status(w),
                                         (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "eviction launch");
-} catch (...) {
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
     return SS_ERR_NO_MEMORY;
 }
 

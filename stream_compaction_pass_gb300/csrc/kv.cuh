@@ -14,7 +14,10 @@ namespace ss {
 
 // Every kernel of this family is launched so that it may start before the
 // kernel ahead of it on the stream has ended (programmatic dependent launch),
-// and waits for that end here, first of all: only its launch overlaps.
+// and waits for that end here, first of all: only its launch overlaps.  What
+// the kernel ahead may have written is therefore written while this one runs,
+// so none of it is read as constant (no non-coherent loads, no const
+// __restrict__ parameters).
 __device__ __forceinline__ void begin_dependent() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -80,8 +83,8 @@ __device__ __forceinline__ int kv_page(const KvTable& t, int64_t num_pages, int 
     return -1;
 }
 
-// A 16-byte vector through the non-coherent path, and one streamed out.
-__device__ __forceinline__ uint4 ldg_vec(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// A 16-byte vector from L2, and one stored.
+__device__ __forceinline__ uint4 ldg_vec(const void* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void stg_vec(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -71,9 +71,9 @@ __device__ __forceinline__ float inverse_of(float s) {
 }
 
 template <typename T, bool QUANT>
-__global__ void __launch_bounds__(kAppendThreads, QUANT ? 4 : 6) k_kv_append(KvPages c, KvTable t, const T* __restrict__ k_new,
-                                                             const T* __restrict__ v_new, int64_t token_stride,
-                                                             int64_t head_stride, const int32_t* __restrict__ offsets,
+__global__ void __launch_bounds__(kAppendThreads, QUANT ? 4 : 6) k_kv_append(KvPages c, KvTable t, const T* k_new,
+                                                             const T* v_new, int64_t token_stride,
+                                                             int64_t head_stride, const int32_t* offsets,
                                                              int64_t rows, int per, int vecs, FastDiv by_vecs, FastDiv page,
                                                              uint32_t* status) {
     constexpr int kVecs = kAppendVecs<QUANT>;

@@ -71,8 +71,8 @@ constexpr int select_bytes(int threads, bool staged, int share) { return select_
 // in shared memory; keeping the keys of long rows too takes clusters of 8 and
 // four waves of them, 130 us.
 template <int N, bool STAGED, int V>
-__global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* __restrict__ kept,
-                                                 int32_t* __restrict__ new_lens, uint32_t* status) {
+__global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* kept,
+                                                 int32_t* new_lens, uint32_t* status) {
     constexpr int kWarps = N / 32, kPer = kBins / N;  // bins a thread adds up
     __shared__ SelectShared<N> sh;
     extern __shared__ __align__(16) unsigned char s_share[];
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     const float* weight = c.weight + (int64_t)h * c.page_size;
     const int64_t per_page = (int64_t)c.kv_heads * c.page_size;
     auto place = [&](int p, bool& good) {
-        const int index = ch.page.div(p), page = __ldg(pages + index);
+        const int index = ch.page.div(p), page = pages[index];
         good = (uint32_t)page < (uint32_t)c.num_pages;
         return weight + ((good ? page : 0) * per_page + (p - index * c.page_size));
     };
@@ -118,12 +118,12 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
         float w[4];
         bool good[4];
         if constexpr (V == 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(place(p, good[0])));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(place(p, good[0])));
             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
             good[1] = good[2] = good[3] = good[0];
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = __ldg(place(min(p + e, len - 1), good[e]));
+            for (int e = 0; e < 4; ++e) w[e] = __ldcg(place(min(p + e, len - 1), good[e]));
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) k[e] = evict_key(w[e]);
@@ -354,7 +354,7 @@ struct Move {
     FastDiv src_page, dst_page, by_vecs;
 };
 __global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, KvPages d, KvTable dt, Move mv,
-                                                         const int32_t* __restrict__ kept, uint32_t* status) {
+                                                         const int32_t* kept, uint32_t* status) {
     const int keep = mv.keep, rows = mv.rows, vecs = mv.vecs;
     __shared__ int64_t s_src[kMoveThreads], s_dst[kMoveThreads];  // byte offsets, or -1
     begin_dependent();

@@ -605,3 +605,62 @@ def test_evict_rows_alone_and_together(ss, rows):
     c = Cache(rng.integers(17000, 21000, rows).tolist() if rows <= 3 else rng.integers(3000, 5000, rows).tolist(), heads=1, dim=16, page=32,
               seed=rows, kind="e4m3")
     run_evict(ss, c, random_weights(c, rows), 2500, 4, 700)
+
+
+def test_back_to_back_calls_read_what_the_calls_before_them_wrote(ss):
+    """Kernels of these calls may start before the ones ahead have ended; a run
+    that waits between any two of them gives the same bits."""
+    import torch
+
+    def chain(wait):
+        c = Cache([700, 350, 3000], heads=4, dim=128, page=16, seed=61)
+        c.weight.nan_to_num_(0.0)
+        d = Cache([256, 256, 256], heads=4, dim=128, page=16, seed=62)
+        pages, table = c.ss(ss)
+        new_pages, new_table = d.ss(ss)
+        q0, x0 = torch.full((3, 16, 128), 0.01, device="cuda"), torch.full((3, 2, 4, 128), 0.5, device="cuda")
+        outs = []
+        kept = torch.empty(3, 4, 256, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for step in range(30):
+            x = (x0 * (step + 1)).sin().to(torch.bfloat16)
+            wait()
+            ss.ss_kv_append(pages, table, x[:, 0], x[:, 1])
+            wait()
+            q = (q0 * (step + 3)).cos().to(torch.bfloat16)
+            out = torch.empty_like(q)
+            wait()
+            ss.ss_kv_attend(pages, table, q, out, weight_in=c.weight, weight_out=c.weight)
+            wait()
+            ss.ss_kv_evict(pages, table, new_pages, new_table, 256, sinks=4, recent=100, kept=kept)
+            wait()
+            again = torch.empty_like(q)
+            ss.ss_kv_attend(new_pages, new_table, out, again)
+            wait()
+            outs += [out, again, kept.clone(), d.weight.clone()]
+        ok(ss)
+        return outs
+
+    plain = chain(lambda: None)
+    waited = chain(torch.cuda.synchronize)
+    for i, (a, b) in enumerate(zip(plain, waited)):
+        assert torch.equal(a.nan_to_num(7.0) if a.is_floating_point() else a, b.nan_to_num(7.0) if b.is_floating_point() else b), i
+
+
+def test_evict_keeping_more_than_there_is(ss):
+    """A budget past every length moves whole sequences and needs no scratch of its size."""
+    import torch
+    c = Cache([40, 0, 300], heads=2, dim=64, page=16, seed=63)
+    d = Cache([40, 0, 300], heads=2, dim=64, page=16, seed=64)
+    pages, table = c.ss(ss)
+    new_pages, new_table = d.ss(ss)
+    d.lens_dev.fill_(-1)
+    ss.ss_kv_evict(pages, table, new_pages, new_table, 2 ** 31 - 1, sinks=4, recent=16)
+    ok(ss)
+    assert d.lens_dev.tolist() == [40, 0, 300]
+    for new, host in ((d.k, c.k_host), (d.v, c.v_host), (d.weight, c.w_host)):
+        got = new.float().cpu().numpy()
+        for b in range(3):
+            for h in range(2):
+                assert np.array_equal(d.rows(got, b, h), c.rows(host, b, h).astype(np.float32))
+    torch.cuda.synchronize()

@@ -178,3 +178,28 @@ def test_e4m3_reference_matches_the_type():
     x = x[torch.isfinite(x)]
     want = x.clamp(-448, 448).to(torch.float8_e4m3fn).float().numpy()
     assert np.array_equal(e4m3_reference(x.numpy()), want)
+
+
+@pytest.mark.parametrize("bad", [dict(page_stride=1 << 60), dict(slot_stride=1 << 58), dict(head_stride=1 << 60)], ids=str)
+def test_strides_past_the_address_space(lib, bad):
+    assert attend(lib, p=pages(**bad)) == INV
+    assert append(lib, p=pages(**bad)) == INV
+    assert evict(lib, d=pages(**bad)) == INV
+
+
+@pytest.mark.parametrize("bad", [dict(slot_stride=0), dict(head_stride=32), dict(page_stride=0)], ids=str)
+def test_rows_that_are_written_do_not_overlap(lib, bad):
+    assert append(lib, p=pages(**bad)) == INV
+    assert evict(lib, d=pages(**bad)) == INV
+    assert "overlap" in ss.ss_last_error_detail()
+
+
+@pytest.mark.parametrize("bad", [dict(out_seq_stride=0), dict(out_head_stride=0), dict(out_head_stride=56), dict(q_seq_stride=1 << 41),
+                                 dict(out_seq_stride=1 << 41)], ids=str)
+def test_rows_of_out_do_not_overlap(lib, bad):
+    assert attend(lib, a=attention(**bad)) == INV
+
+
+def test_append_strides_past_the_address_space(lib):
+    assert append(lib, ts=1 << 41) == INV
+    assert append(lib, hs=1 << 41) == INV
