@@ -173,8 +173,8 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 
 // What both forms share.  8-bit caches multiply in fp16, which holds every
 // e4m3 value.  P is split into two 16-bit terms (kTwo), so that rounding it
-// adds nothing to the rounding of out (2^-16 against 2^-9 for bf16), except
-// under bf16 outputs of 8-bit caches, where one fp16 term (2^-12) is already
+// adds nothing to the rounding of out (2^-16 against 2^-8 for bf16), except
+// under bf16 outputs of 8-bit caches, where one fp16 term (2^-11) is already
 // finer than out.
 template <typename QT, bool FP8, int DP, int T> struct RowsBase {
     using MT = typename std::conditional<FP8, __half, QT>::type;
