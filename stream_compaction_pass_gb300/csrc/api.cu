@@ -591,13 +591,17 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     Workspace* w = nullptr;
     st = get_workspace((cudaStream_t)stream, &w);
     if (st != SS_OK) return st;
+    const int sms = device_sms(w->device);
+    const size_t hist = ss::kv_evict_scratch(c, t, sms);
+    size_t positions = 0;
     if (kept == nullptr) {  // no longer than the sequences can be
         keep = std::min(keep, std::max(t.max_len, 1));
-        st = ensure_kv(w, (size_t)t.batch * c.kv_heads * keep * 4);
-        if (st != SS_OK) return st;
-        kept = static_cast<int32_t*>(w->kv);
+        positions = (size_t)t.batch * c.kv_heads * keep * 4;
     }
-    cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, device_sms(w->device), ws_status(w),
+    st = ensure_kv(w, hist + positions);
+    if (st != SS_OK) return st;
+    if (kept == nullptr) kept = reinterpret_cast<int32_t*>(static_cast<char*>(w->kv) + hist);
+    cudaError_t e = ss::launch_kv_evict(c, t, d, dt, keep, sinks, recent, kept, static_cast<uint32_t*>(w->kv), sms, ws_status(w),
                                         (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "eviction launch");
 } catch (...) {  // of the host's own allocations

@@ -213,7 +213,9 @@ cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttenti
                              cudaStream_t s);
 constexpr int kKvMaxEvict = 1 << 21;  // the longest sequence an eviction takes
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
-                            int sinks, int recent, int32_t* kept, int sms, uint32_t* status, cudaStream_t s);
+                            int sinks, int recent, int32_t* kept, uint32_t* scratch, int sms, uint32_t* status, cudaStream_t s);
+// Device scratch of one eviction, in bytes, beside the kept positions.
+size_t kv_evict_scratch(const KvPages& c, const KvTable& t, int sms);
 
 // Ablations (reduce-then-scan, three kernels).  `totals` holds one value
 // per 4096-element tile.  tile_scan: 0 = register/shuffle tile scan,

@@ -13,7 +13,8 @@
 // by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  The selection reads 4 bytes a position; it is bound by latency
 // (three passes, each with a histogram, a scan and a barrier).  A row is one
 // CTA's; where there are few rows it is split over a cluster of up to 8 CTAs,
-// which add up their histograms through distributed shared memory.  128 rows of
+// which add up their histograms in L2 and exchange counts through distributed
+// shared memory.  128 rows of
 // 60 to 131 thousand positions take 70 us, 192 rows of up to 9001 17 us, 8 rows
 // of 2049 9 us.
 #include <cooperative_groups.h>
@@ -28,6 +29,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+constexpr int kSplitFrom = 16384, kSplit = 2048;  // the shortest row that pays for a cluster's meetings, and its shortest share
 constexpr int kStagedShare = 16384;            // the longest share whose keys are kept in shared memory
 constexpr int kClassedShare = 256 * 1024;      // the longest share whose classes are
 constexpr int kBlock = 1024;                   // positions a warp compacts at a time
@@ -35,7 +37,7 @@ constexpr int kListed = 16384;                 // candidates a long share keeps,
 static_assert((int64_t)kClassedShare * kMaxCluster == kKvMaxEvict, "the longest sequence is what a cluster can hold");
 
 template <int N> struct SelectShared {
-    uint32_t hist[3][kBins];  // one per pass: nobody clears what another CTA still reads
+    uint32_t hist[3][kBins];  // one per pass
     uint32_t counts[2];       // this CTA's keys below T, and equal to it
     uint32_t warp_lt[N / 32], warp_eq[N / 32];
     uint32_t digit, before, listed;
@@ -46,6 +48,7 @@ struct Choice {
     int keep, sinks, recent;
     int most_share;  // the longest share that the launch provides for, a multiple of 4
     FastDiv page;    // by src's page_size
+    uint32_t* hist;  // of split rows: 3 x kBins words a row
 };
 
 // Shared memory of the selection before its classes, and in all.
@@ -144,6 +147,11 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
 
     for (int i = tid; i < 3 * kBins; i += N) (&sh.hist[0][0])[i] = 0;
     if (tid == 0) sh.listed = 0;
+    uint32_t* row_hist = ch.hist + (int64_t)row * 3 * kBins;
+    if (ranks > 1) {
+        for (int i = rank * N + tid; i < 3 * kBins; i += ranks * N) row_hist[i] = 0;
+        cluster.sync();
+    }
     __syncthreads();
     uint32_t prefix = 0, want = (uint32_t)m;  // T's digits so far; which of the keys sharing them is T, from 1
 #pragma unroll
@@ -209,17 +217,22 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
                 }
             });
         }
+        // A split row's histogram is added up in L2 (its bins are few that are
+        // not empty).  Then every thread takes kPer consecutive bins, and a scan
+        // over the block finds the bin of the want-th key.
+        if (ranks > 1) {
+            __syncthreads();
+            for (int i = tid; i < kBins; i += N)
+                if (const uint32_t x = sh.hist[pass][i]) atomicAdd(row_hist + pass * kBins + i, x);
+        }
         meet();
-        // Every thread sums kPer consecutive bins over the cluster; a scan over the block finds the bin of the want-th key.
-        uint32_t s[kPer] = {}, mine = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const uint32_t* from = (ranks == 1 ? &sh.hist[pass][0] : cluster.map_shared_rank(&sh.hist[pass][0], r)) + tid * kPer;
+        uint32_t s[kPer], mine = 0;
+        const uint32_t* from_bins = (ranks > 1 ? row_hist + pass * kBins : &sh.hist[pass][0]) + tid * kPer;
 #pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                const uint2 x = *reinterpret_cast<const uint2*>(from + e);
-                s[e] += x.x;
-                s[e + 1] += x.y;
-            }
+        for (int e = 0; e < kPer; e += 2) {
+            const uint2 x = ranks > 1 ? __ldcg(reinterpret_cast<const uint2*>(from_bins + e)) : *reinterpret_cast<const uint2*>(from_bins + e);
+            s[e] = x.x;
+            s[e + 1] = x.y;
         }
 #pragma unroll
         for (int e = 0; e < kPer; ++e) mine += s[e];
@@ -344,6 +357,19 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     if (ranks > 1) cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
+// CTAs of a row's cluster: one per row where there are rows for half the SMs;
+// otherwise a long row is split, into shares of kSplit positions or more, while
+// the CTAs fit the SMs.  8 rows in a graph, one CTA / split: 10000 positions
+// 19.1 / 20.9 us with the move, 20000 33.0 / 27.3, 60000 90.0 / 68.7, 131072
+// 173.7 / 124.8.
+int select_ranks(const KvPages& c, const KvTable& t, int sms) {
+    const int64_t rows = (int64_t)t.batch * c.kv_heads;
+    int ranks = 1;
+    auto split = [&](int r) { return rows * r * 2 <= sms && t.max_len >= kSplitFrom && t.max_len / (r * 2) >= kSplit; };
+    while (ranks < kMaxCluster && (split(ranks) || t.max_len / ranks > kClassedShare - 4)) ranks *= 2;
+    return ranks;
+}
+
 constexpr int kMoveThreads = 256;
 constexpr int kMoveLoads = 8;  // 16-byte vectors that a thread has in flight
 
@@ -405,14 +431,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, 
 
 }  // namespace
 
+size_t kv_evict_scratch(const KvPages& c, const KvTable& t, int sms) {
+    return select_ranks(c, t, sms) > 1 ? (size_t)t.batch * c.kv_heads * 3 * kBins * 4 : 0;
+}
+
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
-                            int sinks, int recent, int32_t* kept, int sms, uint32_t* status, cudaStream_t s) {
+                            int sinks, int recent, int32_t* kept, uint32_t* scratch, int sms, uint32_t* status, cudaStream_t s) {
     const unsigned rows = (unsigned)t.batch * (unsigned)c.kv_heads;
-    // One CTA per row where there are rows for half the SMs; otherwise a row is
-    // split, into shares of 2048 positions or more, while the CTAs fit the SMs.
-    int ranks = 1;
-    auto split = [&](int r) { return (int64_t)rows * r * 2 <= sms && t.max_len / (r * 2) >= 2048; };
-    while (ranks < kMaxCluster && (split(ranks) || t.max_len / ranks > kClassedShare - 4)) ranks *= 2;
+    const int ranks = select_ranks(c, t, sms);
     const int share = ((t.max_len + ranks - 1) / ranks + 3) / 4 * 4;
     const bool staged = share <= kStagedShare;
     const bool vec4 = c.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(c.weight) & 15u) == 0;
@@ -423,7 +449,7 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     if (e != cudaSuccess) return e;
 
     e = launch_dependent(kern, (size_t)rows * ranks, threads, (size_t)select_bytes(threads, staged, share), ranks, s, c, t,
-                         Choice{keep, sinks, recent, share, FastDiv(c.page_size)}, kept, dt.lens, status);
+                         Choice{keep, sinks, recent, share, FastDiv(c.page_size), scratch}, kept, dt.lens, status);
     if (e != cudaSuccess) return e;
 
     const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
