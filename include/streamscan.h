@@ -341,8 +341,8 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *   weight_out  device, the layout of ss_kv_pages.weight, or NULL: no weights.
  *   weight_in   the same layout, or NULL (zeros).  weight_in == weight_out
  *               accumulates in place; a partial overlap is not allowed.
- * Scores, softmax and sums are fp32; out is rounded once.  At most 128 query
- * heads per key-value head, and (max_len / 16 + 1) * q_heads < 2^31.
+ * Scores, softmax and sums are fp32; out is rounded once.  q_heads <=
+ * 65536, at most 128 per key-value head, and (max_len / 16 + 1) * q_heads < 2^31.
  */
 typedef struct ss_kv_attention {
     ss_elem type;

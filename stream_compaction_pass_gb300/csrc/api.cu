@@ -516,6 +516,7 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     if (cache->type != SS_E4M3 && cache->type != a.type)
         return fail(SS_ERR_INVALID_ARG, "q must have the cache's type, or the cache be SS_E4M3");
     if (a.q_heads < 1 || a.q_heads % c.kv_heads) return fail(SS_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
+    if (a.q_heads > 65536) return fail(SS_ERR_INVALID_ARG, "q_heads must be at most 65536");
     if (a.q_heads / c.kv_heads > 128) return fail(SS_ERR_INVALID_ARG, "at most 128 query heads per key-value head");
     if (a.sinks < 0) return fail(SS_ERR_INVALID_ARG, "sinks must not be negative");
     if (!(a.scale - a.scale == 0.0f)) return fail(SS_ERR_INVALID_ARG, "scale must be finite");
@@ -545,12 +546,17 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, a.q_seq_stride, a.q_head_stride, a.out,
                             a.out_seq_stride, a.out_head_stride, a.scale, a.window, a.sinks, a.lse, a.weight_in,
                             a.weight_out};
-    size_t bytes = 0;
-    cudaError_t e = ss::kv_attend_scratch(c, t, k, &bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "attention set-up");
-    st = ensure_kv(w, bytes);
-    if (st != SS_OK) return st;
-    e = ss::launch_kv_attend(c, t, k, w->kv, ws_status(w), (cudaStream_t)stream);
+    struct Owner {
+        Workspace* w;
+        ss_status st;
+    } owner{w, SS_OK};
+    const ss::KvScratch mem{&owner, [](void* p, size_t bytes) -> void* {
+                                Owner* o = static_cast<Owner*>(p);
+                                o->st = ensure_kv(o->w, bytes);
+                                return o->st == SS_OK ? o->w->kv : nullptr;
+                            }};
+    cudaError_t e = ss::launch_kv_attend(c, t, k, mem, ws_status(w), (cudaStream_t)stream);
+    if (owner.st != SS_OK) return owner.st;
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "attention launch");
 } catch (...) {  // of the host's own allocations
     g_detail.clear();

@@ -207,9 +207,12 @@ struct KvAttention {
 cudaError_t launch_kv_append(const KvPages& c, const KvTable& t, KvElem type, const void* k_new, const void* v_new,
                              int64_t token_stride, int64_t head_stride, const int32_t* offsets, int64_t tokens,
                              int sms, uint32_t* status, cudaStream_t s);
-// Device scratch of one attention call, in bytes.
-cudaError_t kv_attend_scratch(const KvPages& c, const KvTable& t, const KvAttention& a, size_t* bytes);
-cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, uint32_t* status,
+// Device scratch by request, of at least `bytes` bytes; null: there is none.
+struct KvScratch {
+    void* owner;
+    void* (*get)(void* owner, size_t bytes);
+};
+cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status,
                              cudaStream_t s);
 constexpr int kKvMaxEvict = 1 << 21;  // the longest sequence an eviction takes
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,

@@ -38,6 +38,7 @@ namespace {
 // Sequences per launch: their tile counts' prefix sums are in shared memory,
 // beside a ring that leaves little of it at head_dim 256.
 template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
+
 namespace cg = cooperative_groups;
 
 // Tiles of a warp up to which a call whose units fit the GPU takes the form of
@@ -130,8 +131,8 @@ __device__ __forceinline__ void add_part(float4& x, float& l, const float4& y, f
     x.w += y.w * factor;
 }
 
-// A place in the list of tiles: sequence, key-value head, 16 query heads of
-// its group, tile.
+// A place in the list of tiles: sequence, key-value head, part of its group (8
+// or 16 query heads), tile.
 struct Cursor {
     int b, head, part, j;
     Tiles t;
@@ -714,39 +715,35 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
     p.sc.heads = 8;
     p.sc.max_tiles = tiles;
     p.sc.page = FastDiv(c.page_size);
-    p.bytes = round256(a.weight_out ? (size_t)units * tiles * p.sc.group * tile * 4 : 1);
+    p.bytes = round256((size_t)units * tiles * p.sc.group * tile * 4);
     *out = p;
     return cudaSuccess;
 }
 
 template <typename QT, typename Rows, bool FP8, int DP, int T, int NW, int S>
-cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
+cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
     auto* kern = k_kv_attend<Rows, FP8, DP, T, NW, S, false>;
     constexpr size_t smem = Shape<Rows, FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
-    KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
-    if (e != cudaSuccess) return e;
     if constexpr (Rows::kHeads == 8) {
         auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
         SmallPlan small;
-        e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, NW, T, &small);
+        cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, NW, T, &small);
         if (e != cudaSuccess) return e;
         if (small.ranks > 0) {
-            if (scratch == nullptr) {
-                *bytes = small.bytes;
-                return cudaSuccess;
+            if (a.weight_out) {
+                small.sc.logits = static_cast<float*>(mem.get(mem.owner, small.bytes));
+                if (small.sc.logits == nullptr) return cudaErrorMemoryAllocation;
             }
-            small.sc.logits = a.weight_out ? static_cast<float*>(scratch) : nullptr;
             return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
         }
     }
+    KernelSetup su;
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
+    if (e != cudaSuccess) return e;
     Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, su.sms);
-    if (scratch == nullptr) {
-        *bytes = p.bytes;
-        return cudaSuccess;
-    }
-    char* base = static_cast<char*>(scratch);
+    char* base = static_cast<char*>(mem.get(mem.owner, p.bytes));
+    if (base == nullptr) return cudaErrorMemoryAllocation;
     p.sc.pre = reinterpret_cast<int*>(base);
     p.sc.pre_all = p.sc.pre;
     if (a.window > 0 && a.weight_out && a.weight_in != a.weight_out) p.sc.pre_all = reinterpret_cast<int*>(base + p.at_lse2 / 2);
@@ -768,7 +765,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
         if (e != cudaSuccess) return e;
         // Warps a row by the parts that rows have on average: most rows of more
         // units than workers are whole.
-        const int rows = u.batch * a.q_heads, units = u.batch * p.sc.units;
+        const int64_t rows = (int64_t)u.batch * a.q_heads, units = (int64_t)u.batch * p.sc.units;
         const int team = units * 8 >= p.sc.workers ? 1 : units * 32 >= p.sc.workers ? 4 : kJoinWarps, per = kJoinWarps / team;
         auto* join = team == 1 ? k_kv_join<QT, DP, 1> : team == 4 ? k_kv_join<QT, DP, 4> : k_kv_join<QT, DP, kJoinWarps>;
         e = launch_dependent(join, (rows + per - 1) / per, kJoinThreads, 0, 1, s, c, u, v, p.sc);
@@ -791,32 +788,24 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, void* 
 // tiles of 32 positions, which spreads a tile's fixed instructions over as many
 // bytes (8-bit rows in tiles of 16: 140.6 against 98.5 us).
 template <typename QT, bool FP8>
-cudaError_t run_dim(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
+cudaError_t run_dim(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
     if (a.q_heads / c.kv_heads <= 8) {
-        if (c.head_dim <= 64) return run<QT, Rows8<QT, FP8, 64, 32>, FP8, 64, 32, FP8 ? 16 : 12, FP8 ? 3 : 2>(c, t, a, scratch, bytes, status, s);
-        if (c.head_dim <= 128) return run<QT, Rows8<QT, FP8, 128, FP8 ? 32 : 16>, FP8, 128, FP8 ? 32 : 16, 12, 2>(c, t, a, scratch, bytes, status, s);
-        return run<QT, Rows8<QT, FP8, 256, 16>, FP8, 256, 16, FP8 ? 8 : 4, 3>(c, t, a, scratch, bytes, status, s);
+        if (c.head_dim <= 64) return run<QT, Rows8<QT, FP8, 64, 32>, FP8, 64, 32, FP8 ? 16 : 12, FP8 ? 3 : 2>(c, t, a, mem, status, s);
+        if (c.head_dim <= 128) return run<QT, Rows8<QT, FP8, 128, FP8 ? 32 : 16>, FP8, 128, FP8 ? 32 : 16, 12, 2>(c, t, a, mem, status, s);
+        return run<QT, Rows8<QT, FP8, 256, 16>, FP8, 256, 16, FP8 ? 8 : 4, 3>(c, t, a, mem, status, s);
     }
-    if (c.head_dim <= 64) return run<QT, Rows16<QT, FP8, 64, 32>, FP8, 64, 32, FP8 ? 12 : 8, FP8 ? 4 : 3>(c, t, a, scratch, bytes, status, s);
-    if (c.head_dim <= 128) return run<QT, Rows16<QT, FP8, 128, FP8 ? 32 : 16>, FP8, 128, FP8 ? 32 : 16, 8, 3>(c, t, a, scratch, bytes, status, s);
-    return run<QT, Rows16<QT, FP8, 256, 16>, FP8, 256, 16, FP8 ? 7 : 4, 3>(c, t, a, scratch, bytes, status, s);
-}
-
-cudaError_t run_any(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, size_t* bytes, uint32_t* status, cudaStream_t s) {
-    const bool bf = a.type == KvElem::BF16;
-    if (c.type == KvElem::E4M3)
-        return bf ? run_dim<__nv_bfloat16, true>(c, t, a, scratch, bytes, status, s) : run_dim<__half, true>(c, t, a, scratch, bytes, status, s);
-    return bf ? run_dim<__nv_bfloat16, false>(c, t, a, scratch, bytes, status, s) : run_dim<__half, false>(c, t, a, scratch, bytes, status, s);
+    if (c.head_dim <= 64) return run<QT, Rows16<QT, FP8, 64, 32>, FP8, 64, 32, FP8 ? 12 : 8, FP8 ? 4 : 3>(c, t, a, mem, status, s);
+    if (c.head_dim <= 128) return run<QT, Rows16<QT, FP8, 128, FP8 ? 32 : 16>, FP8, 128, FP8 ? 32 : 16, 8, 3>(c, t, a, mem, status, s);
+    return run<QT, Rows16<QT, FP8, 256, 16>, FP8, 256, 16, FP8 ? 7 : 4, 3>(c, t, a, mem, status, s);
 }
 
 }  // namespace
 
-cudaError_t kv_attend_scratch(const KvPages& c, const KvTable& t, const KvAttention& a, size_t* bytes) {
-    return run_any(c, t, a, nullptr, bytes, nullptr, nullptr);
-}
-
-cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, void* scratch, uint32_t* status, cudaStream_t s) {
-    return run_any(c, t, a, scratch, nullptr, status, s);
+cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
+    const bool bf = a.type == KvElem::BF16;
+    if (c.type == KvElem::E4M3)
+        return bf ? run_dim<__nv_bfloat16, true>(c, t, a, mem, status, s) : run_dim<__half, true>(c, t, a, mem, status, s);
+    return bf ? run_dim<__nv_bfloat16, false>(c, t, a, mem, status, s) : run_dim<__half, false>(c, t, a, mem, status, s);
 }
 
 }  // namespace ss

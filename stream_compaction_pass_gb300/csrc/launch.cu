@@ -54,33 +54,38 @@ cudaError_t kernel_setup(const void* kern, int threads, size_t max_smem, KernelS
 }
 
 cudaError_t cluster_limit(const void* kern, int threads, size_t smem, int ranks, int* clusters) {
-    KernelSetup su;
-    cudaError_t e = kernel_setup(kern, threads, smem, &su);
-    if (e != cudaSuccess) return e;
     ClusterKey key{kern, 0, ranks};
-    e = cudaGetDevice(&key.dev);
+    cudaError_t e = cudaGetDevice(&key.dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(g_setup_mu);
-    auto it = g_clusters.find(key);
-    if (it == g_clusters.end()) {
-        int n = su.sms * su.blocks_per_sm;
-        if (ranks > 1) {
-            cudaLaunchAttribute at;
-            at.id = cudaLaunchAttributeClusterDimension;
-            at.val.clusterDim.x = (unsigned)ranks;
-            at.val.clusterDim.y = at.val.clusterDim.z = 1;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(ranks * su.sms));
-            cfg.blockDim = dim3((unsigned)threads);
-            cfg.dynamicSmemBytes = smem;
-            cfg.attrs = &at;
-            cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-            if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(g_setup_mu);
+        auto it = g_clusters.find(key);
+        if (it != g_clusters.end()) {
+            *clusters = it->second;
+            return cudaSuccess;
         }
-        it = g_clusters.emplace(key, n).first;
     }
-    *clusters = it->second;
+    KernelSetup su;
+    e = kernel_setup(kern, threads, smem, &su);
+    if (e != cudaSuccess) return e;
+    int n = su.sms * su.blocks_per_sm;
+    if (ranks > 1) {
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = (unsigned)ranks;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(ranks * su.sms));
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    g_clusters[key] = n;
+    *clusters = n;
     return cudaSuccess;
 }
 

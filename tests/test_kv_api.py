@@ -203,3 +203,8 @@ def test_rows_of_out_do_not_overlap(lib, bad):
 def test_append_strides_past_the_address_space(lib):
     assert append(lib, ts=1 << 41) == INV
     assert append(lib, hs=1 << 41) == INV
+
+
+def test_attend_head_counts(lib):
+    assert attend(lib, p=pages(kv_heads=1024), a=attention(q_heads=1024 * 65)) == INV
+    assert attend(lib, t=table(max_pages=1 << 24), a=attention(q_heads=256)) == INV  # more tiles than a list counts
