@@ -650,6 +650,14 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTabl
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Tiles of one sequence and unit, at most.
+int most_tiles(const KvTable& t, const KvAttention& a, int tile) {
+    const int all = (t.max_len + tile - 1) / tile;
+    if (a.window <= 0 || a.window >= t.max_len) return all;
+    const int64_t seen = ((int64_t)a.window + tile - 1) / tile + 1 + ((int64_t)a.sinks + tile - 1) / tile;
+    return seen < all ? (int)seen : all;
+}
+
 // How one call is cut into launches, and the scratch of the largest.
 struct Plan {
     int batch;  // sequences per launch
@@ -666,7 +674,7 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     p.sc.heads = heads;
     p.sc.units = c.kv_heads * ((p.sc.group + heads - 1) / heads);
     p.sc.rows = p.sc.group < heads ? p.sc.group : heads;
-    const size_t tiles = ((size_t)t.max_len + tile - 1) / tile;  // of one sequence and unit, at most
+    const size_t tiles = most_tiles(t, a, tile);
     const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
     size_t batch = t.batch < most_batch ? t.batch : most_batch;
     if (seq_logits * batch > kMaxLogits) batch = kMaxLogits / seq_logits;
@@ -685,20 +693,21 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     return p;
 }
 
-// Whether a call is small: a cluster of up to 8 CTAs for every unit (group <= 8:
-// one per key-value head) fits the GPU at a time, with few tiles a warp.  ranks
-// 0: it is not.
+// Whether a call is small: a cluster of up to 8 CTAs for every key-value head of
+// every sequence (whose group is one unit) fits the GPU at a time, with few
+// tiles a warp.  ranks 0: it is not.
 struct SmallPlan {
     int ranks;
     Scratch sc;
     size_t bytes;
 };
 
-cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const KvTable& t, const KvAttention& a, int warps, int tile,
+cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const KvTable& t, const KvAttention& a, int heads, int warps, int tile,
                        SmallPlan* out) {
     SmallPlan p{};
     *out = p;
-    const int tiles = (t.max_len + tile - 1) / tile;
+    if (a.q_heads / c.kv_heads > heads) return cudaSuccess;
+    const int tiles = most_tiles(t, a, tile);
     const int64_t units = (int64_t)t.batch * c.kv_heads;
     int ranks = 1;
     while (ranks < 8 && ranks * warps < tiles) ranks *= 2;
@@ -712,7 +721,7 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
     p.ranks = p.sc.ranks = ranks;
     p.sc.group = a.q_heads / c.kv_heads;
     p.sc.units = c.kv_heads;
-    p.sc.heads = 8;
+    p.sc.heads = heads;
     p.sc.max_tiles = tiles;
     p.sc.page = FastDiv(c.page_size);
     p.bytes = round256((size_t)units * tiles * p.sc.group * tile * 4);
@@ -725,21 +734,19 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     auto* kern = k_kv_attend<Rows, FP8, DP, T, NW, S, false>;
     constexpr size_t smem = Shape<Rows, FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
-    if constexpr (Rows::kHeads == 8) {
-        auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
-        SmallPlan small;
-        cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, NW, T, &small);
-        if (e != cudaSuccess) return e;
-        if (small.ranks > 0) {
-            if (a.weight_out) {
-                small.sc.logits = static_cast<float*>(mem.get(mem.owner, small.bytes));
-                if (small.sc.logits == nullptr) return cudaErrorMemoryAllocation;
-            }
-            return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
+    auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
+    SmallPlan small;
+    cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, &small);
+    if (e != cudaSuccess) return e;
+    if (small.ranks > 0) {
+        if (a.weight_out) {
+            small.sc.logits = static_cast<float*>(mem.get(mem.owner, small.bytes));
+            if (small.sc.logits == nullptr) return cudaErrorMemoryAllocation;
         }
+        return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
     }
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
+    e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
     if (e != cudaSuccess) return e;
     Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, su.sms);
     char* base = static_cast<char*>(mem.get(mem.owner, p.bytes));
