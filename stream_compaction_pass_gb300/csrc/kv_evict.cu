@@ -1,5 +1,6 @@
 // kv_evict.cu -- eviction from a paged key-value cache by gathered attention
-// weight (streamscan.h, ss_kv_evict), in two launches.
+// weight (streamscan.h, ss_kv_evict), in two launches, or one where rows keep
+// little.
 //
 // The selection is a compaction whose predicate is a rank: with weights as
 // 32-bit keys, best first (kv.cuh, evict_key), it finds the m-th smallest key
@@ -33,6 +34,10 @@ constexpr int kSplitFrom = 16384, kSplit = 2048;  // the shortest row that pays 
 constexpr int kStagedShare = 16384;            // the longest share whose keys are kept in shared memory
 constexpr int kClassedShare = 256 * 1024;      // the longest share whose classes are
 constexpr int kBlock = 1024;                   // positions a warp compacts at a time
+// Bytes of a row's kept k and v up to which its selection moves them, in one
+// launch, which also costs the host 3 to 4 us less: 300 rows of 141 x 512 bytes
+// 12.5 against 15.0 us in a graph, 8 of 256 x 512 11.5 / 10.5, 8 of 512 x 512 16.2 / 10.5.
+constexpr int64_t kFusedBytes = 128 * 1024;
 constexpr int kListed = 16384;                 // candidates a long share keeps, 8 bytes each
 static_assert((int64_t)kClassedShare * kMaxCluster == kKvMaxEvict, "the longest sequence is what a cluster can hold");
 
@@ -58,6 +63,62 @@ __host__ __device__ constexpr int select_front(int threads, bool staged, int sha
 }
 constexpr int select_bytes(int threads, bool staged, int share) { return select_front(threads, staged, share) + (share / 4 + 15) / 16 * 16; }
 
+constexpr int kMoveThreads = 256;
+constexpr int kMoveLoads = 8;  // 16-byte vectors that a thread has in flight
+
+struct Move {
+    int keep, rows, groups, vecs, elem_bytes;  // groups of `rows` kept rows per (sequence, head); `vecs` vectors a row
+    FastDiv src_page, dst_page, by_vecs;
+};
+
+// Copies kept rows j0 .. j0 + mv.rows - 1 of one (sequence, head), k and v, by
+// the N threads of a CTA: all of a thread's loads are issued before its first
+// store.  `kept` is that row's list; s_place holds 2 mv.rows offsets.
+template <int N, int LOADS>
+__device__ __forceinline__ void move_rows(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, const Move& mv,
+                                          const int32_t* kept, int b, int h, int j0, int64_t* s_place, uint32_t* status) {
+    const int tid = threadIdx.x, rows = mv.rows, vecs = mv.vecs;
+    int64_t *s_src = s_place, *s_dst = s_place + rows;  // byte offsets, or -1
+    for (int r = tid; r < rows; r += N) {
+        const int j = j0 + r, p = j < mv.keep ? kept[j] : -1;
+        int64_t src = -1, dst = -1;
+        if (p >= 0) {
+            const int fi = mv.src_page.div(p), ti = mv.dst_page.div(j);
+            const int from = kv_page(t, c.num_pages, b, fi, status);
+            const int to = kv_page(dt, d.num_pages, b, ti, status);
+            if (from >= 0 && to >= 0) {
+                const int fs = p - fi * c.page_size, ts = j - ti * d.page_size;
+                src = ((int64_t)from * c.page_stride + (int64_t)h * c.head_stride + (int64_t)fs * c.slot_stride) * mv.elem_bytes;
+                dst = ((int64_t)to * d.page_stride + (int64_t)h * d.head_stride + (int64_t)ts * d.slot_stride) * mv.elem_bytes;
+                if (d.weight)
+                    d.weight[((int64_t)to * d.kv_heads + h) * d.page_size + ts] = c.weight[((int64_t)from * c.kv_heads + h) * c.page_size + fs];
+            }
+        }
+        s_src[r] = src;
+        s_dst[r] = dst;
+    }
+    __syncthreads();
+    const int half = rows * vecs;  // k's vectors, then v's
+    for (int i0 = tid; i0 < 2 * half; i0 += N * LOADS) {
+        uint4 x[LOADS];
+        char* to[LOADS];
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) {
+            const int i = i0 + l * N;
+            to[l] = nullptr;
+            if (i >= 2 * half) continue;
+            const bool is_v = i >= half;
+            const int k = is_v ? i - half : i, r = mv.by_vecs.div(k), v = k - r * vecs;
+            if (s_src[r] < 0) continue;
+            x[l] = ldg_vec((is_v ? c.v : c.k) + s_src[r] + v * 16);
+            to[l] = (is_v ? d.v : d.k) + s_dst[r] + v * 16;
+        }
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l)
+            if (to[l]) stg_vec(to[l], x[l]);
+    }
+}
+
 // One cluster per (sequence, head); its CTAs take consecutive shares of the
 // positions, each a multiple of 4 long.  N threads.  V: weights are read in
 // fours, which lie in one page and are 16-byte aligned.
@@ -73,9 +134,11 @@ constexpr int select_bytes(int threads, bool staged, int share) { return select_
 // read every weight, 95 with the classes, 70 with the list and the compaction
 // in shared memory; keeping the keys of long rows too takes clusters of 8 and
 // four waves of them, 130 us.
-template <int N, bool STAGED, int V>
-__global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch, int32_t* kept,
-                                                 int32_t* new_lens, uint32_t* status) {
+//
+// FUSED: the CTA (one a row) also moves its row, where that is little.
+template <int N, bool STAGED, int V, bool FUSED>
+__global__ void __launch_bounds__(N, N == 512 ? 2 : 1) k_kv_select(KvPages c, KvTable t, KvPages d, KvTable dt, Move mv, Choice ch, int32_t* kept,
+                                                                   int32_t* new_lens, uint32_t* status) {
     constexpr int kWarps = N / 32, kPer = kBins / N;  // bins a thread adds up
     __shared__ SelectShared<N> sh;
     extern __shared__ __align__(16) unsigned char s_share[];
@@ -93,8 +156,18 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     const int m = min(len, ch.keep);
     int32_t* out = kept + (int64_t)row * ch.keep;
     if (h == 0 && rank == 0 && tid == 0) new_lens[b] = m;
+    auto move_row = [&]() {
+        if constexpr (FUSED) {
+            __syncthreads();  // the row's list is written, and shared memory free
+            for (int j0 = 0; j0 < m; j0 += mv.rows) {
+                move_rows<N, 4>(c, t, d, dt, mv, out, b, h, j0, reinterpret_cast<int64_t*>(s_share), status);
+                __syncthreads();
+            }
+        }
+    };
     if (len <= ch.keep) {  // the same for the whole cluster
         for (int j = rank * N + tid; j < ch.keep; j += ranks * N) out[j] = j < m ? j : -1;
+        move_row();
         return;
     }
     const int share = ((len + ranks - 1) / ranks + 3) / 4 * 4;
@@ -355,6 +428,7 @@ __global__ void __launch_bounds__(N) k_kv_select(KvPages c, KvTable t, Choice ch
     }
     if (bad) record_error(status, kErrKvTable, (uint32_t)(t.first + b));
     if (ranks > 1) cluster.sync();  // no CTA leaves while another may read its shared memory
+    move_row();
 }
 
 // CTAs of a row's cluster: one per row where there are rows for half the SMs;
@@ -370,63 +444,15 @@ int select_ranks(const KvPages& c, const KvTable& t, int sms) {
     return ranks;
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 8;  // 16-byte vectors that a thread has in flight
-
-// Copies `rows` kept rows of one (sequence, head) per CTA, k and v: all of a
-// thread's loads are issued before its first store.
-struct Move {
-    int keep, rows, groups, vecs, elem_bytes;  // groups of `rows` kept rows per (sequence, head); `vecs` vectors a row
-    FastDiv src_page, dst_page, by_vecs;
-};
-__global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, KvPages d, KvTable dt, Move mv,
-                                                         const int32_t* kept, uint32_t* status) {
-    const int keep = mv.keep, rows = mv.rows, vecs = mv.vecs;
-    __shared__ int64_t s_src[kMoveThreads], s_dst[kMoveThreads];  // byte offsets, or -1
+// One CTA per group of a row's kept positions.
+__global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, KvPages d, KvTable dt, Move mv, const int32_t* kept, uint32_t* status) {
+    __shared__ int64_t s_place[2 * kMoveThreads];
     begin_dependent();
-    const int tid = threadIdx.x;
-    const int row = blockIdx.x / mv.groups, j0 = (blockIdx.x - row * mv.groups) * rows;
-    const int b = row / c.kv_heads, h = row % c.kv_heads;
-    if (kept[(int64_t)row * keep + j0] < 0) return;
-    if (tid < rows) {
-        const int j = j0 + tid;
-        const int p = j < keep ? kept[(int64_t)row * keep + j] : -1;
-        int64_t src = -1, dst = -1;
-        if (p >= 0) {
-            const int fi = mv.src_page.div(p), ti = mv.dst_page.div(j);
-            const int from = kv_page(t, c.num_pages, b, fi, status);
-            const int to = kv_page(dt, d.num_pages, b, ti, status);
-            if (from >= 0 && to >= 0) {
-                const int fs = p - fi * c.page_size, ts = j - ti * d.page_size;
-                src = ((int64_t)from * c.page_stride + (int64_t)h * c.head_stride + (int64_t)fs * c.slot_stride) * mv.elem_bytes;
-                dst = ((int64_t)to * d.page_stride + (int64_t)h * d.head_stride + (int64_t)ts * d.slot_stride) * mv.elem_bytes;
-                if (d.weight)
-                    d.weight[((int64_t)to * d.kv_heads + h) * d.page_size + ts] = c.weight[((int64_t)from * c.kv_heads + h) * c.page_size + fs];
-            }
-        }
-        s_src[tid] = src;
-        s_dst[tid] = dst;
-    }
-    __syncthreads();
-    const int half = rows * vecs;  // k's vectors, then v's
-    for (int i0 = tid; i0 < 2 * half; i0 += kMoveThreads * kMoveLoads) {
-        uint4 x[kMoveLoads];
-        char* to[kMoveLoads];
-#pragma unroll
-        for (int l = 0; l < kMoveLoads; ++l) {
-            const int i = i0 + l * kMoveThreads;
-            to[l] = nullptr;
-            if (i >= 2 * half) continue;
-            const bool is_v = i >= half;
-            const int k = is_v ? i - half : i, r = mv.by_vecs.div(k), v = k - r * vecs;
-            if (s_src[r] < 0) continue;
-            x[l] = ldg_vec((is_v ? c.v : c.k) + s_src[r] + v * 16);
-            to[l] = (is_v ? d.v : d.k) + s_dst[r] + v * 16;
-        }
-#pragma unroll
-        for (int l = 0; l < kMoveLoads; ++l)
-            if (to[l]) stg_vec(to[l], x[l]);
-    }
+    const int row = blockIdx.x / mv.groups, j0 = (blockIdx.x - row * mv.groups) * mv.rows;
+    kept += (int64_t)row * mv.keep;
+    if (kept[j0] < 0) return;
+    const int b = row / c.kv_heads;
+    move_rows<kMoveThreads, kMoveLoads>(c, t, d, dt, mv, kept, b, row - b * c.kv_heads, j0, s_place, status);
 }
 
 }  // namespace
@@ -442,22 +468,23 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     const int share = ((t.max_len + ranks - 1) / ranks + 3) / 4 * 4;
     const bool staged = share <= kStagedShare;
     const bool vec4 = c.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(c.weight) & 15u) == 0;
-    auto* kern = staged ? (vec4 ? k_kv_select<512, true, 4> : k_kv_select<512, true, 1>) : (vec4 ? k_kv_select<1024, false, 4> : k_kv_select<1024, false, 1>);
+    const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
+    const int most = keep < t.max_len ? keep : t.max_len;
+    const bool fused = staged && ranks == 1 && (int64_t)most * vecs * 32 <= kFusedBytes;
+    auto* kern = !staged ? (vec4 ? k_kv_select<1024, false, 4, false> : k_kv_select<1024, false, 1, false>)
+                 : fused ? (vec4 ? k_kv_select<512, true, 4, true> : k_kv_select<512, true, 1, true>)
+                         : (vec4 ? k_kv_select<512, true, 4, false> : k_kv_select<512, true, 1, false>);
     const int threads = staged ? 512 : 1024, bytes_most = select_bytes(threads, staged, staged ? kStagedShare : kClassedShare);
     KernelSetup su;
     cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), threads, (size_t)bytes_most, &su);
     if (e != cudaSuccess) return e;
 
-    e = launch_dependent(kern, (size_t)rows * ranks, threads, (size_t)select_bytes(threads, staged, share), ranks, s, c, t,
-                         Choice{keep, sinks, recent, share, FastDiv(c.page_size), scratch}, kept, dt.lens, status);
-    if (e != cudaSuccess) return e;
-
-    const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
-    const int most = keep < t.max_len ? keep : t.max_len;
-    const int per = kv_rows_per_cta(kMoveThreads * kMoveLoads / (2 * vecs), kMoveThreads, (int64_t)rows * most, sms);
+    const int per = fused ? 256 : kv_rows_per_cta(kMoveThreads * kMoveLoads / (2 * vecs), kMoveThreads, (int64_t)rows * most, sms);
     const int groups = (most + per - 1) / per;
-    if (groups == 0) return cudaSuccess;
     const Move mv{keep, per, groups, vecs, bytes, FastDiv(c.page_size), FastDiv(d.page_size), FastDiv(vecs)};
+    e = launch_dependent(kern, (size_t)rows * ranks, threads, (size_t)select_bytes(threads, staged, share), ranks, s, c, t, d, dt, mv,
+                         Choice{keep, sinks, recent, share, FastDiv(c.page_size), scratch}, kept, dt.lens, status);
+    if (e != cudaSuccess || fused || groups == 0) return e;
     return launch_dependent(k_kv_move, (size_t)rows * groups, kMoveThreads, 0, 1, s, c, t, d, dt, mv, kept, status);
 }
 
