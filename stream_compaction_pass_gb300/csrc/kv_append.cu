@@ -31,7 +31,7 @@ template <> __device__ __forceinline__ float2 open_pair<__half>(uint32_t u) {
 }
 
 // 16 elements over the scale, as e4m3, by a reciprocal and one correction: q =
-// x r, then q + (x - q s) r, with r = 1 / s rounded.  That is the rounded
+// x r, then q - (q s - x) r, with r = 1 / s rounded.  That is the rounded
 // quotient unless x / s lies within 2^-22 of a unit in the last place of the
 // middle of two floats, which could matter only next to a tie of two e4m3
 // values.  There, with X (11 bits), S (24) and T (5, of the tie) the integer
@@ -39,8 +39,10 @@ template <> __device__ __forceinline__ float2 open_pair<__half>(uint32_t u) {
 // S1 2^20 + e with |e| < 8, 8 <= S1 <= 16 and T e + S1 = 0: only S = 2^24 - 1
 // with T = 16, whose corrected quotient is (1 + 2^-24 + 2^-70) times the tie,
 // on the same side of the middle as x / s.  (On the lower side, T e = S1 has no
-// solution.)  So the e4m3 result is that of the division.  Scales for which a
-// step could leave fp32's normal range, and non-finite elements, are divided.
+// solution.)  So the e4m3 result is that of the division, and a zero keeps its
+// sign: q s - x is then +0, and the correction -0, which changes no q, where
+// r > 0.  Other scales, those for which a step could leave fp32's normal range,
+// and non-finite elements are divided.
 template <typename T> __device__ __forceinline__ uint4 quant16(const uint4 (&x)[2], float scale, float inverse) {
     const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     float y[16], sum = 0.0f;
@@ -48,8 +50,8 @@ template <typename T> __device__ __forceinline__ uint4 quant16(const uint4 (&x)[
     for (int i = 0; i < 8; ++i) {
         const float2 a = open_pair<T>(w[i]);
         const float q0 = a.x * inverse, q1 = a.y * inverse;
-        y[2 * i] = fmaf(fmaf(-q0, scale, a.x), inverse, q0);
-        y[2 * i + 1] = fmaf(fmaf(-q1, scale, a.y), inverse, q1);
+        y[2 * i] = fmaf(-fmaf(q0, scale, -a.x), inverse, q0);
+        y[2 * i + 1] = fmaf(-fmaf(q1, scale, -a.y), inverse, q1);
         sum += fabsf(y[2 * i]) + fabsf(y[2 * i + 1]);
     }
     if (!(sum < INFINITY)) {  // an infinity or NaN among them, or no inverse
@@ -64,10 +66,9 @@ template <typename T> __device__ __forceinline__ uint4 quant16(const uint4 (&x)[
                       quant4(y[12], y[13], y[14], y[15]));
 }
 
-// The reciprocal of a scale, NaN for those outside [2^-60, 2^60].
+// The reciprocal of a scale, NaN for those outside [2^-60, 2^60] and negative ones.
 __device__ __forceinline__ float inverse_of(float s) {
-    const float a = fabsf(s);
-    return a >= 0x1p-60f && a <= 0x1p60f ? __frcp_rn(s) : NAN;
+    return s >= 0x1p-60f && s <= 0x1p60f ? __frcp_rn(s) : NAN;
 }
 
 template <typename T, bool QUANT>

@@ -664,3 +664,24 @@ def test_evict_keeping_more_than_there_is(ss):
             for h in range(2):
                 assert np.array_equal(d.rows(got, b, h), c.rows(host, b, h).astype(np.float32))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("src", ["bf16", "f16"])
+def test_append_keeps_the_sign_of_zeros(ss, src):
+    """x / scale in an 8-bit cache, bit for bit: also -0, quotients that round
+    to a zero, and negative scales."""
+    import torch
+    heads, n = 4, 8
+    c = Cache([n], heads=heads, dim=16, page=16, kind="e4m3", seed=53)
+    c.ks, c.vs = torch.tensor([1.0, 0.37, -0.37, 2.0 ** 70]), torch.tensor([24.0, -1.0, 2.0 ** -70, -3.0])
+    x = torch.tensor([0.0, -0.0, 6e-5, -6e-5, 1e-7, -1e-7, 1.0, -1.0]).repeat(n, 2, heads, 2).to(torch_type(src))
+    pages, table = c.ss(ss)
+    ss.ss_kv_append(pages, table, x[:, 0].contiguous().cuda(), x[:, 1].contiguous().cuda(),
+                    offsets=torch.tensor([0, n], dtype=torch.int32).cuda())
+    ok(ss)
+    for i, (pool, scale) in enumerate(((c.k, c.ks), (c.v, c.vs))):
+        q = x[:, i].float().numpy() / scale.numpy()[:, None]
+        want = np.copysign(e4m3_reference(q), q)
+        p = np.arange(n)
+        got = pool.float().cpu().numpy()[c.table_host[0, p // 16], :, p % 16]
+        assert np.array_equal(got, want.astype(np.float32)) and np.array_equal(np.signbit(got), np.signbit(want))
