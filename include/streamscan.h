@@ -331,8 +331,9 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *   weight_out(h, p) = weight_in(h, p) + sum over h's query heads of
  *                      exp(s(p) - lse), for every position p < len.
  * A row with no visible position, or all of whose scores are -inf, gives
- * out = 0 and lse = -inf and adds no weight.  A NaN in a visible row spreads
- * as in the formula; rows that are not visible are not read.
+ * out = 0 and lse = -inf and adds no weight.  NaN and infinities in a visible
+ * row spread as in the formula (an infinite v may do so at any weight, also
+ * one of 0); rows that are not visible are not read.
  *   type        of q and out, SS_BF16 or SS_F16: the cache's, or either with
  *               an SS_E4M3 cache.
  *   q, out      row (b, j) at b * seq_stride + j * head_stride (each its own

@@ -42,7 +42,7 @@ template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
 namespace cg = cooperative_groups;
 
 // Tiles of a warp up to which a call whose units fit the GPU takes the form of
-// one launch.  Measured on 8 heads of 128, one sequence: 517 positions 5.2
+// one launch.  Measured on 8 heads of 128, one sequence: 517 positions 5.4
 // against 9.7 us, 16000 (10 tiles) 17.2 / 22.3 and with weights 24.3 / 25.2,
 // 32000 (21 tiles) 27.7 / 31.1 and with weights 40.4 / 35.1.
 constexpr int kSmallTiles = 24, kSmallTilesWeights = 12;

@@ -11,8 +11,9 @@
 //           transposition in registers.  For groups of up to 8.
 //
 // Both keep, per query head, the largest X so far, l = sum 2^(X - R) and O,
-// with R that maximum (less 15 where products are fp16, so that small weights
-// stay normal numbers).
+// with R that maximum less 15 where products are fp16, so that small weights
+// stay normal numbers, or plus 24 where they are bf16, so that O stays below
+// the largest number whatever the values are.
 #pragma once
 
 #include "kv.cuh"
@@ -106,10 +107,36 @@ template <typename T> __device__ __forceinline__ float2 open2(uint32_t u) {
     return Pair<T>::open(*reinterpret_cast<const typename Pair<T>::type*>(&u));
 }
 
-// What rounding (x, y) to `high` left out, as 16-bit values.
-template <typename T> __device__ __forceinline__ uint32_t rest2(float x, float y, uint32_t high) {
+// Two 16-bit numbers, at least 2^-24 (fp16) or 2^-126 (bf16); NaN stays.
+template <typename T> __device__ __forceinline__ uint32_t least2(uint32_t x) {
+    uint32_t y;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x00010001u));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x00800080u));
+    return y;
+}
+// Two numbers as 16-bit ones, rounded toward zero.
+template <typename T> __device__ __forceinline__ uint32_t trunc2(float x, float y) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    else
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+
+// Weights (x, y) >= 0 as two 16-bit terms, of which the second has what the
+// first leaves out.  POSITIVE: the first is truncated, so that the second is not
+// negative, and both are kept above zero: an infinite value that they multiply
+// stays infinite instead of becoming inf - inf or 0 inf (0.2 % of the long
+// ragged batch's time, 0.2 us of a call of 517 positions).  That adds at most 2^-38 of the row's largest weight in fp16,
+// 2^-101 in bf16.
+template <typename T, bool POSITIVE> __device__ __forceinline__ void split2(float x, float y, uint32_t& high, uint32_t& rest) {
+    high = POSITIVE ? least2<T>(trunc2<T>(x, y)) : pack2<T>(x, y);
     const float2 h = open2<T>(high);
-    return pack2<T>(x - h.x, y - h.y);
+    rest = pack2<T>(x - h.x, y - h.y);
+    if constexpr (POSITIVE) rest = least2<T>(rest);
 }
 
 // Two e4m3 bytes as two fp16 (exact).
@@ -178,7 +205,7 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 // finer than out.
 template <typename QT, bool FP8, int DP, int T> struct RowsBase {
     using MT = typename std::conditional<FP8, __half, QT>::type;
-    static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : 0.0f;
+    static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
     static constexpr bool kTwo = !(FP8 && std::is_same<QT, __nv_bfloat16>::value);
     static constexpr bool kFit = FP8 && !std::is_same<QT, __half>::value;
     static constexpr int kBytes = FP8 ? 1 : 2, kRowBytes = DP * kBytes, kKS = DP / 16;
@@ -382,11 +409,12 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 const float b0 = exp2_fast(y[2] - ref1), b1 = exp2_fast(y[3] - ref1);
                 l0 += a0 + a1;
                 l1 += b0 + b1;
-                ph[k * 2] = pack2<MT>(a0, a1);
-                ph[k * 2 + 1] = pack2<MT>(b0, b1);
                 if constexpr (kTwo) {
-                    pl[k * 2] = rest2<MT>(a0, a1, ph[k * 2]);
-                    pl[k * 2 + 1] = rest2<MT>(b0, b1, ph[k * 2 + 1]);
+                    split2<MT, !FP8>(a0, a1, ph[k * 2], pl[k * 2]);
+                    split2<MT, !FP8>(b0, b1, ph[k * 2 + 1], pl[k * 2 + 1]);
+                } else {
+                    ph[k * 2] = pack2<MT>(a0, a1);
+                    ph[k * 2 + 1] = pack2<MT>(b0, b1);
                 }
             }
             const uint32_t vh = vt + 16 * h * kRowBytes;
@@ -460,11 +488,11 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     }
     __device__ __forceinline__ void store_out(const KvAttention& a, const Unit& u, float vs, int dim, int lane) const {
         const int g = lane >> 2, q4 = lane & 3;
-        const float f[2] = {l0 == 0.0f ? 0.0f : vs / l0, l1 == 0.0f ? 0.0f : vs / l1};
-        const bool in[2] = {u.row0 + g < u.group, u.row0 + g + 8 < u.group};
+        const float f[2] = {vs / l0, vs / l1};
+        const bool in[2] = {u.row0 + g < u.group, u.row0 + g + 8 < u.group}, some[2] = {l0 != 0.0f, l1 != 0.0f};
         QT* out = static_cast<QT*>(a.out) + (int64_t)u.b * a.out_seq_stride + (int64_t)(u.head * u.group + u.row0 + g) * a.out_head_stride;
         each_pair(q4, [&](int half, int d, float x, float y) {
-            if (in[half] && d < dim) *reinterpret_cast<uint32_t*>(out + half * 8 * a.out_head_stride + d) = pack2<QT>(x * f[half], y * f[half]);
+            if (in[half] && d < dim) *reinterpret_cast<uint32_t*>(out + half * 8 * a.out_head_stride + d) = some[half] ? pack2<QT>(x * f[half], y * f[half]) : 0u;
         });
     }
     __device__ __forceinline__ void store_part(float* part, const Unit& u, int lane) const {
@@ -606,13 +634,18 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             l0 += a0 + b0;
             l1 += a1 + b1;
             // 8 positions x 8 heads, then transposed: a lane's pair is two positions of head g
-            const uint32_t pa = pack2<MT>(a0, a1), pb = pack2<MT>(b0, b1);
-            const uint32_t ph[2] = {transpose8(pa), transpose8(pb)};
-            uint32_t pl[2] = {0u, 0u};
+            uint32_t ph[2], pl[2];
             if constexpr (kTwo) {
-                pl[0] = transpose8(rest2<MT>(a0, a1, pa));
-                pl[1] = transpose8(rest2<MT>(b0, b1, pb));
+                split2<MT, !FP8>(a0, a1, ph[0], pl[0]);
+                split2<MT, !FP8>(b0, b1, ph[1], pl[1]);
+                pl[0] = transpose8(pl[0]);
+                pl[1] = transpose8(pl[1]);
+            } else {
+                ph[0] = pack2<MT>(a0, a1);
+                ph[1] = pack2<MT>(b0, b1);
             }
+            ph[0] = transpose8(ph[0]);
+            ph[1] = transpose8(ph[1]);
             const uint32_t vh = vt + 16 * h * kRowBytes;
             if constexpr (!FP8) {
                 const int row = (lane >> 4) * 8 + (lane & 7);
@@ -660,7 +693,8 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
     }
     __device__ __forceinline__ void store_out(const KvAttention& a, const Unit& u, float vs, int dim, int lane) const {
         const int g = lane >> 2, q4 = lane & 3;
-        const float f0 = l0 == 0.0f ? 0.0f : vs / l0, f1 = l1 == 0.0f ? 0.0f : vs / l1;
+        const float f0 = vs / l0, f1 = vs / l1;
+        const bool some0 = l0 != 0.0f, some1 = l1 != 0.0f;
         QT* out = static_cast<QT*>(a.out) + (int64_t)u.b * a.out_seq_stride + (int64_t)(u.head * u.group + u.row0 + 2 * q4) * a.out_head_stride;
         const bool in0 = u.row0 + 2 * q4 < u.group, in1 = u.row0 + 2 * q4 + 1 < u.group;
         if constexpr (FP8) {
@@ -668,14 +702,14 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             for (int i = 0; i < kMT; ++i) {
                 const int d = g * (DP / 8) + 2 * i;
                 if (d >= dim) continue;
-                if (in0) *reinterpret_cast<uint32_t*>(out + d) = pack2<QT>(o[i][0] * f0, o[i][2] * f0);
-                if (in1) *reinterpret_cast<uint32_t*>(out + a.out_head_stride + d) = pack2<QT>(o[i][1] * f1, o[i][3] * f1);
+                if (in0) *reinterpret_cast<uint32_t*>(out + d) = some0 ? pack2<QT>(o[i][0] * f0, o[i][2] * f0) : 0u;
+                if (in1) *reinterpret_cast<uint32_t*>(out + a.out_head_stride + d) = some1 ? pack2<QT>(o[i][1] * f1, o[i][3] * f1) : 0u;
             }
         } else {
             // lanes g and g ^ 1 trade, so that each holds two dimensions of one head
             const bool odd = g & 1;
             QT* mine = out + (odd ? a.out_head_stride : 0);
-            const bool in = odd ? in1 : in0;
+            const bool in = odd ? in1 : in0, some = odd ? some1 : some0;
 #pragma unroll
             for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -683,7 +717,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
                     const float x0 = o[i][2 * half] * f0, x1 = o[i][2 * half + 1] * f1;
                     const float other = __shfl_xor_sync(kFullMask, odd ? x0 : x1, 4);
                     const int d = 16 * i + 8 * half + (g & ~1);
-                    if (in && d < dim) *reinterpret_cast<uint32_t*>(mine + d) = odd ? pack2<QT>(other, x1) : pack2<QT>(x0, other);
+                    if (in && d < dim) *reinterpret_cast<uint32_t*>(mine + d) = !some ? 0u : odd ? pack2<QT>(other, x1) : pack2<QT>(x0, other);
                 }
         }
     }

@@ -685,3 +685,64 @@ def test_append_keeps_the_sign_of_zeros(ss, src):
         p = np.arange(n)
         got = pool.float().cpu().numpy()[c.table_host[0, p // 16], :, p % 16]
         assert np.array_equal(got, want.astype(np.float32)) and np.array_equal(np.signbit(got), np.signbit(want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("lens", [[40, 1, 700], [20] * 200, [50000]], ids=["small", "many", "long"])
+def test_attend_infinite_visible_values(ss, kind, group, lens):
+    """w v(p) is infinite in the dimensions where a visible v is, and the
+    others are as if it were not there."""
+    c = Cache(lens, heads=1, dim=64, page=16, kind=kind, seed=61)
+    for b, n in enumerate(lens):
+        for p, d, x in ((n // 2, 3, math.inf), (n - 1, 5, -math.inf), (0, 7, math.inf)):
+            at = int(c.table_host[b, p // 16]), 0, p % 16, d
+            c.v[at] = x
+            c.v_host[at] = x
+    q, out, _, _ = run_attend(ss, c, group, kind, weights=None)
+    infinite = [3, 5, 7]
+    want = np.zeros(out.shape)
+    want[..., 3] = want[..., 7] = math.inf
+    want[..., 5] = -math.inf
+    assert np.array_equal(out[..., infinite], want[..., infinite])
+    c.v_host[..., infinite] = 0.0
+    want, _, _ = attend_reference(c, q, 64 ** -0.5)
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11
+    for b in range(len(lens)):
+        k, v = np.abs(c.rows(c.k_host, b, 0)), np.abs(c.rows(c.v_host, b, 0))
+        for j in range(group):
+            e = 64 * 2.0 ** -23 / 8 * float((k @ np.abs(q[b, j]).astype(np.float64)).max()) + 1e-6
+            off = np.abs(np.delete(out[b, j] - want[b, j], infinite))
+            assert (off <= np.delete(u * np.abs(want[b, j]), infinite) + (2 * e + 4e-6 + 2.0 ** -16) * v.max()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("lens", [[40, 1, 700], [20] * 200, [50000]], ids=["small", "many", "long"])
+def test_attend_rows_of_minus_infinity_ignore_their_values(ss, kind, group, lens):
+    import torch
+    c = Cache(lens, heads=1, dim=64, page=16, kind=kind, seed=62)
+    c.k[:] = 0.0
+    c.k[..., 0] = -math.inf
+    c.v[..., 1] = math.inf
+    q = torch.ones(len(lens), group, 64, dtype=c.k.dtype, device="cuda")
+    pages, table = c.ss(ss)
+    out, lse = torch.full_like(q, math.nan), torch.full((len(lens), group), math.nan, device="cuda")
+    ss.ss_kv_attend(pages, table, q, out, lse=lse)
+    ok(ss)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("lens", [[40, 700], [200] * 200, [50000]], ids=["small", "many", "long"])
+def test_attend_values_near_the_largest_number(ss, lens):
+    """The mean of values of 3e38 is 3e38, though their sum is not a number of fp32."""
+    import torch
+    c = Cache(lens, heads=1, dim=64, page=16, kind="bf16", seed=63)
+    c.v[:] = 3e38
+    q = torch.randn(len(lens), 4, 64, device="cuda").to(torch.bfloat16)
+    pages, table = c.ss(ss)
+    out = torch.empty_like(q)
+    ss.ss_kv_attend(pages, table, q, out)
+    ok(ss)
+    # u, the exponential's and the sums' 4e-6, 2^-16 of the weights' rounding
+    assert bool(((out.double() / c.v[0, 0, 0, 0].double() - 1).abs() <= 2.0 ** -8 + 4e-6 + 2.0 ** -16).all())
