@@ -678,7 +678,9 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
     size_t batch = t.batch < most_batch ? t.batch : most_batch;
     if (seq_logits * batch > kMaxLogits) batch = kMaxLogits / seq_logits;
-    while (batch > 1 && batch * tiles * p.sc.units > 0x7fffffff) batch /= 2;  // lists are counted in 32 bits
+    // lists are counted in 32 bits, also that of all positions, which the weights' launch may go over
+    const size_t all = (size_t)((t.max_len + tile - 1) / tile) * c.kv_heads, longest = tiles * p.sc.units;
+    while (batch > 1 && batch * (longest < all ? all : longest) > 0x7fffffff) batch /= 2;
     p.batch = batch < 1 ? 1 : (int)batch;
     const size_t most = (size_t)p.batch * tiles * p.sc.units;
     p.grid = most < (size_t)sms ? (most < 1 ? 1 : (int)most) : sms;
