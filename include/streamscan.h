@@ -340,6 +340,8 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *               strides); must not overlap each other or the cache.
  *   lse         device, batch * q_heads floats (natural logarithm), or NULL.
  *   weight_out  device, the layout of ss_kv_pages.weight, or NULL: no weights.
+ *               Sequences may share pages (a common prefix) only without
+ *               weights: a page's weights are one sequence's.
  *   weight_in   the same layout, or NULL (zeros).  weight_in == weight_out
  *               accumulates in place; a partial overlap is not allowed.
  * Scores, softmax and sums are fp32; out is rounded once.  q_heads <=

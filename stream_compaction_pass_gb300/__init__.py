@@ -579,7 +579,8 @@ def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int 
     """Attention of q, (batch, q_heads, head_dim), over the cached positions
     into out; scale defaults to head_dim ** -0.5.  lse: float32 (batch,
     q_heads).  weight_out, weight_in: float32 tensors of the pool's weight
-    shape (weight_out = weight_in = cache.weight accumulates in place)."""
+    shape (weight_out = weight_in = cache.weight accumulates in place);
+    sequences may share pages only without them."""
     if q.dim() != 3 or q.shape != out.shape or q.dtype != out.dtype:
         raise ValueError("q and out must be 3-dimensional, of one shape and type")
     batch, heads, dim = q.shape

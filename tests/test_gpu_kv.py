@@ -746,3 +746,20 @@ def test_attend_values_near_the_largest_number(ss, lens):
     ok(ss)
     # u, the exponential's and the sums' 4e-6, 2^-16 of the weights' rounding
     assert bool(((out.double() / c.v[0, 0, 0, 0].double() - 1).abs() <= 2.0 ** -8 + 4e-6 + 2.0 ** -16).all())
+
+
+def shared(lens, **kw):
+    """A cache whose sequences are beginnings of its longest one."""
+    import torch
+    c = Cache([max(lens)], **kw)
+    c.lens, c.table_host = list(lens), np.repeat(c.table_host, len(lens), 0)
+    c.table, c.lens_dev = torch.from_numpy(c.table_host).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    return c
+
+
+@pytest.mark.parametrize("lens", [[100, 60, 1, 0, 100], [777] * 100 + [5000, 4999]])
+def test_attend_and_evict_sequences_that_share_pages(ss, lens):
+    check_attend(ss, shared(lens, heads=2, dim=64, page=16, seed=71), 4, "bf16", weights=None)
+    check_attend(ss, shared(lens, heads=2, dim=64, page=16, kind="e4m3", seed=72), 4, "bf16", window=50, sinks=3, weights=None)
+    c = shared(lens, heads=2, dim=64, page=16, seed=73)
+    run_evict(ss, c, random_weights(c, 74), 40, 4, 10)
