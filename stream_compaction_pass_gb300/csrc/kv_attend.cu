@@ -57,6 +57,7 @@ struct Scratch {
     float* lse2;    // batch x q_heads: R + log2 l of every row, for the weights
     float2* ml;     // workers x 2 x 16: (R, l) of a part
     float* o;       // workers x 2 x rows x DP: its O
+    void* aside;    // workers: O of the row at hand while it is long (kv_rows.cuh)
     float* logits;  // per (sequence, key-value head) tile: group x 16 scores, log2 units; or null
     int group, units, rows, workers;  // units per sequence, of `heads` query heads; rows = min(group, heads)
     int heads;
@@ -299,12 +300,17 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     Rows rows;
     Unit unit{};
     bool began = false;  // whether this row started in this share
+    int chain = 0;       // tiles since the row began, or since its O was set aside
+    bool aside = false;
     auto open_row = [&]() {
+        chain = 0;
+        aside = false;
         unit = Unit{cur.b, cur.head, cur.part * Rows::kHeads, sc.group};
         began = cur.j == 0;
         rows.open(c, a, unit, queries, lane);
     };
     auto close_row = [&](bool ended) {
+        if (aside) add_aside(rows, static_cast<const Aside<Rows>*>(sc.aside)[me], lane);
         rows.gather();
         if (began && ended) {
             const int64_t at = (int64_t)unit.b * a.q_heads + unit.head * sc.group + unit.row0;
@@ -345,7 +351,14 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
             if (i + 1 < n) open_row();
         } else {
             advance(cur);
-            if (!SMALL && i + 1 == n) close_row(false);
+            if constexpr (!SMALL) {
+                if (++chain == Rows::kChain) {
+                    put_aside(rows, static_cast<Aside<Rows>*>(sc.aside)[me], aside, lane);
+                    chain = 0;
+                    aside = true;
+                }
+                if (i + 1 == n) close_row(false);
+            }
         }
     }
     cp_wait<0>();
@@ -663,10 +676,10 @@ struct Plan {
     int batch;  // sequences per launch
     int dp, warps, grid;
     Scratch sc;
-    size_t at_lse2, at_ml, at_o, at_logits, bytes;
+    size_t at_lse2, at_ml, at_o, at_aside, at_logits, bytes;
 };
 
-Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int most_batch, int heads, int warps, int dp, int tile, int sms) {
+Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int most_batch, int heads, int warps, int dp, int tile, size_t aside, int sms) {
     Plan p{};
     p.dp = dp;
     p.warps = warps;
@@ -690,7 +703,8 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     p.at_lse2 = 2 * round256(((size_t)p.batch + 1) * 4);
     p.at_ml = p.at_lse2 + round256((size_t)p.batch * a.q_heads * 4);
     p.at_o = p.at_ml + round256((size_t)p.sc.workers * 2 * 16 * 8);
-    p.at_logits = p.at_o + round256((size_t)p.sc.workers * 2 * p.sc.rows * dp * 4);
+    p.at_aside = p.at_o + round256((size_t)p.sc.workers * 2 * p.sc.rows * dp * 4);
+    p.at_logits = p.at_aside + round256(p.sc.workers * aside);
     p.bytes = p.at_logits + round256(seq_logits * p.batch);
     return p;
 }
@@ -737,6 +751,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     constexpr size_t smem = Shape<Rows, FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
     auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
+    static_assert(kSmallTiles <= Rows::kChain && kSmallTilesWeights <= Rows::kChain, "a small call sets nothing aside");
     SmallPlan small;
     cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, &small);
     if (e != cudaSuccess) return e;
@@ -750,7 +765,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     KernelSetup su;
     e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
     if (e != cudaSuccess) return e;
-    Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, su.sms);
+    Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms);
     char* base = static_cast<char*>(mem.get(mem.owner, p.bytes));
     if (base == nullptr) return cudaErrorMemoryAllocation;
     p.sc.pre = reinterpret_cast<int*>(base);
@@ -759,6 +774,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     p.sc.lse2 = reinterpret_cast<float*>(base + p.at_lse2);
     p.sc.ml = reinterpret_cast<float2*>(base + p.at_ml);
     p.sc.o = reinterpret_cast<float*>(base + p.at_o);
+    p.sc.aside = base + p.at_aside;
     p.sc.logits = a.weight_out ? reinterpret_cast<float*>(base + p.at_logits) : nullptr;
     for (int b0 = 0; b0 < t.batch; b0 += p.batch) {
         KvTable u = t;

@@ -203,11 +203,18 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 // adds nothing to the rounding of out (2^-16 against 2^-8 for bf16), except
 // under bf16 outputs of 8-bit caches, where one fp16 term (2^-11) is already
 // finer than out.
+//
+// O is added up in the products' accumulators, which cut what falls below 24
+// bits instead of rounding it: an error of one sign, up to 2^-24 a product.  So
+// after kChain tiles, 128 products in a row (2^-17), O is set aside in memory, where
+// fp32 additions go on (put_aside): rows of 131,072 equal values in fp16 came
+// out 0.06 % low without that.
 template <typename QT, bool FP8, int DP, int T> struct RowsBase {
     using MT = typename std::conditional<FP8, __half, QT>::type;
     static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
     static constexpr bool kTwo = !(FP8 && std::is_same<QT, __nv_bfloat16>::value);
     static constexpr bool kFit = FP8 && !std::is_same<QT, __half>::value;
+    static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
     static constexpr int kBytes = FP8 ? 1 : 2, kRowBytes = DP * kBytes, kKS = DP / 16;
 
     // Four elements of a query row for an 8-bit cache.  The products' index runs
@@ -244,7 +251,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
     using Query = QT;
-    static constexpr int kHeads = 16, kNT = DP / 8, kPT = T / 8;
+    static constexpr int kHeads = 16, kNT = DP / 8, kPT = T / 8, kVectors = kNT;  // of four O's a lane
     static constexpr bool kQShared = DP == 256;  // Q's fragments in shared memory: registers are short
     static constexpr int kQBytes = kQShared ? kKS * 32 * 16 : 0;
 
@@ -471,6 +478,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 }
         }
     }
+    static __device__ __forceinline__ float4 factors(float f0, float f1) { return make_float4(f0, f0, f1, f1); }
     // Adds l up over the lanes that share a head: to be called before store_*.
     __device__ __forceinline__ void gather() {
 #pragma unroll
@@ -509,7 +517,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
     using Query = QT;
-    static constexpr int kHeads = 8, kMT = DP / 16, kHB = T / 16;
+    static constexpr int kHeads = 8, kMT = DP / 16, kHB = T / 16, kVectors = kMT;  // of four O's a lane
     static constexpr int kQBytes = 0;
 
     uint32_t qf[kKS][2];
@@ -679,6 +687,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
         }
     }
 
+    static __device__ __forceinline__ float4 factors(float f0, float f1) { return make_float4(f0, f1, f0, f1); }
     __device__ __forceinline__ void gather() {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
@@ -745,5 +754,36 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
         }
     }
 };
+
+// What a warp sets aside of its row: every lane its own vectors of O, and the
+// largest X that they go with.
+template <typename Rows> struct Aside {
+    float4 o[Rows::kVectors][32];
+    float2 most[32];
+};
+// Adds what was set aside to the row again.
+template <typename Rows> __device__ __forceinline__ void add_aside(Rows& r, const Aside<Rows>& a, int lane) {
+    const float2 m = a.most[lane];
+    const float4 f = Rows::factors(m.x == r.m0 ? 1.0f : exp2_fast(m.x - r.m0), m.y == r.m1 ? 1.0f : exp2_fast(m.y - r.m1));
+#pragma unroll
+    for (int i = 0; i < Rows::kVectors; ++i) {
+        const float4 x = a.o[i][lane];
+        r.o[i][0] += x.x * f.x;
+        r.o[i][1] += x.y * f.y;
+        r.o[i][2] += x.z * f.z;
+        r.o[i][3] += x.w * f.w;
+    }
+}
+// Sets the row's O aside, with what already was (`some`), and goes on from zero.
+template <typename Rows> __device__ __forceinline__ void put_aside(Rows& r, Aside<Rows>& a, bool some, int lane) {
+    if (some) add_aside(r, a, lane);
+    a.most[lane] = make_float2(r.m0, r.m1);
+#pragma unroll
+    for (int i = 0; i < Rows::kVectors; ++i) {
+        a.o[i][lane] = make_float4(r.o[i][0], r.o[i][1], r.o[i][2], r.o[i][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.o[i][e] = 0.0f;
+    }
+}
 
 }  // namespace ss

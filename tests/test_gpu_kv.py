@@ -763,3 +763,47 @@ def test_attend_and_evict_sequences_that_share_pages(ss, lens):
     check_attend(ss, shared(lens, heads=2, dim=64, page=16, kind="e4m3", seed=72), 4, "bf16", window=50, sinks=3, weights=None)
     c = shared(lens, heads=2, dim=64, page=16, seed=73)
     run_evict(ss, c, random_weights(c, 74), 40, 4, 10)
+
+
+# ---- rows that are long within one warp's share: more of them than the GPU has warps ----
+
+@pytest.mark.parametrize("kind,group,dim", [("f16", 8, 64), ("f16", 8, 256), ("f16", 12, 128), ("e4m3", 4, 128), ("e4m3", 12, 64)])
+def test_attend_the_mean_of_ones_is_one(ss, kind, group, dim):
+    """4e-6 of the exponential and the sums and 2^-16 of the weights are less
+    than 2^-12, so that out rounds to one itself."""
+    import torch
+    c = shared([131072] * 2600, heads=1, dim=dim, page=128, kind=kind, seed=81, scales=False)
+    c.v[:] = 1.0
+    q = torch.randn(2600, group, dim, device="cuda").to(torch.float16)
+    pages, table = c.ss(ss)
+    out = torch.empty_like(q)
+    ss.ss_kv_attend(pages, table, q, out)
+    ok(ss)
+    assert bool((out == 1.0).all()), float((out.float() - 1).abs().max())
+
+
+@pytest.mark.parametrize("kind,group", [("f16", 5), ("f16", 12), ("bf16", 8), ("e4m3", 8), ("e4m3", 16)])
+@pytest.mark.parametrize("slope", [8.0, -8.0])
+def test_attend_scores_that_rise_or_fall_along_long_rows(ss, kind, group, slope):
+    import torch
+    n, B, dim = 9000, 2600, 64
+    c = shared([n] * B, heads=1, dim=dim, page=16, kind=kind, seed=82, scales=False)
+    p = np.arange(n)
+    at = c.table_host[0, p // 16], 0, p % 16, 0
+    c.k[at] = torch.linspace(-slope, slope, n, device="cuda").to(c.k.dtype)
+    c.k_host[at] = c.k[at].float().cpu().numpy()
+    row = torch.randn(1, group, dim, generator=torch.Generator().manual_seed(83)) * (0.05 if kind == "e4m3" else 1.0)
+    row[..., 0] = 8.0
+    q = row.to(torch_type("bf16" if kind == "bf16" else "f16")).cuda().expand(B, -1, -1).contiguous()
+    pages, table = c.ss(ss)
+    out, lse = torch.empty_like(q), torch.empty(B, group, device="cuda")
+    ss.ss_kv_attend(pages, table, q, out, lse=lse)
+    ok(ss)
+    c.lens = [n]
+    host = q[:1].float().cpu().numpy()
+    want, want_lse, _ = attend_reference(c, host, dim ** -0.5)
+    e = dim * 2.0 ** -23 * dim ** -0.5 * float((np.abs(c.rows(c.k_host, 0, 0)) @ np.abs(host[0].T.astype(np.float64))).max()) + 1e-6
+    u, r = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11, 2.0 ** -11 if kind == "e4m3" else 2.0 ** -16
+    tol = u * np.abs(want) + (2 * e + 4e-6 + r) * np.abs(c.rows(c.v_host, 0, 0)).max()
+    assert (np.abs(out.float().cpu().numpy() - want) <= tol).all()
+    assert (np.abs(lse.cpu().numpy() - want_lse) <= e + 1e-6 * (1 + np.abs(want_lse))).all()
