@@ -332,8 +332,10 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *                      exp(s(p) - lse), for every position p < len.
  * A row with no visible position, or all of whose scores are -inf, gives
  * out = 0 and lse = -inf and adds no weight.  NaN and infinities in a visible
- * row spread as in the formula (an infinite v may do so at any weight, also
- * one of 0); rows that are not visible are not read.
+ * row spread as in the formula, whatever the other sequences are: the weight
+ * of a finite score is positive, so that an infinite v stays infinite, however
+ * small the weight; that of a score of -inf is 0, and 0 times an infinite v is
+ * NaN.  Rows that are not visible are not read.
  *   type        of q and out, SS_BF16 or SS_F16: the cache's, or either with
  *               an SS_E4M3 cache.
  *   q, out      row (b, j) at b * seq_stride + j * head_stride (each its own

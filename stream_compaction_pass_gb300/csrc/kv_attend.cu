@@ -121,9 +121,7 @@ template <typename QT> __device__ __forceinline__ void empty_row(const KvAttenti
     if (first == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + j] = -INFINITY;
 }
 
-__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.0f : exp2_fast(from - to); }
-
-// A part's O and l, by their factor; a part of nothing but -inf (factor 0) has no O.
+// A part's O and l, by their factor.
 __device__ __forceinline__ void add_part(float4& x, float& l, const float4& y, float l_part, float factor) {
     l += l_part * factor;
     x.x += y.x * factor;
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int w = 0; w < NW; ++w) {
                 const float2 ml = w_ml[w * Rows::kHeads + r];
-                add_part(x, l, reinterpret_cast<const float4*>(w_o + (w * Rows::kHeads + r) * DP)[d], ml.y, rescale(ml.x, top));
+                add_part(x, l, reinterpret_cast<const float4*>(w_o + (w * Rows::kHeads + r) * DP)[d], ml.y, shrink(ml.x, top));
             }
             reinterpret_cast<float4*>(c_o + r * DP)[d] = x;
             if (d == 0) c_ml[r] = make_float2(top, l);
@@ -400,7 +398,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int k = 0; k < sc.ranks; ++k) {
                 const float2 ml = cluster.map_shared_rank(c_ml, k)[r];
-                add_part(x, l, reinterpret_cast<const float4*>(cluster.map_shared_rank(c_o, k) + r * DP)[d], ml.y, rescale(ml.x, top));
+                add_part(x, l, reinterpret_cast<const float4*>(cluster.map_shared_rank(c_o, k) + r * DP)[d], ml.y, shrink(ml.x, top));
             }
             using QT = typename Rows::Query;
             const float inv = l == 0.0f ? 0.0f : vs / l;
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
                 for (int k = 0; k < sc.ranks; ++k) top = fmaxf(top, cluster.map_shared_rank(c_ml, k)[tid].x);
                 for (int k = 0; k < sc.ranks; ++k) {
                     const float2 ml = cluster.map_shared_rank(c_ml, k)[tid];
-                    l += ml.y * rescale(ml.x, top);
+                    l += ml.y * shrink(ml.x, top);
                 }
                 s_lse[tid] = l == 0.0f ? INFINITY : top + log2f(l);
             }
@@ -492,7 +490,7 @@ template <int DP> struct RowSum {
             float up = top;
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) up = fmaxf(up, ml[q].x);
-            const float f = rescale(top, up);
+            const float f = shrink(top, up);
             l *= f;
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {
@@ -504,7 +502,7 @@ template <int DP> struct RowSum {
             top = up;
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) {
-                const float e = rescale(ml[q].x, up);
+                const float e = shrink(ml[q].x, up);
                 l += e * ml[q].y;
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) {
@@ -541,13 +539,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
         const int b = r / a.q_heads, j = r % a.q_heads;
         float top = -INFINITY, l = 0.0f;
         for (int i = w; i < w + n; ++i) top = fmaxf(top, s_ml[i].x);
-        for (int i = w; i < w + n; ++i) l += s_ml[i].y * rescale(s_ml[i].x, top);
+        for (int i = w; i < w + n; ++i) l += s_ml[i].y * shrink(s_ml[i].x, top);
         const float vs = c.v_scale ? c.v_scale[j / sc.group] : 1.0f;
         const float inv = l == 0.0f ? 0.0f : vs / l;
         QT* out = static_cast<QT*>(a.out) + (int64_t)b * a.out_seq_stride + (int64_t)j * a.out_head_stride;
         for (int d = d0; d < c.head_dim; d += step) {
             float x = 0.0f;
-            for (int i = w; i < w + n; ++i) x += reinterpret_cast<const float*>(s_o[i])[d] * rescale(s_ml[i].x, top);
+            for (int i = w; i < w + n; ++i) x += reinterpret_cast<const float*>(s_o[i])[d] * shrink(s_ml[i].x, top);
             out[d] = from_f32<QT>(l == 0.0f ? 0.0f : x * inv);
         }
         if (d0 == 0) store_lse(sc, a, r, top, l);

@@ -46,6 +46,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// What sums shrink by when their largest X grows.  Not below 2^-126: an infinite
+// sum stays infinite, however far its scores lie below the others.  (A sum whose
+// largest X is -inf is 0, or NaN where it met an infinite value, whatever it is
+// multiplied by.)
+__device__ __forceinline__ float shrink(float from, float to) { return fmaxf(exp2_fast(from - to), 0x1p-126f); }
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -107,14 +113,20 @@ template <typename T> __device__ __forceinline__ float2 open2(uint32_t u) {
     return Pair<T>::open(*reinterpret_cast<const typename Pair<T>::type*>(&u));
 }
 
-// Two 16-bit numbers, at least 2^-24 (fp16) or 2^-126 (bf16); NaN stays.
-template <typename T> __device__ __forceinline__ uint32_t least2(uint32_t x) {
-    uint32_t y;
+// The least weights of two positions by their scores: 2^-24 (fp16) or 2^-126
+// (bf16), and 0 of a score of -inf.
+template <typename T> __device__ __forceinline__ uint32_t least2(float x, float y) {
+    constexpr uint32_t kLeast = std::is_same<T, __half>::value ? 0x0001u : 0x0080u;
+    return (x > -INFINITY ? kLeast : 0u) | (y > -INFINITY ? kLeast << 16 : 0u);
+}
+// The larger ones of two pairs of 16-bit numbers; NaN stays.
+template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+    uint32_t z;
     if constexpr (std::is_same<T, __half>::value)
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x00010001u));
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
     else
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x00800080u));
-    return y;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
 }
 // Two numbers as 16-bit ones, rounded toward zero.
 template <typename T> __device__ __forceinline__ uint32_t trunc2(float x, float y) {
@@ -128,15 +140,16 @@ template <typename T> __device__ __forceinline__ uint32_t trunc2(float x, float 
 
 // Weights (x, y) >= 0 as two 16-bit terms, of which the second has what the
 // first leaves out.  POSITIVE: the first is truncated, so that the second is not
-// negative, and both are kept above zero: an infinite value that they multiply
-// stays infinite instead of becoming inf - inf or 0 inf (0.2 % of the long
-// ragged batch's time, 0.2 us of a call of 517 positions).  That adds at most 2^-38 of the row's largest weight in fp16,
-// 2^-101 in bf16.
-template <typename T, bool POSITIVE> __device__ __forceinline__ void split2(float x, float y, uint32_t& high, uint32_t& rest) {
-    high = POSITIVE ? least2<T>(trunc2<T>(x, y)) : pack2<T>(x, y);
+// negative, and both are kept at `least` or more: an infinite value that they
+// multiply stays infinite instead of becoming inf - inf or 0 inf, unless its
+// score is -inf and its weight therefore 0 (together 0.2 % of the long ragged
+// batch's time, 0.2 us of a call of 517 positions).  That adds at most 2^-38 of
+// the row's largest weight to each in fp16, 2^-101 in bf16.
+template <typename T, bool POSITIVE> __device__ __forceinline__ void split2(float x, float y, uint32_t least, uint32_t& high, uint32_t& rest) {
+    high = POSITIVE ? max2<T>(trunc2<T>(x, y), least) : pack2<T>(x, y);
     const float2 h = open2<T>(high);
     rest = pack2<T>(x - h.x, y - h.y);
-    if constexpr (POSITIVE) rest = least2<T>(rest);
+    if constexpr (POSITIVE) rest = max2<T>(rest, least);
 }
 
 // Two e4m3 bytes as two fp16 (exact).
@@ -391,7 +404,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
             top1 = fmaxf(top1, __shfl_xor_sync(kFullMask, top1, s));
         }
         if (__any_sync(kFullMask, top0 != m0 || top1 != m1)) {
-            const float f0 = top0 == m0 ? 1.0f : exp2_fast(m0 - top0), f1 = top1 == m1 ? 1.0f : exp2_fast(m1 - top1);
+            const float f0 = shrink(m0, top0), f1 = shrink(m1, top1);
             m0 = top0;
             m1 = top1;
             l0 *= f0;
@@ -417,8 +430,8 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 l0 += a0 + a1;
                 l1 += b0 + b1;
                 if constexpr (kTwo) {
-                    split2<MT, !FP8>(a0, a1, ph[k * 2], pl[k * 2]);
-                    split2<MT, !FP8>(b0, b1, ph[k * 2 + 1], pl[k * 2 + 1]);
+                    split2<MT, !FP8>(a0, a1, least2<MT>(y[0], y[1]), ph[k * 2], pl[k * 2]);
+                    split2<MT, !FP8>(b0, b1, least2<MT>(y[2], y[3]), ph[k * 2 + 1], pl[k * 2 + 1]);
                 } else {
                     ph[k * 2] = pack2<MT>(a0, a1);
                     ph[k * 2 + 1] = pack2<MT>(b0, b1);
@@ -621,7 +634,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             top1 = fmaxf(top1, __shfl_xor_sync(kFullMask, top1, s));
         }
         if (__any_sync(kFullMask, top0 != m0 || top1 != m1)) {
-            const float f0 = top0 == m0 ? 1.0f : exp2_fast(m0 - top0), f1 = top1 == m1 ? 1.0f : exp2_fast(m1 - top1);
+            const float f0 = shrink(m0, top0), f1 = shrink(m1, top1);
             m0 = top0;
             m1 = top1;
             l0 *= f0;
@@ -644,8 +657,8 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             // 8 positions x 8 heads, then transposed: a lane's pair is two positions of head g
             uint32_t ph[2], pl[2];
             if constexpr (kTwo) {
-                split2<MT, !FP8>(a0, a1, ph[0], pl[0]);
-                split2<MT, !FP8>(b0, b1, ph[1], pl[1]);
+                split2<MT, !FP8>(a0, a1, least2<MT>(x[h][0], x[h][1]), ph[0], pl[0]);
+                split2<MT, !FP8>(b0, b1, least2<MT>(x[h][2], x[h][3]), ph[1], pl[1]);
                 pl[0] = transpose8(pl[0]);
                 pl[1] = transpose8(pl[1]);
             } else {
@@ -764,7 +777,7 @@ template <typename Rows> struct Aside {
 // Adds what was set aside to the row again.
 template <typename Rows> __device__ __forceinline__ void add_aside(Rows& r, const Aside<Rows>& a, int lane) {
     const float2 m = a.most[lane];
-    const float4 f = Rows::factors(m.x == r.m0 ? 1.0f : exp2_fast(m.x - r.m0), m.y == r.m1 ? 1.0f : exp2_fast(m.y - r.m1));
+    const float4 f = Rows::factors(shrink(m.x, r.m0), shrink(m.y, r.m1));
 #pragma unroll
     for (int i = 0; i < Rows::kVectors; ++i) {
         const float4 x = a.o[i][lane];

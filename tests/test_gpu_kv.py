@@ -807,3 +807,41 @@ def test_attend_scores_that_rise_or_fall_along_long_rows(ss, kind, group, slope)
     tol = u * np.abs(want) + (2 * e + 4e-6 + r) * np.abs(c.rows(c.v_host, 0, 0)).max()
     assert (np.abs(out.float().cpu().numpy() - want) <= tol).all()
     assert (np.abs(lse.cpu().numpy() - want_lse) <= e + 1e-6 * (1 + np.abs(want_lse))).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [4, 12])
+@pytest.mark.parametrize("lens", [[40, 1, 700], [20, 400] * 100, [50000]], ids=["small", "many", "long"])
+def test_attend_infinite_values_of_scores_that_are_far_below_or_minus_infinity(ss, kind, group, lens):
+    """The first quarter of a row scores 400 less than its second half and has
+    infinite values in dimension 2: inf, as their weights are positive.  The
+    second quarter scores -inf, with infinite values in dimension 1: NaN, as 0
+    times them is.  Both fill whole tiles, shares and parts of the longer rows."""
+    c = Cache(lens, heads=1, dim=64, page=16, kind=kind, seed=84)
+    c.k[...] = 0.0
+    c.k_host[...] = 0.0
+    for b, n in enumerate(lens):
+        for lo, hi, score, d in ((0, n // 4, -400.0, 2), (n // 4, n // 2, -math.inf, 1)):
+            p = np.arange(lo, hi)
+            at = c.table_host[b, p // 16], 0, p % 16
+            for pool in (c.k, c.k_host):
+                pool[at + (0,)] = score
+            c.v[at + (d,)] = math.inf
+            c.v_host[at + (d,)] = 0.0
+    import torch
+    q = torch.zeros(len(lens), group, 64)
+    q[..., 0] = 1.0
+    pages, table = c.ss(ss)
+    dev = q.to(c.k.dtype).cuda()
+    out = torch.empty_like(dev)
+    ss.ss_kv_attend(pages, table, dev, out, scale=1.0)
+    ok(ss)
+    out = out.float().cpu().numpy()
+    want, _, _ = attend_reference(c, q.numpy(), 1.0)
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11
+    for b, n in enumerate(lens):
+        assert np.isposinf(out[b, :, 2]).all() if n >= 4 else np.isfinite(out[b, :, 2]).all(), (b, n)
+        assert np.isnan(out[b, :, 1]).all() if n // 2 > n // 4 else np.isfinite(out[b, :, 1]).all(), (b, n)
+        # the scores are exact
+        off, mean = np.delete(out[b] - want[b], [1, 2], 1), np.delete(want[b], [1, 2], 1)
+        assert (np.abs(off) <= u * np.abs(mean) + (4e-6 + 2.0 ** -16) * np.abs(c.rows(c.v_host, b, 0)).max()).all()
