@@ -82,6 +82,8 @@ struct Workspace {
     size_t moe_acc_cap = 0;       // words
     void* kv = nullptr;           // scratch of the key-value cache calls
     size_t kv_cap = 0;            // bytes
+    bool kv_captured = false;     // a captured graph may use kv
+    std::vector<void*> kv_before; // earlier scratch that a captured graph may use
     uint64_t launches_since_clear = 0;
     HostPipe pipe;
     std::mutex pipe_mu;  // one host pipeline at a time per workspace
@@ -96,7 +98,16 @@ void* ws_carry(Workspace* w) { return w->header + 16; }
 uint32_t* ws_ticket(Workspace* w) { return reinterpret_cast<uint32_t*>(w->header + 24); }
 uint32_t* ws_reduce_ticket(Workspace* w) { return reinterpret_cast<uint32_t*>(w->header + 28); }
 
-ss_status get_workspace(cudaStream_t s, Workspace** out) {
+ss_status is_capturing(cudaStream_t s, bool* out) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &st);
+    *out = st != cudaStreamCaptureStatusNone;
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "cudaStreamIsCapturing");
+}
+
+// `in_capture`: whether a workspace may be made while the stream is being
+// captured; its memory is then the graph's, and there only while it runs.
+ss_status get_workspace(cudaStream_t s, Workspace** out, bool in_capture = true) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -106,6 +117,12 @@ ss_status get_workspace(cudaStream_t s, Workspace** out) {
     if (it != g_ws.end()) {
         *out = it->second;
         return SS_OK;
+    }
+    if (!in_capture) {
+        bool capturing = false;
+        const ss_status st = is_capturing(s, &capturing);
+        if (st != SS_OK) return st;
+        if (capturing) return fail(SS_ERR_NO_MEMORY, "the stream has no workspace yet: make one call before capturing it");
     }
     Workspace* w = new Workspace();
     w->device = dev;
@@ -187,13 +204,29 @@ ss_status ensure_moe_acc(Workspace* w, size_t words) {
     return SS_OK;
 }
 
+// Nothing is allocated while the stream is being captured, and scratch that a
+// captured graph may use is kept until ss_shutdown.
 ss_status ensure_kv(Workspace* w, size_t bytes) {
-    if (bytes <= w->kv_cap) return SS_OK;
+    if (bytes == 0) return SS_OK;
+    bool capturing = false;
+    const ss_status st = is_capturing(w->stream, &capturing);
+    if (st != SS_OK) return st;
+    if (bytes <= w->kv_cap) {
+        w->kv_captured |= capturing;
+        return SS_OK;
+    }
+    if (capturing)
+        return fail(SS_ERR_NO_MEMORY, "key-value cache scratch has to grow: make one call of this size before capturing the stream");
     if (w->kv) {
-        cudaError_t e = cudaFreeAsync(w->kv, w->stream);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync");
+        if (w->kv_captured) {
+            w->kv_before.push_back(w->kv);
+        } else {
+            cudaError_t e = cudaFreeAsync(w->kv, w->stream);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync");
+        }
         w->kv = nullptr;
         w->kv_cap = 0;
+        w->kv_captured = false;
     }
     cudaError_t e = cudaMallocAsync(&w->kv, bytes, w->stream);
     if (e != cudaSuccess)
@@ -492,7 +525,7 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 || token_stride > 1ll << 40 || head_stride > 1ll << 40)
         return fail(SS_ERR_INVALID_ARG, "token_stride and head_stride must be non-negative multiples of 16 bytes, at most 2^40 elements");
     Workspace* w = nullptr;
-    st = get_workspace((cudaStream_t)stream, &w);
+    st = get_workspace((cudaStream_t)stream, &w, false);
     if (st != SS_OK) return st;
     cudaError_t e = ss::launch_kv_append(c, t, static_cast<ss::KvElem>(type), k_new, v_new, token_stride, head_stride,
                                          offsets, (int64_t)tokens, device_sms(w->device), ws_status(w), (cudaStream_t)stream);
@@ -541,7 +574,7 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     const size_t ob = (size_t)((t.batch - 1) * strides[2] + (a.q_heads - 1) * strides[3] + c.head_dim) * 2;
     if (overlaps(a.q, qb, a.out, ob)) return fail(SS_ERR_INVALID_ARG, "q and out overlap");
     Workspace* w = nullptr;
-    st = get_workspace((cudaStream_t)stream, &w);
+    st = get_workspace((cudaStream_t)stream, &w, false);
     if (st != SS_OK) return st;
     const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, a.q_seq_stride, a.q_head_stride, a.out,
                             a.out_seq_stride, a.out_head_stride, a.scale, a.window, a.sinks, a.lse, a.weight_in,
@@ -595,7 +628,7 @@ ss_status ss_kv_evict(const ss_kv_pages* src, const ss_kv_table* src_seqs, const
     if (std::min(keep, t.max_len) > (int64_t)dt.max_pages * d.page_size)
         return fail(SS_ERR_INVALID_ARG, "dst_seqs cannot hold the kept positions");
     Workspace* w = nullptr;
-    st = get_workspace((cudaStream_t)stream, &w);
+    st = get_workspace((cudaStream_t)stream, &w, false);
     if (st != SS_OK) return st;
     const int sms = device_sms(w->device);
     const size_t hist = ss::kv_evict_scratch(c, t, sms);
@@ -1100,6 +1133,7 @@ void ss_shutdown(void) {
         if (w->totals) cudaFree(w->totals);
         if (w->moe_acc) cudaFree(w->moe_acc);
         if (w->kv) cudaFree(w->kv);
+        for (void* p : w->kv_before) cudaFree(p);
         if (w->header) cudaFree(w->header);
         HostPipe& p = w->pipe;
         if (p.ready) {

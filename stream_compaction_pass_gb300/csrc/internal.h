@@ -217,7 +217,8 @@ cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttenti
 constexpr int kKvMaxEvict = 1 << 21;  // the longest sequence an eviction takes
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
                             int sinks, int recent, int32_t* kept, uint32_t* scratch, int sms, uint32_t* status, cudaStream_t s);
-// Device scratch of one eviction, in bytes, beside the kept positions.
+// Device scratch of one eviction, in bytes, beside the kept positions; a
+// smaller call needs no more.
 size_t kv_evict_scratch(const KvPages& c, const KvTable& t, int sms);
 
 // Ablations (reduce-then-scan, three kernels).  `totals` holds one value

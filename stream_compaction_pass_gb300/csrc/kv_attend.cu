@@ -687,23 +687,26 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     p.sc.rows = p.sc.group < heads ? p.sc.group : heads;
     const size_t tiles = most_tiles(t, a, tile);
     const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
-    size_t batch = t.batch < most_batch ? t.batch : most_batch;
+    const size_t seqs = t.batch < most_batch ? t.batch : most_batch;
+    size_t batch = seqs;
     if (seq_logits * batch > kMaxLogits) batch = kMaxLogits / seq_logits;
     // lists are counted in 32 bits, also that of all positions, which the weights' launch may go over
     const size_t all = (size_t)((t.max_len + tile - 1) / tile) * c.kv_heads, longest = tiles * p.sc.units;
     while (batch > 1 && batch * (longest < all ? all : longest) > 0x7fffffff) batch /= 2;
     p.batch = batch < 1 ? 1 : (int)batch;
-    const size_t most = (size_t)p.batch * tiles * p.sc.units;
+    // The scratch grows with the sequences, not with those that a launch takes:
+    // a smaller call never needs more.
+    const size_t most = seqs * tiles * p.sc.units, scores = seq_logits * seqs;
     p.grid = most < (size_t)sms ? (most < 1 ? 1 : (int)most) : sms;
     p.sc.workers = p.grid * warps;
     p.sc.shift = tile == 16 ? 4 : 5;
     p.sc.page = FastDiv(c.page_size);
-    p.at_lse2 = 2 * round256(((size_t)p.batch + 1) * 4);
-    p.at_ml = p.at_lse2 + round256((size_t)p.batch * a.q_heads * 4);
+    p.at_lse2 = 2 * round256((seqs + 1) * 4);
+    p.at_ml = p.at_lse2 + round256(seqs * a.q_heads * 4);
     p.at_o = p.at_ml + round256((size_t)p.sc.workers * 2 * 16 * 8);
     p.at_aside = p.at_o + round256((size_t)p.sc.workers * 2 * p.sc.rows * dp * 4);
     p.at_logits = p.at_aside + round256(p.sc.workers * aside);
-    p.bytes = p.at_logits + round256(seq_logits * p.batch);
+    p.bytes = p.at_logits + round256(scores <= kMaxLogits ? scores : seq_logits < kMaxLogits ? kMaxLogits : seq_logits);
     return p;
 }
 

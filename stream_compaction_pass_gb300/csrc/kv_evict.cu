@@ -457,8 +457,12 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(KvPages c, KvTable t, 
 
 }  // namespace
 
+// For a smaller call (fewer rows, shorter ones) it is never more: the
+// histograms of as many rows as can be split (select_ranks).
 size_t kv_evict_scratch(const KvPages& c, const KvTable& t, int sms) {
-    return select_ranks(c, t, sms) > 1 ? (size_t)t.batch * c.kv_heads * 3 * kBins * 4 : 0;
+    const int64_t rows = (int64_t)t.batch * c.kv_heads, few = sms / 2;
+    const int64_t split = t.max_len > kClassedShare - 4 ? rows : t.max_len < kSplitFrom ? 0 : rows < few ? rows : few;
+    return (size_t)split * 3 * kBins * 4;
 }
 
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,

@@ -845,3 +845,142 @@ def test_attend_infinite_values_of_scores_that_are_far_below_or_minus_infinity(s
         # the scores are exact
         off, mean = np.delete(out[b] - want[b], [1, 2], 1), np.delete(want[b], [1, 2], 1)
         assert (np.abs(off) <= u * np.abs(mean) + (4e-6 + 2.0 ** -16) * np.abs(c.rows(c.v_host, b, 0)).max()).all()
+
+
+# ---- scratch and stream capture ----
+
+def captured(stream, work):
+    import torch
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        work()
+    return g
+
+
+def test_evict_of_few_long_rows_in_a_graph_after_a_larger_call(ss):
+    """Few rows are split and have histograms in scratch, where a larger batch
+    is not split and has none; one call of the largest size provides for both."""
+    import torch
+    n, keep = 60000, 300
+    c = shared([n] * 512, heads=1, dim=16, page=64, kind="e4m3", seed=91)
+    w = random_weights(c, 92)
+    c.weight.copy_(torch.from_numpy(w))
+    kept = torch.full((512, 1, keep), -5, dtype=torch.int32, device="cuda")
+    dst = Cache([keep] * 512, heads=1, dim=16, page=64, kind="e4m3", seed=93)
+    pages, table = c.ss(ss)
+    new_pages, new_table = dst.ss(ss)
+    few, new_few = ss.KVTable(c.table[:8], c.lens_dev[:8]), ss.KVTable(dst.table[:8], dst.lens_dev[:8])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def evict(src, new):
+        ss.ss_kv_evict(pages, src, new_pages, new, keep, sinks=4, recent=50, kept=kept[:src.batch], stream=side)
+
+    evict(table, new_table)
+    ok(ss, side)
+    c.lens = [n]
+    want = torch.from_numpy(evict_reference(c, w, keep, 4, 50)).cuda()
+    assert bool((kept == want).all())
+    g = captured(side, lambda: evict(few, new_few))
+    for _ in range(3):
+        kept.fill_(-5)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert bool((kept[:8] == want).all()) and bool((kept[8:] == -5).all())
+        kept.fill_(-5)
+        torch.cuda.synchronize()
+        evict(few, new_few)  # an eager call between replays
+        ok(ss, side)
+        assert bool((kept[:8] == want).all())
+
+
+def test_attend_in_a_graph_after_a_larger_call_that_took_more_launches(ss):
+    """Scores of more than 2 GB are cut into launches: 8 sequences of up to
+    2.2 million positions are eight, 5 of 1.9 million take two at a time."""
+    import torch
+    c = Cache([300, 40, 0, 700, 1, 90, 33, 16], heads=1, dim=16, page=1024, seed=94)
+    q = torch.randn(8, 128, 16, device="cuda").to(torch.bfloat16)
+    wide = torch.full((8, 2200), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.width] = c.table
+    pages, _ = c.ss(ss)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def attend(batch, out, w, max_len):
+        t = ss.KVTable(wide[:batch], c.lens_dev[:batch], max_len=max_len)
+        ss.ss_kv_attend(pages, t, q[:batch], out[:batch], weight_out=w, stream=side)
+
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    ws = [torch.zeros_like(c.weight) for _ in range(2)]
+    torch.cuda.synchronize()
+    attend(8, outs[0], ws[0], 2_200_000)
+    ok(ss, side)
+    g = captured(side, lambda: attend(5, outs[1], ws[1], 1_900_000))
+    g.replay()
+    torch.cuda.synchronize()
+    ok(ss, side)
+    # sums in another order, and one rounding more
+    assert bool(((outs[1] - outs[0])[:5].float().abs() <= 2.0 ** -7 * outs[0][:5].float().abs() + 1e-4).all())
+    for b in range(5):
+        assert np.allclose(*(c.rows(w.cpu().numpy(), b, 0) for w in ws), rtol=1e-4, atol=0)
+
+
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+def test_nothing_is_allocated_in_a_capture(ss):
+    """The call says so and enqueues nothing; one outside the capture, then a
+    capture, work as ever, and the graph keeps its scratch when a larger call
+    follows."""
+    import torch
+    c = Cache([5000, 300], heads=2, dim=64, page=16, seed=95)
+    d = Cache([64, 64], heads=2, dim=64, page=16, seed=96)
+    pages, table = c.ss(ss)
+    new_pages, new_table = d.ss(ss)
+    q = torch.randn(2, 8, 64, device="cuda").to(torch.bfloat16)
+    out, w = torch.zeros_like(q), torch.zeros_like(c.weight)
+    x = torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ss.ss_shutdown()  # no stream has a workspace
+    attend = lambda: ss.ss_kv_attend(pages, table, q, out, weight_out=w, stream=side)
+    evict = lambda: ss.ss_kv_evict(pages, table, new_pages, new_table, 64, stream=side)
+    append = lambda: ss.ss_kv_append(pages, table, x, x, stream=side)
+
+    def refused():
+        for call in (append, attend, evict):  # the stream's first calls
+            with pytest.raises(ss.StreamScanError) as e:
+                call()
+            assert e.value.status == ss.SS_ERR_NO_MEMORY and "captur" in str(e.value)
+
+    g = captured(side, refused)
+    side.synchronize()
+    assert float(out.abs().max()) == 0.0
+    append()  # makes the workspace, and no scratch
+
+    def refused():
+        for call in (attend, evict):
+            with pytest.raises(ss.StreamScanError) as e:
+                call()
+            assert e.value.status == ss.SS_ERR_NO_MEMORY and "captur" in str(e.value)
+
+    captured(side, refused)
+    attend()
+    ok(ss, side)
+    want, want_w = out.clone(), w.clone()
+    g = captured(side, attend)
+    big = Cache([30000] * 4, heads=2, dim=64, page=16, seed=97)
+    big_pages, big_table = big.ss(ss)
+    big_q, big_w = torch.randn(4, 8, 64, device="cuda").to(torch.bfloat16), torch.zeros_like(big.weight)
+    torch.cuda.synchronize()
+    big_out = torch.empty_like(big_q)
+    ss.ss_kv_attend(big_pages, big_table, big_q, big_out, weight_out=big_w, stream=side)
+    fill = torch.full((1 << 26,), math.nan, device="cuda")  # whoever else allocates
+    for _ in range(2):
+        out.zero_()
+        w.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(w, want_w)
+    ok(ss, side)
+    del fill
