@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(N, N == 512 ? 2 : 1) k_kv_select(KvPages c, Kv
         }
     };
     if (len <= ch.keep) {  // the same for the whole cluster
-        for (int j = rank * N + tid; j < ch.keep; j += ranks * N) out[j] = j < m ? j : -1;
+        for (int64_t j = rank * N + tid; j < ch.keep; j += ranks * N) out[j] = j < m ? (int32_t)j : -1;  // keep may be up to 2^31 - 1
         move_row();
         return;
     }

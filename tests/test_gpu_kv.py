@@ -984,3 +984,20 @@ def test_nothing_is_allocated_in_a_capture(ss):
         assert torch.equal(out, want) and torch.equal(w, want_w)
     ok(ss, side)
     del fill
+
+
+def test_evict_lists_the_kept_positions_of_the_largest_budget(ss):
+    """A list of 2^31 - 1 places, past a counter's range with its last step."""
+    import torch
+    keep = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    c = Cache([100], heads=1, dim=16, page=16, kind="e4m3", seed=98)
+    d = Cache([100], heads=1, dim=16, page=16, kind="e4m3", seed=99)
+    kept = torch.full((1, 1, keep), -7, dtype=torch.int32, device="cuda")
+    pages, table = c.ss(ss)
+    new_pages, new_table = d.ss(ss)
+    ss.ss_kv_evict(pages, table, new_pages, new_table, keep, kept=kept)
+    ok(ss)
+    assert kept[0, 0, :100].tolist() == list(range(100)) and d.lens_dev.tolist() == [100]
+    assert int(kept[0, 0, 100:].max()) == -1 and int(kept[0, 0, 100:].min()) == -1
