@@ -506,6 +506,13 @@ def _like(name: str, t, shape, dtype: str) -> int:
     return t.data_ptr()
 
 
+def _int32(**values) -> None:
+    """Checks integers that the C ABI takes in 32 bits, where ctypes would keep the low ones."""
+    for name, x in values.items():
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{name} = {x} is not a 32-bit integer")
+
+
 class KVPages:
     """The pool of a paged key-value cache (ss_kv_pages).
 
@@ -545,6 +552,7 @@ class KVTable:
         if pages.dim() != 2 or str(pages.dtype) != "torch.int32" or (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("pages must be a 2-dimensional int32 tensor with contiguous rows")
         _like("lens", lens, (pages.shape[0],), "int32")
+        _int32(max_len=max_len or 0)
         self.pages, self.lens, self.batch = pages, lens, pages.shape[0]
         self._c = _KvTable(_addr(pages), pages.stride(0), pages.shape[1], pages.shape[0], _addr(lens),
                            0 if max_len is None else max_len)
@@ -556,6 +564,7 @@ class KVTable:
 
     @max_len.setter
     def max_len(self, n):
+        _int32(max_len=n)
         self._c.max_len = n
 
 
@@ -591,6 +600,8 @@ def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int 
     d_lse = _like("lse", lse, (batch, heads), "float32")
     d_in, d_out = (_like("weight_in", weight_in, cache.weight_shape, "float32"),
                    _like("weight_out", weight_out, cache.weight_shape, "float32"))
+    if window >> 31 or sinks >> 31:  # also the negative ones
+        _int32(window=window, sinks=sinks)
     a = _KvAttention(_elem(q), heads, q.data_ptr(), q_seq, q_head, out.data_ptr(), out_seq, out_head,
                      dim ** -0.5 if scale is None else scale, window, sinks, d_lse, d_in, d_out)
     _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a), _stream(stream, q)), "ss_kv_attend")
@@ -600,6 +611,8 @@ def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable
                 recent: int = 0, kept=None, stream=None) -> None:
     """Moves the kept rows of every sequence and head into dst's pages and
     their number into dst_seqs.lens; kept: int32 (batch, kv_heads, keep)."""
+    if keep >> 31 or sinks >> 31 or recent >> 31:
+        _int32(keep=keep, sinks=sinks, recent=recent)
     d_kept = _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32")
     _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, d_kept,
                              _stream(stream, src.k)), "ss_kv_evict")

@@ -208,3 +208,25 @@ def test_append_strides_past_the_address_space(lib):
 def test_attend_head_counts(lib):
     assert attend(lib, p=pages(kv_heads=1024), a=attention(q_heads=1024 * 65)) == INV
     assert attend(lib, t=table(max_pages=1 << 24), a=attention(q_heads=256)) == INV  # more tiles than a list counts
+
+
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 8, -(1 << 31) - 1, -(1 << 32)])
+def test_the_binding_refuses_integers_that_do_not_fit(n):
+    """None is cut to its low 32 bits on the way to the library."""
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    pool = ss.KVPages(k, k.clone(), weight=torch.zeros(4, 2, 16))
+    lens = torch.zeros(3, dtype=torch.int32)
+    seqs, new = (ss.KVTable(torch.zeros(3, 5, dtype=torch.int32), x) for x in (lens, lens.clone()))
+    with pytest.raises(ValueError, match="max_len"):
+        ss.KVTable(seqs.pages, lens, max_len=n)
+    with pytest.raises(ValueError, match="max_len"):
+        seqs.max_len = n
+    assert seqs.max_len == 0
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    for name in ("window", "sinks"):
+        with pytest.raises(ValueError, match=name):
+            ss.ss_kv_attend(pool, seqs, q, q.clone(), **{name: n})
+    for name in ("keep", "sinks", "recent"):
+        with pytest.raises(ValueError, match=name):
+            ss.ss_kv_evict(pool, seqs, pool, new, **{"keep": 8, name: n})
