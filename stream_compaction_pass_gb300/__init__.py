@@ -493,9 +493,9 @@ def _elem(t) -> int:
     return kind
 
 
-def _like(name: str, t, shape, dtype: str) -> int:
+def _like(name: str, t, shape, dtype: str, device: int) -> int:
     """The address of an optional contiguous tensor argument (0 for None), its
-    shape and type checked; the C ABI sees only addresses."""
+    shape, type and device checked; the C ABI sees only addresses."""
     if t is None:
         return 0
     if not _dtypes:
@@ -503,7 +503,23 @@ def _like(name: str, t, shape, dtype: str) -> int:
     if t.shape != shape or t.dtype is not _dtypes[dtype] or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                          f"{str(t.dtype)[6:]} {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
     return t.data_ptr()
+
+
+def _elsewhere(name: str, t, device: int) -> ValueError:
+    return ValueError(f"{name} is on {t.device}, where {'the CPU' if device < 0 else f'cuda:{device}'} was expected")
+
+
+def _refuse(device: int, **args) -> None:
+    """Raises for the argument (a tensor, KVPages or KVTable) that is not on the cache's GPU."""
+    if device < 0:
+        raise ValueError("the cache is not on a GPU")
+    for name, x in args.items():
+        t = x if hasattr(x, "get_device") else x.k if isinstance(x, KVPages) else x.pages
+        if t.get_device() != device:
+            raise _elsewhere(name, t, device)
 
 
 def _int32(**values) -> None:
@@ -530,8 +546,11 @@ class KVPages:
         if k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must have the same strides and a contiguous last dimension")
         pages, heads, page, dim = k.shape
-        d_weight = _like("weight", weight, (pages, heads, page), "float32")
-        d_scales = [_like(name, x, (heads,), "float32") for name, x in (("k_scale", k_scale), ("v_scale", v_scale))]
+        self.device = k.get_device()  # -1: the CPU, where no call works
+        if v.get_device() != self.device:
+            raise _elsewhere("v", v, self.device)
+        d_weight = _like("weight", weight, (pages, heads, page), "float32", self.device)
+        d_scales = [_like(name, x, (heads,), "float32", self.device) for name, x in (("k_scale", k_scale), ("v_scale", v_scale))]
         self.k, self.v, self.weight, self.k_scale, self.v_scale = k, v, weight, k_scale, v_scale
         self.kv_heads, self.head_dim, self.weight_shape = heads, dim, k.shape[:3]
         self._c = _KvPages(_elem(k), heads, dim, page, pages, _addr(k), _addr(v), k.stride(0), k.stride(1),
@@ -551,7 +570,8 @@ class KVTable:
     def __init__(self, pages, lens, max_len=None):
         if pages.dim() != 2 or str(pages.dtype) != "torch.int32" or (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("pages must be a 2-dimensional int32 tensor with contiguous rows")
-        _like("lens", lens, (pages.shape[0],), "int32")
+        self.device = pages.get_device()
+        _like("lens", lens, (pages.shape[0],), "int32", self.device)
         _int32(max_len=max_len or 0)
         self.pages, self.lens, self.batch = pages, lens, pages.shape[0]
         self._c = _KvTable(_addr(pages), pages.stride(0), pages.shape[1], pages.shape[0], _addr(lens),
@@ -578,9 +598,12 @@ def ss_kv_append(cache: KVPages, seqs: KVTable, k_new, v_new, offsets=None, stre
     token_stride, head_stride, unit = k_new.stride()
     if heads != cache.kv_heads or dim != cache.head_dim or unit != 1:
         raise ValueError(f"k_new must be (tokens, {cache.kv_heads}, {cache.head_dim}) with a contiguous last dimension")
-    d_offsets = _like("offsets", offsets, (seqs.batch + 1,), "int32")
+    device = cache.device
+    if device < 0 or seqs.device != device or k_new.get_device() != device or v_new.get_device() != device:
+        _refuse(device, seqs=seqs, k_new=k_new, v_new=v_new)
+    d_offsets = _like("offsets", offsets, (seqs.batch + 1,), "int32", device)
     _check(lib().ss_kv_append(cache._ref, seqs._ref, _elem(k_new), k_new.data_ptr(), v_new.data_ptr(), token_stride,
-                              head_stride, d_offsets, tokens, _stream(stream, k_new)), "ss_kv_append")
+                              head_stride, d_offsets, tokens, _current_stream(device) if stream is None else _stream(stream)), "ss_kv_append")
 
 
 def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int = 0, sinks: int = 0, lse=None,
@@ -597,14 +620,18 @@ def ss_kv_attend(cache: KVPages, seqs: KVTable, q, out, scale=None, window: int 
     out_seq, out_head, out_unit = out.stride()
     if batch != seqs.batch or dim != cache.head_dim or q_unit != 1 or out_unit != 1:
         raise ValueError(f"q and out must be ({seqs.batch}, q_heads, {cache.head_dim}) with a contiguous last dimension")
-    d_lse = _like("lse", lse, (batch, heads), "float32")
-    d_in, d_out = (_like("weight_in", weight_in, cache.weight_shape, "float32"),
-                   _like("weight_out", weight_out, cache.weight_shape, "float32"))
     if window >> 31 or sinks >> 31:  # also the negative ones
         _int32(window=window, sinks=sinks)
+    device = cache.device
+    if device < 0 or seqs.device != device or q.get_device() != device or out.get_device() != device:
+        _refuse(device, seqs=seqs, q=q, out=out)
+    d_lse = _like("lse", lse, (batch, heads), "float32", device)
+    d_in, d_out = (_like("weight_in", weight_in, cache.weight_shape, "float32", device),
+                   _like("weight_out", weight_out, cache.weight_shape, "float32", device))
     a = _KvAttention(_elem(q), heads, q.data_ptr(), q_seq, q_head, out.data_ptr(), out_seq, out_head,
                      dim ** -0.5 if scale is None else scale, window, sinks, d_lse, d_in, d_out)
-    _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a), _stream(stream, q)), "ss_kv_attend")
+    _check(lib().ss_kv_attend(cache._ref, seqs._ref, ctypes.addressof(a),
+                              _current_stream(device) if stream is None else _stream(stream)), "ss_kv_attend")
 
 
 def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable, keep: int, sinks: int = 0,
@@ -613,6 +640,9 @@ def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable
     their number into dst_seqs.lens; kept: int32 (batch, kv_heads, keep)."""
     if keep >> 31 or sinks >> 31 or recent >> 31:
         _int32(keep=keep, sinks=sinks, recent=recent)
-    d_kept = _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32")
+    device = src.device
+    if device < 0 or src_seqs.device != device or dst.device != device or dst_seqs.device != device:
+        _refuse(device, src_seqs=src_seqs, dst=dst, dst_seqs=dst_seqs)
+    d_kept = _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32", device)
     _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, d_kept,
-                             _stream(stream, src.k)), "ss_kv_evict")
+                             _current_stream(device) if stream is None else _stream(stream)), "ss_kv_evict")

@@ -1001,3 +1001,29 @@ def test_evict_lists_the_kept_positions_of_the_largest_budget(ss):
     ok(ss)
     assert kept[0, 0, :100].tolist() == list(range(100)) and d.lens_dev.tolist() == [100]
     assert int(kept[0, 0, 100:].max()) == -1 and int(kept[0, 0, 100:].min()) == -1
+
+
+def test_tensors_that_are_not_on_the_gpu_are_refused(ss):
+    import torch
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    w, lens, pages = torch.zeros(4, 2, 16), torch.zeros(3, dtype=torch.int32), torch.zeros(3, 5, dtype=torch.int32)
+    for args in (dict(k=k.cuda(), v=k), dict(k=k, v=k.cuda()), dict(k=k.cuda(), v=k.cuda(), weight=w)):
+        with pytest.raises(ValueError, match="is on"):
+            ss.KVPages(**args)
+    for args in ((pages.cuda(), lens), (pages, lens.cuda())):
+        with pytest.raises(ValueError, match="lens is on"):
+            ss.KVTable(*args)
+    pool, seqs = ss.KVPages(k.cuda(), k.cuda(), weight=w.cuda()), ss.KVTable(pages.cuda(), lens.cuda())
+    q, x = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    g, y = q.cuda(), x.cuda()
+    for args in (dict(q=q), dict(out=q), dict(lse=torch.zeros(3, 4)), dict(weight_out=w), dict(weight_in=w, weight_out=w.cuda()), dict(seqs=ss.KVTable(pages, lens)),
+                 dict(cache=ss.KVPages(k, k))):
+        with pytest.raises(ValueError, match="on a GPU" if "cache" in args else "is on cpu"):
+            ss.ss_kv_attend(**{"cache": pool, "seqs": seqs, "q": g, "out": g.clone(), **args})
+    for args in (dict(k_new=x), dict(v_new=x), dict(offsets=torch.zeros(4, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="is on cpu"):
+            ss.ss_kv_append(**{"cache": pool, "seqs": seqs, "k_new": y, "v_new": y, **args})
+    for args in (dict(dst=ss.KVPages(k, k)), dict(dst_seqs=ss.KVTable(pages, lens)), dict(kept=torch.zeros(3, 2, 8, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="is on cpu"):
+            ss.ss_kv_evict(**{"src": pool, "src_seqs": seqs, "dst": pool, "dst_seqs": seqs, "keep": 8, **args})
+    ok(ss)

@@ -230,3 +230,28 @@ def test_the_binding_refuses_integers_that_do_not_fit(n):
     for name in ("keep", "sinks", "recent"):
         with pytest.raises(ValueError, match=name):
             ss.ss_kv_evict(pool, seqs, pool, new, **{"keep": 8, name: n})
+
+
+def test_the_binding_refuses_tensors_that_are_not_on_the_caches_gpu(monkeypatch):
+    """Nothing reaches the library: it would follow their addresses on the GPU."""
+    torch = pytest.importorskip("torch")
+
+    class Nothing:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+
+    monkeypatch.setattr(ss, "lib", lambda: Nothing())
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    pool = ss.KVPages(k, k.clone(), weight=torch.zeros(4, 2, 16))
+    seqs, new = (ss.KVTable(torch.zeros(3, 5, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)) for _ in range(2))
+    q, x = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    calls = [lambda: ss.ss_kv_attend(pool, seqs, q, q.clone()), lambda: ss.ss_kv_append(pool, seqs, x, x),
+             lambda: ss.ss_kv_evict(pool, seqs, pool, new, 8)]
+    for call in calls:
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
+    # the pool on a GPU, for all that the binding knows, and the tables elsewhere
+    pool.device = 0
+    for call, name in zip(calls, ("seqs", "seqs", "src_seqs")):
+        with pytest.raises(ValueError, match=f"{name} is on cpu"):
+            call()
