@@ -757,7 +757,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, &small);
     if (e != cudaSuccess) return e;
     if (small.ranks > 0) {
-        if (a.weight_out) {
+        if (a.weight_out && small.bytes > 0) {  // 0: no sequence can have a position
             small.sc.logits = static_cast<float*>(mem.get(mem.owner, small.bytes));
             if (small.sc.logits == nullptr) return cudaErrorMemoryAllocation;
         }

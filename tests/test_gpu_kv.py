@@ -1027,3 +1027,19 @@ def test_tensors_that_are_not_on_the_gpu_are_refused(ss):
         with pytest.raises(ValueError, match="is on cpu"):
             ss.ss_kv_evict(**{"src": pool, "src_seqs": seqs, "dst": pool, "dst_seqs": seqs, "keep": 8, **args})
     ok(ss)
+
+
+@pytest.mark.parametrize("batch", [2, 700])
+def test_attend_with_weights_over_tables_without_pages(ss, batch):
+    """On a stream that has no scratch yet."""
+    import torch
+    c = Cache([5], heads=2, dim=64, page=16, seed=100)
+    pages, _ = c.ss(ss)
+    q = torch.randn(batch, 4, 64, device="cuda").to(torch.bfloat16)
+    out, lse, w = torch.full_like(q, 3.0), torch.zeros(batch, 4, device="cuda"), torch.full_like(c.weight, -3.0)
+    seqs = ss.KVTable(torch.empty(batch, 0, dtype=torch.int32, device="cuda"), torch.zeros(batch, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    ss.ss_shutdown()
+    ss.ss_kv_attend(pages, seqs, q, out, lse=lse, weight_out=w)
+    ok(ss)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and bool((w == -3.0).all())
