@@ -272,13 +272,14 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *     undefined, and nothing outside the arrays is touched.
  *   - batch == 0 is a no-op.  Results do not change from run to run.
  *   - attend and evict keep scratch in the stream's workspace, sized by
- *     batch, heads and max_len (with weights 4 bytes a score, at most 2 GB); as
- *     for the other calls, make one call of the largest size before capturing a
- *     stream into a graph: calls of no more sequences, heads and positions, all
- *     else alike, then need no more.  A call whose scratch would have to grow
- *     while its stream is being captured (or that is the first on that stream)
- *     returns SS_ERR_NO_MEMORY and enqueues nothing; one that makes it grow
- *     later leaves a captured graph its own.
+ *     batch, heads and max_len and grown by half at least.  With weights that
+ *     is 4 bytes a score: of all sequences, or of as many as 2 GB hold, but of
+ *     one at least.  As for the other calls, make one call of the largest size
+ *     before capturing a stream into a graph: calls of no more sequences,
+ *     heads and positions, all else alike, then need no more.  A call whose
+ *     scratch would have to grow while its stream is being captured (or that
+ *     is the first on that stream) returns SS_ERR_NO_MEMORY and enqueues
+ *     nothing; one that makes it grow later leaves a captured graph its own.
  */
 typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2 } ss_elem;
 

@@ -205,7 +205,9 @@ ss_status ensure_moe_acc(Workspace* w, size_t words) {
 }
 
 // Nothing is allocated while the stream is being captured, and scratch that a
-// captured graph may use is kept until ss_shutdown.
+// captured graph may use is kept until ss_shutdown.  It grows by half at least,
+// so that calls over sequences that get longer seldom make it grow, unless only
+// what the call needs is to be had.
 ss_status ensure_kv(Workspace* w, size_t bytes) {
     if (bytes == 0) return SS_OK;
     bool capturing = false;
@@ -217,6 +219,7 @@ ss_status ensure_kv(Workspace* w, size_t bytes) {
     }
     if (capturing)
         return fail(SS_ERR_NO_MEMORY, "key-value cache scratch has to grow: make one call of this size before capturing the stream");
+    size_t cap = std::max(bytes, w->kv_cap + w->kv_cap / 2);
     if (w->kv) {
         if (w->kv_captured) {
             w->kv_before.push_back(w->kv);
@@ -228,11 +231,18 @@ ss_status ensure_kv(Workspace* w, size_t bytes) {
         w->kv_cap = 0;
         w->kv_captured = false;
     }
-    cudaError_t e = cudaMallocAsync(&w->kv, bytes, w->stream);
-    if (e != cudaSuccess)
+    cudaError_t e = cudaMallocAsync(&w->kv, cap, w->stream);
+    if (e == cudaErrorMemoryAllocation && cap > bytes) {
+        cudaGetLastError();
+        cap = bytes;
+        e = cudaMallocAsync(&w->kv, cap, w->stream);
+    }
+    if (e != cudaSuccess) {
+        w->kv = nullptr;
         return e == cudaErrorMemoryAllocation ? fail(SS_ERR_NO_MEMORY, "key-value cache scratch")
                                               : cuda_fail(e, "cudaMallocAsync");
-    w->kv_cap = bytes;
+    }
+    w->kv_cap = cap;
     return SS_OK;
 }
 

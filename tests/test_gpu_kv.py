@@ -1043,3 +1043,37 @@ def test_attend_with_weights_over_tables_without_pages(ss, batch):
     ss.ss_kv_attend(pages, seqs, q, out, lse=lse, weight_out=w)
     ok(ss)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and bool((w == -3.0).all())
+
+
+def test_scratch_grows_in_steps_where_the_longest_length_grows(ss):
+    """A decode loop that sets max_len to the longest length in use: the
+    scratch of the scores grows by half at least, in a few steps."""
+    import ctypes
+
+    import torch
+    cuda = ctypes.CDLL("libcuda.so.1")
+    pool, used = ctypes.c_void_p(), ctypes.c_uint64()
+    assert cuda.cuDeviceGetDefaultMemPool(ctypes.byref(pool), torch.cuda.current_device()) == 0
+
+    def held():  # CU_MEMPOOL_ATTR_USED_MEM_CURRENT
+        assert cuda.cuMemPoolGetAttribute(pool, 7, ctypes.byref(used)) == 0
+        return used.value
+
+    c = Cache([100], heads=4, dim=64, page=64, seed=101)
+    pages, _ = c.ss(ss)
+    table = torch.full((40, 1200), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(40, dtype=torch.int32, device="cuda")
+    q = torch.randn(40, 16, 64, device="cuda").to(torch.bfloat16)
+    out, w = torch.empty_like(q), torch.zeros_like(c.weight)
+    torch.cuda.synchronize()
+    ss.ss_shutdown()
+    sizes = []
+    for n in range(64, 64 * 1200, 64):
+        ss.ss_kv_attend(pages, ss.KVTable(table, lens, max_len=n), q, out, weight_out=w)
+        torch.cuda.synchronize()
+        sizes.append(held())
+    ok(ss)
+    steps = [(a, b) for a, b in zip(sizes, sizes[1:]) if a != b]
+    # 16 scores of 4 bytes a position and sequence, beside some MB of parts
+    assert sizes[-1] - sizes[0] >= 40 * 64 * 1190 * 16 * 4 - (64 << 20)
+    assert len(steps) <= 12, steps
