@@ -1077,3 +1077,89 @@ def test_scratch_grows_in_steps_where_the_longest_length_grows(ss):
     # 16 scores of 4 bytes a position and sequence, beside some MB of parts
     assert sizes[-1] - sizes[0] >= 40 * 64 * 1190 * 16 * 4 - (64 << 20)
     assert len(steps) <= 12, steps
+
+
+# ---- the forms that only larger calls take ----
+
+@pytest.mark.parametrize("page", [64, 7])
+@pytest.mark.parametrize("levels", [1, 2, None])
+def test_evict_very_long_rows_with_more_candidates_than_they_can_list(ss, page, levels):
+    """One row over 8 CTAs, each with more positions than shared memory holds
+    keys of, of which (but for spread weights) more share T's digits than a
+    CTA lists."""
+    c = Cache([300_007], heads=1, dim=16, page=page, seed=111, kind="e4m3")
+    run_evict(ss, c, random_weights(c, 112, 0.0 if levels == 1 else 0.3, levels), 100_001, 4, 1000)
+
+
+@pytest.mark.parametrize("page", [64, 7])
+@pytest.mark.parametrize("levels", [1, 3, None])
+def test_evict_many_long_rows_of_one_cta_each(ss, page, levels):
+    """Rows for more than half the SMs are not split, however long; some are
+    below the budget."""
+    lens = [17000 + 287 * i for i in range(80)] + [16385, 9000, 12345, 12346, 0, 3]
+    c = shared(lens, heads=1, dim=16, page=page, seed=113, kind="e4m3")
+    run_evict(ss, c, random_weights(c, 114, 0.2, levels), 12_345, 4, 700)
+
+
+RAGGED = [int(n) for n in np.random.default_rng(115).integers(0, 400, 60)] + [1500, 777, 0, 1]
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (33, 5), (200, 0), (256, 40), (900, 4)])
+@pytest.mark.parametrize("weights", ["add", "apart", "new"])
+@pytest.mark.parametrize("group,page", [(4, 16), (3, 7), (12, 16)])
+def test_attend_windows_and_weights_of_batches(ss, window, sinks, weights, group, page):
+    """More rows than clusters: the list over all sequences, cut anywhere."""
+    check_attend(ss, Cache(RAGGED, heads=3, dim=64, page=page, seed=116), group, "bf16", window, sinks, weights)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,qkind", [(4, "bf16"), (8, "f16"), (12, "bf16"), (16, "f16")])
+@pytest.mark.parametrize("window", [0, 100])
+def test_attend_8_bit_batches(ss, dim, group, qkind, window):
+    check_attend(ss, Cache(RAGGED, heads=3, dim=dim, page=32, kind="e4m3", seed=117), group, qkind, window, 3, "apart")
+
+
+@pytest.mark.parametrize("kind,dim,group", [("bf16", 128, 4), ("f16", 256, 8), ("bf16", 256, 9), ("f16", 128, 16), ("bf16", 80, 5)])
+def test_attend_16_bit_batches(ss, kind, dim, group):
+    check_attend(ss, Cache(RAGGED, heads=3, dim=dim, page=16, kind=kind, seed=118), group, kind)
+
+
+@pytest.mark.parametrize("n,heads,group,dim,kind", [(80011, 2, 1, 64, "f16"), (50021, 1, 5, 128, "e4m3"), (12007, 1, 2, 256, "bf16"), (30011, 1, 12, 128, "f16")])
+@pytest.mark.parametrize("weights", ["add", None])
+def test_attend_one_sequence_too_long_for_one_launch(ss, n, heads, group, dim, kind, weights):
+    check_attend(ss, Cache([n], heads=heads, dim=dim, page=64, kind=kind, seed=n), group, "f16" if kind == "f16" else "bf16", weights=weights)
+
+
+@pytest.mark.parametrize("lens", [[100, 64, 0, 7], [100, 64, 0, 7] * 60], ids=["small", "many"])
+def test_a_tight_bound_on_the_lengths_and_a_length_above_it(ss, lens):
+    """max_len is all that a launch provides for; a longer length, though its
+    table has the pages, is clamped and reported."""
+    import torch
+    c = Cache(lens, heads=3, dim=64, page=16, seed=119)
+    pages, table = c.ss(ss)
+    d = Cache([50] * len(lens), heads=3, dim=64, page=16, seed=120)
+    new_pages, new_table = d.ss(ss)
+    q = torch.randn(len(lens), 12, 64, device="cuda").to(torch.bfloat16)
+    outs, ws, kepts = [], [], []
+    for max_len in (None, 100, 80):
+        seqs = ss.KVTable(c.table, c.lens_dev, max_len=max_len)
+        out, w = torch.empty_like(q), torch.zeros_like(c.weight)
+        kept = torch.empty(len(lens), 3, 50, dtype=torch.int32, device="cuda")
+        ss.ss_kv_attend(pages, seqs, q, out, weight_out=w)
+        late = max_len == 80
+        assert ss.ss_stream_status()[0] == (ss.SS_ERR_INVALID_ARG if late else ss.SS_OK)
+        ss.ss_kv_evict(pages, seqs, new_pages, new_table, 50, sinks=4, recent=10, kept=kept)
+        st, where = ss.ss_stream_status()
+        assert st == (ss.SS_ERR_INVALID_ARG if late else ss.SS_OK) and (not late or lens[where] == 100)
+        outs.append(out)
+        ws.append(w)
+        kepts.append(kept)
+    short = [b for b, n in enumerate(lens) if n <= 80]
+    for i in (1, 2):
+        rows = range(len(lens)) if i == 1 else short
+        assert bool(((outs[i] - outs[0])[rows].float().abs() <= 2.0 ** -7 * outs[0][rows].float().abs() + 1e-4).all())
+        assert torch.equal(kepts[i][rows], kepts[0][rows])
+    for b, n in enumerate(lens):
+        if n != 100:
+            assert np.allclose(c.rows(ws[2].cpu().numpy(), b, 1), c.rows(ws[0].cpu().numpy(), b, 1), rtol=1e-4, atol=0)
+    assert np.allclose(ws[1].cpu().numpy(), ws[0].cpu().numpy(), rtol=1e-4, atol=0)
