@@ -3,8 +3,10 @@
 Prompts enter the cache, then every step appends one token per sequence,
 attends over what is cached while gathering the weights, and, whenever the
 sequences have outgrown the budget, evicts the least attended positions into
-fresh pages and frees the old ones.  Random weights and inputs; `--check`
-recomputes every step in 64 bits from a plain list of the kept rows.
+fresh pages and frees the old ones.  The prompts' own tokens do not attend
+here, so the first eviction goes by the attention of the first new token.
+Random weights and inputs; `--check` recomputes every step in 64 bits from a
+plain list of the kept rows.
 
     python examples/paged_decode.py --batch 8 --prompt 600 --steps 200 --budget 512 --check
 """
@@ -106,6 +108,17 @@ def run(batch=8, heads=8, group=4, dim=128, page=16, prompt=600, steps=200, budg
     torch.cuda.synchronize()
     t0 = time.perf_counter()
     for _ in range(steps):
+        lens = [n + 1 for n in lens]
+        d_lens.add_(1)
+        q, k, v = project(torch.randn(batch, hidden, generator=gen, device="cuda", dtype=torch.bfloat16))
+        ss.ss_kv_append(pool.cache, seqs, k, v)
+        ss.ss_kv_attend(pool.cache, seqs, q, out, weight_in=pool.cache.weight, weight_out=pool.cache.weight)
+        if check:
+            for b in range(batch):
+                ref.append(b, *cached(b, lens[b] - 1))
+                want = ref.attend(b, q[b], group)
+                worst = max(worst, float((out[b].double() - want).abs().max() / want.abs().max()))
+        # after the attention: a prompt's weights are zero until a token has attended to it
         if max(lens) >= budget + slack or evictions == 0 and max(lens) > budget:
             fresh = [pool.take(width * page) for _ in range(batch)]
             new_lens = torch.empty(batch, dtype=torch.int32, device="cuda")
@@ -117,16 +130,6 @@ def run(batch=8, heads=8, group=4, dim=128, page=16, prompt=600, steps=200, budg
             if check:
                 for b in range(batch):
                     ref.keep(b, kept[b].tolist())
-        lens = [n + 1 for n in lens]
-        d_lens.add_(1)
-        q, k, v = project(torch.randn(batch, hidden, generator=gen, device="cuda", dtype=torch.bfloat16))
-        ss.ss_kv_append(pool.cache, seqs, k, v)
-        ss.ss_kv_attend(pool.cache, seqs, q, out, weight_in=pool.cache.weight, weight_out=pool.cache.weight)
-        if check:
-            for b in range(batch):
-                ref.append(b, *cached(b, lens[b] - 1))
-                want = ref.attend(b, q[b], group)
-                worst = max(worst, float((out[b].double() - want).abs().max() / want.abs().max()))
     torch.cuda.synchronize()
     seconds = time.perf_counter() - t0
     status, where = ss.ss_stream_status()

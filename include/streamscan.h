@@ -381,7 +381,9 @@ ss_status ss_kv_attend(const ss_kv_pages *cache, const ss_kv_table *seqs, const 
  * lower position first (-0 equals +0; NaN ranks below -inf).  Kept row i, in
  * the order of positions, goes to position i of the destination: k, v (bit
  * for bit) and, where dst->weight is not NULL, the weight.  Heads choose
- * independently.  dst_seqs->lens receives m; its tables have room for the
+ * independently.  A token's weight is 0 from its append to the first attention
+ * that keeps weights, and rows of equal weights keep their first positions.
+ * dst_seqs->lens receives m; its tables have room for the
  * smaller of keep and src_seqs' max_len.  `dst` has src's type, heads,
  * head_dim and scales (not moved); its page_size and strides are its own,
  * and it may be the same pool.  The destination pages must not be pages that

@@ -1163,3 +1163,25 @@ def test_a_tight_bound_on_the_lengths_and_a_length_above_it(ss, lens):
         if n != 100:
             assert np.allclose(c.rows(ws[2].cpu().numpy(), b, 1), c.rows(ws[0].cpu().numpy(), b, 1), rtol=1e-4, atol=0)
     assert np.allclose(ws[1].cpu().numpy(), ws[0].cpu().numpy(), rtol=1e-4, atol=0)
+
+
+def test_example_evicts_by_weights_that_attention_has_gathered(ss, monkeypatch):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_decode.py")
+    spec = importlib.util.spec_from_file_location("paged_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    evict, seen = ss.ss_kv_evict, []
+
+    def check(src, src_seqs, *args, **kw):
+        page = src.weight.shape[2]
+        for row, n in zip(src_seqs.pages.tolist(), src_seqs.lens.tolist()):
+            w = src.weight[row].transpose(1, 2).flatten(0, 1)[:n]
+            assert len(row) * page >= n and float(w.sum(0).min()) > 0.0
+        seen.append(1)
+        evict(src, src_seqs, *args, **kw)
+
+    monkeypatch.setattr(ss, "ss_kv_evict", check)
+    got = example.run(batch=3, heads=2, group=4, dim=64, prompt=90, steps=20, budget=64, slack=16, sinks=2, recent=16, check=True)
+    assert got["evictions"] == len(seen) == 2 and got["worst"] <= 2.0 ** -8 + 2.0 ** -10
