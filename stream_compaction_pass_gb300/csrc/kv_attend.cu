@@ -42,10 +42,29 @@ template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
 namespace cg = cooperative_groups;
 
 // Tiles of a warp up to which a call whose units fit the GPU takes the form of
-// one launch.  Measured on 8 heads of 128, one sequence: 517 positions 5.4
-// against 9.7 us, 16000 (10 tiles) 17.2 / 22.3 and with weights 24.3 / 25.2,
-// 32000 (21 tiles) 27.7 / 31.1 and with weights 40.4 / 35.1.
-constexpr int kSmallTiles = 24, kSmallTilesWeights = 12;
+// one launch, without and with weights (which that form adds up with the same
+// warps).  Measured, one launch against three, in us:
+//   8 heads of 128, bf16: 1 x 16000 positions (10 tiles) 15.1 / 16.7, 1 x 32000
+//     (21) 26.2 / 30.0, 1 x 48000 (31) 37.2 / 39.3; with weights 1 x 8000 (5)
+//     14.6 / 17.3, 1 x 16000 22.5 / 20.0, 4 x 8000 (10, on twice the SMs) 31.7 /
+//     33.2, 1 x 32000 41.3 / 35.4, 1 head x 16000 22.2 / 23.8.
+// 8-bit rows, groups above 8 and head_dim 256, whose tiles take a warp longer or
+// whose CTAs have fewer warps (`slow`), have lower limits, but where the clusters
+// hold three quarters of the SMs:
+//   8-bit: 1 x 16000 (5) 16.9 / 20.6, 1 x 32000 (10) 25.0 / 23.2, 1 x 64000 41.5
+//     / 32.9, 4 x 16000 (10) 26.9 / 31.8; with weights 1 x 8000 (3) 18.0 / 22.8,
+//     1 x 16000 27.1 / 24.9, 1 x 32000 43.0 / 27.8, 4 x 8000 (5) 27.4 / 27.8.
+//   256: 1 x 4000 (8) 11.5 / 13.1, 1 x 8000 (16) 18.0 / 15.2, 32 x 1000 (16) 23.4
+//     / 31.4; with weights 1 x 2000 (4) 11.3 / 13.1, 1 x 6000 (12) 22.2 / 16.9.
+//   group 12: 1 x 8000 (8) 13.8 / 16.8, 1 x 16000 (16) 21.1 / 17.7, 32 x 2000 (16)
+//     24.2 / 33.9; with weights 4 x 2000 (4) 15.6 / 16.8, 4 x 4000 (8) 24.3 / 19.5.
+struct SmallLimits {
+    int few, many;  // on fewer SMs, and on three quarters of them
+};
+constexpr SmallLimits small_limits(bool slow, bool weights) {
+    return slow ? (weights ? SmallLimits{5, 8} : SmallLimits{12, 24}) : weights ? SmallLimits{12, 12} : SmallLimits{24, 24};
+}
+constexpr int kSmallTiles = 24;  // the largest of them
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
@@ -720,7 +739,7 @@ struct SmallPlan {
 };
 
 cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const KvTable& t, const KvAttention& a, int heads, int warps, int tile,
-                       SmallPlan* out) {
+                       bool slow, SmallPlan* out) {
     SmallPlan p{};
     *out = p;
     if (a.q_heads / c.kv_heads > heads) return cudaSuccess;
@@ -734,7 +753,13 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
         if (e != cudaSuccess) return e;
         if (units <= most) break;
     }
-    if (ranks == 0 || tiles > (a.weight_out ? kSmallTilesWeights : kSmallTiles) * ranks * warps) return cudaSuccess;
+    const SmallLimits limits = small_limits(slow, a.weight_out != nullptr);
+    if (ranks == 0 || tiles > limits.many * ranks * warps) return cudaSuccess;
+    if (tiles > limits.few * ranks * warps) {
+        KernelSetup su;
+        const cudaError_t e = kernel_setup(kern, warps * 32, smem, &su);
+        if (e != cudaSuccess || units * ranks * 4 < (int64_t)su.sms * 3) return e;
+    }
     p.ranks = p.sc.ranks = ranks;
     p.sc.group = a.q_heads / c.kv_heads;
     p.sc.units = c.kv_heads;
@@ -752,9 +777,10 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     constexpr size_t smem = Shape<Rows, FP8, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
     auto* one = k_kv_attend<Rows, FP8, DP, T, NW, S, true>;
-    static_assert(kSmallTiles <= Rows::kChain && kSmallTilesWeights <= Rows::kChain, "a small call sets nothing aside");
+    static_assert(kSmallTiles <= Rows::kChain, "a small call sets nothing aside");
+    constexpr bool slow = FP8 || Rows::kHeads == 16 || DP == 256;
     SmallPlan small;
-    cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, &small);
+    cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, slow, &small);
     if (e != cudaSuccess) return e;
     if (small.ranks > 0) {
         if (a.weight_out && small.bytes > 0) {  // 0: no sequence can have a position
