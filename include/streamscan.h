@@ -262,8 +262,8 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *
  * Shared rules:
  *   - head_dim is at most 256 and head_dim * element size a multiple of 16
- *     bytes, as are the strides; k, v, the rows of new tokens, q and out are
- *     16-byte aligned.
+ *     bytes, as are the strides (those of an extent of 1 are not looked at);
+ *     k, v, the rows of new tokens, q and out are 16-byte aligned.
  *   - Lengths and page numbers are device data, checked on the device: a
  *     length below 0 or above max_len (or max_pages * page_size) is clamped,
  *     a page number outside [0, num_pages) is not followed, and either is

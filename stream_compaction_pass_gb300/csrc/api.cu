@@ -466,20 +466,23 @@ ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": head_dim must be at most 256 and a whole number of 16-byte vectors");
     if (!p->k || !p->v) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": null k or v");
     if (!aligned16(p->k) || !aligned16(p->v)) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": k and v must be 16-byte aligned");
-    if (p->page_stride * size % 16 || p->head_stride * size % 16 || p->slot_stride * size % 16)
+    // a stride that nothing steps by may be anything
+    const int64_t page_stride = p->num_pages > 1 ? p->page_stride : 0, head_stride = p->kv_heads > 1 ? p->head_stride : 0,
+                  slot_stride = p->page_size > 1 ? p->slot_stride : 0;
+    if (page_stride * size % 16 || head_stride * size % 16 || slot_stride * size % 16)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be multiples of 16 bytes");
-    if (p->page_stride < 0 || p->head_stride < 0 || p->slot_stride < 0)
+    if (page_stride < 0 || head_stride < 0 || slot_stride < 0)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must not be negative");
-    if (p->page_stride > (1ll << 60) / p->num_pages || p->head_stride > (1ll << 60) / p->kv_heads ||
-        p->slot_stride > (1ll << 60) / p->page_size)
+    if (page_stride > (1ll << 60) / p->num_pages || head_stride > (1ll << 60) / p->kv_heads ||
+        slot_stride > (1ll << 60) / p->page_size)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides reach past 2^60 elements");
     if (p->type != SS_E4M3 && (p->k_scale || p->v_scale))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales belong to an SS_E4M3 cache");
     if (!aligned4(p->k_scale) || !aligned4(p->v_scale) || !aligned4(p->weight))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales and weight must be 4-byte aligned");
     *out = ss::KvPages{static_cast<ss::KvElem>(p->type), p->kv_heads, p->head_dim, p->page_size, p->num_pages,
-                       static_cast<char*>(p->k), static_cast<char*>(p->v), p->page_stride, p->head_stride,
-                       p->slot_stride, p->k_scale, p->v_scale, p->weight};
+                       static_cast<char*>(p->k), static_cast<char*>(p->v), page_stride, head_stride,
+                       slot_stride, p->k_scale, p->v_scale, p->weight};
     return SS_OK;
 }
 
@@ -532,6 +535,8 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     if (tokens == 0 || t.batch == 0) return SS_OK;
     if (!k_new || !v_new) return fail(SS_ERR_INVALID_ARG, "null k_new or v_new");
     if (!aligned16(k_new) || !aligned16(v_new)) return fail(SS_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    if (tokens == 1) token_stride = 0;
+    if (c.kv_heads == 1) head_stride = 0;
     if (token_stride < 0 || head_stride < 0 || token_stride % 8 || head_stride % 8 || token_stride > 1ll << 40 || head_stride > 1ll << 40)
         return fail(SS_ERR_INVALID_ARG, "token_stride and head_stride must be non-negative multiples of 16 bytes, at most 2^40 elements");
     Workspace* w = nullptr;
@@ -574,11 +579,13 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     if (t.batch == 0) return SS_OK;
     if (!a.q || !a.out) return fail(SS_ERR_INVALID_ARG, "null q or out");
     if (!aligned16(a.q) || !aligned16(a.out)) return fail(SS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-    const int64_t strides[] = {a.q_seq_stride, a.q_head_stride, a.out_seq_stride, a.out_head_stride};
+    const bool seqs_step = t.batch > 1, heads_step = a.q_heads > 1;
+    const int64_t strides[] = {seqs_step ? a.q_seq_stride : 0, heads_step ? a.q_head_stride : 0, seqs_step ? a.out_seq_stride : 0,
+                               heads_step ? a.out_head_stride : 0};
     for (int64_t x : strides)
         if (x < 0 || x % 8 || x > 1ll << 40)
             return fail(SS_ERR_INVALID_ARG, "strides of q and out must be non-negative multiples of 16 bytes, at most 2^40 elements");
-    if ((t.batch > 1 && a.out_seq_stride < c.head_dim) || (a.q_heads > 1 && a.out_head_stride < c.head_dim))
+    if ((seqs_step && a.out_seq_stride < c.head_dim) || (heads_step && a.out_head_stride < c.head_dim))
         return fail(SS_ERR_INVALID_ARG, "rows of out overlap");
     const size_t qb = (size_t)((t.batch - 1) * strides[0] + (a.q_heads - 1) * strides[1] + c.head_dim) * 2;
     const size_t ob = (size_t)((t.batch - 1) * strides[2] + (a.q_heads - 1) * strides[3] + c.head_dim) * 2;
@@ -586,8 +593,8 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     Workspace* w = nullptr;
     st = get_workspace((cudaStream_t)stream, &w, false);
     if (st != SS_OK) return st;
-    const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, a.q_seq_stride, a.q_head_stride, a.out,
-                            a.out_seq_stride, a.out_head_stride, a.scale, a.window, a.sinks, a.lse, a.weight_in,
+    const ss::KvAttention k{static_cast<ss::KvElem>(a.type), a.q_heads, a.q, strides[0], strides[1], a.out,
+                            strides[2], strides[3], a.scale, a.window, a.sinks, a.lse, a.weight_in,
                             a.weight_out};
     struct Owner {
         Workspace* w;

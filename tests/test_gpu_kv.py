@@ -1185,3 +1185,33 @@ def test_example_evicts_by_weights_that_attention_has_gathered(ss, monkeypatch):
     monkeypatch.setattr(ss, "ss_kv_evict", check)
     got = example.run(batch=3, heads=2, group=4, dim=64, prompt=90, steps=20, budget=64, slack=16, sinks=2, recent=16, check=True)
     assert got["evictions"] == len(seen) == 2 and got["worst"] <= 2.0 ** -8 + 2.0 ** -10
+
+
+def test_strides_of_extents_of_one_are_not_looked_at(ss):
+    """As a slice of one row of a wider buffer leaves them."""
+    import torch
+    c = Cache([9], heads=1, dim=64, page=16, seed=121)
+    pages, table = c.ss(ss)
+    q = torch.randn(1, 1, 64, device="cuda").to(torch.bfloat16)
+    want, out = torch.empty_like(q), torch.zeros_like(q)
+
+    def odd(x):
+        return x.as_strided(x.shape, [n if m > 1 else 13 for n, m in zip(x.stride(), x.shape)])
+
+    ss.ss_kv_attend(pages, table, q, want)
+    ss.ss_kv_attend(pages, table, odd(q), odd(out))
+    ok(ss)
+    assert torch.equal(out, want)
+    x = torch.randn(1, 1, 64, device="cuda").to(torch.bfloat16)
+    one = ss.KVPages(odd(c.k), odd(c.v), weight=c.weight)  # one head
+    assert one._c.head_stride == 13
+    ss.ss_kv_append(one, table, odd(x), odd(x))
+    ok(ss)
+    assert torch.equal(c.k[int(c.table[0, 0]), 0, 8], x[0, 0])
+    dst = Cache([4], heads=1, dim=64, page=4, spare=0, seed=122)  # one page
+    new = ss.KVPages(odd(dst.k), odd(dst.v), weight=dst.weight)
+    assert new._c.page_stride == 13
+    c.weight.fill_(1.0)
+    ss.ss_kv_evict(one, table, new, ss.KVTable(dst.table, dst.lens_dev), 4, sinks=1, recent=3)
+    ok(ss)
+    assert torch.equal(dst.k[0, 0], c.k[int(c.table[0, 0]), 0, [0, 6, 7, 8]])
