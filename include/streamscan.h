@@ -351,8 +351,16 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *               weights: a page's weights are one sequence's.
  *   weight_in   the same layout, or NULL (zeros).  weight_in == weight_out
  *               accumulates in place; a partial overlap is not allowed.
- * Scores, softmax and sums are fp32; out is rounded once.  q_heads <=
- * 65536, at most 128 per key-value head, and (max_len / 16 + 1) * q_heads < 2^31.
+ * Scores, softmax statistics and sums are fp32 (sums of products 128 at a
+ * time, each cut below 2^-24 of its sum), exponentials are good to 2^-22, and
+ * out is rounded once.  In the sum over v a weight has 16 bits (bf16 caches) or
+ * 22 (fp16 and e4m3 caches), and up to 2^-38 of the row's largest weight more
+ * (fp16); it has 11 bits where q is bf16, the cache e4m3, and head_dim at most
+ * 64 or q_heads more than 8 per key-value head.  lse and the gathered weights
+ * are of the fp32 scores.  bf16 queries of an e4m3 cache are held to 2^-32 of
+ * their row's largest element.
+ * q_heads <= 65536, at most 128 per key-value head, and (max_len / 16 + 1) *
+ * q_heads < 2^31.
  */
 typedef struct ss_kv_attention {
     ss_elem type;

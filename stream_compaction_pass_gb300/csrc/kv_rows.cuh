@@ -212,20 +212,26 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 }
 
 // What both forms share.  8-bit caches multiply in fp16, which holds every
-// e4m3 value.  P is split into two 16-bit terms (kTwo), so that rounding it
-// adds nothing to the rounding of out (2^-16 against 2^-8 for bf16), except
-// under bf16 outputs of 8-bit caches, where one fp16 term (2^-11) is already
-// finer than out.
+// e4m3 value.  P enters the product with V as two 16-bit terms (kTwo), good to
+// 2^-16 of itself in bf16 and 2^-22 in fp16, below the rounding of out (2^-8,
+// 2^-11): 0.28 % of the ragged bf16 batch's outputs round to the other neighbour,
+// 0.13 % of an 8-bit cache's, against 0.07 and 0.12 % with fp32 weights.  One fp16
+// term, 2^-11, is left to bf16 outputs of 8-bit caches where two cost much (16
+// query heads a key-value head 84 / 95 us, head_dim 64 71 / 77): 7 % of them
+// round to the other neighbour, with the same error against the formula,
+// 1.65e-3.  (At head_dim 128 two terms cost nothing of 100 us, at 256 123 / 124.5,
+// at 80 60.7 / 64.4.)
 //
 // O is added up in the products' accumulators, which cut what falls below 24
 // bits instead of rounding it: an error of one sign, up to 2^-24 a product.  So
 // after kChain tiles, 128 products in a row (2^-17), O is set aside in memory, where
 // fp32 additions go on (put_aside): rows of 131,072 equal values in fp16 came
 // out 0.06 % low without that.
-template <typename QT, bool FP8, int DP, int T> struct RowsBase {
+template <typename QT, bool FP8, int DP, int T, int HEADS> struct RowsBase {
     using MT = typename std::conditional<FP8, __half, QT>::type;
     static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
-    static constexpr bool kTwo = !(FP8 && std::is_same<QT, __nv_bfloat16>::value);
+    static constexpr int kHeads = HEADS;
+    static constexpr bool kTwo = !FP8 || std::is_same<QT, __half>::value || (HEADS == 8 && DP > 64);
     static constexpr bool kFit = FP8 && !std::is_same<QT, __half>::value;
     static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
     static constexpr int kBytes = FP8 ? 1 : 2, kRowBytes = DP * kBytes, kKS = DP / 16;
@@ -259,12 +265,12 @@ template <typename QT, bool FP8, int DP, int T> struct RowsBase {
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8, DP, T> {
-    using Base = RowsBase<QT, FP8, DP, T>;
+template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8, DP, T, 16> {
+    using Base = RowsBase<QT, FP8, DP, T, 16>;
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
     using Query = QT;
-    static constexpr int kHeads = 16, kNT = DP / 8, kPT = T / 8, kVectors = kNT;  // of four O's a lane
+    static constexpr int kNT = DP / 8, kPT = T / 8, kVectors = kNT;  // of four O's a lane
     static constexpr bool kQShared = DP == 256;  // Q's fragments in shared memory: registers are short
     static constexpr int kQBytes = kQShared ? kKS * 32 * 16 : 0;
 
@@ -525,12 +531,12 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     }
 };
 
-template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8, DP, T> {
-    using Base = RowsBase<QT, FP8, DP, T>;
+template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8, DP, T, 8> {
+    using Base = RowsBase<QT, FP8, DP, T, 8>;
     using MT = typename Base::MT;
     using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
     using Query = QT;
-    static constexpr int kHeads = 8, kMT = DP / 16, kHB = T / 16, kVectors = kMT;  // of four O's a lane
+    static constexpr int kMT = DP / 16, kHB = T / 16, kVectors = kMT;  // of four O's a lane
     static constexpr int kQBytes = 0;
 
     uint32_t qf[kKS][2];

@@ -1215,3 +1215,29 @@ def test_strides_of_extents_of_one_are_not_looked_at(ss):
     ss.ss_kv_evict(one, table, new, ss.KVTable(dst.table, dst.lens_dev), 4, sinks=1, recent=3)
     ok(ss)
     assert torch.equal(dst.k[0, 0], c.k[int(c.table[0, 0]), 0, [0, 6, 7, 8]])
+
+
+@pytest.mark.parametrize("kind,qkind", [("e4m3", "bf16"), ("e4m3", "f16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("batch", [10, 600], ids=["small", "many"])
+def test_attend_weights_are_finer_than_the_rounding_of_out(ss, kind, qkind, dim, group, batch):
+    """Two positions of scores s and 0 and values 1 and -1: out = tanh(s / 2),
+    which for small s shows what rounds a weight: 2^-16 of it and 4e-6 of the
+    exponential and the sums, beside the rounding of out."""
+    c = Cache([2] * batch, heads=1, dim=dim, page=16, kind=kind, seed=123, scales=False)
+    c.k[:] = 0.0
+    c.k[c.table[:, 0].long(), 0, 0, 0] = 1.0
+    c.v[:] = -1.0
+    c.v[c.table[:, 0].long(), 0, 0] = 1.0
+    import torch
+    s = (torch.arange(1, batch * group + 1).view(batch, group) * (0.3 / (batch * group))).to(torch_type(qkind))
+    q = torch.zeros(batch, group, dim, dtype=s.dtype)
+    q[..., 0] = s
+    pages, table = c.ss(ss)
+    out = torch.empty_like(q, device="cuda")
+    ss.ss_kv_attend(pages, table, q.cuda(), out, scale=1.0)
+    ok(ss)
+    want = torch.tanh(s.double() / 2)[..., None]
+    u = 2.0 ** -8 if qkind == "bf16" else 2.0 ** -11
+    assert bool(((out.cpu().double() - want).abs() <= u * want + 4e-6 + 2.0 ** -16).all())
