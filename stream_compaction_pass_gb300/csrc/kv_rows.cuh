@@ -113,12 +113,6 @@ template <typename T> __device__ __forceinline__ float2 open2(uint32_t u) {
     return Pair<T>::open(*reinterpret_cast<const typename Pair<T>::type*>(&u));
 }
 
-// The least weights of two positions by their scores: 2^-24 (fp16) or 2^-126
-// (bf16), and 0 of a score of -inf.
-template <typename T> __device__ __forceinline__ uint32_t least2(float x, float y) {
-    constexpr uint32_t kLeast = std::is_same<T, __half>::value ? 0x0001u : 0x0080u;
-    return (x > -INFINITY ? kLeast : 0u) | (y > -INFINITY ? kLeast << 16 : 0u);
-}
 // The larger ones of two pairs of 16-bit numbers; NaN stays.
 template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
     uint32_t z;
@@ -140,16 +134,23 @@ template <typename T> __device__ __forceinline__ uint32_t trunc2(float x, float 
 
 // Weights (x, y) >= 0 as two 16-bit terms, of which the second has what the
 // first leaves out.  POSITIVE: the first is truncated, so that the second is not
-// negative, and both are kept at `least` or more: an infinite value that they
-// multiply stays infinite instead of becoming inf - inf or 0 inf, unless its
-// score is -inf and its weight therefore 0 (together 0.2 % of the long ragged
-// batch's time, 0.2 us of a call of 517 positions).  That adds at most 2^-38 of
-// the row's largest weight to each in fp16, 2^-101 in bf16.
-template <typename T, bool POSITIVE> __device__ __forceinline__ void split2(float x, float y, uint32_t least, uint32_t& high, uint32_t& rest) {
-    high = POSITIVE ? max2<T>(trunc2<T>(x, y), least) : pack2<T>(x, y);
+// negative, and both are kept at 2^-24 (fp16) or 2^-126 (bf16) and above: an
+// infinite value that they multiply stays infinite instead of becoming inf - inf
+// or 0 inf (0.2 % of the long ragged batch's time, 0.2 us of a call of 517
+// positions).  That adds at most 2^-38 of the row's largest weight in fp16, 2^-101
+// in bf16; scores of -inf get their 0 back (drop2).
+template <typename T, bool POSITIVE> __device__ __forceinline__ void split2(float x, float y, uint32_t& high, uint32_t& rest) {
+    constexpr uint32_t kLeast = std::is_same<T, __half>::value ? 0x00010001u : 0x00800080u;
+    high = POSITIVE ? max2<T>(trunc2<T>(x, y), kLeast) : pack2<T>(x, y);
     const float2 h = open2<T>(high);
     rest = pack2<T>(x - h.x, y - h.y);
-    if constexpr (POSITIVE) rest = max2<T>(rest, least);
+    if constexpr (POSITIVE) rest = max2<T>(rest, kLeast);
+}
+// Makes 0 of both terms of the weights whose scores x and y are -inf.
+__device__ __forceinline__ void drop2(float x, float y, uint32_t& high, uint32_t& rest) {
+    const uint32_t stay = (x == -INFINITY ? 0u : 0xffffu) | (y == -INFINITY ? 0u : 0xffff0000u);
+    high &= stay;
+    rest &= stay;
 }
 
 // Two e4m3 bytes as two fp16 (exact).
@@ -398,12 +399,14 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 if (u.row0 + g + 8 < u.group) *reinterpret_cast<float2*>(scores + (g + 8) * T + 2 * q4 + pt * 8) = make_float2(x[pt][2], x[pt][3]);
             }
         }
-        float top0 = m0, top1 = m1;
+        float top0 = m0, top1 = m1, low = INFINITY;
 #pragma unroll
         for (int pt = 0; pt < kPT; ++pt) {
             top0 = fmaxf(top0, fmaxf(x[pt][0], x[pt][1]));
             top1 = fmaxf(top1, fmaxf(x[pt][2], x[pt][3]));
+            low = fminf(low, fminf(fminf(x[pt][0], x[pt][1]), fminf(x[pt][2], x[pt][3])));
         }
+        const bool some_inf = !FP8 && __any_sync(kFullMask, low == -INFINITY);
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) {
             top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, s));
@@ -436,11 +439,20 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 l0 += a0 + a1;
                 l1 += b0 + b1;
                 if constexpr (kTwo) {
-                    split2<MT, !FP8>(a0, a1, least2<MT>(y[0], y[1]), ph[k * 2], pl[k * 2]);
-                    split2<MT, !FP8>(b0, b1, least2<MT>(y[2], y[3]), ph[k * 2 + 1], pl[k * 2 + 1]);
+                    split2<MT, !FP8>(a0, a1, ph[k * 2], pl[k * 2]);
+                    split2<MT, !FP8>(b0, b1, ph[k * 2 + 1], pl[k * 2 + 1]);
                 } else {
                     ph[k * 2] = pack2<MT>(a0, a1);
                     ph[k * 2 + 1] = pack2<MT>(b0, b1);
+                }
+            }
+            if constexpr (!FP8) {
+                if (some_inf) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        drop2(x[2 * h + k][0], x[2 * h + k][1], ph[k * 2], pl[k * 2]);
+                        drop2(x[2 * h + k][2], x[2 * h + k][3], ph[k * 2 + 1], pl[k * 2 + 1]);
+                    }
                 }
             }
             const uint32_t vh = vt + 16 * h * kRowBytes;
@@ -628,12 +640,14 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
                 for (int e = 0; e < 4; ++e)
                     if (u.row0 + 2 * q4 + (e & 1) < u.group) scores[(2 * q4 + (e & 1)) * T + 16 * h + g + (e >> 1) * 8] = x[h][e];
         }
-        float top0 = m0, top1 = m1;
+        float top0 = m0, top1 = m1, low = INFINITY;
 #pragma unroll
         for (int h = 0; h < kHB; ++h) {
             top0 = fmaxf(top0, fmaxf(x[h][0], x[h][2]));
             top1 = fmaxf(top1, fmaxf(x[h][1], x[h][3]));
+            low = fminf(low, fminf(fminf(x[h][0], x[h][1]), fminf(x[h][2], x[h][3])));
         }
+        const bool some_inf = !FP8 && __any_sync(kFullMask, low == -INFINITY);
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
             top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, s));
@@ -663,8 +677,12 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             // 8 positions x 8 heads, then transposed: a lane's pair is two positions of head g
             uint32_t ph[2], pl[2];
             if constexpr (kTwo) {
-                split2<MT, !FP8>(a0, a1, least2<MT>(x[h][0], x[h][1]), ph[0], pl[0]);
-                split2<MT, !FP8>(b0, b1, least2<MT>(x[h][2], x[h][3]), ph[1], pl[1]);
+                split2<MT, !FP8>(a0, a1, ph[0], pl[0]);
+                split2<MT, !FP8>(b0, b1, ph[1], pl[1]);
+                if (!FP8 && some_inf) {
+                    drop2(x[h][0], x[h][1], ph[0], pl[0]);
+                    drop2(x[h][2], x[h][3], ph[1], pl[1]);
+                }
                 pl[0] = transpose8(pl[0]);
                 pl[1] = transpose8(pl[1]);
             } else {
