@@ -13,8 +13,8 @@
 // and serves `group` query heads: 4 group / (element bytes) flops a byte, far
 // below the ridge, so the kernel is a stream of 16-byte asynchronous copies
 // that the arithmetic has to stay under.  64 sequences of 155 thousand
-// positions in all (8 x 4 heads of 128, bf16): 98 us for 634 MB, 6.4 TB/s,
-// tensor pipe 12 %; without the arithmetic 4 us less.
+// positions in all (8 x 4 heads of 128, bf16): 102 us for 634 MB, 6.2 TB/s,
+// tensor pipe 12 %; without the arithmetic about 4 us less.
 //
 // Split.  The tiles of every (sequence, unit), a unit being 8 or 16 query
 // heads of one key-value head, form one long list; a warp takes one contiguous
@@ -26,7 +26,7 @@
 // last row may be parts, which go to scratch, and the second launch joins
 // them (7 us for 2048 rows of 3.6 parts).  Where weights are kept, the first
 // launch leaves X (fp32) in scratch and the third turns it into weights, since
-// they need the joined sums (11 us for 1.2 million positions x 4 heads).
+// they need the joined sums (10 us for 1.2 million positions x 4 heads).
 #include <cooperative_groups.h>
 
 #include "kv_rows.cuh"
@@ -838,7 +838,11 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
 // better than stages do (ragged batch in bf16, in a graph: 8 warps x 3 stages
 // 113.6 us, 12 x 2 110.3, 13 x 2 spills 116.7).  8-bit and narrow rows take
 // tiles of 32 positions, which spreads a tile's fixed instructions over as many
-// bytes (8-bit rows in tiles of 16: 140.6 against 98.5 us).
+// bytes (8-bit rows in tiles of 16: 140.6 against 98.5 us).  Others, over 32 x
+// 4000 to 8000 positions: Rows8 of 256 with 4 x 3 123.7 us, 6 x 2 121.6, 8-bit 8 x
+// 3 124.7, 12 x 2 125.4; Rows16 of 64 with 8 x 3 131.6, 12 x 2 128.1 (spills),
+// 8-bit 12 x 4 93.5, 16 x 3 92.3 (spills); of 128 with 8 x 3 126.6, 12 x 2 125.1
+// (spills), 8-bit 84.0 / 106.4; of 256 in 8 bits with 7 x 3 114.6, 6 x 3 116.8.
 template <typename QT, bool FP8>
 cudaError_t run_dim(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
     if (a.q_heads / c.kv_heads <= 8) {

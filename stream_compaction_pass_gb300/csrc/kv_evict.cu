@@ -11,13 +11,13 @@
 // counts.  The move copies the kept rows.
 //
 // What bounds it.  The move reads and writes every kept row once and is bound
-// by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  The selection reads 4 bytes a position; it is bound by latency
-// (three passes, each with a histogram, a scan and a barrier).  A row is one
-// CTA's; where there are few rows it is split over a cluster of up to 8 CTAs,
-// which add up their histograms in L2 and exchange counts through distributed
-// shared memory.  128 rows of
-// 60 to 131 thousand positions take 70 us, 192 rows of up to 9001 17 us, 8 rows
-// of 2049 9 us.
+// by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  The
+// selection reads 4 bytes a position and is bound by latency: three passes, each
+// with a histogram, a scan and a barrier.  A row is one CTA's; where there are
+// few rows it is split over a cluster of up to 8 CTAs, which add up their
+// histograms in L2 and exchange counts through distributed shared memory.  128
+// rows of 60 to 131 thousand positions take 77 us, 118 where all weights are
+// equal, 192 rows of up to 9001 16 us, 8 rows of 2049 10 us.
 #include <cooperative_groups.h>
 
 #include "kv.cuh"
@@ -433,9 +433,13 @@ __global__ void __launch_bounds__(N, N == 512 ? 2 : 1) k_kv_select(KvPages c, Kv
 
 // CTAs of a row's cluster: one per row where there are rows for half the SMs;
 // otherwise a long row is split, into shares of kSplit positions or more, while
-// the CTAs fit the SMs.  8 rows in a graph, one CTA / split: 10000 positions
-// 19.1 / 20.9 us with the move, 20000 33.0 / 27.3, 60000 90.0 / 68.7, 131072
-// 173.7 / 124.8.
+// the CTAs fit the SMs.  With the move, in a graph, one CTA / split, half kept:
+//   1 row: 6000 positions 12.6 / 15.3 us, 14000 16.4 / 15.6, 20000 21.5 / 16.6,
+//     131072 80.4 / 29.9;
+//   8 rows: 10000 19.5 / 20.2, 14000 22.2 / 21.7, 20000 31.9 / 26.6, 131072 170 /
+//     115, and with equal weights 240 / 128;
+//   32 rows: 10000 46.8 / 46.0, 20000 78.2 / 75.5, 131072 411 / 362;
+//   72 rows: 20000 136.0 / 136.9, 32000 208.4 / 207.7, 131072 810 / 780.
 int select_ranks(const KvPages& c, const KvTable& t, int sms) {
     const int64_t rows = (int64_t)t.batch * c.kv_heads;
     int ranks = 1;
