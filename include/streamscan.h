@@ -276,7 +276,8 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *     is 4 bytes a score: of all sequences, or of as many as 2 GB hold, but of
  *     one at least.  As for the other calls, make one call of the largest size
  *     before capturing a stream into a graph: calls of no more sequences,
- *     heads and positions, all else alike, then need no more.  A call whose
+ *     key-value heads and positions, all else alike (also the query heads per
+ *     key-value head, weights and `kept`), then need no more.  A call whose
  *     scratch would have to grow while its stream is being captured (or that
  *     is the first on that stream) returns SS_ERR_NO_MEMORY and enqueues
  *     nothing; one that makes it grow later leaves a captured graph its own.

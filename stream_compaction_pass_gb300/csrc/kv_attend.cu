@@ -29,6 +29,8 @@
 // they need the joined sums (10 us for 1.2 million positions x 4 heads).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "kv_rows.cuh"
 
 namespace ss {
@@ -734,6 +736,7 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
 // tiles a warp.  ranks 0: it is not.
 struct SmallPlan {
     int ranks;
+    bool reserve;  // a smaller call may not be: scratch is kept for it
     Scratch sc;
     size_t bytes;
 };
@@ -759,6 +762,7 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
         KernelSetup su;
         const cudaError_t e = kernel_setup(kern, warps * 32, smem, &su);
         if (e != cudaSuccess || units * ranks * 4 < (int64_t)su.sms * 3) return e;
+        p.reserve = true;
     }
     p.ranks = p.sc.ranks = ranks;
     p.sc.group = a.q_heads / c.kv_heads;
@@ -782,16 +786,21 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     SmallPlan small;
     cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, slow, &small);
     if (e != cudaSuccess) return e;
+    KernelSetup su;
+    if (small.ranks == 0 || small.reserve) {
+        e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
+        if (e != cudaSuccess) return e;
+    }
     if (small.ranks > 0) {
-        if (a.weight_out && small.bytes > 0) {  // 0: no sequence can have a position
-            small.sc.logits = static_cast<float*>(mem.get(mem.owner, small.bytes));
-            if (small.sc.logits == nullptr) return cudaErrorMemoryAllocation;
+        size_t bytes = a.weight_out ? small.bytes : 0;  // 0 too where no sequence can have a position
+        if (small.reserve) bytes = std::max(bytes, make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms).bytes);
+        if (bytes > 0) {
+            void* base = mem.get(mem.owner, bytes);
+            if (base == nullptr) return cudaErrorMemoryAllocation;
+            if (a.weight_out) small.sc.logits = static_cast<float*>(base);
         }
         return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
     }
-    KernelSetup su;
-    e = kernel_setup(reinterpret_cast<const void*>(kern), NW * 32, smem, &su);
-    if (e != cudaSuccess) return e;
     Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms);
     char* base = static_cast<char*>(mem.get(mem.owner, p.bytes));
     if (base == nullptr) return cudaErrorMemoryAllocation;

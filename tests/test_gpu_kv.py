@@ -1241,3 +1241,39 @@ def test_attend_weights_are_finer_than_the_rounding_of_out(ss, kind, qkind, dim,
     want = torch.tanh(s.double() / 2)[..., None]
     u = 2.0 ** -8 if qkind == "bf16" else 2.0 ** -11
     assert bool(((out.cpu().double() - want).abs() <= u * want + 4e-6 + 2.0 ** -16).all())
+
+
+@pytest.mark.parametrize("kind,dim,group", [("bf16", 256, 4), ("f16", 128, 12)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_attend_in_a_graph_after_a_larger_call_that_took_one_launch(ss, kind, dim, group, weights):
+    """Where clusters fill the GPU a call takes one launch, and no scratch for
+    parts, which a call of fewer sequences needs."""
+    import torch
+    n = 1000 if dim == 256 else 2000
+    if weights:
+        n //= 3
+    c = Cache([n] * 32, heads=4, dim=dim, page=16, kind=kind, seed=125)
+    pages, _ = c.ss(ss)
+    q = torch.randn(32, 4 * group, dim, device="cuda").to(c.k.dtype)
+    out, lse = torch.zeros_like(q), torch.zeros(32, 4 * group, device="cuda")
+    w = torch.zeros_like(c.weight) if weights else None
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ss.ss_shutdown()
+
+    def attend(batch):
+        t = ss.KVTable(c.table[:batch], c.lens_dev[:batch], max_len=n)
+        ss.ss_kv_attend(pages, t, q[:batch], out[:batch], lse=lse[:batch], weight_out=w, stream=side)
+
+    attend(32)
+    ok(ss, side)
+    want, want_lse = out.clone(), lse.clone()
+    for batch in (31, 20, 10, 5, 2, 1):
+        g = captured(side, lambda: attend(batch))
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        ok(ss, side)
+        assert bool(((out - want)[:batch].float().abs() <= 2.0 ** -7 * want[:batch].float().abs() + 1e-4).all())
+        assert torch.allclose(lse[:batch], want_lse[:batch], rtol=1e-5, atol=1e-5)
