@@ -250,7 +250,12 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  * elements; [page][head][slot][dim] and [page][slot][head][dim] are both
  * strides of this), and the same offset in v.  An SS_E4M3 cache holds
  * value / scale: k_scale and v_scale are device arrays of kv_heads floats
- * (NULL: 1), and must be NULL for the other types.  `weight` (device,
+ * (NULL: 1), and must be NULL for the 16-bit types.  An SS_E2M1 cache packs
+ * two elements to a byte, the lower index in the low half, and holds beside them
+ * a scale for every 16 elements: element d is e2m1(code d) * e4m3(k_block[((p *
+ * kv_heads + h) * page_size + s) * head_dim / 16 + d / 16]) * k_scale[h], and the
+ * same in v (k_block and v_block: device, contiguous, 16-byte aligned; read for
+ * this type only).  `weight` (device,
  * contiguous [page][head][slot] floats, NULL: none) holds the attention that
  * each cached token has gathered.
  *
@@ -262,7 +267,8 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *
  * Shared rules:
  *   - head_dim is at most 256 and head_dim * element size a multiple of 16
- *     bytes, as are the strides (those of an extent of 1 are not looked at);
+ *     bytes, as are the strides (those of an extent of 1 are not looked at); an
+ *     SS_E2M1 cache has a head_dim of 64, 128 or 256;
  *     k, v, the rows of new tokens, q and out are 16-byte aligned.
  *   - Lengths and page numbers are device data, checked on the device: a
  *     length below 0 or above max_len (or max_pages * page_size) is clamped,
@@ -282,7 +288,7 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *     is the first on that stream) returns SS_ERR_NO_MEMORY and enqueues
  *     nothing; one that makes it grow later leaves a captured graph its own.
  */
-typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2 } ss_elem;
+typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2, SS_E2M1 = 3, SS_ELEM_F32 = 4 } ss_elem;
 
 typedef struct ss_kv_pages {
     ss_elem type;
@@ -298,6 +304,8 @@ typedef struct ss_kv_pages {
     const float *k_scale;
     const float *v_scale;
     float *weight;
+    uint8_t *k_block;
+    uint8_t *v_block;
 } ss_kv_pages;
 
 typedef struct ss_kv_table {
@@ -318,7 +326,11 @@ typedef struct ss_kv_table {
  * the strides serve a fused projection's output in place).  The cache holds
  * `type`, or SS_E4M3: each element is then x / scale[h] (fp32 division)
  * clamped to [-448, 448] and rounded to the nearest e4m3, ties to even; NaN
- * stays NaN.  The new slots' weights become 0 (where weight is not NULL).
+ * stays NaN.  Or it holds SS_E2M1: with y = x * (1 / scale[h]) (both fp32), a
+ * block's scale is max |y| / 6 as the nearest e4m3, at most 448 (NaN where an
+ * element is NaN), and a code that of y over its block's scale, the nearest of 0,
+ * 0.5, 1, 1.5, 2, 3, 4 and 6 with y's sign (0 where the scale is 0), ties to the
+ * even code, in fp32.  The new slots' weights become 0 (where weight is not NULL).
  *   offsets  device, batch + 1 int32, offsets[0] = 0, non-decreasing, or NULL.
  *   tokens   offsets[batch]; batch where offsets is NULL.  tokens *
  *            kv_heads < 2^31.
@@ -327,6 +339,112 @@ typedef struct ss_kv_table {
 ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_elem type, const void *k_new,
                        const void *v_new, int64_t token_stride, int64_t head_stride, const int32_t *offsets,
                        size_t tokens, ss_stream_t stream);
+
+/*
+ * Page tables and slot maps from the lengths that sequences grow by.  Sequence
+ * b has lens[b] tokens (none where restart[b] is not 0: another request takes
+ * its place) and gets counts[b] more.  The pages that it needs beyond those that
+ * it holds come from the front of a ring of free pages, in the order of the
+ * sequences; the pages of restarted sequences go to the ring's end, in the same
+ * order, and are handed out from the next call on.  A sequence is served where it
+ * needs no page, or where the needs up to and including its own do not exceed the
+ * ring's count; otherwise it gets nothing and its length stays (0 if restarted).
+ *   into       receives the table and the lengths; NULL: seqs itself.  It may
+ *              share either array with seqs.  Its max_pages and max_len are at
+ *              least seqs', and its max_len bounds the new lengths: a count that
+ *              is negative or leads past it is not served, and reported.
+ *              Entries past a sequence's pages are left as they were.
+ *   page_size, num_pages  of the pool, for the numbers that pages may have.
+ *   counts     device, batch int32, or NULL: one token each.
+ *   restart    device, batch bytes, or NULL: none.
+ *   free_pages the ring: `capacity` page numbers (at least all of the pool's that
+ *              are handed out this way) and state = {head, count}, device: the place
+ *              of the first one, taken modulo the capacity, and how many there are.
+ *   left       device, two int32: the state afterwards; NULL: state itself.
+ *   offsets    device, batch + 1 int32, or NULL: the counts' exclusive sums,
+ *              served or not (a negative count is 0).
+ *   positions  device, `tokens` int32, or NULL: of token offsets[b] + i, lens[b] + i.
+ *   slots      device, `tokens` int64, or NULL: page * page_size + slot of that
+ *              position, -1 where the sequence is not served.
+ *   tokens     the room of positions and slots: tokens behind offsets[batch] get
+ *              position 0 and slot -1, so that a fixed size serves every call; more
+ *              counts than room are reported.
+ * Lengths, counts and page numbers are checked on the device, as for the other
+ * calls.  batch <= 8192 and batch * max_pages < 2^31.
+ */
+typedef struct ss_kv_free {
+    int32_t *pages;
+    int64_t capacity;
+    int32_t *state;
+} ss_kv_free;
+ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t page_size, int64_t num_pages,
+                       const int32_t *counts, const uint8_t *restart, const ss_kv_free *free_pages, int32_t *left,
+                       int32_t *offsets, int32_t *positions, int64_t *slots, size_t tokens, ss_stream_t stream);
+
+/*
+ * Norms of query and key rows with the rotation by their positions, in one
+ * pass: for every token's and head's row x
+ *   y = R(p) (x / sqrt(mean(x^2) + eps) * w),
+ * where R(p) turns the pairs (x_i, x_{i + r/2}), or (x_2i, x_2i+1) where
+ * interleaved, i < r/2, by the angle of position p, and leaves elements from r =
+ * rotary_dim on as they are:  (a, b) -> (a cos - b sin, b cos + a sin).  Angles
+ * are p * turns[i] / 2^64 turns modulo 1, exact for every p; sums and products
+ * are fp32, and y is rounded once.
+ *   type       of q, k and the outputs: SS_BF16, SS_F16 or SS_ELEM_F32.
+ *   q, k       rows (token, head) of head_dim consecutive elements; strides in
+ *              elements, multiples of 16 bytes, 16-byte aligned.  Either may have
+ *              no heads (then it is not read).
+ *   q_weight, k_weight  device, head_dim numbers of weight_type (SS_BF16, SS_F16
+ *              or SS_ELEM_F32), or NULL: ones.
+ *   positions  device, a token each; may be negative.
+ *   q_out, k_out  each is its own input's rows, or shares no memory with either.
+ *   head_dim a multiple of 8, at most 256; rotary_dim a positive multiple of 16,
+ *   at most head_dim.  tokens == 0 is a no-op.
+ *
+ * ss_qk_norm_rope_backward: from the gradients of the outputs, dq_out and dk_out,
+ * those of the inputs (dq and dk: the rows of an input or of a gradient of their
+ * own, or apart from all) and of the weights, summed over all tokens and heads
+ * in a fixed order (fp32, head_dim numbers each, or NULL).  The partial sums lie
+ * in the stream's workspace: make one call before capturing a stream into a graph.
+ *
+ * ss_kv_append_rope: the same with k's and v's rows written into a cache, v's as
+ * they are: token t's to slot slots[t] (page * page_size + slot in the page, as
+ * ss_kv_assign gives them; a negative one: nowhere).  What the cache holds is as
+ * after ss_kv_append of y, which is not rounded to `type` before; the slots'
+ * weights become 0.  Slots behind the pool are reported with the token.  No two
+ * tokens share a slot.  type: SS_BF16 or SS_F16; rotary_dim a multiple of 32 for
+ * an SS_E2M1 cache.
+ */
+typedef struct ss_rows {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} ss_rows;
+typedef struct ss_rope {
+    const uint64_t *turns; /* device, rotary_dim / 2: the angle of one position in units of 2^-64 turns */
+    int32_t rotary_dim;
+    int32_t interleaved;
+} ss_rope;
+typedef struct ss_qk {
+    ss_elem type;
+    ss_elem weight_type;
+    int32_t head_dim;
+    int32_t q_heads;
+    int32_t kv_heads;
+    float eps;
+    int64_t tokens;
+    ss_rows q;
+    ss_rows k;
+    const void *q_weight;
+    const void *k_weight;
+    const int32_t *positions;
+    ss_rope rope;
+} ss_qk;
+ss_status ss_qk_norm_rope(const ss_qk *x, const ss_rows *q_out, const ss_rows *k_out, ss_stream_t stream);
+ss_status ss_qk_norm_rope_backward(const ss_qk *x, const ss_rows *dq_out, const ss_rows *dk_out, const ss_rows *dq,
+                                   const ss_rows *dk, float *dq_weight, float *dk_weight, ss_stream_t stream);
+ss_status ss_kv_append_rope(const ss_kv_pages *cache, const int64_t *slots, const ss_qk *x, const ss_rows *v,
+                            const ss_rows *q_out, ss_stream_t stream);
 
 /*
  * Attention of one token per sequence over its cached positions.  Query head
@@ -343,7 +461,7 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  * small the weight; that of a score of -inf is 0, and 0 times an infinite v is
  * NaN.  Rows that are not visible are not read.
  *   type        of q and out, SS_BF16 or SS_F16: the cache's, or either with
- *               an SS_E4M3 cache.
+ *               an SS_E4M3 or SS_E2M1 cache.
  *   q, out      row (b, j) at b * seq_stride + j * head_stride (each its own
  *               strides); must not overlap each other or the cache.
  *   lse         device, batch * q_heads floats (natural logarithm), or NULL.
@@ -355,11 +473,11 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  * Scores, softmax statistics and sums are fp32 (sums of products 128 at a
  * time, each cut below 2^-24 of its sum), exponentials are good to 2^-22, and
  * out is rounded once.  In the sum over v a weight has 16 bits (bf16 caches) or
- * 22 (fp16 and e4m3 caches), and up to 2^-38 of the row's largest weight more
- * (fp16); it has 11 bits where q is bf16, the cache e4m3, and head_dim at most
- * 64 or q_heads more than 8 per key-value head.  lse and the gathered weights
- * are of the fp32 scores.  bf16 queries of an e4m3 cache are held to 2^-32 of
- * their row's largest element.
+ * 22 (fp16, e4m3 and e2m1 caches), and up to 2^-38 of the row's largest weight
+ * more (fp16); it has 11 bits where q is bf16, the cache e4m3 or e2m1, and
+ * head_dim at most 64 or q_heads more than 8 per key-value head.  lse and the
+ * gathered weights are of the fp32 scores.  bf16 queries of an e4m3 or e2m1 cache
+ * are held to 2^-32 of their row's largest element.
  * q_heads <= 65536, at most 128 per key-value head, and (max_len / 16 + 1) *
  * q_heads < 2^31.
  */

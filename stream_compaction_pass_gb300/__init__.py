@@ -40,7 +40,7 @@ SS_ALGO_RTS_BLELLOCH_PAD2 = 4
 
 SS_WIDE_U32_U64, SS_WIDE_I32_I64, SS_WIDE_I64, SS_WIDE_F64 = 0, 1, 2, 3
 
-SS_BF16, SS_F16, SS_E4M3 = 0, 1, 2
+SS_BF16, SS_F16, SS_E4M3, SS_E2M1, SS_ELEM_F32 = 0, 1, 2, 3, 4
 
 
 class LibraryMissing(ImportError):
@@ -59,7 +59,7 @@ class _KvPages(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("slot_stride", ctypes.c_int64), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("weight", ctypes.c_void_p)]
+                ("weight", ctypes.c_void_p), ("k_block", ctypes.c_void_p), ("v_block", ctypes.c_void_p)]
 
 
 class _KvTable(ctypes.Structure):
@@ -73,6 +73,24 @@ class _KvAttention(ctypes.Structure):
                 ("out_seq_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64), ("scale", ctypes.c_float),
                 ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("lse", ctypes.c_void_p),
                 ("weight_in", ctypes.c_void_p), ("weight_out", ctypes.c_void_p)]
+
+
+class _KvFree(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("capacity", ctypes.c_int64), ("state", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class _Qk(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("weight_type", ctypes.c_int), ("head_dim", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("eps", ctypes.c_float), ("tokens", ctypes.c_int64), ("q", _Rows), ("k", _Rows),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rope", _Rope)]
 
 
 _lib = None
@@ -122,6 +140,10 @@ def _declare(lib):
         "ss_kv_append": [P, P, I, P, P, I64, I64, P, SZ, P],
         "ss_kv_attend": [P, P, P, P],
         "ss_kv_evict": [P, P, P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P],
+        "ss_kv_assign": [P, P, ctypes.c_int32, I64, P, P, P, P, P, P, P, SZ, P],
+        "ss_qk_norm_rope": [P, P, P, P],
+        "ss_qk_norm_rope_backward": [P, P, P, P, P, P, P, P],
+        "ss_kv_append_rope": [P, P, P, P, P, P],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -480,7 +502,7 @@ _dtypes = {}  # name -> torch dtype
 def _load_dtypes() -> None:
     import torch
     _elems.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float8_e4m3fn: SS_E4M3})
-    _dtypes.update({"float32": torch.float32, "int32": torch.int32})
+    _dtypes.update({"float32": torch.float32, "int32": torch.int32, "int64": torch.int64})
 
 
 def _elem(t) -> int:
@@ -535,26 +557,47 @@ class KVPages:
     k, v    CUDA tensors of shape (num_pages, kv_heads, page_size, head_dim),
             bfloat16, float16 or float8_e4m3fn, with the same strides (any
             order of the first three dimensions; the last one contiguous).
+            Of 4-bit caches uint8 (..., head_dim / 2): two codes to a byte, the
+            lower index in the low half.
     weight  float32 (num_pages, kv_heads, page_size), contiguous, or None.
-    k_scale, v_scale  float32 (kv_heads,), for a float8 cache, or None (1).
+    k_scale, v_scale  float32 (kv_heads,), for a float8 or 4-bit cache, or None (1).
+    k_block, v_block  of a 4-bit cache: float8_e4m3fn (num_pages, kv_heads,
+            page_size, head_dim / 16), contiguous: a scale for every 16 elements.
     The tensors are kept alive and may be updated in place.
     """
 
-    def __init__(self, k, v, weight=None, k_scale=None, v_scale=None):
+    def __init__(self, k, v, weight=None, k_scale=None, v_scale=None, k_block=None, v_block=None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be 4-dimensional, of one shape and type")
         if k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must have the same strides and a contiguous last dimension")
         pages, heads, page, dim = k.shape
+        strides = k.stride()[:3]
         self.device = k.get_device()  # -1: the CPU, where no call works
+        if (k_block is None) != (v_block is None):
+            raise ValueError("a 4-bit cache has both k_block and v_block")
+        blocks = [0, 0]
+        if k_block is not None:
+            if str(k.dtype) != "torch.uint8":
+                raise TypeError(f"a cache with k_block and v_block holds uint8 pairs of codes, not {k.dtype}")
+            dim, strides, kind = dim * 2, [2 * x for x in strides], SS_E2M1
+            for i, (name, x) in enumerate((("k_block", k_block), ("v_block", v_block))):
+                if x.shape != (pages, heads, page, dim // 16) or str(x.dtype) != "torch.float8_e4m3fn" or not x.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous float8_e4m3fn tensor of shape {(pages, heads, page, dim // 16)}, got "
+                                     f"{str(x.dtype)[6:]} {tuple(x.shape)}")
+                if x.get_device() != self.device:
+                    raise _elsewhere(name, x, self.device)
+                blocks[i] = x.data_ptr()
+        else:
+            kind = _elem(k)
         if v.get_device() != self.device:
             raise _elsewhere("v", v, self.device)
         d_weight = _like("weight", weight, (pages, heads, page), "float32", self.device)
         d_scales = [_like(name, x, (heads,), "float32", self.device) for name, x in (("k_scale", k_scale), ("v_scale", v_scale))]
         self.k, self.v, self.weight, self.k_scale, self.v_scale = k, v, weight, k_scale, v_scale
+        self.k_block, self.v_block = k_block, v_block
         self.kv_heads, self.head_dim, self.weight_shape = heads, dim, k.shape[:3]
-        self._c = _KvPages(_elem(k), heads, dim, page, pages, _addr(k), _addr(v), k.stride(0), k.stride(1),
-                           k.stride(2), *d_scales, d_weight)
+        self._c = _KvPages(kind, heads, dim, page, pages, _addr(k), _addr(v), *strides, *d_scales, d_weight, *blocks)
         self._ref = ctypes.addressof(self._c)
 
 
@@ -646,3 +689,168 @@ def ss_kv_evict(src: KVPages, src_seqs: KVTable, dst: KVPages, dst_seqs: KVTable
     d_kept = _like("kept", kept, (src_seqs.batch, src.kv_heads, keep), "int32", device)
     _check(lib().ss_kv_evict(src._ref, src_seqs._ref, dst._ref, dst_seqs._ref, keep, sinks, recent, d_kept,
                              _current_stream(device) if stream is None else _stream(stream)), "ss_kv_evict")
+
+
+class KVFree:
+    """The free pages of a pool, a ring (ss_kv_free).
+
+    pages      int32 (capacity,), contiguous: page numbers; capacity is at least
+               the number of pages that are handed out this way.
+    state      int32 (2,): the place of the first free page, and how many there
+               are from it on (going around the end).
+    num_pages  of the pool (default: capacity).
+    """
+
+    def __init__(self, pages, state, num_pages=None):
+        self.device = pages.get_device()
+        _like("pages", pages, (pages.numel(),), "int32", self.device)
+        _like("state", state, (2,), "int32", self.device)
+        self.pages, self.state, self.num_pages = pages, state, pages.numel() if num_pages is None else num_pages
+        _int32(num_pages=self.num_pages)
+        self._c = _KvFree(pages.data_ptr(), pages.numel(), state.data_ptr())
+        self._ref = ctypes.addressof(self._c)
+
+    def get_device(self):
+        return self.device
+
+
+def ss_kv_assign(seqs: KVTable, free: KVFree, page_size: int, counts=None, restart=None, into: KVTable = None, left=None, offsets=None,
+                 positions=None, slots=None, stream=None) -> None:
+    """Pages for counts more tokens of every sequence (int32 (batch,); None: one
+    each), from the front of the ring of free pages; those of sequences with
+    restart set (bool (batch,)) go to its end.  into receives table and lengths,
+    left (int32 (2,)) the ring's state; by default both are updated in place.
+    offsets: int32 (batch + 1,); positions int32 and slots int64, (tokens,) each."""
+    device = seqs.device
+    to = seqs if into is None else into
+    if device < 0 or free.device != device or to.device != device:
+        _refuse(device, free=free, into=to)
+    if page_size >> 31:
+        _int32(page_size=page_size)
+    batch = (seqs.batch,)
+    tokens = (positions if slots is None else slots).numel() if positions is not None or slots is not None else 0
+    if restart is not None and (restart.shape != batch or str(restart.dtype) not in ("torch.bool", "torch.uint8") or not restart.is_contiguous()):
+        raise ValueError(f"restart must be a contiguous bool tensor of shape {batch}")
+    if restart is not None and restart.get_device() != device:
+        raise _elsewhere("restart", restart, device)
+    d = (_like("counts", counts, batch, "int32", device), 0 if restart is None else restart.data_ptr(), _like("left", left, (2,), "int32", device),
+         _like("offsets", offsets, (seqs.batch + 1,), "int32", device), _like("positions", positions, (tokens,), "int32", device),
+         _like("slots", slots, (tokens,), "int64", device))
+    _check(lib().ss_kv_assign(seqs._ref, to._ref, page_size, free.num_pages, d[0], d[1], free._ref, d[2], d[3], d[4], d[5], tokens,
+                              _current_stream(device) if stream is None else _stream(stream)), "ss_kv_assign")
+
+
+class Rope:
+    """The rotation's frequencies (ss_rope).
+
+    inv_freq     the angles of one position in radians, (rotary_dim / 2,), on the
+                 GPU; best float64, as far positions multiply its error.
+    interleaved  pairs are adjacent elements (else rotary_dim / 2 apart).
+    """
+
+    def __init__(self, inv_freq, interleaved: bool = False):
+        import math
+
+        import torch
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have one dimension")
+        x = inv_freq.detach().to(torch.float64) / (2 * math.pi)
+        x = x - torch.floor(x + 0.5)
+        self.device = x.get_device()
+        self.turns = (x * 2.0 ** 64).to(torch.int64)  # modulo one turn; exact
+        self.rotary_dim, self.interleaved = 2 * x.numel(), bool(interleaved)
+        self._c = _Rope(self.turns.data_ptr(), self.rotary_dim, int(self.interleaved))
+
+    def get_device(self):
+        return self.device
+
+
+_row_kinds = {}  # torch dtype -> element type, of rows and weights
+
+
+def _row_kind(name: str, t) -> int:
+    if not _row_kinds:
+        import torch
+        _row_kinds.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float32: SS_ELEM_F32})
+    kind = _row_kinds.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} is {t.dtype}: bfloat16, float16 and float32 are taken")
+    return kind
+
+
+def _rows(name: str, t, like, device: int) -> _Rows:
+    """A (tokens, heads, head_dim) tensor of like's shape and type; None: no heads."""
+    if t is None:
+        if like is not None:
+            raise ValueError(f"{name} is missing")
+        return _Rows()
+    if like is None or t.shape != like.shape or t.dtype != like.dtype or t.stride(2) != 1:
+        raise ValueError(f"{name} must have its input's shape and type, and a contiguous last dimension")
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _qk(q, k, q_weight, k_weight, rope, positions, eps: float):
+    """The description of q and k (either may be None), and their device."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q and k are both None")
+    if one.dim() != 3 or (q is not None and k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype)):
+        raise ValueError("q and k must be (tokens, heads, head_dim), of one type and head_dim")
+    tokens, _, dim = one.shape
+    device = one.get_device()
+    if device < 0:
+        raise ValueError("q and k are not on a GPU")
+    if rope.device != device:
+        raise _elsewhere("rope", rope.turns, device)
+    weight = q_weight if q_weight is not None else k_weight
+    w = []
+    for name, x, of in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
+        if x is None or of is None:
+            w.append(0)
+            continue
+        if x.shape != (dim,) or x.dtype != weight.dtype or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, of shape {(dim,)}, and of the other weight's type")
+        if x.get_device() != device:
+            raise _elsewhere(name, x, device)
+        w.append(x.data_ptr())
+    c = _Qk(_row_kind("q" if q is not None else "k", one), SS_ELEM_F32 if weight is None else _row_kind("q_weight", weight), dim, 0 if q is None else q.shape[1],
+            0 if k is None else k.shape[1], eps, tokens, _rows("q", q, q, device), _rows("k", k, k, device), w[0], w[1],
+            _like("positions", positions, (tokens,), "int32", device), rope._c)
+    return c, device
+
+
+def ss_qk_norm_rope(q, k, q_weight, k_weight, rope: Rope, positions, q_out, k_out, eps: float = 1e-6, stream=None) -> None:
+    """Root-mean-square norms of the heads' rows of q and k, (tokens, heads,
+    head_dim), times their weights (head_dim,) or None, rotated by positions, int32
+    (tokens,), into q_out and k_out (which may be q and k).  Either of q and k may
+    be None."""
+    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    yq, yk = _rows("q_out", q_out, q, device), _rows("k_out", k_out, k, device)
+    _check(lib().ss_qk_norm_rope(ctypes.addressof(c), ctypes.addressof(yq), ctypes.addressof(yk),
+                                 _current_stream(device) if stream is None else _stream(stream)), "ss_qk_norm_rope")
+
+
+def ss_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, rope: Rope, positions, dq, dk, dq_weight=None, dk_weight=None,
+                             eps: float = 1e-6, stream=None) -> None:
+    """The gradients of ss_qk_norm_rope from those of its outputs: dq and dk (which
+    may be dq_out and dk_out), and float32 dq_weight and dk_weight (head_dim,)."""
+    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    g = [_rows(name, x, like, device) for name, x, like in (("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k))]
+    w = _like("dq_weight", dq_weight, (c.head_dim,), "float32", device), _like("dk_weight", dk_weight, (c.head_dim,), "float32", device)
+    _check(lib().ss_qk_norm_rope_backward(ctypes.addressof(c), *(ctypes.addressof(x) for x in g), *w,
+                                          _current_stream(device) if stream is None else _stream(stream)), "ss_qk_norm_rope_backward")
+
+
+def ss_kv_append_rope(cache: KVPages, slots, q, k, v, q_weight, k_weight, rope: Rope, positions, q_out, eps: float = 1e-6, stream=None) -> None:
+    """ss_qk_norm_rope whose k rows go to the cache, with v's as they are, at slots,
+    int64 (tokens,), as ss_kv_assign gives them (-1: nowhere)."""
+    if k is None:
+        raise ValueError("k is missing")
+    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    if cache.device != device:
+        _refuse(cache.device, k=k)
+    rows, yq = _rows("v", v, k, device), _rows("q_out", q_out, q, device)
+    _check(lib().ss_kv_append_rope(cache._ref, _like("slots", slots, (c.tokens,), "int64", device), ctypes.addressof(c), ctypes.addressof(rows),
+                                   ctypes.addressof(yq), _current_stream(device) if stream is None else _stream(stream)), "ss_kv_append_rope")

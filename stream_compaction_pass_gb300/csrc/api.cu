@@ -450,47 +450,55 @@ ss_status read_status_words(uint32_t* d_status, cudaStream_t s, int64_t* failing
 // ---- the paged key-value cache ----
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool narrow_cache(ss_elem t) { return t == SS_E4M3 || t == SS_E2M1; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The public description as the kernels take it; `name` says which argument
 // an error is about.
 ss_status kv_pages(const ss_kv_pages* p, const char* name, ss::KvPages* out) {
     if (p == nullptr) return fail(SS_ERR_INVALID_ARG, std::string(name) + " is null");
-    if (p->type != SS_BF16 && p->type != SS_F16 && p->type != SS_E4M3)
+    if (p->type != SS_BF16 && p->type != SS_F16 && p->type != SS_E4M3 && p->type != SS_E2M1)
         return fail(SS_ERR_UNSUPPORTED, std::string(name) + ": unknown element type");
-    const int64_t size = p->type == SS_E4M3 ? 1 : 2;
+    const bool narrow = narrow_cache(p->type), blocks = p->type == SS_E2M1;
+    const int64_t per = blocks ? 32 : narrow ? 16 : 8;  // elements of 16 bytes
     if (p->kv_heads < 1 || p->page_size < 1 || p->num_pages < 1)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": kv_heads, page_size and num_pages must be positive");
     if (p->num_pages > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": num_pages must be below 2^31");
-    if (p->head_dim < 1 || p->head_dim > 256 || p->head_dim * size % 16 != 0)
+    if (p->head_dim < 1 || p->head_dim > 256 || p->head_dim % per != 0)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": head_dim must be at most 256 and a whole number of 16-byte vectors");
+    if (blocks && p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": head_dim of an SS_E2M1 cache must be 64, 128 or 256");
     if (!p->k || !p->v) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": null k or v");
     if (!aligned16(p->k) || !aligned16(p->v)) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": k and v must be 16-byte aligned");
     // a stride that nothing steps by may be anything
     const int64_t page_stride = p->num_pages > 1 ? p->page_stride : 0, head_stride = p->kv_heads > 1 ? p->head_stride : 0,
                   slot_stride = p->page_size > 1 ? p->slot_stride : 0;
-    if (page_stride * size % 16 || head_stride * size % 16 || slot_stride * size % 16)
+    if (page_stride % per || head_stride % per || slot_stride % per)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be multiples of 16 bytes");
     if (page_stride < 0 || head_stride < 0 || slot_stride < 0)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must not be negative");
     if (page_stride > (1ll << 60) / p->num_pages || head_stride > (1ll << 60) / p->kv_heads ||
         slot_stride > (1ll << 60) / p->page_size)
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides reach past 2^60 elements");
-    if (p->type != SS_E4M3 && (p->k_scale || p->v_scale))
-        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales belong to an SS_E4M3 cache");
+    if (!narrow && (p->k_scale || p->v_scale))
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales belong to an SS_E4M3 or SS_E2M1 cache");
+    // (a caller of another type may have been built without these members)
+    if (blocks && (!p->k_block || !p->v_block || !aligned16(p->k_block) || !aligned16(p->v_block)))
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": an SS_E2M1 cache needs k_block and v_block, 16-byte aligned");
     if (!aligned4(p->k_scale) || !aligned4(p->v_scale) || !aligned4(p->weight))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": scales and weight must be 4-byte aligned");
     *out = ss::KvPages{static_cast<ss::KvElem>(p->type), p->kv_heads, p->head_dim, p->page_size, p->num_pages,
-                       static_cast<char*>(p->k), static_cast<char*>(p->v), page_stride, head_stride,
-                       slot_stride, p->k_scale, p->v_scale, p->weight};
+                       static_cast<char*>(p->k), static_cast<char*>(p->v), blocks ? page_stride / 2 : page_stride,
+                       blocks ? head_stride / 2 : head_stride, blocks ? slot_stride / 2 : slot_stride, p->k_scale, p->v_scale, p->weight,
+                       blocks ? p->k_block : nullptr, blocks ? p->v_block : nullptr};
     return SS_OK;
 }
 
 // Rows that are written must not be one another's: each stride of more than
 // one row reaches past a row.
 ss_status kv_writable(const ss::KvPages& c, const char* name) {
-    if ((c.page_size > 1 && c.slot_stride < c.head_dim) || (c.kv_heads > 1 && c.head_stride < c.head_dim) ||
-        (c.num_pages > 1 && c.page_stride < c.head_dim))
+    const int row = ss::kv_row_bytes(c) / ss::kv_stride_bytes(c);
+    if ((c.page_size > 1 && c.slot_stride < row) || (c.kv_heads > 1 && c.head_stride < row) || (c.num_pages > 1 && c.page_stride < row))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
     return SS_OK;
 }
@@ -510,9 +518,278 @@ ss_status kv_table(const ss_kv_table* t, const ss::KvPages& c, const char* name,
     return SS_OK;
 }
 
+// ---- norms and rotation of query and key rows ----
+
+// The bytes from a row tensor's first element to its last.
+size_t rows_bytes(const ss_rows& r, int64_t tokens, int heads, int dim, int size) {
+    return (size_t)((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + dim) * size;
+}
+
+// Rows (token, head) of one tensor: null where it has no heads.  Strides that
+// nothing steps by become 0.
+ss_status rows_arg(const ss_rows* in, const char* name, int64_t tokens, int heads, int dim, int size, bool written, ss_rows* out) {
+    *out = ss_rows{nullptr, 0, 0};
+    if (heads == 0) return SS_OK;
+    if (in == nullptr || in->data == nullptr) return fail(SS_ERR_INVALID_ARG, std::string(name) + " is null");
+    if (!aligned16(in->data)) return fail(SS_ERR_INVALID_ARG, std::string(name) + " must be 16-byte aligned");
+    *out = ss_rows{in->data, tokens > 1 ? in->token_stride : 0, heads > 1 ? in->head_stride : 0};
+    for (const int64_t x : {out->token_stride, out->head_stride})
+        if (x < 0 || x % (16 / size) || x > 1ll << 40)
+            return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be non-negative multiples of 16 bytes, at most 2^40 elements");
+    if (written && ((tokens > 1 && out->token_stride < dim) || (heads > 1 && out->head_stride < dim)))
+        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
+    return SS_OK;
+}
+
+// Whether two row tensors share memory: their ranges do, and they are not
+// columns of one buffer beside each other.
+bool rows_clash(const ss_rows& a, int a_heads, const ss_rows& b, int b_heads, int64_t tokens, int dim, int size) {
+    if (a_heads == 0 || b_heads == 0) return false;
+    if (!overlaps(a.data, rows_bytes(a, tokens, a_heads, dim, size), b.data, rows_bytes(b, tokens, b_heads, dim, size))) return false;
+    if (tokens == 1 || a.token_stride != b.token_stride || a.token_stride == 0) return true;
+    const int64_t step = a.token_stride * size, a_span = (int64_t)rows_bytes(a, 1, a_heads, dim, size), b_span = (int64_t)rows_bytes(b, 1, b_heads, dim, size);
+    int64_t d = ((int64_t)reinterpret_cast<intptr_t>(b.data) - (int64_t)reinterpret_cast<intptr_t>(a.data)) % step;
+    if (d < 0) d += step;
+    return d < a_span || d + b_span > step;
+}
+bool same_rows(const ss_rows& a, const ss_rows& b) { return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride; }
+
+ss::QkRows qk_rows(const ss_rows& x, const ss_rows& y, const void* weight, int heads) {
+    return ss::QkRows{static_cast<const char*>(x.data), x.token_stride, x.head_stride, static_cast<char*>(y.data), y.token_stride, y.head_stride,
+                      nullptr, 0, 0, static_cast<const char*>(weight), heads};
+}
+
+// What the calls share: the description's checks, and the inputs' rows.
+ss_status qk_arg(const ss_qk* x, bool with_f32, ss_rows* q, ss_rows* k, ss::QkRope* out, int* size) {
+    if (x == nullptr) return fail(SS_ERR_INVALID_ARG, "x is null");
+    if (x->type != SS_BF16 && x->type != SS_F16 && !(with_f32 && x->type == SS_ELEM_F32))
+        return fail(SS_ERR_UNSUPPORTED, with_f32 ? "rows must be SS_BF16, SS_F16 or SS_ELEM_F32" : "rows must be SS_BF16 or SS_F16");
+    if (x->weight_type != SS_BF16 && x->weight_type != SS_F16 && x->weight_type != SS_ELEM_F32)
+        return fail(SS_ERR_UNSUPPORTED, "weights must be SS_BF16, SS_F16 or SS_ELEM_F32");
+    if (x->tokens < 0 || x->tokens > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, "tokens must be below 2^31");
+    if (x->q_heads < 0 || x->kv_heads < 0 || x->q_heads + (int64_t)x->kv_heads < 1 || x->q_heads > 65536 || x->kv_heads > 65536)
+        return fail(SS_ERR_INVALID_ARG, "q_heads and kv_heads must be at most 65536, not negative, and not both 0");
+    if (x->head_dim < 8 || x->head_dim > 256 || x->head_dim % 8) return fail(SS_ERR_INVALID_ARG, "head_dim must be a multiple of 8, at most 256");
+    const ss_rope& r = x->rope;
+    if (r.rotary_dim < 16 || r.rotary_dim % 16 || r.rotary_dim > x->head_dim)
+        return fail(SS_ERR_INVALID_ARG, "rotary_dim must be a positive multiple of 16, at most head_dim");
+    if (!(x->eps >= 0.0f) || !(x->eps - x->eps == 0.0f)) return fail(SS_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (x->tokens > 0 && (!x->positions || !r.turns)) return fail(SS_ERR_INVALID_ARG, "null positions or turns");
+    const int weight_size = x->weight_type == SS_ELEM_F32 ? 4 : 2;
+    if (!aligned4(x->positions) || (reinterpret_cast<uintptr_t>(r.turns) & 7u) ||
+        ((reinterpret_cast<uintptr_t>(x->q_weight) | reinterpret_cast<uintptr_t>(x->k_weight)) & (uintptr_t)(weight_size - 1)))
+        return fail(SS_ERR_INVALID_ARG, "positions, turns and weights must be aligned to their elements");
+    *size = x->type == SS_ELEM_F32 ? 4 : 2;
+    ss_status st = SS_OK;
+    if (x->tokens > 0) st = rows_arg(&x->q, "q", x->tokens, x->q_heads, x->head_dim, *size, false, q);
+    if (st == SS_OK && x->tokens > 0) st = rows_arg(&x->k, "k", x->tokens, x->kv_heads, x->head_dim, *size, false, k);
+    *out = ss::QkRope{};
+    out->type = static_cast<ss::KvElem>(x->type);
+    out->weight_type = static_cast<ss::KvElem>(x->weight_type);
+    out->head_dim = x->head_dim;
+    out->rotary_dim = r.rotary_dim;
+    out->interleaved = r.interleaved != 0;
+    out->tokens = x->tokens;
+    out->eps = x->eps;
+    out->positions = x->positions;
+    out->turns = reinterpret_cast<const unsigned long long*>(r.turns);
+    return st;
+}
+
+// The outputs of rows of q and k: each its own input's rows, or apart from both.
+ss_status qk_outputs(const ss_qk* x, const ss_rows* q_out, const ss_rows* k_out, const char* q_name, const char* k_name, int size, const ss_rows& q, const ss_rows& k,
+                     bool in_place, ss_rows* yq, ss_rows* yk) {
+    ss_status st = rows_arg(q_out, q_name, x->tokens, x->q_heads, x->head_dim, size, true, yq);
+    if (st == SS_OK) st = rows_arg(k_out, k_name, x->tokens, x->kv_heads, x->head_dim, size, true, yk);
+    if (st != SS_OK) return st;
+    const int hq = x->q_heads, hk = x->kv_heads, dim = x->head_dim;
+    if (rows_clash(*yq, hq, *yk, hk, x->tokens, dim, size) || rows_clash(*yq, hq, k, hk, x->tokens, dim, size) ||
+        rows_clash(*yk, hk, q, hq, x->tokens, dim, size) || (!(in_place && same_rows(*yq, q)) && rows_clash(*yq, hq, q, hq, x->tokens, dim, size)) ||
+        (!(in_place && same_rows(*yk, k)) && rows_clash(*yk, hk, k, hk, x->tokens, dim, size)))
+        return fail(SS_ERR_INVALID_ARG, std::string(q_name) + " or " + k_name + " overlaps rows that are not its own");
+    return SS_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+ss_status ss_kv_assign(const ss_kv_table* seqs, const ss_kv_table* into, int32_t page_size, int64_t num_pages, const int32_t* counts,
+                       const uint8_t* restart, const ss_kv_free* free_pages, int32_t* left, int32_t* offsets, int32_t* positions, int64_t* slots,
+                       size_t tokens, ss_stream_t stream) try {
+    if (page_size < 1 || num_pages < 1 || num_pages > 0x7fffffff)
+        return fail(SS_ERR_INVALID_ARG, "page_size and num_pages must be positive, num_pages below 2^31");
+    ss::KvPages sized{};
+    sized.page_size = page_size;
+    ss::KvTable t, d;
+    ss_status st = kv_table(seqs, sized, "seqs", &t);
+    if (st != SS_OK) return st;
+    if (into == nullptr) into = seqs;
+    st = kv_table(into, sized, "into", &d);
+    if (st != SS_OK) return st;
+    if (d.batch != t.batch) return fail(SS_ERR_INVALID_ARG, "seqs and into must have the same batch");
+    if (d.max_pages < t.max_pages || d.max_len < t.max_len) return fail(SS_ERR_INVALID_ARG, "into must hold what seqs can");
+    if (t.batch > ss::kKvMaxAssign) return fail(SS_ERR_INVALID_ARG, "batch must be at most 8192");
+    if ((int64_t)d.batch * d.max_pages > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, "batch * max_pages must be below 2^31");
+    if (t.batch > 1 && d.max_pages > 0 && d.row_stride < d.max_pages) return fail(SS_ERR_INVALID_ARG, "rows of pages that are written overlap");
+    if (free_pages == nullptr || !free_pages->pages || !free_pages->state) return fail(SS_ERR_INVALID_ARG, "null free pages or state");
+    if (free_pages->capacity < 1 || free_pages->capacity > 0x7fffffff) return fail(SS_ERR_INVALID_ARG, "capacity must be positive and below 2^31");
+    if (left == nullptr) left = free_pages->state;
+    if (tokens > 0x7fffffff - 4096) return fail(SS_ERR_INVALID_ARG, "tokens must be below 2^31 - 4096");
+    if (!aligned4(counts) || !aligned4(free_pages->pages) || !aligned4(free_pages->state) || !aligned4(left) || !aligned4(offsets) || !aligned4(positions) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return fail(SS_ERR_INVALID_ARG, "counts, free pages, state, left, offsets and positions must be 4-byte aligned, slots 8-byte aligned");
+    if (!positions && !slots) tokens = 0;
+    struct Range {
+        const void* p;
+        size_t bytes;
+    };
+    auto table = [](const ss::KvTable& x) {
+        return Range{x.pages, x.batch && x.max_pages ? ((size_t)(x.batch - 1) * x.row_stride + x.max_pages) * 4 : 0};
+    };
+    const size_t batch = (size_t)t.batch;
+    // an output may be the input of its own kind
+    const Range in[] = {{t.lens, batch * 4}, table(t), {free_pages->state, 8}, {counts, counts ? batch * 4 : 0}, {restart, restart ? batch : 0}};
+    const Range out[] = {{d.lens, batch * 4}, table(d), {left, 8}, {free_pages->pages, (size_t)free_pages->capacity * 4},
+                         {offsets, offsets ? (batch + 1) * 4 : 0}, {positions, positions ? tokens * 4 : 0}, {slots, slots ? tokens * 8 : 0}};
+    const bool same_table = t.pages == d.pages && (t.row_stride == d.row_stride || t.batch < 2);
+    auto meet = [](const Range& a, const Range& b) { return a.bytes && b.bytes && overlaps(a.p, a.bytes, b.p, b.bytes); };
+    for (size_t i = 0; i < sizeof(out) / sizeof(out[0]); ++i) {
+        for (size_t j = 0; j < sizeof(in) / sizeof(in[0]); ++j)
+            if (meet(out[i], in[j]) && !(i == j && i < 3 && out[i].p == in[j].p && (i != 1 || same_table)))
+                return fail(SS_ERR_INVALID_ARG, "an output overlaps an input that is not its own");
+        for (size_t j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return fail(SS_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w, false);
+    if (st != SS_OK) return st;
+    ss::KvAssign a{};
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.counts = counts;
+    a.restart = restart;
+    a.ring = free_pages->pages;
+    a.capacity = free_pages->capacity;
+    a.state = free_pages->state;
+    a.left = left;
+    a.pages = const_cast<int32_t*>(d.pages);
+    a.row_stride = d.row_stride;
+    a.lens = d.lens;
+    a.limit = d.max_len;
+    a.copy = !(t.pages == d.pages && same_table);
+    a.vectors = aligned16(positions) && aligned16(slots);
+    a.given = positions || slots;
+    a.tokens = (int)tokens;
+    a.offsets = offsets;
+    a.positions = positions;
+    a.slots = slots;
+    const bool in_place = t.batch > 0 && t.lens == d.lens;
+    cudaError_t e = ss::launch_kv_assign(t, a, in_place || left == free_pages->state, device_sms(w->device), ws_status(w), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "assignment launch");
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
+    return SS_ERR_NO_MEMORY;
+}
+
+ss_status ss_qk_norm_rope(const ss_qk* x, const ss_rows* q_out, const ss_rows* k_out, ss_stream_t stream) try {
+    ss_rows q{}, k{}, yq, yk;
+    ss::QkRope a;
+    int size = 2;
+    ss_status st = qk_arg(x, true, &q, &k, &a, &size);
+    if (st != SS_OK || x->tokens == 0) return st;
+    st = qk_outputs(x, q_out, k_out, "q_out", "k_out", size, q, k, true, &yq, &yk);
+    if (st != SS_OK) return st;
+    a.q = qk_rows(q, yq, x->q_weight, x->q_heads);
+    a.k = qk_rows(k, yk, x->k_weight, x->kv_heads);
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w, false);
+    if (st != SS_OK) return st;
+    cudaError_t e = ss::launch_qk_rope(a, device_sms(w->device), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "norm and rotation launch");
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
+    return SS_ERR_NO_MEMORY;
+}
+
+ss_status ss_qk_norm_rope_backward(const ss_qk* x, const ss_rows* dq_out, const ss_rows* dk_out, const ss_rows* dq, const ss_rows* dk, float* dq_weight,
+                                   float* dk_weight, ss_stream_t stream) try {
+    ss_rows q{}, k{}, gq, gk, yq, yk;
+    ss::QkRope a;
+    int size = 2;
+    ss_status st = qk_arg(x, true, &q, &k, &a, &size);
+    if (st != SS_OK) return st;
+    if (!aligned4(dq_weight) || !aligned4(dk_weight)) return fail(SS_ERR_INVALID_ARG, "dq_weight and dk_weight must be 4-byte aligned");
+    const size_t bytes = (size_t)x->head_dim * 4;
+    if (dq_weight && dk_weight && overlaps(dq_weight, bytes, dk_weight, bytes)) return fail(SS_ERR_INVALID_ARG, "dq_weight and dk_weight overlap");
+    if (x->tokens == 0) {
+        for (float* p : {dq_weight, dk_weight}) {
+            const cudaError_t e = p ? cudaMemsetAsync(p, 0, bytes, (cudaStream_t)stream) : cudaSuccess;
+            if (e != cudaSuccess) return cuda_fail(e, "weight gradient clear");
+        }
+        return SS_OK;
+    }
+    st = rows_arg(dq_out, "dq_out", x->tokens, x->q_heads, x->head_dim, size, false, &gq);
+    if (st == SS_OK) st = rows_arg(dk_out, "dk_out", x->tokens, x->kv_heads, x->head_dim, size, false, &gk);
+    if (st == SS_OK) st = qk_outputs(x, dq, dk, "dq", "dk", size, q, k, true, &yq, &yk);
+    if (st == SS_OK) st = qk_outputs(x, dq, dk, "dq", "dk", size, gq, gk, true, &yq, &yk);
+    if (st != SS_OK) return st;
+    a.q = qk_rows(q, yq, x->q_weight, x->q_heads);
+    a.k = qk_rows(k, yk, x->k_weight, x->kv_heads);
+    a.q.g = static_cast<const char*>(gq.data);
+    a.q.g_token_stride = gq.token_stride;
+    a.q.g_head_stride = gq.head_stride;
+    a.k.g = static_cast<const char*>(gk.data);
+    a.k.g_token_stride = gk.token_stride;
+    a.k.g_head_stride = gk.head_stride;
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w, false);
+    if (st != SS_OK) return st;
+    const int sms = device_sms(w->device);
+    st = ensure_kv(w, ss::qk_rope_scratch(a, sms));
+    if (st != SS_OK) return st;
+    cudaError_t e = ss::launch_qk_rope_backward(a, dq_weight, dk_weight, static_cast<float*>(w->kv), sms, (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "norm and rotation gradient launch");
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
+    return SS_ERR_NO_MEMORY;
+}
+
+ss_status ss_kv_append_rope(const ss_kv_pages* cache, const int64_t* slots, const ss_qk* x, const ss_rows* v, const ss_rows* q_out, ss_stream_t stream) try {
+    ss::KvPages c;
+    ss_status st = kv_pages(cache, "cache", &c);
+    if (st == SS_OK) st = kv_writable(c, "cache");
+    if (st != SS_OK) return st;
+    ss_rows q{}, k{}, vr{}, yq{}, none{};
+    ss::QkRope a;
+    int size = 2;
+    st = qk_arg(x, false, &q, &k, &a, &size);
+    if (st != SS_OK) return st;
+    if (x->kv_heads != c.kv_heads || x->head_dim != c.head_dim) return fail(SS_ERR_INVALID_ARG, "k must have the cache's kv_heads and head_dim");
+    if (!narrow_cache(cache->type) && cache->type != x->type)
+        return fail(SS_ERR_INVALID_ARG, "rows must have the cache's type, or the cache be SS_E4M3 or SS_E2M1");
+    if (cache->type == SS_E2M1 && x->rope.rotary_dim % 32) return fail(SS_ERR_INVALID_ARG, "rotary_dim must be a multiple of 32 with an SS_E2M1 cache");
+    if (x->tokens == 0) return SS_OK;
+    if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u)) return fail(SS_ERR_INVALID_ARG, "slots must be 8-byte aligned and not null");
+    st = rows_arg(v, "v", x->tokens, x->kv_heads, x->head_dim, size, false, &vr);
+    if (st == SS_OK) st = rows_arg(q_out, "q_out", x->tokens, x->q_heads, x->head_dim, size, true, &yq);
+    if (st != SS_OK) return st;
+    const int hq = x->q_heads, hk = x->kv_heads, dim = x->head_dim;
+    if (rows_clash(yq, hq, k, hk, x->tokens, dim, size) || rows_clash(yq, hq, vr, hk, x->tokens, dim, size) ||
+        (!same_rows(yq, q) && rows_clash(yq, hq, q, hq, x->tokens, dim, size)))
+        return fail(SS_ERR_INVALID_ARG, "q_out overlaps rows that are not its own");
+    a.q = qk_rows(q, yq, x->q_weight, hq);
+    a.k = qk_rows(k, none, x->k_weight, hk);
+    a.v = qk_rows(vr, none, nullptr, hk);
+    Workspace* w = nullptr;
+    st = get_workspace((cudaStream_t)stream, &w, false);
+    if (st != SS_OK) return st;
+    cudaError_t e = ss::launch_kv_append_rope(c, slots, a, device_sms(w->device), ws_status(w), (cudaStream_t)stream);
+    return e == cudaSuccess ? SS_OK : cuda_fail(e, "norm, rotation and append launch");
+} catch (...) {  // of the host's own allocations
+    g_detail.clear();
+    return SS_ERR_NO_MEMORY;
+}
 
 ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_elem type, const void* k_new,
                        const void* v_new, int64_t token_stride, int64_t head_stride, const int32_t* offsets,
@@ -526,8 +803,8 @@ ss_status ss_kv_append(const ss_kv_pages* cache, const ss_kv_table* seqs, ss_ele
     st = kv_writable(c, "cache");
     if (st != SS_OK) return st;
     if (type != SS_BF16 && type != SS_F16) return fail(SS_ERR_UNSUPPORTED, "new tokens must be SS_BF16 or SS_F16");
-    if (cache->type != SS_E4M3 && cache->type != type)
-        return fail(SS_ERR_INVALID_ARG, "new tokens must have the cache's type, or the cache be SS_E4M3");
+    if (!narrow_cache(cache->type) && cache->type != type)
+        return fail(SS_ERR_INVALID_ARG, "new tokens must have the cache's type, or the cache be SS_E4M3 or SS_E2M1");
     if (offsets == nullptr && tokens != (size_t)t.batch)
         return fail(SS_ERR_INVALID_ARG, "without offsets there is one token for each sequence");
     if (!aligned4(offsets)) return fail(SS_ERR_INVALID_ARG, "offsets must be 4-byte aligned");
@@ -561,8 +838,8 @@ ss_status ss_kv_attend(const ss_kv_pages* cache, const ss_kv_table* seqs, const 
     if (args == nullptr) return fail(SS_ERR_INVALID_ARG, "args is null");
     const ss_kv_attention& a = *args;
     if (a.type != SS_BF16 && a.type != SS_F16) return fail(SS_ERR_UNSUPPORTED, "q and out must be SS_BF16 or SS_F16");
-    if (cache->type != SS_E4M3 && cache->type != a.type)
-        return fail(SS_ERR_INVALID_ARG, "q must have the cache's type, or the cache be SS_E4M3");
+    if (!narrow_cache(cache->type) && cache->type != a.type)
+        return fail(SS_ERR_INVALID_ARG, "q must have the cache's type, or the cache be SS_E4M3 or SS_E2M1");
     if (a.q_heads < 1 || a.q_heads % c.kv_heads) return fail(SS_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
     if (a.q_heads > 65536) return fail(SS_ERR_INVALID_ARG, "q_heads must be at most 65536");
     if (a.q_heads / c.kv_heads > 128) return fail(SS_ERR_INVALID_ARG, "at most 128 query heads per key-value head");

@@ -171,9 +171,10 @@ cudaError_t launch_reduce_sum(Dtype dt, const void* in, size_t n, void* partials
 
 // The paged key-value cache (kv_append.cu, kv_attend.cu, kv_evict.cu): the
 // public descriptions as the kernels take them, checked by api.cu.  Strides
-// are in elements; max_len is resolved (never 0 unless nothing can be held).
-enum class KvElem : int { BF16 = 0, F16 = 1, E4M3 = 2 };
-inline int kv_elem_bytes(KvElem t) { return t == KvElem::E4M3 ? 1 : 2; }
+// are in elements, of 4-bit caches in bytes; max_len is resolved (never 0
+// unless nothing can be held).
+enum class KvElem : int { BF16 = 0, F16 = 1, E4M3 = 2, E2M1 = 3, F32 = 4 };
+inline int kv_elem_bits(KvElem t) { return t == KvElem::E2M1 ? 4 : t == KvElem::E4M3 ? 8 : t == KvElem::F32 ? 32 : 16; }
 struct KvPages {
     KvElem type;
     int kv_heads, head_dim, page_size;
@@ -182,7 +183,11 @@ struct KvPages {
     int64_t page_stride, head_stride, slot_stride;
     const float *k_scale, *v_scale;
     float* weight;
+    uint8_t *k_block, *v_block;  // e4m3 scales of 16 elements each, of a 4-bit cache
 };
+// Bytes of a row of k, and of what strides count in.
+inline int kv_row_bytes(const KvPages& c) { return c.head_dim * kv_elem_bits(c.type) / 8; }
+inline int kv_stride_bytes(const KvPages& c) { return c.type == KvElem::E2M1 ? 1 : kv_elem_bits(c.type) / 8; }
 struct KvTable {
     const int32_t* pages;
     int64_t row_stride;
@@ -214,12 +219,66 @@ struct KvScratch {
 };
 cudaError_t launch_kv_attend(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status,
                              cudaStream_t s);
+cudaError_t launch_kv_attend4(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status,
+                              cudaStream_t s);
 constexpr int kKvMaxEvict = 1 << 21;  // the longest sequence an eviction takes
 cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d, const KvTable& dt, int keep,
                             int sinks, int recent, int32_t* kept, uint32_t* scratch, int sms, uint32_t* status, cudaStream_t s);
 // Device scratch of one eviction, in bytes, beside the kept positions; a
 // smaller call needs no more.
 size_t kv_evict_scratch(const KvPages& c, const KvTable& t, int sms);
+
+// Page tables and slot maps from lengths (kv_assign.cu).  `lens` and `pages` are
+// written, `left` too; `copy`: pages is another table than the one read.
+constexpr int kKvMaxAssign = 8192;  // sequences
+struct KvAssign {
+    int page_size;
+    int64_t num_pages;
+    const int32_t* counts;   // or null: one token each
+    const uint8_t* restart;  // or null
+    int32_t* ring;           // free pages, `capacity` places
+    int64_t capacity;
+    const int32_t* state;    // head and count of the ring
+    int32_t* left;
+    int32_t* pages;
+    int64_t row_stride;
+    int32_t* lens;
+    int limit;               // of the new lengths
+    bool copy, vectors, given;  // vectors: positions and slots take 16-byte stores; given: one of them is
+    int tokens;
+    int32_t *offsets, *positions;  // each or null, as slots
+    int64_t* slots;
+};
+// in_place: lens or left is what is read.
+cudaError_t launch_kv_assign(const KvTable& t, const KvAssign& a, bool in_place, int sms, uint32_t* status, cudaStream_t s);
+
+// Norms of query and key rows with the rotation by their positions
+// (qk_rope.cu): rows of one tensor, strides in elements.
+struct QkRows {
+    const char* x;
+    int64_t token_stride, head_stride;
+    char* y;  // what is written
+    int64_t y_token_stride, y_head_stride;
+    const char* g;  // backward: the gradient of the outputs
+    int64_t g_token_stride, g_head_stride;
+    const char* weight;
+    int heads;
+};
+struct QkRope {
+    KvElem type, weight_type;
+    int head_dim, rotary_dim;
+    bool interleaved;
+    int64_t tokens;
+    QkRows q, k, v;  // v: of the form that writes to a cache
+    float eps;
+    const int32_t* positions;
+    const unsigned long long* turns;  // rotary_dim / 2: angles of a position in units of 2^-64 turns
+};
+cudaError_t launch_qk_rope(const QkRope& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_append_rope(const KvPages& c, const int64_t* slots, const QkRope& a, int sms, uint32_t* status, cudaStream_t s);
+// Device scratch of the gradients of the weights, in bytes: never less for a larger call.
+size_t qk_rope_scratch(const QkRope& a, int sms);
+cudaError_t launch_qk_rope_backward(const QkRope& a, float* dq_weight, float* dk_weight, float* scratch, int sms, cudaStream_t s);
 
 // Ablations (reduce-then-scan, three kernels).  `totals` holds one value
 // per 4096-element tile.  tile_scan: 0 = register/shuffle tile scan,

@@ -67,7 +67,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveLoads = 8;  // 16-byte vectors that a thread has in flight
 
 struct Move {
-    int keep, rows, groups, vecs, elem_bytes;  // groups of `rows` kept rows per (sequence, head); `vecs` vectors a row
+    int keep, rows, groups, vecs, stride_bytes;  // groups of `rows` kept rows per (sequence, head); `vecs` vectors a row
     FastDiv src_page, dst_page, by_vecs;
 };
 
@@ -88,10 +88,18 @@ __device__ __forceinline__ void move_rows(const KvPages& c, const KvTable& t, co
             const int to = kv_page(dt, d.num_pages, b, ti, status);
             if (from >= 0 && to >= 0) {
                 const int fs = p - fi * c.page_size, ts = j - ti * d.page_size;
-                src = ((int64_t)from * c.page_stride + (int64_t)h * c.head_stride + (int64_t)fs * c.slot_stride) * mv.elem_bytes;
-                dst = ((int64_t)to * d.page_stride + (int64_t)h * d.head_stride + (int64_t)ts * d.slot_stride) * mv.elem_bytes;
-                if (d.weight)
-                    d.weight[((int64_t)to * d.kv_heads + h) * d.page_size + ts] = c.weight[((int64_t)from * c.kv_heads + h) * c.page_size + fs];
+                src = ((int64_t)from * c.page_stride + (int64_t)h * c.head_stride + (int64_t)fs * c.slot_stride) * mv.stride_bytes;
+                dst = ((int64_t)to * d.page_stride + (int64_t)h * d.head_stride + (int64_t)ts * d.slot_stride) * mv.stride_bytes;
+                const int64_t src_row = ((int64_t)from * c.kv_heads + h) * c.page_size + fs, dst_row = ((int64_t)to * d.kv_heads + h) * d.page_size + ts;
+                if (d.weight) d.weight[dst_row] = c.weight[src_row];
+                if (c.type == KvElem::E2M1) {  // the blocks' scales: 4, 8 or 16 bytes of k and of v
+                    const int words = c.head_dim / 64;
+                    auto words_of = [&](uint8_t* p, int64_t row) { return reinterpret_cast<uint32_t*>(p) + row * words; };
+                    for (int i = 0; i < words; ++i) {
+                        words_of(d.k_block, dst_row)[i] = words_of(c.k_block, src_row)[i];
+                        words_of(d.v_block, dst_row)[i] = words_of(c.v_block, src_row)[i];
+                    }
+                }
             }
         }
         s_src[r] = src;
@@ -476,7 +484,7 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
     const int share = ((t.max_len + ranks - 1) / ranks + 3) / 4 * 4;
     const bool staged = share <= kStagedShare;
     const bool vec4 = c.page_size % 4 == 0 && (reinterpret_cast<uintptr_t>(c.weight) & 15u) == 0;
-    const int bytes = kv_elem_bytes(c.type), vecs = c.head_dim * bytes / 16;
+    const int vecs = kv_row_bytes(c) / 16;
     const int most = keep < t.max_len ? keep : t.max_len;
     const bool fused = staged && ranks == 1 && (int64_t)most * vecs * 32 <= kFusedBytes;
     auto* kern = !staged ? (vec4 ? k_kv_select<1024, false, 4, false> : k_kv_select<1024, false, 1, false>)
@@ -489,7 +497,7 @@ cudaError_t launch_kv_evict(const KvPages& c, const KvTable& t, const KvPages& d
 
     const int per = fused ? 256 : kv_rows_per_cta(kMoveThreads * kMoveLoads / (2 * vecs), kMoveThreads, (int64_t)rows * most, sms);
     const int groups = (most + per - 1) / per;
-    const Move mv{keep, per, groups, vecs, bytes, FastDiv(c.page_size), FastDiv(d.page_size), FastDiv(vecs)};
+    const Move mv{keep, per, groups, vecs, kv_stride_bytes(c), FastDiv(c.page_size), FastDiv(d.page_size), FastDiv(vecs)};
     e = launch_dependent(kern, (size_t)rows * ranks, threads, (size_t)select_bytes(threads, staged, share), ranks, s, c, t, d, dt, mv,
                          Choice{keep, sinks, recent, share, FastDiv(c.page_size), scratch}, kept, dt.lens, status);
     if (e != cudaSuccess || fused || groups == 0) return e;

@@ -52,6 +52,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // multiplied by.)
 __device__ __forceinline__ float shrink(float from, float to) { return fmaxf(exp2_fast(from - to), 0x1p-126f); }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+    uint32_t v;
+    asm volatile("{.reg .b16 t; ld.shared.u16 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("{.reg .b16 t; ld.shared.u8 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -170,22 +186,48 @@ __device__ __forceinline__ void pairs4(uint32_t w0, uint32_t w1, uint32_t (&f)[4
     f[3] = e4m3x2_f16x2(b >> 16);
 }
 
-// Where 16-byte vector `v` of row `row` of a tile lies within that row.  The
-// exclusive-ors spread the addresses that one shared-memory access of a
-// quarter warp touches over all banks: 16-bit tiles are read by ldmatrix (8
-// rows of one vector), 8-bit keys by lanes (row g, vector t * DP / 64 + i) and
-// 8-bit values by lanes (rows 2 t and on, vector g * DP / 128 + i).
-template <bool FP8, int DP> __device__ __forceinline__ int k_vec(int row, int v) {
-    if (!FP8) return v ^ (row & 7);
-    if (DP == 64) return v;
-    if (DP == 128) return v ^ (row & 1);
-    return v ^ ((v >> 3) & 1) ^ ((row & 1) << 1);
+// Four bytes of two e2m1 codes each, the low half first, as pairs of fp16 (exact).
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&f)[4]) {
+    asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; "
+        "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(w));
 }
-template <bool FP8, int DP> __device__ __forceinline__ int v_vec(int row, int v) {
-    if (!FP8) return v ^ (row & 7);
-    if (DP == 64) return v ^ ((row >> 1) & 3);
-    if (DP == 128) return v ^ (((row >> 1) & 3) << 1);
-    return v ^ ((row >> 1) & 1) ^ (((row >> 2) & 1) << 2);
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+    uint32_t z;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+// A word of 4-bit values of each of two positions as eight pairs of fp16, a pair
+// per dimension, times their blocks' scales.
+__device__ __forceinline__ void pairs8(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t (&f)[8]) {
+    uint32_t even[4], odd[4];
+    e2m1x8_f16((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), even);
+    e2m1x8_f16(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), odd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = mul_f16x2(even[i], scale);
+        f[2 * i + 1] = mul_f16x2(odd[i], scale);
+    }
+}
+
+// Where 16-byte vector `v` of row `row` of a tile lies within the tile.  The
+// exclusive-ors spread the addresses that one shared-memory access touches over
+// all banks: 16-bit tiles are read by ldmatrix (8 rows of one vector), narrow
+// keys by lanes (row g, DP / 4 consecutive elements) and narrow values by lanes
+// (rows 2 t and on, DP / 8 consecutive elements).
+template <int BITS, int DP> __device__ __forceinline__ int k_at(int row, int v) {
+    constexpr int kRowBytes = DP * BITS / 8;
+    const int u = BITS == 16 ? v ^ (row & 7) : kRowBytes <= 64 ? v : kRowBytes == 128 ? v ^ (row & 1) : v ^ ((v >> 3) & 1) ^ ((row & 1) << 1);
+    return row * kRowBytes + u * 16;
+}
+template <int BITS, int DP> __device__ __forceinline__ int v_at(int row, int v) {
+    constexpr int kRowBytes = DP * BITS / 8;
+    // 4-bit rows of 32 and 64 bytes: four and two of them share 128 bytes
+    if (BITS == 4 && DP == 64) return (row >> 2) * 128 + (((row & 3) * 2 + v) ^ (((row >> 2) & 1) << 1)) * 16;
+    if (BITS == 4 && DP == 128) return (row >> 1) * 128 + (((row & 1) * 4 + v) ^ (((row >> 1) & 1) << 2 | ((row >> 2) & 1) << 1)) * 16;
+    const int u = BITS == 16 ? v ^ (row & 7) : kRowBytes == 64 ? v ^ ((row >> 1) & 3) : kRowBytes == 128 ? v ^ (((row >> 1) & 3) << 1)
+                                                                                            : v ^ ((row >> 1) & 1) ^ (((row >> 2) & 1) << 2);
+    return row * kRowBytes + u * 16;
 }
 
 
@@ -231,16 +273,19 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 // of a 4.4 GB batch, 211 against 199 where 128 query heads share one key-value
 // head; fp32 additions of every tile take more, 106.9 against 100.5 us over an
 // 8-bit cache.
-template <typename QT, bool FP8, int DP, int T, int HEADS> struct RowsBase {
-    using MT = typename std::conditional<FP8, __half, QT>::type;
+template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
+    static constexpr bool kNarrow = BITS < 16;
+    using MT = typename std::conditional<kNarrow, __half, QT>::type;
     static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
     static constexpr int kHeads = HEADS;
-    static constexpr bool kTwo = !FP8 || std::is_same<QT, __half>::value || (HEADS == 8 && DP > 64);
-    static constexpr bool kFit = FP8 && !std::is_same<QT, __half>::value;
+    static constexpr bool kTwo = !kNarrow || std::is_same<QT, __half>::value || (HEADS == 8 && DP > 64);
+    static constexpr bool kFit = kNarrow && !std::is_same<QT, __half>::value;
     static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
-    static constexpr int kBytes = FP8 ? 1 : 2, kRowBytes = DP * kBytes, kKS = DP / 16;
+    static constexpr int kRowBytes = DP * BITS / 8, kKS = DP / 16;
+    static constexpr int kBlocks = DP / 16;  // scales of a 4-bit row; a tile's keys' scales follow its values, then the values'
 
-    // Four elements of a query row for an 8-bit cache.  The products' index runs
+
+    // Four elements of a query row for a narrow cache.  The products' index runs
     // over head_dim in another order there: step ks of lane q4 holds the four
     // dimensions q4 * DP / 4 + 4 ks and on, so that a lane's keys are
     // consecutive bytes.
@@ -252,27 +297,97 @@ template <typename QT, bool FP8, int DP, int T, int HEADS> struct RowsBase {
         return in && d < dim ? *reinterpret_cast<const uint32_t*>(p + d) : 0u;
     }
     static __device__ __forceinline__ float row_scale(const KvPages& c, const KvAttention& a, int head) {
-        return a.scale * 1.4426950408889634f * (FP8 && c.k_scale ? c.k_scale[head] : 1.0f);
+        return a.scale * 1.4426950408889634f * (kNarrow && c.k_scale ? c.k_scale[head] : 1.0f);
     }
     // The values of 8-bit row `row` that this lane needs from vector v on: DP /
     // 8 bytes a row, in vectors of 16 (8 at DP = 64).
     static __device__ __forceinline__ uint4 values(uint32_t vt, int row, int g, int v) {
         if constexpr (DP == 64) {
-            const uint2 w = lds64(vt + row * kRowBytes + v_vec<FP8, DP>(row, g >> 1) * 16 + (g & 1) * 8);
+            const uint2 w = lds64(vt + v_at<BITS, DP>(row, g >> 1) + (g & 1) * 8);
             return make_uint4(w.x, w.y, 0u, 0u);
         } else {
-            return lds128(vt + row * kRowBytes + v_vec<FP8, DP>(row, g * (DP / 128) + v) * 16);
+            return lds128(vt + v_at<BITS, DP>(row, g * (DP / 128) + v));
         }
     }
     static constexpr int kValueVecs = DP == 64 ? 1 : DP / 128, kValueWords = DP == 64 ? 2 : 4;
+
+    // 4-bit rows: the words of keys that this lane needs of row `row` (8
+    // dimensions each, from q4 * DP / 4 on) times their blocks' scales, as the
+    // fp16 pairs of word i.
+    struct Keys4 {
+        uint4 w[DP == 256 ? 2 : 1];
+        uint32_t s[(DP + 64) / 128];  // pairs of blocks' scales as fp16
+        __device__ __forceinline__ void load(uint32_t kt, uint32_t scales, int row, int q4) {
+            if constexpr (DP == 64) {
+                const uint2 x = lds64(kt + k_at<BITS, DP>(row, q4 >> 1) + (q4 & 1) * 8);
+                w[0] = make_uint4(x.x, x.y, 0u, 0u);
+                s[0] = e4m3x2_f16x2(lds8(scales + row * kBlocks + q4));
+            } else {
+#pragma unroll
+                for (int i = 0; i < DP / 128; ++i) w[i] = lds128(kt + k_at<BITS, DP>(row, q4 * (DP / 128) + i));
+                if constexpr (DP == 128) {
+                    s[0] = e4m3x2_f16x2(lds16(scales + row * kBlocks + q4 * 2));
+                } else {
+                    const uint32_t x = lds32(scales + row * kBlocks + q4 * 4);
+                    s[0] = e4m3x2_f16x2(x);
+                    s[1] = e4m3x2_f16x2(x >> 16);
+                }
+            }
+        }
+        __device__ __forceinline__ void word(int i, uint32_t (&f)[4]) const {
+            const uint4& x = w[i / 4];
+            e2m1x8_f16(i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w, f);
+            const uint32_t scale = __byte_perm(s[i / 4], 0, i / 2 % 2 ? 0x3232 : 0x1010);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = mul_f16x2(f[k], scale);
+        }
+    };
+    static constexpr int kKeyWords = DP / 32;
+    // The values of 4-bit rows 2 q4, 2 q4 + 1 and 8 later (from `row` on): word i
+    // has dimensions g * DP / 8 + 8 i and on, as pairs of the first and of the last two.
+    struct Values4 {
+        uint4 w[4];
+        uint32_t lo[DP == 256 ? 2 : 1], hi[DP == 256 ? 2 : 1];  // pairs of the two rows' scales
+        __device__ __forceinline__ void load(uint32_t vt, uint32_t scales, int row, int q4, int g) {
+            uint32_t s[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = row + 2 * q4 + (k & 1) + (k >> 1) * 8;
+                if constexpr (DP == 64) {
+                    w[k].x = lds32(vt + v_at<BITS, DP>(r, g >> 2) + (g & 3) * 4);
+                    s[k] = lds8(scales + r * kBlocks + (g >> 1));
+                } else if constexpr (DP == 128) {
+                    const uint2 x = lds64(vt + v_at<BITS, DP>(r, g >> 1) + (g & 1) * 8);
+                    w[k].x = x.x;
+                    w[k].y = x.y;
+                    s[k] = lds8(scales + r * kBlocks + g);
+                } else {
+                    w[k] = lds128(vt + v_at<BITS, DP>(r, g));
+                    s[k] = lds16(scales + r * kBlocks + 2 * g);
+                }
+            }
+            lo[0] = e4m3x2_f16x2(__byte_perm(s[0], s[1], 0x0040));
+            hi[0] = e4m3x2_f16x2(__byte_perm(s[2], s[3], 0x0040));
+            if constexpr (DP == 256) {
+                lo[1] = e4m3x2_f16x2(__byte_perm(s[0], s[1], 0x0051));
+                hi[1] = e4m3x2_f16x2(__byte_perm(s[2], s[3], 0x0051));
+            }
+        }
+        __device__ __forceinline__ void word(int i, uint32_t (&a)[8], uint32_t (&b)[8]) const {
+            auto at = [&](int k) { return i == 0 ? w[k].x : i == 1 ? w[k].y : i == 2 ? w[k].z : w[k].w; };
+            pairs8(at(0), at(1), lo[i / 2 % (DP == 256 ? 2 : 1)], a);
+            pairs8(at(2), at(3), hi[i / 2 % (DP == 256 ? 2 : 1)], b);
+        }
+    };
+    static constexpr int kValueWords4 = DP / 64;
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8, DP, T, 16> {
-    using Base = RowsBase<QT, FP8, DP, T, 16>;
+template <typename QT, int BITS, int DP, int T> struct Rows16 : RowsBase<QT, BITS, DP, T, 16> {
+    using Base = RowsBase<QT, BITS, DP, T, 16>;
     using MT = typename Base::MT;
-    using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
+    using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo; using Base::kNarrow;
     using Query = QT;
     static constexpr int kNT = DP / 8, kPT = T / 8, kVectors = kNT;  // of four O's a lane
     static constexpr bool kQShared = DP == 256;  // Q's fragments in shared memory: registers are short
@@ -310,7 +425,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks) {
             uint32_t f[4];
-            if constexpr (FP8) {
+            if constexpr (kNarrow) {
                 const uint2 x = Base::query4(pa, ina, c.head_dim, q4, ks), y = Base::query4(pb, inb, c.head_dim, q4, ks);
                 f[0] = x.x; f[1] = y.x; f[2] = x.y; f[3] = y.y;
                 if constexpr (Base::kFit) {
@@ -354,7 +469,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t qs, const Tiles& t, int p0, float* scores, const Unit& u, int lane) {
         const int g = lane >> 2, q4 = lane & 3;
         float x[kPT][4] = {};
-        if constexpr (!FP8) {
+        if constexpr (!kNarrow) {
             const int row = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks) {
@@ -363,9 +478,26 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
 #pragma unroll
                 for (int h = 0; h < kPT / 2; ++h) {
                     uint32_t kf[4];
-                    ldmatrix4(kf, kt + (row + 16 * h) * kRowBytes + k_vec<FP8, DP>(row, 2 * ks + ((lane >> 3) & 1)) * 16);
+                    ldmatrix4(kf, kt + k_at<BITS, DP>(row + 16 * h, 2 * ks + ((lane >> 3) & 1)));
                     mma16816<MT>(x[2 * h], f, kf[0], kf[1]);
                     mma16816<MT>(x[2 * h + 1], f, kf[2], kf[3]);
+                }
+            }
+        } else if constexpr (BITS == 4) {
+            typename Base::Keys4 keys[kPT];
+#pragma unroll
+            for (int pt = 0; pt < kPT; ++pt) keys[pt].load(kt, vt + T * kRowBytes, g + 8 * pt, q4);
+#pragma unroll
+            for (int i = 0; i < Base::kKeyWords; ++i) {
+                uint32_t fa[4], fb[4];
+                query(qs, 2 * i, lane, fa);
+                query(qs, 2 * i + 1, lane, fb);
+#pragma unroll
+                for (int pt = 0; pt < kPT; ++pt) {
+                    uint32_t kf[4];
+                    keys[pt].word(i, kf);
+                    mma16816<MT>(x[pt], fa, kf[0], kf[1]);
+                    mma16816<MT>(x[pt], fb, kf[2], kf[3]);
                 }
             }
         } else {
@@ -373,7 +505,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
             for (int v = 0; v < DP / 64; ++v) {
                 uint4 kw[kPT];
 #pragma unroll
-                for (int pt = 0; pt < kPT; ++pt) kw[pt] = lds128(kt + (g + 8 * pt) * kRowBytes + k_vec<FP8, DP>(g, q4 * (DP / 64) + v) * 16);
+                for (int pt = 0; pt < kPT; ++pt) kw[pt] = lds128(kt + k_at<BITS, DP>(g + 8 * pt, q4 * (DP / 64) + v));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t f[4];
@@ -409,7 +541,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
             top1 = fmaxf(top1, fmaxf(x[pt][2], x[pt][3]));
             low = fminf(low, fminf(fminf(x[pt][0], x[pt][1]), fminf(x[pt][2], x[pt][3])));
         }
-        const bool some_inf = !FP8 && __any_sync(kFullMask, low == -INFINITY);
+        const bool some_inf = !kNarrow && __any_sync(kFullMask, low == -INFINITY);
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) {
             top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, s));
@@ -442,14 +574,14 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 l0 += a0 + a1;
                 l1 += b0 + b1;
                 if constexpr (kTwo) {
-                    split2<MT, !FP8>(a0, a1, ph[k * 2], pl[k * 2]);
-                    split2<MT, !FP8>(b0, b1, ph[k * 2 + 1], pl[k * 2 + 1]);
+                    split2<MT, !kNarrow>(a0, a1, ph[k * 2], pl[k * 2]);
+                    split2<MT, !kNarrow>(b0, b1, ph[k * 2 + 1], pl[k * 2 + 1]);
                 } else {
                     ph[k * 2] = pack2<MT>(a0, a1);
                     ph[k * 2 + 1] = pack2<MT>(b0, b1);
                 }
             }
-            if constexpr (!FP8) {
+            if constexpr (!kNarrow) {
                 if (some_inf) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -459,17 +591,30 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
                 }
             }
             const uint32_t vh = vt + 16 * h * kRowBytes;
-            if constexpr (!FP8) {
+            if constexpr (!kNarrow) {
                 const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
                 for (int nt = 0; nt < kNT; nt += 2) {
                     uint32_t vf[4];
-                    ldmatrix4_t(vf, vh + row * kRowBytes + v_vec<FP8, DP>(row, nt + (lane >> 4)) * 16);
+                    ldmatrix4_t(vf, vh + v_at<BITS, DP>(row, nt + (lane >> 4)));
                     mma16816<MT>(o[nt], ph, vf[0], vf[1]);
                     mma16816<MT>(o[nt + 1], ph, vf[2], vf[3]);
                     if constexpr (kTwo) {
                         mma16816<MT>(o[nt], pl, vf[0], vf[1]);
                         mma16816<MT>(o[nt + 1], pl, vf[2], vf[3]);
+                    }
+                }
+            } else if constexpr (BITS == 4) {
+                typename Base::Values4 values;
+                values.load(vt, vt + T * (kRowBytes + Base::kBlocks), 16 * h, q4, g);
+#pragma unroll
+                for (int i = 0; i < Base::kValueWords4; ++i) {
+                    uint32_t lo[8], hi[8];  // column n of product j is dimension n * DP / 8 + j
+                    values.word(i, lo, hi);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        mma16816<MT>(o[i * 8 + k], ph, lo[k], hi[k]);
+                        if constexpr (kTwo) mma16816<MT>(o[i * 8 + k], pl, lo[k], hi[k]);
                     }
                 }
             } else {
@@ -496,7 +641,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
 
     // Visits this lane's outputs as (row half, first dimension, two values).
     template <typename F> __device__ __forceinline__ void each_pair(int q4, F&& f) const {
-        if constexpr (!FP8) {
+        if constexpr (!kNarrow) {
 #pragma unroll
             for (int i = 0; i < kNT; ++i) {
                 f(0, i * 8 + 2 * q4, o[i][0], o[i][1]);
@@ -546,10 +691,10 @@ template <typename QT, bool FP8, int DP, int T> struct Rows16 : RowsBase<QT, FP8
     }
 };
 
-template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8, DP, T, 8> {
-    using Base = RowsBase<QT, FP8, DP, T, 8>;
+template <typename QT, int BITS, int DP, int T> struct Rows8 : RowsBase<QT, BITS, DP, T, 8> {
+    using Base = RowsBase<QT, BITS, DP, T, 8>;
     using MT = typename Base::MT;
-    using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo;
+    using Base::kKS; using Base::kRowBytes; using Base::kShift; using Base::kTwo; using Base::kNarrow;
     using Query = QT;
     static constexpr int kMT = DP / 16, kHB = T / 16, kVectors = kMT;  // of four O's a lane
     static constexpr int kQBytes = 0;
@@ -578,7 +723,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
         sl1 = __shfl_sync(kFullMask, sl, q4 * 8 + 4);
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks) {
-            if constexpr (FP8) {
+            if constexpr (kNarrow) {
                 const uint2 x = Base::query4(p, in, c.head_dim, q4, ks);
                 qf[ks][0] = Base::kFit ? scaled_f16x2<QT>(x.x, factor) : x.x;
                 qf[ks][1] = Base::kFit ? scaled_f16x2<QT>(x.y, factor) : x.y;
@@ -598,25 +743,42 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
     __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t, const Tiles& t, int p0, float* scores, const Unit& u, int lane) {
         const int g = lane >> 2, q4 = lane & 3;
         float x[kHB][4] = {}, z[kHB][4] = {};  // positions 16 h + g and 8 later; two sums, so that products wait less for each other
-        if constexpr (!FP8) {
+        if constexpr (!kNarrow) {
             const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
                 for (int h = 0; h < kHB; ++h) {
                     uint32_t kf[4];
-                    ldmatrix4(kf, kt + (row + 16 * h) * kRowBytes + k_vec<FP8, DP>(row, 2 * ks + (lane >> 4)) * 16);
+                    ldmatrix4(kf, kt + k_at<BITS, DP>(row + 16 * h, 2 * ks + (lane >> 4)));
                     mma16816<MT>(ks & 1 ? z[h] : x[h], kf, qf[ks][0], qf[ks][1]);
+                }
+        } else if constexpr (BITS == 4) {
+            typename Base::Keys4 ka[kHB], kb[kHB];
+#pragma unroll
+            for (int h = 0; h < kHB; ++h) {
+                ka[h].load(kt, vt + T * kRowBytes, 16 * h + g, q4);
+                kb[h].load(kt, vt + T * kRowBytes, 16 * h + g + 8, q4);
+            }
+#pragma unroll
+            for (int i = 0; i < Base::kKeyWords; ++i)
+#pragma unroll
+                for (int h = 0; h < kHB; ++h) {
+                    uint32_t fa[4], fb[4];
+                    ka[h].word(i, fa);
+                    kb[h].word(i, fb);
+                    const uint32_t k0[4] = {fa[0], fb[0], fa[1], fb[1]}, k1[4] = {fa[2], fb[2], fa[3], fb[3]};
+                    mma16816<MT>(x[h], k0, qf[2 * i][0], qf[2 * i][1]);
+                    mma16816<MT>(z[h], k1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
                 }
         } else {
 #pragma unroll
             for (int v = 0; v < DP / 64; ++v) {
-                const int vec = k_vec<FP8, DP>(g, q4 * (DP / 64) + v) * 16;
                 uint4 ka[kHB], kb[kHB];
 #pragma unroll
                 for (int h = 0; h < kHB; ++h) {
-                    ka[h] = lds128(kt + (16 * h + g) * kRowBytes + vec);
-                    kb[h] = lds128(kt + (16 * h + g + 8) * kRowBytes + vec);
+                    ka[h] = lds128(kt + k_at<BITS, DP>(16 * h + g, q4 * (DP / 64) + v));
+                    kb[h] = lds128(kt + k_at<BITS, DP>(16 * h + g + 8, q4 * (DP / 64) + v));
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -650,7 +812,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             top1 = fmaxf(top1, fmaxf(x[h][1], x[h][3]));
             low = fminf(low, fminf(fminf(x[h][0], x[h][1]), fminf(x[h][2], x[h][3])));
         }
-        const bool some_inf = !FP8 && __any_sync(kFullMask, low == -INFINITY);
+        const bool some_inf = !kNarrow && __any_sync(kFullMask, low == -INFINITY);
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
             top0 = fmaxf(top0, __shfl_xor_sync(kFullMask, top0, s));
@@ -680,9 +842,9 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             // 8 positions x 8 heads, then transposed: a lane's pair is two positions of head g
             uint32_t ph[2], pl[2];
             if constexpr (kTwo) {
-                split2<MT, !FP8>(a0, a1, ph[0], pl[0]);
-                split2<MT, !FP8>(b0, b1, ph[1], pl[1]);
-                if (!FP8 && some_inf) {
+                split2<MT, !kNarrow>(a0, a1, ph[0], pl[0]);
+                split2<MT, !kNarrow>(b0, b1, ph[1], pl[1]);
+                if (!kNarrow && some_inf) {
                     drop2(x[h][0], x[h][1], ph[0], pl[0]);
                     drop2(x[h][2], x[h][3], ph[1], pl[1]);
                 }
@@ -695,14 +857,28 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
             ph[0] = transpose8(ph[0]);
             ph[1] = transpose8(ph[1]);
             const uint32_t vh = vt + 16 * h * kRowBytes;
-            if constexpr (!FP8) {
+            if constexpr (!kNarrow) {
                 const int row = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) {
                     uint32_t vf[4];
-                    ldmatrix4_t(vf, vh + row * kRowBytes + v_vec<FP8, DP>(row, 2 * i + ((lane >> 3) & 1)) * 16);
+                    ldmatrix4_t(vf, vh + v_at<BITS, DP>(row, 2 * i + ((lane >> 3) & 1)));
                     mma16816<MT>(o[i], vf, ph[0], ph[1]);
                     if constexpr (kTwo) mma16816<MT>(o[i], vf, pl[0], pl[1]);
+                }
+            } else if constexpr (BITS == 4) {
+                typename Base::Values4 values;
+                values.load(vt, vt + T * (kRowBytes + Base::kBlocks), 16 * h, q4, g);
+#pragma unroll
+                for (int i = 0; i < Base::kValueWords4; ++i) {
+                    uint32_t lo[8], hi[8];
+                    values.word(i, lo, hi);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // row g of product j is dimension g * DP / 8 + 2 j, row g + 8 the next
+                        const uint32_t vf[4] = {lo[2 * k], lo[2 * k + 1], hi[2 * k], hi[2 * k + 1]};
+                        mma16816<MT>(o[i * 4 + k], vf, ph[0], ph[1]);
+                        if constexpr (kTwo) mma16816<MT>(o[i * 4 + k], vf, pl[0], pl[1]);
+                    }
                 }
             } else {
 #pragma unroll
@@ -746,7 +922,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
         const bool some0 = l0 != 0.0f, some1 = l1 != 0.0f;
         QT* out = static_cast<QT*>(a.out) + (int64_t)u.b * a.out_seq_stride + (int64_t)(u.head * u.group + u.row0 + 2 * q4) * a.out_head_stride;
         const bool in0 = u.row0 + 2 * q4 < u.group, in1 = u.row0 + 2 * q4 + 1 < u.group;
-        if constexpr (FP8) {
+        if constexpr (kNarrow) {
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
                 const int d = g * (DP / 8) + 2 * i;
@@ -776,7 +952,7 @@ template <typename QT, bool FP8, int DP, int T> struct Rows8 : RowsBase<QT, FP8,
         float *p0 = part + 2 * q4 * DP, *p1 = p0 + DP;
 #pragma unroll
         for (int i = 0; i < kMT; ++i) {
-            if constexpr (FP8) {
+            if constexpr (kNarrow) {
                 const int d = g * (DP / 8) + 2 * i;
                 if (in0) *reinterpret_cast<float2*>(p0 + d) = make_float2(o[i][0], o[i][2]);
                 if (in1) *reinterpret_cast<float2*>(p1 + d) = make_float2(o[i][1], o[i][3]);
