@@ -370,7 +370,8 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *              position 0 and slot -1, so that a fixed size serves every call; more
  *              counts than room are reported.
  * Lengths, counts and page numbers are checked on the device, as for the other
- * calls.  batch <= 8192 and batch * max_pages < 2^31.
+ * calls.  batch <= 8192, batch * max_pages < 2^31, and all counts' sum is below
+ * 2^31 (reported otherwise).
  */
 typedef struct ss_kv_free {
     int32_t *pages;

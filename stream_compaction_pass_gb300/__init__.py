@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libstreamscan.so")
@@ -77,20 +78,6 @@ class _KvAttention(ctypes.Structure):
 
 class _KvFree(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("capacity", ctypes.c_int64), ("state", ctypes.c_void_p)]
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
-
-
-class _Qk(ctypes.Structure):
-    _fields_ = [("type", ctypes.c_int), ("weight_type", ctypes.c_int), ("head_dim", ctypes.c_int32), ("q_heads", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("eps", ctypes.c_float), ("tokens", ctypes.c_int64), ("q", _Rows), ("k", _Rows),
-                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rope", _Rope)]
 
 
 _lib = None
@@ -759,66 +746,75 @@ class Rope:
         self.device = x.get_device()
         self.turns = (x * 2.0 ** 64).to(torch.int64)  # modulo one turn; exact
         self.rotary_dim, self.interleaved = 2 * x.numel(), bool(interleaved)
-        self._c = _Rope(self.turns.data_ptr(), self.rotary_dim, int(self.interleaved))
-
-    def get_device(self):
-        return self.device
+        self._c = self.turns.data_ptr(), self.rotary_dim, int(self.interleaved)
 
 
+# ss_qk and ss_rows as bytes, which cost less to make than ctypes structures
+_QK = struct.Struct("@iiiiifqPqqPqqPPPPii")
+_ROWS = struct.Struct("@Pqq")
+_NO_ROWS = (0, 0, 0)
 _row_kinds = {}  # torch dtype -> element type, of rows and weights
 
 
-def _row_kind(name: str, t) -> int:
+def _row_kind(name: str, dtype) -> int:
     if not _row_kinds:
         import torch
         _row_kinds.update({torch.bfloat16: SS_BF16, torch.float16: SS_F16, torch.float32: SS_ELEM_F32})
-    kind = _row_kinds.get(t.dtype)
+    kind = _row_kinds.get(dtype)
     if kind is None:
-        raise TypeError(f"{name} is {t.dtype}: bfloat16, float16 and float32 are taken")
+        raise TypeError(f"{name} is {dtype}: bfloat16, float16 and float32 are taken")
     return kind
 
 
-def _rows(name: str, t, like, device: int) -> _Rows:
-    """A (tokens, heads, head_dim) tensor of like's shape and type; None: no heads."""
-    if t is None:
-        if like is not None:
-            raise ValueError(f"{name} is missing")
-        return _Rows()
-    if like is None or t.shape != like.shape or t.dtype != like.dtype or t.stride(2) != 1:
-        raise ValueError(f"{name} must have its input's shape and type, and a contiguous last dimension")
+def _rows(name: str, t, shape, dtype, device: int):
+    """Address and strides of a (tokens, heads, head_dim) tensor; shape None: no heads."""
+    if t is None or shape is None:
+        if (t is None) != (shape is None):
+            raise ValueError(f"{name} is missing" if t is None else f"{name} has no input")
+        return _NO_ROWS
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {str(dtype)[6:]} of shape {tuple(shape)}, got {str(t.dtype)[6:]} {tuple(t.shape)}")
+    token, head, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
     if t.get_device() != device:
         raise _elsewhere(name, t, device)
-    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return t.data_ptr(), token, head
+
+
+def _weight(name: str, t, dim: int, dtype, device: int) -> int:
+    if t is None:
+        return 0
+    if t.dim() != 1 or t.shape[0] != dim or t.dtype is not dtype or (dim > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous, of shape {(dim,)}, and of the other weight's type")
+    if t.get_device() != device:
+        raise _elsewhere(name, t, device)
+    return t.data_ptr()
 
 
 def _qk(q, k, q_weight, k_weight, rope, positions, eps: float):
-    """The description of q and k (either may be None), and their device."""
-    one = q if q is not None else k
+    """The description of q and k (either may be None), their shapes, type and device."""
+    one = k if q is None else q
     if one is None:
         raise ValueError("q and k are both None")
-    if one.dim() != 3 or (q is not None and k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype)):
-        raise ValueError("q and k must be (tokens, heads, head_dim), of one type and head_dim")
+    if one.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be (tokens, heads, head_dim)")
     tokens, _, dim = one.shape
-    device = one.get_device()
+    dtype, device = one.dtype, one.get_device()
+    q_shape, k_shape = None if q is None else q.shape, None if k is None else k.shape
+    if k is not None and (k_shape[0] != tokens or k_shape[2] != dim):
+        raise ValueError(f"q and k must be of the same tokens and head_dim, got {tuple(one.shape)} and {tuple(k_shape)}")
     if device < 0:
         raise ValueError("q and k are not on a GPU")
     if rope.device != device:
         raise _elsewhere("rope", rope.turns, device)
-    weight = q_weight if q_weight is not None else k_weight
-    w = []
-    for name, x, of in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
-        if x is None or of is None:
-            w.append(0)
-            continue
-        if x.shape != (dim,) or x.dtype != weight.dtype or not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, of shape {(dim,)}, and of the other weight's type")
-        if x.get_device() != device:
-            raise _elsewhere(name, x, device)
-        w.append(x.data_ptr())
-    c = _Qk(_row_kind("q" if q is not None else "k", one), SS_ELEM_F32 if weight is None else _row_kind("q_weight", weight), dim, 0 if q is None else q.shape[1],
-            0 if k is None else k.shape[1], eps, tokens, _rows("q", q, q, device), _rows("k", k, k, device), w[0], w[1],
-            _like("positions", positions, (tokens,), "int32", device), rope._c)
-    return c, device
+    weight = k_weight if q_weight is None else q_weight
+    weight_type = None if weight is None else weight.dtype
+    c = _QK.pack(_row_kind("q" if q is not None else "k", dtype), SS_ELEM_F32 if weight is None else _row_kind("q_weight", weight_type), dim,
+                 0 if q is None else q_shape[1], 0 if k is None else k_shape[1], eps, tokens, *_rows("q", q, q_shape, dtype, device),
+                 *_rows("k", k, k_shape, dtype, device), _weight("q_weight", q_weight, dim, weight_type, device), _weight("k_weight", k_weight, dim, weight_type, device),
+                 _like("positions", positions, (tokens,), "int32", device), *rope._c)
+    return c, q_shape, k_shape, dtype, device
 
 
 def ss_qk_norm_rope(q, k, q_weight, k_weight, rope: Rope, positions, q_out, k_out, eps: float = 1e-6, stream=None) -> None:
@@ -826,9 +822,8 @@ def ss_qk_norm_rope(q, k, q_weight, k_weight, rope: Rope, positions, q_out, k_ou
     head_dim), times their weights (head_dim,) or None, rotated by positions, int32
     (tokens,), into q_out and k_out (which may be q and k).  Either of q and k may
     be None."""
-    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
-    yq, yk = _rows("q_out", q_out, q, device), _rows("k_out", k_out, k, device)
-    _check(lib().ss_qk_norm_rope(ctypes.addressof(c), ctypes.addressof(yq), ctypes.addressof(yk),
+    c, qs, ks, dtype, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    _check(lib().ss_qk_norm_rope(c, _ROWS.pack(*_rows("q_out", q_out, qs, dtype, device)), _ROWS.pack(*_rows("k_out", k_out, ks, dtype, device)),
                                  _current_stream(device) if stream is None else _stream(stream)), "ss_qk_norm_rope")
 
 
@@ -836,21 +831,22 @@ def ss_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, rope: Rop
                              eps: float = 1e-6, stream=None) -> None:
     """The gradients of ss_qk_norm_rope from those of its outputs: dq and dk (which
     may be dq_out and dk_out), and float32 dq_weight and dk_weight (head_dim,)."""
-    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
-    g = [_rows(name, x, like, device) for name, x, like in (("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k))]
-    w = _like("dq_weight", dq_weight, (c.head_dim,), "float32", device), _like("dk_weight", dk_weight, (c.head_dim,), "float32", device)
-    _check(lib().ss_qk_norm_rope_backward(ctypes.addressof(c), *(ctypes.addressof(x) for x in g), *w,
+    c, qs, ks, dtype, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    dim = (ks if qs is None else qs)[2:]
+    _check(lib().ss_qk_norm_rope_backward(c, _ROWS.pack(*_rows("dq_out", dq_out, qs, dtype, device)), _ROWS.pack(*_rows("dk_out", dk_out, ks, dtype, device)),
+                                          _ROWS.pack(*_rows("dq", dq, qs, dtype, device)), _ROWS.pack(*_rows("dk", dk, ks, dtype, device)),
+                                          _like("dq_weight", dq_weight, dim, "float32", device), _like("dk_weight", dk_weight, dim, "float32", device),
                                           _current_stream(device) if stream is None else _stream(stream)), "ss_qk_norm_rope_backward")
 
 
 def ss_kv_append_rope(cache: KVPages, slots, q, k, v, q_weight, k_weight, rope: Rope, positions, q_out, eps: float = 1e-6, stream=None) -> None:
     """ss_qk_norm_rope whose k rows go to the cache, with v's as they are, at slots,
-    int64 (tokens,), as ss_kv_assign gives them (-1: nowhere)."""
+    int64 (tokens,), as ss_kv_assign gives them (-1: nowhere).  q may be None."""
     if k is None:
         raise ValueError("k is missing")
-    c, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
+    c, qs, ks, dtype, device = _qk(q, k, q_weight, k_weight, rope, positions, eps)
     if cache.device != device:
-        _refuse(cache.device, k=k)
-    rows, yq = _rows("v", v, k, device), _rows("q_out", q_out, q, device)
-    _check(lib().ss_kv_append_rope(cache._ref, _like("slots", slots, (c.tokens,), "int64", device), ctypes.addressof(c), ctypes.addressof(rows),
-                                   ctypes.addressof(yq), _current_stream(device) if stream is None else _stream(stream)), "ss_kv_append_rope")
+        raise _elsewhere("cache.k", cache.k, device)
+    _check(lib().ss_kv_append_rope(cache._ref, _like("slots", slots, ks[:1], "int64", device), c, _ROWS.pack(*_rows("v", v, ks, dtype, device)),
+                                   _ROWS.pack(*_rows("q_out", q_out, qs, dtype, device)),
+                                   _current_stream(device) if stream is None else _stream(stream)), "ss_kv_append_rope")

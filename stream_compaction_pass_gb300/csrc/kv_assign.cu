@@ -48,25 +48,7 @@ struct Sums {  // exclusive sums before a sequence
     int take, back, entries;
 };
 
-// One sequence.
-struct Seq {
-    int old, count;        // length before (0 where it is restarted), new tokens
-    int had, held, need;   // pages that it had, that it keeps, and that it needs more
-    bool fits;             // its new length is within the limit
-    __device__ __forceinline__ Seq(const KvTable& t, const Args& a, int b, uint32_t* status) {
-        const int len = kv_len(t, b, status);
-        const bool again = a.restart && a.restart[b];
-        old = again ? 0 : len;
-        count = a.counts ? a.counts[b] : 1;
-        had = pages(a, len);
-        held = again ? 0 : had;
-        fits = count >= 0 && (count == 0 || count <= a.limit - old);
-        if (!fits) record_error(status, kErrKvTable, (uint32_t)b);
-        count = max(count, 0);
-        need = fits ? pages(a, old + count) - held : 0;
-    }
-    static __device__ __forceinline__ int pages(const Args& a, int n) { return n == 0 ? 0 : a.page.div(n - 1) + 1; }
-};
+__device__ __forceinline__ int pages_of(const Args& a, int n) { return n == 0 ? 0 : a.page.div(n - 1) + 1; }
 
 __device__ __forceinline__ int find(const int* x, int n, int at) {  // the last i < n with x[i] <= at
     int lo = 0, hi = n;
@@ -82,8 +64,10 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
     __shared__ Sums s_warp[kWarps];
     __shared__ int s_taken;
     const int n = t.batch, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // Sums before sequence i: tokens (at most 2^31 - 1), pages taken, given back, table entries.
-    int *tokens = s_sums, *take = tokens + n + 1, *back = take + n + 1, *entries = back + n + 1;
+    // Sums before sequence i: tokens (at most 2^31 - 1), pages taken, given back, table
+    // entries; and its length before (0 where it is restarted), ~ of it where its new
+    // length is not allowed.
+    int *tokens = s_sums, *take = tokens + n + 1, *back = take + n + 1, *entries = back + n + 1, *before_of = entries + n + 1;
     begin_dependent();
 
     const int head_in = a.state[0], free_in = a.state[1];
@@ -97,12 +81,16 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
         const int i = i0 + tid;
         Sums mine{0, 0, 0, 0};
         if (i < n) {
-            const Seq q(t, a, i, status);
-            const int back_of = q.held == 0 ? q.had : 0;  // of a restarted sequence: all
-            mine.tokens = q.count;
-            mine.take = q.need;
-            mine.back = a.restart && a.restart[i] ? back_of : 0;
-            mine.entries = max(mine.back, q.held + q.need) - (a.copy ? 0 : q.held);
+            const int len = kv_len(t, i, status), asked = a.counts ? a.counts[i] : 1;
+            const bool again = a.restart && a.restart[i];
+            const int old = again ? 0 : len, had = pages_of(a, len), held = again ? 0 : had, count = max(asked, 0);
+            const bool fits = asked >= 0 && (count == 0 || count <= a.limit - old);
+            if (!fits) record_error(status, kErrKvTable, (uint32_t)i);
+            before_of[i] = fits ? old : ~old;
+            mine.tokens = count;
+            mine.take = fits ? pages_of(a, old + count) - held : 0;
+            mine.back = again ? had : 0;
+            mine.entries = max(mine.back, held + mine.take) - (a.copy ? 0 : held);
         }
         Sums x;
         x.tokens = warp_inclusive_scan<int64_t>(mine.tokens, lane);
@@ -135,9 +123,23 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
         __syncthreads();
     }
     if (tid < 4) s_sums[tid * (n + 1)] = 0;
+    if (run.tokens > INT_MAX && tid == 0) record_error(status, kErrKvTable, (uint32_t)(n - 1));
     __syncthreads();
 
-    auto served = [&](const Seq& q, int b) { return q.fits && (q.need == 0 || take[b + 1] <= free); };
+    // A sequence, from the sums.
+    struct Seq {
+        int old, held, need;
+        bool served;
+    };
+    auto sequence = [&](int b) {
+        const int x = before_of[b], first = take[b], last = take[b + 1];
+        Seq q;
+        q.old = x < 0 ? ~x : x;
+        q.held = pages_of(a, q.old);
+        q.need = last - first;
+        q.served = x >= 0 && (q.need == 0 || last <= free);
+        return q;
+    };
     auto ring_at = [&](int i) {  // place i of the ring, counted from its head
         const int64_t x = (int64_t)head + i;
         return (int)(x < a.capacity ? x : x - a.capacity);
@@ -154,9 +156,9 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
         const int all = entries[n];
         for (int64_t e = me; e < all; e += threads) {
             const int b = find(entries, n, (int)e);
-            const Seq q(t, a, b, nullptr);
+            const Seq q = sequence(b);
             const int col = (int)e - entries[b] + (a.copy ? 0 : q.held);
-            const int fresh = q.held + q.need, mine = served(q, b) ? fresh : q.held;
+            const int mine = q.served ? q.held + q.need : q.held;
             const int had = back[b + 1] - back[b];
             int page = 0;
             if (col < had || (a.copy && col < q.held)) page = t.pages[(int64_t)b * t.row_stride + col];
@@ -194,8 +196,8 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
                     }
                     first = tokens[b];
                     end = tokens[b + 1];
-                    const Seq q(t, a, b, nullptr);
-                    ok = served(q, b);
+                    const Seq q = sequence(b);
+                    ok = q.served;
                     old = q.old;
                     held = q.held;
                     index = -1;
@@ -234,10 +236,9 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + tid;
         if (i >= n) continue;
-        const Seq q(t, a, i, nullptr);
-        const bool ok = served(q, i);
-        if (ok && q.need > 0) atomicMax(&s_taken, take[i + 1]);
-        a.lens[i] = ok ? q.old + q.count : q.old;  // after Seq has read it, by the same thread
+        const Seq q = sequence(i);
+        if (q.served && q.need > 0) atomicMax(&s_taken, take[i + 1]);
+        a.lens[i] = q.served ? q.old + tokens[i + 1] - tokens[i] : q.old;
     }
     if (a.offsets)
         for (int i = tid; i <= n; i += kThreads) a.offsets[i] = tokens[i];
@@ -252,7 +253,7 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
 }  // namespace
 
 cudaError_t launch_kv_assign(const KvTable& t, const KvAssign& a, bool in_place, int sms, uint32_t* status, cudaStream_t s) {
-    const size_t smem = (size_t)4 * (t.batch + 1) * 4, most = (size_t)4 * (kKvMaxAssign + 1) * 4;
+    const size_t smem = (size_t)5 * (t.batch + 1) * 4, most = (size_t)5 * (kKvMaxAssign + 1) * 4;
     // A thread's four tokens, or its entries: those of the table where it is
     // copied, and else about as many as there are pages in the new tokens.
     const int64_t entries = a.copy ? (int64_t)t.batch * t.max_pages : t.batch;

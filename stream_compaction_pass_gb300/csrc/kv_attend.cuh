@@ -41,7 +41,7 @@ namespace {
 
 // Sequences per launch: their tile counts' prefix sums are in shared memory,
 // beside a ring that leaves little of it at head_dim 256.
-template <int DP> constexpr int kMaxBatch = DP == 256 ? 512 : 4096;
+template <int BITS, int DP> constexpr int kMaxBatch = DP == 256 ? 512 : BITS == 4 ? 2048 : 4096;
 
 namespace cg = cooperative_groups;
 
@@ -69,6 +69,7 @@ constexpr SmallLimits small_limits(bool slow, bool weights) {
     return slow ? (weights ? SmallLimits{5, 8} : SmallLimits{12, 24}) : weights ? SmallLimits{12, 12} : SmallLimits{24, 24};
 }
 constexpr int kSmallTiles = 24;  // the largest of them
+constexpr int small_tiles(int limit, int tile) { return tile == 64 ? limit / 2 : limit; }  // they are of tiles of 16 or 32
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
@@ -167,8 +168,13 @@ struct Cursor {
 // DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros in shared
 // memory).  T positions per tile (16 or 32), NW warps of a CTA, S stages of
 // each warp's ring.  Rows: Rows8 or Rows16.
+template <typename Rows, int BITS, int DP, int T, int NW, int S, bool SMALL>
+__global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status);
 template <typename Rows, int BITS, int DP, int T, int NW, int S>
 struct Shape {
+    using RowsOf = Rows;
+    static constexpr int kTile = T, kWarps = NW;
+    static constexpr auto small_kernel() { return k_kv_attend<Rows, BITS, DP, T, NW, S, true>; }
     static constexpr int kUnit = BITS == 16 ? 2 : 1;  // bytes that strides count in
     static constexpr int kRowBytes = DP * BITS / 8;
     static constexpr int kVecs = kRowBytes / 16;
@@ -176,7 +182,7 @@ struct Shape {
     static constexpr int kScaleBytes = BITS == 4 ? DP / 16 : 0;  // of a row
     static constexpr int kStage = 2 * (kTileBytes + T * kScaleBytes);
     static constexpr int kRing = S * kStage;  // of a warp
-    static constexpr size_t kSmem = (size_t)NW * (kRing + Rows::kQBytes) + (kMaxBatch<DP> + 1) * 4;
+    static constexpr size_t kSmem = (size_t)NW * (kRing + Rows::kQBytes) + (kMaxBatch<BITS, DP> + 1) * 4;
 };
 
 // SMALL: a call of few rows, a cluster of CTAs each.  The warps of a cluster
@@ -186,7 +192,7 @@ struct Shape {
 template <typename Rows, int BITS, int DP, int T, int NW, int S, bool SMALL>
 __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
     using Sh = Shape<Rows, BITS, DP, T, NW, S>;
-    constexpr int kShift2 = T == 16 ? 4 : 5;
+    constexpr int kShift2 = T == 16 ? 4 : T == 32 ? 5 : 6;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     begin_dependent();
@@ -264,31 +270,130 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
     uint64_t policy;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     Cursor ld = cur;
-    int ld_page = 0, ld_slot = 0;  // page and slot of this lane's row (lane % T) of the next tile, fetched one tile ahead
+    constexpr int kPerLane = T > 32 ? T / 32 : 1;  // rows of a tile that a lane looks up
+    // 4-bit rows that lie side by side in pages of T positions and more, or a half or
+    // a quarter of T: a whole tile is 1, 2 or 4 stretches, whose copies need an
+    // address each and constant offsets (50 instructions a tile for 200; a bulk copy
+    // for every stretch is no less, since its operands are of the whole warp).
+    constexpr bool kDense = BITS == 4 && !SMALL;  // (small calls: more code to fetch than it saves)
+    [[maybe_unused]] int stretches = 0;  // 0: not so
+    [[maybe_unused]] bool ld_dense = false;
+    [[maybe_unused]] int ld_before = 0;
+    [[maybe_unused]] int ld_stretch[4] = {};
+    if constexpr (kDense) {
+        const int n = c.page_size % T == 0 ? 1 : T % c.page_size == 0 ? T / c.page_size : 0;
+        if (c.slot_stride == Sh::kRowBytes && c.page_stride < 1ll << 32 && c.head_stride < 1ll << 32 && (int64_t)c.page_size * c.kv_heads < 1 << 27 &&
+            (n == 1 || n == 2 || n == 4) && n <= T / kRows)
+            stretches = n;
+    }
+    // Pages and slots of this lane's rows (lane % T, and 32 later) of the next tile, or
+    // the pages of its stretches, fetched one tile ahead.
+    int ld_page[kPerLane] = {}, ld_slot[kPerLane] = {};
     auto fetch_page = [&]() {
-        const int p = (ld.t.tile(ld.j) << kShift2) + (lane & (T - 1));
-        const int index = sc.page.div(p);
-        ld_slot = p - index * c.page_size;
-        ld_page = ld.b < t.batch && ld.t.visible(p) ? t.pages[(int64_t)ld.b * t.row_stride + index] : -1;
+        const int p0 = ld.t.tile(ld.j) << kShift2;
+        if constexpr (kDense) {
+            ld_dense = stretches && ld.b < t.batch && ld.t.whole(p0, T);
+            if (ld_dense) {
+                const int first = sc.page.div(p0);
+                ld_before = p0 - first * c.page_size;  // 0 where there are more stretches
+                const int32_t* pages = t.pages + (int64_t)ld.b * t.row_stride + first;
+                ld_stretch[0] = pages[0];
+                if (stretches > 1) ld_stretch[1] = pages[1];
+                if (stretches > 2) {
+                    ld_stretch[2] = pages[2];
+                    ld_stretch[3] = pages[3];
+                }
+                return;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+            const int p = p0 + (lane & (T - 1)) + 32 * r;
+            const int index = sc.page.div(p);
+            ld_slot[r] = p - index * c.page_size;
+            ld_page[r] = ld.b < t.batch && ld.t.visible(p) ? t.pages[(int64_t)ld.b * t.row_stride + index] : -1;
+        }
+    };
+    // The copies of a whole tile of N stretches.
+    [[maybe_unused]] auto issue_dense = [&](auto count, uint32_t dst) {
+        constexpr int N = decltype(count)::value, kSlots = T / N, kBytes = Sh::kScaleBytes;
+        uint32_t page[N];
+        bool good = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const bool in = ld_stretch[k] >= 0 && ld_stretch[k] < c.num_pages;
+            good = good && in;
+            page[k] = in ? ld_stretch[k] : 0;  // an error: any page will do
+        }
+        if (!good) record_error(status, kErrKvTable, (uint32_t)(t.first + ld.b));
+        const uint32_t page_step = (uint32_t)c.page_stride, head_step = (uint32_t)c.head_stride;
+        const uint64_t in_head = (uint64_t)(uint32_t)ld.head * head_step + (uint32_t)(lane * 16) + (uint64_t)(uint32_t)(N == 1 ? ld_before : 0) * Sh::kRowBytes;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint64_t at = in_head + (uint64_t)page[k] * page_step;
+            const char *pk = c.k + at, *pv = c.v + at;
+#pragma unroll
+            for (int i = 0; i < kSlots / kRows; ++i) {
+                const uint32_t to = dst + k * kSlots * Sh::kRowBytes + i * 512 + lane * 16;
+                cp_async16(to, pk + i * 512, 16, policy);
+                cp_async16(to + Sh::kTileBytes, pv + i * 512, 16, policy);
+            }
+        }
+        const uint32_t block_step = (uint32_t)(c.page_size * c.kv_heads);
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+            const int row = (lane & (T - 1)) + 32 * r, k = row / kSlots;
+            uint32_t p = page[0];
+#pragma unroll
+            for (int e = 1; e < N; ++e) p = k == e ? page[e] : p;
+            const uint32_t slot = (uint32_t)(ld.head * c.page_size + (N == 1 ? ld_before + row : row % kSlots));
+            const uint64_t at = ((uint64_t)p * block_step + slot) * kBytes;
+            const uint32_t to = dst + 2 * Sh::kTileBytes + row * kBytes;
+            if (T >= 32 || lane < T) cp_async_small<kBytes>(to, c.k_block + at, kBytes, policy);
+            if (T >= 32 || lane >= T) cp_async_small<kBytes>(to + T * kBytes, c.v_block + at, kBytes, policy);
+        }
     };
     auto issue = [&](int stage) {
         const uint32_t dst = ring_a + stage * Sh::kStage;
-        const int p0 = ld.t.tile(ld.j) << kShift2;
-        const bool good = ld_page >= 0 && ld_page < c.num_pages;
-        const int64_t off = ld_page * page_bytes + ld.head * head_bytes + ld_slot * slot_bytes;
-        if constexpr (BITS == 4) {
-            // the scales of this lane's row: a lane a row, of k and then of v where a tile has 16
-            constexpr int kBytes = Sh::kScaleBytes;
-            const bool ok = good && ld.t.visible(p0 + (lane & (T - 1)));
-            const int64_t at = ok ? (((int64_t)ld_page * c.kv_heads + ld.head) * c.page_size + ld_slot) * kBytes : 0;
-            const uint32_t to = dst + 2 * Sh::kTileBytes + (lane & (T - 1)) * kBytes;
-            if (T == 32 || lane < T) cp_async_small<kBytes>(to, c.k_block + at, ok ? kBytes : 0, policy);
-            if (T == 32 || lane >= T) cp_async_small<kBytes>(to + T * kBytes, c.v_block + at, ok ? kBytes : 0, policy);
+        if constexpr (kDense) {
+            if (ld_dense) {
+                if (stretches == 1) issue_dense(std::integral_constant<int, 1>(), dst);
+                if constexpr (T / kRows >= 2) {
+                    if (stretches == 2) issue_dense(std::integral_constant<int, 2>(), dst);
+                }
+                if constexpr (T / kRows >= 4) {
+                    if (stretches == 4) issue_dense(std::integral_constant<int, 4>(), dst);
+                }
+                return;
+            }
         }
-        if (paged_whole && ld.t.whole(p0, T) && __all_sync(kFullMask, good)) {
+        const int p0 = ld.t.tile(ld.j) << kShift2;
+        bool good[kPerLane];
+        int64_t off[kPerLane];
+        bool all_good = true;
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+            good[r] = ld_page[r] >= 0 && ld_page[r] < c.num_pages;
+            all_good = all_good && good[r];
+            off[r] = ld_page[r] * page_bytes + ld.head * head_bytes + ld_slot[r] * slot_bytes;
+        }
+        if constexpr (BITS == 4) {
+            // the scales of this lane's rows: a lane a row, of k and then of v where a tile has 16
+            constexpr int kBytes = Sh::kScaleBytes;
+#pragma unroll
+            for (int r = 0; r < kPerLane; ++r) {
+                const int row = (lane & (T - 1)) + 32 * r;
+                const bool ok = good[r] && ld.t.visible(p0 + row);
+                const int64_t at = ok ? (((int64_t)ld_page[r] * c.kv_heads + ld.head) * c.page_size + ld_slot[r]) * kBytes : 0;
+                const uint32_t to = dst + 2 * Sh::kTileBytes + row * kBytes;
+                if (T >= 32 || lane < T) cp_async_small<kBytes>(to, c.k_block + at, ok ? kBytes : 0, policy);
+                if (T >= 32 || lane >= T) cp_async_small<kBytes>(to + T * kBytes, c.v_block + at, ok ? kBytes : 0, policy);
+            }
+        }
+        if (paged_whole && ld.t.whole(p0, T) && __all_sync(kFullMask, all_good)) {
             // every row is there, one slot after the other from row 0's
             const char *pk = c.k + cp_at, *pv = c.v + cp_at;
-            const int64_t base = __shfl_sync(kFullMask, off, 0);
+            const int64_t base = __shfl_sync(kFullMask, off[0], 0);
             pk += base;
             pv += base;
             const int size = in_row ? 16 : 0;
@@ -307,13 +412,17 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
             }
             return;
         }
-        const bool see = ld.t.visible(p0 + (lane & (T - 1)));
-        if (see && !good) record_error(status, kErrKvTable, (uint32_t)(t.first + ld.b));
-        const int64_t mine = see && good ? off : -1;
+        int64_t mine[kPerLane];
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+            const bool see = ld.t.visible(p0 + (lane & (T - 1)) + 32 * r);
+            if (see && !good[r]) record_error(status, kErrKvTable, (uint32_t)(t.first + ld.b));
+            mine[r] = see && good[r] ? off[r] : -1;
+        }
 #pragma unroll
         for (int i = 0; i < T / kRows; ++i) {
             const int row = cp_row + i * kRows;
-            const int64_t o = __shfl_sync(kFullMask, mine, row);
+            const int64_t o = __shfl_sync(kFullMask, mine[i * kRows / 32], row);
             const bool ok = o >= 0 && in_row;  // otherwise the vector is filled with zeros
             const int64_t at = ok ? o + cp_v * 16 : 0;
             cp_async16(dst + k_at<BITS, DP>(row, cp_v), c.k + at, ok ? 16 : 0, policy);
@@ -630,7 +739,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
 // only visible positions change.
 template <int V>
 __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
-    __shared__ int s_pre[kMaxBatch<0> + 1];
+    __shared__ int s_pre[kMaxBatch<16, 0> + 1];
     begin_dependent();
     for (int i = threadIdx.x; i <= t.batch; i += kWeightThreads) s_pre[i] = sc.pre_all[i];
     __syncthreads();
@@ -736,7 +845,7 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     const size_t most = seqs * tiles * p.sc.units, scores = seq_logits * seqs;
     p.grid = most < (size_t)sms ? (most < 1 ? 1 : (int)most) : sms;
     p.sc.workers = p.grid * warps;
-    p.sc.shift = tile == 16 ? 4 : 5;
+    p.sc.shift = tile == 16 ? 4 : tile == 32 ? 5 : 6;
     p.sc.page = FastDiv(c.page_size);
     p.at_lse2 = 2 * round256((seqs + 1) * 4);
     p.at_ml = p.at_lse2 + round256(seqs * a.q_heads * 4);
@@ -773,8 +882,8 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
         if (units <= most) break;
     }
     const SmallLimits limits = small_limits(slow, a.weight_out != nullptr);
-    if (ranks == 0 || tiles > limits.many * ranks * warps) return cudaSuccess;
-    if (tiles > limits.few * ranks * warps) {
+    if (ranks == 0 || tiles > small_tiles(limits.many, tile) * ranks * warps) return cudaSuccess;
+    if (tiles > small_tiles(limits.few, tile) * ranks * warps) {
         KernelSetup su;
         const cudaError_t e = kernel_setup(kern, warps * 32, smem, &su);
         if (e != cudaSuccess || units * ranks * 4 < (int64_t)su.sms * 3) return e;
@@ -791,16 +900,18 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
     return cudaSuccess;
 }
 
-template <typename QT, typename Rows, int BITS, int DP, int T, int NW, int S>
+// Small: the tile and the warps of the form of one launch, where they differ.
+template <typename QT, typename Rows, int BITS, int DP, int T, int NW, int S, typename Small = Shape<Rows, BITS, DP, T, NW, S>>
 cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
     auto* kern = k_kv_attend<Rows, BITS, DP, T, NW, S, false>;
     constexpr size_t smem = Shape<Rows, BITS, DP, T, NW, S>::kSmem;
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
-    auto* one = k_kv_attend<Rows, BITS, DP, T, NW, S, true>;
-    static_assert(kSmallTiles <= Rows::kChain, "a small call sets nothing aside");
+    auto* one = Small::small_kernel();
+    static_assert(Small::kSmem <= 227 * 1024, "the ring does not fit in shared memory");
+    static_assert(small_tiles(kSmallTiles, Small::kTile) <= Small::RowsOf::kChain, "a small call sets nothing aside");
     constexpr bool slow = BITS < 16 || Rows::kHeads == 16 || DP == 256;
     SmallPlan small;
-    cudaError_t e = small_plan(reinterpret_cast<const void*>(one), smem, c, t, a, Rows::kHeads, NW, T, slow, &small);
+    cudaError_t e = small_plan(reinterpret_cast<const void*>(one), Small::kSmem, c, t, a, Rows::kHeads, Small::kWarps, Small::kTile, slow, &small);
     if (e != cudaSuccess) return e;
     KernelSetup su;
     if (small.ranks == 0 || small.reserve) {
@@ -809,15 +920,15 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     }
     if (small.ranks > 0) {
         size_t bytes = a.weight_out ? small.bytes : 0;  // 0 too where no sequence can have a position
-        if (small.reserve) bytes = std::max(bytes, make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms).bytes);
+        if (small.reserve) bytes = std::max(bytes, make_plan(c, t, a, kMaxBatch<BITS, DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms).bytes);
         if (bytes > 0) {
             void* base = mem.get(mem.owner, bytes);
             if (base == nullptr) return cudaErrorMemoryAllocation;
             if (a.weight_out) small.sc.logits = static_cast<float*>(base);
         }
-        return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, NW * 32, smem, small.ranks, s, c, t, a, small.sc, status);
+        return launch_dependent(one, (size_t)t.batch * c.kv_heads * small.ranks, Small::kWarps * 32, Small::kSmem, small.ranks, s, c, t, a, small.sc, status);
     }
-    Plan p = make_plan(c, t, a, kMaxBatch<DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms);
+    Plan p = make_plan(c, t, a, kMaxBatch<BITS, DP>, Rows::kHeads, NW, DP, T, sizeof(Aside<Rows>), su.sms);
     char* base = static_cast<char*>(mem.get(mem.owner, p.bytes));
     if (base == nullptr) return cudaErrorMemoryAllocation;
     p.sc.pre = reinterpret_cast<int*>(base);

@@ -6,14 +6,27 @@ namespace ss {
 
 namespace {
 
+// A row is a quarter of a 16-bit one, but its codes take as many instructions to
+// open as 16-bit values take bytes to load, so tiles are bound by instructions,
+// and large ones spread what a tile costs at least: of 64 positions, with as many
+// warps, in fours for the SM's four schedulers, as registers and shared memory
+// allow, two stages each.  2.2 million positions of 8 x 8 heads of 128: tiles of 64
+// with 12 warps 477 us, 11 507, 8 580 (with two terms of P); of 32 with 16 warps
+// 530, 12 556, of 16 with 16 797 (at first).  32 x 4000 to 8000 positions, tiles of
+// 64 / 32: 16 heads of 64 59.7 / 70.6 us (16 warps), 16 query heads a key-value head
+// 76.8 / 84.4 (8 warps), of 64 84.7 / 96.5 (12); heads of 256, tiles of 32 / 16 58.0
+// / 69.7 (8).
+// Calls of one launch want few warps to start and more of them at work, hence
+// tiles of 32 with 8 warps: 1021 positions 6.8 us (12 warps 7.0, 16 9.0, tiles of 64
+// 8.3), 4000 8.3, 16,000 16.4.
 template <typename QT> cudaError_t run_dim(const KvPages& c, const KvTable& t, const KvAttention& a, const KvScratch& mem, uint32_t* status, cudaStream_t s) {
     if (a.q_heads / c.kv_heads <= 8) {
-        if (c.head_dim == 64) return run<QT, Rows8<QT, 4, 64, 32>, 4, 64, 32, 16, 4>(c, t, a, mem, status, s);
-        if (c.head_dim == 128) return run<QT, Rows8<QT, 4, 128, 32>, 4, 128, 32, 12, 3>(c, t, a, mem, status, s);
-        return run<QT, Rows8<QT, 4, 256, 16>, 4, 256, 16, 8, 4>(c, t, a, mem, status, s);
+        if (c.head_dim == 64) return run<QT, Rows8<QT, 4, 64, 64>, 4, 64, 64, 16, 2, Shape<Rows8<QT, 4, 64, 32>, 4, 64, 32, 8, 3>>(c, t, a, mem, status, s);
+        if (c.head_dim == 128) return run<QT, Rows8<QT, 4, 128, 64>, 4, 128, 64, 12, 2, Shape<Rows8<QT, 4, 128, 32>, 4, 128, 32, 8, 3>>(c, t, a, mem, status, s);
+        return run<QT, Rows8<QT, 4, 256, 32>, 4, 256, 32, 8, 2>(c, t, a, mem, status, s);
     }
-    if (c.head_dim == 64) return run<QT, Rows16<QT, 4, 64, 32>, 4, 64, 32, 12, 4>(c, t, a, mem, status, s);
-    if (c.head_dim == 128) return run<QT, Rows16<QT, 4, 128, 32>, 4, 128, 32, 8, 4>(c, t, a, mem, status, s);
+    if (c.head_dim == 64) return run<QT, Rows16<QT, 4, 64, 64>, 4, 64, 64, 12, 2, Shape<Rows16<QT, 4, 64, 32>, 4, 64, 32, 8, 3>>(c, t, a, mem, status, s);
+    if (c.head_dim == 128) return run<QT, Rows16<QT, 4, 128, 64>, 4, 128, 64, 8, 2, Shape<Rows16<QT, 4, 128, 32>, 4, 128, 32, 8, 3>>(c, t, a, mem, status, s);
     return run<QT, Rows16<QT, 4, 256, 16>, 4, 256, 16, 7, 5>(c, t, a, mem, status, s);
 }
 

@@ -61,6 +61,22 @@ __device__ __forceinline__ float inverse_of(float s) {
     return s >= 0x1p-60f && s <= 0x1p60f ? __frcp_rn(s) : NAN;
 }
 
+// Eight fp32 numbers over the scale, in the same way: within 2^-23 of the quotient,
+// and the same e4m3 value as quant16's where they have 11 bits.
+__device__ __forceinline__ void quotients(const float (&x)[8], float scale, float inverse, float (&y)[8]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = x[i] * inverse;
+        y[i] = fmaf(-fmaf(q, scale, -x[i]), inverse, q);
+        sum += fabsf(y[i]);
+    }
+    if (!(sum < INFINITY)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+    }
+}
+
 // Eight numbers as e2m1 codes, the first one lowest; ties to even, beyond 6 to 6.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&z)[8]) {
     uint32_t w;

@@ -212,24 +212,28 @@ __device__ __forceinline__ void pairs8(uint32_t w0, uint32_t w1, uint32_t scale,
 
 // Where 16-byte vector `v` of row `row` of a tile lies within the tile.  The
 // exclusive-ors spread the addresses that one shared-memory access touches over
-// all banks: 16-bit tiles are read by ldmatrix (8 rows of one vector), narrow
-// keys by lanes (row g, DP / 4 consecutive elements) and narrow values by lanes
-// (rows 2 t and on, DP / 8 consecutive elements).
+// all banks: 16-bit tiles are read by ldmatrix (8 rows of one vector), 8-bit
+// keys by lanes (row g, DP / 4 consecutive elements) and 8-bit values by lanes
+// (rows 2 t and on, DP / 8 consecutive elements).  4-bit rows lie as in the cache,
+// which lets their copies have constant offsets; the order in which a product
+// takes the positions (row4) does for them what it can.
 template <int BITS, int DP> __device__ __forceinline__ int k_at(int row, int v) {
     constexpr int kRowBytes = DP * BITS / 8;
-    const int u = BITS == 16 ? v ^ (row & 7) : kRowBytes <= 64 ? v : kRowBytes == 128 ? v ^ (row & 1) : v ^ ((v >> 3) & 1) ^ ((row & 1) << 1);
+    const int u = BITS == 4 ? v : BITS == 16 ? v ^ (row & 7) : kRowBytes <= 64 ? v : kRowBytes == 128 ? v ^ (row & 1) : v ^ ((v >> 3) & 1) ^ ((row & 1) << 1);
     return row * kRowBytes + u * 16;
 }
 template <int BITS, int DP> __device__ __forceinline__ int v_at(int row, int v) {
     constexpr int kRowBytes = DP * BITS / 8;
-    // 4-bit rows of 32 and 64 bytes: four and two of them share 128 bytes
-    if (BITS == 4 && DP == 64) return (row >> 2) * 128 + (((row & 3) * 2 + v) ^ (((row >> 2) & 1) << 1)) * 16;
-    if (BITS == 4 && DP == 128) return (row >> 1) * 128 + (((row & 1) * 4 + v) ^ (((row >> 1) & 1) << 2 | ((row >> 2) & 1) << 1)) * 16;
-    const int u = BITS == 16 ? v ^ (row & 7) : kRowBytes == 64 ? v ^ ((row >> 1) & 3) : kRowBytes == 128 ? v ^ (((row >> 1) & 3) << 1)
+    const int u = BITS == 4 ? v : BITS == 16 ? v ^ (row & 7) : kRowBytes == 64 ? v ^ ((row >> 1) & 3) : kRowBytes == 128 ? v ^ (((row >> 1) & 3) << 1)
                                                                                             : v ^ ((row >> 1) & 1) ^ (((row >> 2) & 1) << 2);
     return row * kRowBytes + u * 16;
 }
 
+
+// The position, within its 16, of a product's row i over a 4-bit cache: of the
+// rows 0, 2, 4, 6 that one access to the values reads, half are odd positions,
+// and so are one of each two neighbours, for the keys.
+__device__ __forceinline__ int row4(int i) { return i ^ ((i >> 1) & 1); }
 
 // What a unit's outputs need to know: which sequence and heads it is.
 struct Unit {
@@ -278,7 +282,7 @@ template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
     using MT = typename std::conditional<kNarrow, __half, QT>::type;
     static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
     static constexpr int kHeads = HEADS;
-    static constexpr bool kTwo = !kNarrow || std::is_same<QT, __half>::value || (HEADS == 8 && DP > 64);
+    static constexpr bool kTwo = !kNarrow || std::is_same<QT, __half>::value || (BITS == 8 && HEADS == 8 && DP > 64);
     static constexpr bool kFit = kNarrow && !std::is_same<QT, __half>::value;
     static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
     static constexpr int kRowBytes = DP * BITS / 8, kKS = DP / 16;
@@ -352,7 +356,7 @@ template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
             uint32_t s[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int r = row + 2 * q4 + (k & 1) + (k >> 1) * 8;
+                const int r = row + row4(2 * q4 + (k & 1)) + (k >> 1) * 8;
                 if constexpr (DP == 64) {
                     w[k].x = lds32(vt + v_at<BITS, DP>(r, g >> 2) + (g & 3) * 4);
                     s[k] = lds8(scales + r * kBlocks + (g >> 1));
@@ -486,7 +490,7 @@ template <typename QT, int BITS, int DP, int T> struct Rows16 : RowsBase<QT, BIT
         } else if constexpr (BITS == 4) {
             typename Base::Keys4 keys[kPT];
 #pragma unroll
-            for (int pt = 0; pt < kPT; ++pt) keys[pt].load(kt, vt + T * kRowBytes, g + 8 * pt, q4);
+            for (int pt = 0; pt < kPT; ++pt) keys[pt].load(kt, vt + T * kRowBytes, row4(g) + 8 * pt, q4);
 #pragma unroll
             for (int i = 0; i < Base::kKeyWords; ++i) {
                 uint32_t fa[4], fb[4];
@@ -523,15 +527,18 @@ template <typename QT, int BITS, int DP, int T> struct Rows16 : RowsBase<QT, BIT
         for (int pt = 0; pt < kPT; ++pt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool see = whole || t.visible(p0 + 2 * q4 + pt * 8 + e);
+                const bool see = whole || t.visible(p0 + (BITS == 4 ? row4(2 * q4 + e) : 2 * q4 + e) + pt * 8);
                 x[pt][e] = see ? x[pt][e] * sl0 : -INFINITY;
                 x[pt][2 + e] = see ? x[pt][2 + e] * sl1 : -INFINITY;
             }
         if (scores) {
 #pragma unroll
             for (int pt = 0; pt < kPT; ++pt) {
-                if (u.row0 + g < u.group) *reinterpret_cast<float2*>(scores + g * T + 2 * q4 + pt * 8) = make_float2(x[pt][0], x[pt][1]);
-                if (u.row0 + g + 8 < u.group) *reinterpret_cast<float2*>(scores + (g + 8) * T + 2 * q4 + pt * 8) = make_float2(x[pt][2], x[pt][3]);
+                const bool turned = BITS == 4 && (q4 & 1);  // row4: the second one first
+                if (u.row0 + g < u.group)
+                    *reinterpret_cast<float2*>(scores + g * T + 2 * q4 + pt * 8) = turned ? make_float2(x[pt][1], x[pt][0]) : make_float2(x[pt][0], x[pt][1]);
+                if (u.row0 + g + 8 < u.group)
+                    *reinterpret_cast<float2*>(scores + (g + 8) * T + 2 * q4 + pt * 8) = turned ? make_float2(x[pt][3], x[pt][2]) : make_float2(x[pt][2], x[pt][3]);
             }
         }
         float top0 = m0, top1 = m1, low = INFINITY;
@@ -742,7 +749,11 @@ template <typename QT, int BITS, int DP, int T> struct Rows8 : RowsBase<QT, BITS
 
     __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, uint32_t, const Tiles& t, int p0, float* scores, const Unit& u, int lane) {
         const int g = lane >> 2, q4 = lane & 3;
-        float x[kHB][4] = {}, z[kHB][4] = {};  // positions 16 h + g and 8 later; two sums, so that products wait less for each other
+        // positions 16 h + g and 8 later; two sums, so that products wait less for
+        // each other (4-bit keys take longer to open than their products)
+        constexpr bool kSplit = BITS != 4;
+        float x[kHB][4] = {};
+        [[maybe_unused]] float z[kSplit ? kHB : 1][4] = {};
         if constexpr (!kNarrow) {
             const int row = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
@@ -754,23 +765,27 @@ template <typename QT, int BITS, int DP, int T> struct Rows8 : RowsBase<QT, BITS
                     mma16816<MT>(ks & 1 ? z[h] : x[h], kf, qf[ks][0], qf[ks][1]);
                 }
         } else if constexpr (BITS == 4) {
-            typename Base::Keys4 ka[kHB], kb[kHB];
+            constexpr int kTogether = kHB < 2 ? 1 : 2;
 #pragma unroll
-            for (int h = 0; h < kHB; ++h) {
-                ka[h].load(kt, vt + T * kRowBytes, 16 * h + g, q4);
-                kb[h].load(kt, vt + T * kRowBytes, 16 * h + g + 8, q4);
-            }
+            for (int h0 = 0; h0 < kHB; h0 += kTogether) {
+                typename Base::Keys4 ka[kTogether], kb[kTogether];
 #pragma unroll
-            for (int i = 0; i < Base::kKeyWords; ++i)
-#pragma unroll
-                for (int h = 0; h < kHB; ++h) {
-                    uint32_t fa[4], fb[4];
-                    ka[h].word(i, fa);
-                    kb[h].word(i, fb);
-                    const uint32_t k0[4] = {fa[0], fb[0], fa[1], fb[1]}, k1[4] = {fa[2], fb[2], fa[3], fb[3]};
-                    mma16816<MT>(x[h], k0, qf[2 * i][0], qf[2 * i][1]);
-                    mma16816<MT>(z[h], k1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                for (int h = 0; h < kTogether; ++h) {
+                    ka[h].load(kt, vt + T * kRowBytes, 16 * (h0 + h) + row4(g), q4);
+                    kb[h].load(kt, vt + T * kRowBytes, 16 * (h0 + h) + row4(g) + 8, q4);
                 }
+#pragma unroll
+                for (int i = 0; i < Base::kKeyWords; ++i)
+#pragma unroll
+                    for (int h = 0; h < kTogether; ++h) {
+                        uint32_t fa[4], fb[4];
+                        ka[h].word(i, fa);
+                        kb[h].word(i, fb);
+                        const uint32_t k0[4] = {fa[0], fb[0], fa[1], fb[1]}, k1[4] = {fa[2], fb[2], fa[3], fb[3]};
+                        mma16816<MT>(x[h0 + h], k0, qf[2 * i][0], qf[2 * i][1]);
+                        mma16816<MT>(x[h0 + h], k1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                    }
+            }
         } else {
 #pragma unroll
             for (int v = 0; v < DP / 64; ++v) {
@@ -791,19 +806,20 @@ template <typename QT, int BITS, int DP, int T> struct Rows8 : RowsBase<QT, BITS
             }
         }
         const bool whole = t.whole(p0, T);
+        const int at = BITS == 4 ? row4(g) : g;  // position of this lane's rows
 #pragma unroll
         for (int h = 0; h < kHB; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool see = whole || t.visible(p0 + 16 * h + g + (e >> 1) * 8);
-                x[h][e] = see ? (x[h][e] + z[h][e]) * (e & 1 ? sl1 : sl0) : -INFINITY;
+                const bool see = whole || t.visible(p0 + 16 * h + at + (e >> 1) * 8);
+                x[h][e] = see ? (kSplit ? x[h][e] + z[kSplit ? h : 0][e] : x[h][e]) * (e & 1 ? sl1 : sl0) : -INFINITY;
             }
         if (scores) {
 #pragma unroll
             for (int h = 0; h < kHB; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (u.row0 + 2 * q4 + (e & 1) < u.group) scores[(2 * q4 + (e & 1)) * T + 16 * h + g + (e >> 1) * 8] = x[h][e];
+                    if (u.row0 + 2 * q4 + (e & 1) < u.group) scores[(2 * q4 + (e & 1)) * T + 16 * h + at + (e >> 1) * 8] = x[h][e];
         }
         float top0 = m0, top1 = m1, low = INFINITY;
 #pragma unroll

@@ -24,6 +24,8 @@ namespace ss {
 namespace {
 
 constexpr int kMostThreads = 256;
+// Rows of a ring: those on their way, and the one at hand.
+template <typename T> constexpr int kStages = sizeof(T) == 4 ? 3 : 4;
 
 __device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16, float x, float y) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
@@ -37,13 +39,16 @@ __device__ __forceinline__ uint32_t pack_pair(__half, float x, float y) {
 // Eight elements as they lie in memory, and as fp32.
 template <typename T> struct Eight {
     uint4 v[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p) {
+    static constexpr int kVecs = sizeof(T) / 2;
+    // The copies of eight elements to vectors v and on of a ring's stage (zeros where
+    // there are none), and they from there.
+    template <typename R> static __device__ __forceinline__ void copy(const R& ring, int stage, int v, const T* p, bool in) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ldg_vec(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < kVecs; ++i) ring.copy(stage, v + i, reinterpret_cast<const uint4*>(p) + i, in);
     }
-    __device__ __forceinline__ void clear() {
+    template <typename R> __device__ __forceinline__ Eight(const R& ring, int stage, int at) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kVecs; ++i) v[i] = ring.get(stage, at + i);
     }
     __device__ __forceinline__ void open(float (&x)[8]) const {
         if constexpr (sizeof(T) == 4) {
@@ -74,6 +79,26 @@ template <typename T> struct Eight {
     }
 };
 
+// A lane's own vectors of the rows to come, in shared memory: only the thread that
+// copied them reads them, so nothing but its own copies is waited for.  NV vectors
+// of 16 bytes a row, S rows.
+template <int NV, int S> struct Ring {
+    uint32_t base, step;
+    __device__ __forceinline__ Ring(void* smem) : base((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
+    static size_t bytes(int threads) { return (size_t)NV * S * threads * 16; }
+    __device__ __forceinline__ void copy(int stage, int v, const void* from, bool in) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + (stage * NV + v) * step), "l"(from), "r"(in ? 16 : 0) : "memory");
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory"); }
+    static __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+    __device__ __forceinline__ uint4 get(int stage, int v) const {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + (stage * NV + v) * step) : "memory");
+        return x;
+    }
+};
+
 // How a row of head_dim = 8 vecs elements lies over its lanes: lane p < pairs
 // has the vectors p and p + pairs, which are turned with each other (or each in
 // itself, where pairs are adjacent), the lanes after them 2 p and 2 p + 1.
@@ -98,6 +123,7 @@ struct Tables {
         turn = static_cast<float4*>(smem);
         weight = turn + (size_t)tokens * 4 * pairs;
     }
+    __device__ __forceinline__ void* end() const { return weight + 8 * lanes; }
     static size_t bytes(int vecs, int pairs, int tokens) { return ((size_t)tokens * 4 * pairs + 8 * ((vecs + 1) / 2)) * 16; }
     __device__ __forceinline__ void get(const float4* plane, int stride, int p, float (&x)[8], float (&y)[8]) const {
         const float4 v[4] = {plane[p], plane[stride + p], plane[2 * stride + p], plane[3 * stride + p]};
@@ -184,11 +210,10 @@ __device__ __forceinline__ void store_cached(const KvPages& c, const Place& to, 
         if (second < l.vecs) Eight<T>::store(reinterpret_cast<T*>(pool) + at + second * 8, b);
     } else if constexpr (BITS == 8) {
         if (!in) return;
-        const float s = scales ? scales[h] : 1.0f;
+        const float s = scales ? scales[h] : 1.0f, inverse = inverse_of(s);
         auto put = [&](int vec, const float (&x)[8]) {
             float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+            quotients(x, s, inverse, y);
             *reinterpret_cast<uint2*>(pool + at + vec * 8) = make_uint2(quant4(y[0], y[1], y[2], y[3]), quant4(y[4], y[5], y[6], y[7]));
         };
         put(first, a);
@@ -236,7 +261,45 @@ __global__ void __launch_bounds__(kMostThreads) k_qk_rope(QkRope a, Layout l, Cu
     const int h0 = (int)(blockIdx.x % cut.splits) * cut.heads;
     const int tokens = (int)min((int64_t)cut.tokens, a.tokens - t0);
     const int heads = min(cut.heads, a.q.heads + a.k.heads + a.v.heads - h0);
+    const int rows = tokens * heads, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
+    const int mine = tid / L;  // this lane's rows: mine, mine + groups, ...
+    constexpr int kVecs = Eight<T>::kVecs;
+    const Ring<2 * kVecs, kStages<T>> ring(tables.end());
+    struct Row {
+        const QkRows* of;
+        int token, head;
+        bool in;
+    };
+    auto row_at = [&](int r) {
+        Row x{&a.q, 0, h0, r < rows && p < lanes};
+        if (r < rows) {
+            x.token = cut.by_heads.div(r);
+            x.head = h0 + r - x.token * heads;
+        }
+        if (x.head >= a.q.heads) {
+            x.head -= a.q.heads;
+            x.of = &a.k;
+            if (CACHE && x.head >= a.k.heads) {
+                x.head -= a.k.heads;
+                x.of = &a.v;
+            }
+        }
+        return x;
+    };
+    auto issue = [&](int r, int stage) {
+        const Row x = row_at(r);
+        const T* from = reinterpret_cast<const T*>(x.of->x) + (t0 + x.token) * x.of->token_stride + x.head * x.of->head_stride;
+        Eight<T>::copy(ring, stage, 0, x.in ? from + first * 8 : reinterpret_cast<const T*>(a.positions), x.in);
+        const bool both = x.in && second < l.vecs;
+        Eight<T>::copy(ring, stage, kVecs, both ? from + second * 8 : reinterpret_cast<const T*>(a.positions), both);
+    };
     begin_dependent();
+    // the first rows are on their way while the tables are filled
+#pragma unroll
+    for (int k = 0; k < kStages<T> - 1; ++k) {
+        if (mine / (32 / L) * (32 / L) + k * groups < rows) issue(mine + k * groups, k);
+        ring.commit();
+    }
     tables.fill_turns(a, t0, tokens);
     tables.fill_weights(a, l);
     if constexpr (CACHE) {
@@ -255,220 +318,209 @@ __global__ void __launch_bounds__(kMostThreads) k_qk_rope(QkRope a, Layout l, Cu
     }
     __syncthreads();
 
-    const int rows = tokens * heads, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
-    // Two rows at a time, whose loads are on their way together.
-    for (int r0 = tid / 32 * (32 / L); r0 < rows; r0 += 2 * groups) {
-        Eight<T> va[2], vb[2];
-        int token[2], head[2];
-        const QkRows* of[2];
-        bool in[2];
+    int stage = 0;
+    for (int r0 = tid / 32 * (32 / L); r0 < rows; r0 += groups) {  // the same for a warp
+        const Row row = row_at(r0 + tid % 32 / L);
+        ring.wait();
+        float x[8], y[8];
+        Eight<T>(ring, stage, 0).open(x);
+        Eight<T>(ring, stage, kVecs).open(y);
+        // the stage read in the last step is filled again
+        const int next = r0 + (kStages<T> - 1) * groups;
+        if (next < rows) issue(next + tid % 32 / L, stage == 0 ? kStages<T> - 1 : stage - 1);
+        ring.commit();
+        stage = stage + 1 == kStages<T> ? 0 : stage + 1;
+
+        const bool is_q = row.of == &a.q, is_k = row.of == &a.k, is_v = CACHE && row.of == &a.v;
+        float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = r0 + k * groups + tid % 32 / L;
-            in[k] = r < rows && p < lanes;
-            token[k] = r < rows ? cut.by_heads.div(r) : 0;
-            head[k] = h0 + (r < rows ? r - token[k] * heads : 0);
-            of[k] = &a.q;
-            if (head[k] >= a.q.heads) {
-                head[k] -= a.q.heads;
-                of[k] = &a.k;
-                if (CACHE && head[k] >= a.k.heads) {
-                    head[k] -= a.k.heads;
-                    of[k] = &a.v;
-                }
+        for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
+        sum = row_sum<L>(sum);
+        if (row.in && !is_v) {
+            const float inv = __frsqrt_rn(sum * inv_dim + a.eps);
+            float wa[8], wb[8];
+            tables.weights_of(is_k ? 1 : 0, p, wa, wb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] *= inv * wa[i];
+                y[i] *= inv * wb[i];
             }
-            if (CACHE && of[k] != &a.q && s_place[token[k]].at < 0) in[k] = false;
-            va[k].clear();
-            vb[k].clear();
-            if (in[k]) {
-                const T* x = reinterpret_cast<const T*>(of[k]->x) + (t0 + token[k]) * of[k]->token_stride + head[k] * of[k]->head_stride;
-                va[k].load(x + first * 8);
-                if (second < l.vecs) vb[k].load(x + second * 8);
+            if (p < l.pairs) {
+                float co[8], si[8];
+                tables.turns_of(row.token, p, co, si);
+                turn16<1>(x, y, co, si, a.interleaved);
             }
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float x[8], y[8];
-            va[k].open(x);
-            vb[k].open(y);
-            const bool is_v = CACHE && of[k] == &a.v, is_k = of[k] == &a.k;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
-            sum = row_sum<L>(sum);
-            if (in[k] && !is_v) {
-                const float inv = __frsqrt_rn(sum * inv_dim + a.eps);
-                float wa[8], wb[8];
-                tables.weights_of(is_k ? 1 : 0, p, wa, wb);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= inv * wa[i];
-                    y[i] *= inv * wb[i];
-                }
-                if (p < l.pairs) {
-                    float co[8], si[8];
-                    tables.turns_of(token[k], p, co, si);
-                    turn16<1>(x, y, co, si, a.interleaved);
-                }
-            }
-            if constexpr (CACHE) {
-                if (of[k] != &a.q || BITS == 4) {  // 4 bits: lanes exchange largest elements
-                    const bool mine = in[k] && of[k] != &a.q;
-                    if (BITS == 4) {
-                        store_cached<BITS, T>(c, s_place[token[k]], is_v, mine ? head[k] : 0, l, p, mine, x, y);
-                    } else {
-                        store_cached<BITS, T>(c, s_place[token[k]], is_v, head[k], l, p, mine, x, y);
-                    }
-                    if (mine && is_k && p == 0 && c.weight) c.weight[s_place[token[k]].row + (int64_t)head[k] * c.page_size] = 0.0f;
-                }
-                if (of[k] != &a.q) continue;
-            }
-            if (in[k]) {
-                T* to = reinterpret_cast<T*>(of[k]->y) + (t0 + token[k]) * of[k]->y_token_stride + head[k] * of[k]->y_head_stride;
-                Eight<T>::store(to + first * 8, x);
-                if (second < l.vecs) Eight<T>::store(to + second * 8, y);
-            }
+        if constexpr (CACHE) {
+            const Place to = s_place[row.token];
+            const bool put = row.in && !is_q && to.at >= 0;
+            if (!is_q || BITS == 4) store_cached<BITS, T>(c, to, is_v, put ? row.head : 0, l, p, put, x, y);  // 4 bits: lanes exchange largest elements
+            if (put && is_k && p == 0 && c.weight) c.weight[to.row + (int64_t)row.head * c.page_size] = 0.0f;
+            if (!is_q) continue;
+        }
+        if (row.in) {
+            T* to = reinterpret_cast<T*>(row.of->y) + (t0 + row.token) * row.of->y_token_stride + row.head * row.of->y_head_stride;
+            Eight<T>::store(to + first * 8, x);
+            if (second < l.vecs) Eight<T>::store(to + second * 8, y);
         }
     }
+    ring.wait_all();
 }
 
 // ---- backward ----
 
-// A lane's share of one row: dx is written, and the row's share of dw added.
+// A CTA has rows of q or of k alone, tiles of `per` tokens of them, and leaves its
+// share of the weight's gradient in `parts`, head_dim numbers; which tiles are
+// whose, and so the order of all sums, is fixed.  The first q_ctas CTAs have q's.
 template <typename T, int L>
-__device__ __forceinline__ void back_rows(const QkRope& a, const QkRows& of, const Tables& tables, const Layout& l, int64_t t0, int rows, FastDiv by_heads, int which,
-                                          float inv_dim, float (&da)[8], float (&db)[8]) {
-    const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
-    for (int r0 = tid / 32 * (32 / L); r0 < rows; r0 += groups) {
-        const int r = r0 + tid % 32 / L;
-        const bool in = r < rows && p < lanes;
-        const int token = in ? by_heads.div(r) : 0, head = in ? r - token * of.heads : 0;
-        Eight<T> va, vb, ua, ub;
-        va.clear();
-        vb.clear();
-        ua.clear();
-        ub.clear();
-        if (in) {
-            const T* x = reinterpret_cast<const T*>(of.x) + (t0 + token) * of.token_stride + head * of.head_stride;
-            const T* g = reinterpret_cast<const T*>(of.g) + (t0 + token) * of.g_token_stride + head * of.g_head_stride;
-            va.load(x + first * 8);
-            ua.load(g + first * 8);
-            if (second < l.vecs) {
-                vb.load(x + second * 8);
-                ub.load(g + second * 8);
-            }
-        }
-        float x[8], y[8], g[8], h[8], wa[8], wb[8];
-        va.open(x);
-        vb.open(y);
-        ua.open(g);
-        ub.open(h);
-        if (p < l.pairs) {
-            float co[8], si[8];
-            tables.turns_of(token, p, co, si);
-            turn16<-1>(g, h, co, si, a.interleaved);
-        }
-        if (p < lanes) {
-            tables.weights_of(which, p, wa, wb);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 0.0f;
-        }
-        float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sum += x[i] * x[i] + y[i] * y[i];
-            dot += g[i] * wa[i] * x[i] + h[i] * wb[i] * y[i];
-        }
-        sum = row_sum<L>(sum);
-        dot = row_sum<L>(dot);
-        if (!in) continue;
-        const float inv = __frsqrt_rn(sum * inv_dim + a.eps), mean = inv * inv * dot * inv_dim;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            da[i] += g[i] * (x[i] * inv);
-            db[i] += h[i] * (y[i] * inv);
-            x[i] = inv * (g[i] * wa[i] - x[i] * mean);
-            y[i] = inv * (h[i] * wb[i] - y[i] * mean);
-        }
-        T* to = reinterpret_cast<T*>(of.y) + (t0 + token) * of.y_token_stride + head * of.y_head_stride;
-        Eight<T>::store(to + first * 8, x);
-        if (second < l.vecs) Eight<T>::store(to + second * 8, y);
-    }
-}
-
-// Each CTA takes tiles of cut.tokens tokens and leaves its share of both
-// weights' gradients in `parts`, 2 x head_dim numbers; which tiles are whose, and
-// so the order of all sums, is fixed.
-template <typename T, int L>
-__global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout l, int per, FastDiv by_q, FastDiv by_k, float inv_dim, float* parts) {
+__global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout l, int q_ctas, int per_q, int per_k, FastDiv by_q, FastDiv by_k, float inv_dim, float* parts) {
     extern __shared__ float4 s_tables[];
-    const Tables tables(s_tables, l, per);
-    const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2;
+    const bool is_k = blockIdx.x >= q_ctas;
+    const QkRows& of = is_k ? a.k : a.q;
+    const FastDiv by_heads = is_k ? by_k : by_q;
+    const int per = is_k ? per_k : per_q, cta = is_k ? blockIdx.x - q_ctas : blockIdx.x, ctas = is_k ? gridDim.x - q_ctas : q_ctas;
+    const Tables tables(s_tables, l, max(per_q, per_k));
+    constexpr int kVecs = Eight<T>::kVecs;
+    const Ring<4 * kVecs, kStages<T>> ring(tables.end());
+    const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
+    const int64_t tiles = (a.tokens + per - 1) / per;
     begin_dependent();
+    // A step is one row of every group; the steps of all tiles are one sequence, so
+    // that the ring does not run empty between them.
+    struct At {
+        int64_t tile;
+        int r0;  // of the warp's first row
+    };
+    auto rows_in = [&](int64_t tile) { return (int)min((int64_t)per, a.tokens - tile * per) * of.heads; };
+    const int warp_row = tid / 32 * (32 / L);
+    auto settle = [&](At& x) {  // on to the next tile that has rows for this warp
+        while (x.tile < tiles && x.r0 >= rows_in(x.tile)) {
+            x.tile += ctas;
+            x.r0 = warp_row;
+        }
+    };
+    auto issue = [&](const At& at, int stage) {
+        const int r = at.r0 + tid % 32 / L;
+        const bool in = r < rows_in(at.tile) && p < lanes, both = in && second < l.vecs;
+        const int token = in ? by_heads.div(r) : 0, head = in ? r - token * of.heads : 0;
+        const int64_t t = at.tile * per + token;
+        const T* x = reinterpret_cast<const T*>(of.x) + t * of.token_stride + head * of.head_stride;
+        const T* g = reinterpret_cast<const T*>(of.g) + t * of.g_token_stride + head * of.g_head_stride;
+        const T* any = reinterpret_cast<const T*>(a.positions);
+        Eight<T>::copy(ring, stage, 0, in ? x + first * 8 : any, in);
+        Eight<T>::copy(ring, stage, kVecs, both ? x + second * 8 : any, both);
+        Eight<T>::copy(ring, stage, 2 * kVecs, in ? g + first * 8 : any, in);
+        Eight<T>::copy(ring, stage, 3 * kVecs, both ? g + second * 8 : any, both);
+    };
+    At ld{cta, warp_row};
+#pragma unroll
+    for (int k = 0; k < kStages<T> - 1; ++k) {
+        settle(ld);
+        if (ld.tile < tiles) {
+            issue(ld, k);
+            ld.r0 += groups;
+        }
+        ring.commit();
+    }
     tables.fill_weights(a, l);
-    float sums[2][2][8] = {};
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per) {
-        const int tokens = (int)min((int64_t)per, a.tokens - t0);
+    __syncthreads();
+    float wa[8] = {}, wb[8] = {}, da[8] = {}, db[8] = {};
+    if (p < lanes) tables.weights_of(is_k ? 1 : 0, p, wa, wb);
+    int stage = 0;
+    for (int64_t tile = cta; tile < tiles; tile += ctas) {
+        const int64_t t0 = tile * per;
+        const int tokens = (int)min((int64_t)per, a.tokens - t0), rows = tokens * of.heads;
         __syncthreads();
         tables.fill_turns(a, t0, tokens);
         __syncthreads();
-        back_rows<T, L>(a, a.q, tables, l, t0, tokens * a.q.heads, by_q, 0, inv_dim, sums[0][0], sums[0][1]);
-        back_rows<T, L>(a, a.k, tables, l, t0, tokens * a.k.heads, by_k, 1, inv_dim, sums[1][0], sums[1][1]);
-    }
-    // the CTA's groups, added up in their order
-    float* s_sums = reinterpret_cast<float*>(s_tables);  // groups x lanes x 16
-    const int dim = l.vecs * 8;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        __syncthreads();
-        if (p < lanes) {
+        for (int r0 = warp_row; r0 < rows; r0 += groups) {
+            const int r = r0 + tid % 32 / L;
+            const bool in = r < rows && p < lanes;
+            const int token = in ? by_heads.div(r) : 0, head = in ? r - token * of.heads : 0;
+            ring.wait();
+            float x[8], y[8], g[8], h[8];
+            Eight<T>(ring, stage, 0).open(x);
+            Eight<T>(ring, stage, kVecs).open(y);
+            Eight<T>(ring, stage, 2 * kVecs).open(g);
+            Eight<T>(ring, stage, 3 * kVecs).open(h);
+            settle(ld);
+            if (ld.tile < tiles) {
+                issue(ld, stage == 0 ? kStages<T> - 1 : stage - 1);
+                ld.r0 += groups;
+            }
+            ring.commit();
+            stage = stage + 1 == kStages<T> ? 0 : stage + 1;
+            if (p < l.pairs) {
+                float co[8], si[8];
+                tables.turns_of(token, p, co, si);
+                turn16<-1>(g, h, co, si, a.interleaved);
+            }
+            float sum = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s_sums[(tid / L * lanes + p) * 16 + i] = sums[k][0][i];
-                s_sums[(tid / L * lanes + p) * 16 + 8 + i] = sums[k][1][i];
+                sum += x[i] * x[i] + y[i] * y[i];
+                dot += g[i] * wa[i] * x[i] + h[i] * wb[i] * y[i];
             }
+            sum = row_sum<L>(sum);
+            dot = row_sum<L>(dot);
+            if (!in) continue;
+            const float inv = __frsqrt_rn(sum * inv_dim + a.eps), mean = inv * inv * dot * inv_dim;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                da[i] += g[i] * (x[i] * inv);
+                db[i] += h[i] * (y[i] * inv);
+                x[i] = inv * (g[i] * wa[i] - x[i] * mean);
+                y[i] = inv * (h[i] * wb[i] - y[i] * mean);
+            }
+            T* to = reinterpret_cast<T*>(of.y) + (t0 + token) * of.y_token_stride + head * of.y_head_stride;
+            Eight<T>::store(to + first * 8, x);
+            if (second < l.vecs) Eight<T>::store(to + second * 8, y);
         }
-        __syncthreads();
-        for (int i = tid; i < lanes * 16; i += blockDim.x) {
-            const int lane = i / 16, vec = i % 16 < 8 ? l.first(lane) : l.second(lane);
-            float x = 0.0f;
-            for (int g = 0; g < groups; ++g) x += s_sums[g * lanes * 16 + i];
-            if (vec < l.vecs) parts[((int64_t)blockIdx.x * 2 + k) * dim + vec * 8 + i % 8] = x;
+    }
+    ring.wait_all();
+    // the CTA's groups, added up in their order
+    float* s_sums = reinterpret_cast<float*>(s_tables);  // groups x lanes x 16
+    __syncthreads();
+    if (p < lanes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s_sums[(tid / L * lanes + p) * 16 + i] = da[i];
+            s_sums[(tid / L * lanes + p) * 16 + 8 + i] = db[i];
         }
+    }
+    __syncthreads();
+    for (int i = tid; i < lanes * 16; i += blockDim.x) {
+        const int lane = i / 16, vec = i % 16 < 8 ? l.first(lane) : l.second(lane);
+        float x = 0.0f;
+        for (int g = 0; g < groups; ++g) x += s_sums[g * lanes * 16 + i];
+        if (vec < l.vecs) parts[(int64_t)blockIdx.x * l.vecs * 8 + vec * 8 + i % 8] = x;
     }
 }
 
 // The CTAs' parts of 32 columns of (dq_weight, dk_weight), 32 threads a column.
-__global__ void __launch_bounds__(1024) k_qk_rope_weights(const float* parts, int count, int dim, float* dq_weight, float* dk_weight) {
+__global__ void __launch_bounds__(1024) k_qk_rope_weights(const float* parts, int q_ctas, int ctas, int dim, float* dq_weight, float* dk_weight) {
     __shared__ float s_sum[32][33];
     begin_dependent();
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5, d = col < dim ? col : col - dim;
+    const int from = col < dim ? 0 : q_ctas, to = col < dim ? q_ctas : ctas;
     float x = 0.0f;
     if (col < 2 * dim)
-        for (int i = part; i < count; i += 32) x += parts[(int64_t)i * 2 * dim + col];
+#pragma unroll 4
+        for (int i = from + part; i < to; i += 32) x += parts[(int64_t)i * dim + d];
     s_sum[part][threadIdx.x & 31] = x;
     __syncthreads();
     x = warp_sum<float>(s_sum[threadIdx.x & 31][part]);
-    const int to = blockIdx.x * 32 + part;
-    if ((threadIdx.x & 31) == 0 && to < 2 * dim) {
-        float* out = to < dim ? dq_weight : dk_weight;
-        if (out) out[to < dim ? to : to - dim] = x;
+    const int at = blockIdx.x * 32 + part;
+    if ((threadIdx.x & 31) == 0 && at < 2 * dim) {
+        float* out = at < dim ? dq_weight : dk_weight;
+        if (out) out[at < dim ? at : at - dim] = x;
     }
 }
 
 Layout layout_of(const QkRope& a) { return Layout{a.head_dim / 8, a.rotary_dim / 16}; }
 
 constexpr int kBackThreads = 256;
-
-// Tokens of a backward tile: about 128 rows.
-int back_tokens(const QkRope& a) { return std::max(1, std::min(16, 128 / std::max(1, a.q.heads + a.k.heads))); }
-// CTAs of the backward kernel, up to `per_sm` an SM.
-int back_grid(const QkRope& a, int sms, int per_sm) {
-    const int per = back_tokens(a);
-    return (int)std::min<int64_t>((a.tokens + per - 1) / per, (int64_t)sms * per_sm);
-}
-constexpr int kBackMostPerSm = 8;
+constexpr int kBackMostPerSm = 4;
 
 template <typename F> cudaError_t for_lanes(int lanes, F&& f) {
     if (lanes <= 2) return f(std::integral_constant<int, 2>());
@@ -499,7 +551,10 @@ cudaError_t run(const QkRope& a, const KvPages& c, const int64_t* slots, int sms
     cut.splits = (heads + cut.heads - 1) / cut.heads;
     cut.by_heads = FastDiv(cut.heads);
     auto* kern = k_qk_rope<T, L, BITS>;
-    const size_t smem = Tables::bytes(l.vecs, l.pairs, cut.tokens);
+    const size_t smem = Tables::bytes(l.vecs, l.pairs, cut.tokens) + Ring<2 * Eight<T>::kVecs, kStages<T>>::bytes(threads);
+    KernelSetup su;
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kMostThreads, Tables::bytes(32, 16, 16) + Ring<2 * Eight<T>::kVecs, kStages<T>>::bytes(kMostThreads), &su);
+    if (e != cudaSuccess) return e;
     return launch_dependent(kern, (size_t)((a.tokens + cut.tokens - 1) / cut.tokens) * cut.splits, threads, smem, 1, s, a, l, cut, 1.0f / a.head_dim, c, slots,
                             FastDiv(BITS ? c.page_size : 1), status);
 }
@@ -507,15 +562,23 @@ cudaError_t run(const QkRope& a, const KvPages& c, const int64_t* slots, int sms
 template <typename T, int L> cudaError_t run_back(const QkRope& a, float* dq_weight, float* dk_weight, float* parts, int sms, cudaStream_t s) {
     const Layout l = layout_of(a);
     auto* kern = k_qk_rope_back<T, L>;
-    const int per = back_tokens(a), lanes = (l.vecs + 1) / 2;
-    const size_t smem = std::max(Tables::bytes(l.vecs, l.pairs, per), (size_t)kBackThreads / L * lanes * 16 * 4);
+    const int lanes = (l.vecs + 1) / 2, most_tokens = 16;
+    // tiles of about 8 rows a group
+    auto tokens_of = [&](int heads) { return std::max(1, std::min(most_tokens, 8 * kBackThreads / L / std::max(1, heads))); };
+    const int per_q = tokens_of(a.q.heads), per_k = tokens_of(a.k.heads);
+    const size_t ring = Ring<4 * Eight<T>::kVecs, kStages<T>>::bytes(kBackThreads);
+    const size_t smem = std::max(Tables::bytes(l.vecs, l.pairs, std::max(per_q, per_k)) + ring, (size_t)kBackThreads / L * lanes * 16 * 4);
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kBackThreads, std::max(Tables::bytes(32, 16, 16), (size_t)kBackThreads * 64), &su);
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kBackThreads, std::max(Tables::bytes(32, 16, most_tokens) + ring, (size_t)kBackThreads * 64), &su);
     if (e != cudaSuccess) return e;
-    const int grid = back_grid(a, sms, std::min(su.blocks_per_sm, kBackMostPerSm));
-    e = launch_dependent(kern, grid, kBackThreads, smem, 1, s, a, l, per, FastDiv(std::max(1, a.q.heads)), FastDiv(std::max(1, a.k.heads)), 1.0f / a.head_dim, parts);
+    // CTAs for q and for k by their rows
+    const int64_t most = (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), heads = a.q.heads + a.k.heads;
+    auto ctas_of = [&](int h, int per) { return h == 0 ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>((a.tokens + per - 1) / per, most * h / heads)); };
+    const int q_ctas = ctas_of(a.q.heads, per_q), ctas = q_ctas + ctas_of(a.k.heads, per_k);
+    e = launch_dependent(kern, ctas, kBackThreads, smem, 1, s, a, l, q_ctas, per_q, per_k, FastDiv(std::max(1, a.q.heads)), FastDiv(std::max(1, a.k.heads)), 1.0f / a.head_dim,
+                         parts);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), grid, a.head_dim, dq_weight, dk_weight);
+    return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), q_ctas, ctas, a.head_dim, dq_weight, dk_weight);
 }
 
 }  // namespace
@@ -539,7 +602,7 @@ cudaError_t launch_kv_append_rope(const KvPages& c, const int64_t* slots, const 
     return a.type == KvElem::BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
-size_t qk_rope_scratch(const QkRope& a, int sms) { return (size_t)sms * kBackMostPerSm * 2 * a.head_dim * 4; }
+size_t qk_rope_scratch(const QkRope& a, int sms) { return ((size_t)sms * kBackMostPerSm + 2) * a.head_dim * 4; }
 
 cudaError_t launch_qk_rope_backward(const QkRope& a, float* dq_weight, float* dk_weight, float* scratch, int sms, cudaStream_t s) {
     return for_type(a.type, [&](auto t) {
