@@ -393,8 +393,8 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  * are fp32, and y is rounded once.
  *   type       of q, k and the outputs: SS_BF16, SS_F16 or SS_ELEM_F32.
  *   q, k       rows (token, head) of head_dim consecutive elements; strides in
- *              elements, multiples of 16 bytes, 16-byte aligned.  Either may have
- *              no heads (then it is not read).
+ *              elements, multiples of 16 bytes, at most 2^33, 16-byte aligned.
+ *              Either may have no heads (then it is not read).
  *   q_weight, k_weight  device, head_dim numbers of weight_type (SS_BF16, SS_F16
  *              or SS_ELEM_F32), or NULL: ones.
  *   positions  device, a token each; may be negative.

@@ -534,8 +534,8 @@ ss_status rows_arg(const ss_rows* in, const char* name, int64_t tokens, int head
     if (!aligned16(in->data)) return fail(SS_ERR_INVALID_ARG, std::string(name) + " must be 16-byte aligned");
     *out = ss_rows{in->data, tokens > 1 ? in->token_stride : 0, heads > 1 ? in->head_stride : 0};
     for (const int64_t x : {out->token_stride, out->head_stride})
-        if (x < 0 || x % (16 / size) || x > 1ll << 40)
-            return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be non-negative multiples of 16 bytes, at most 2^40 elements");
+        if (x < 0 || x % (16 / size) || x > 1ll << 33)
+            return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be non-negative multiples of 16 bytes, at most 2^33 elements");
     if (written && ((tokens > 1 && out->token_stride < dim) || (heads > 1 && out->head_stride < dim)))
         return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
     return SS_OK;

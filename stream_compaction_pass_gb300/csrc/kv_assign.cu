@@ -175,7 +175,7 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
         // ---- tokens: four in a row a thread ----
         const int total = tokens[n];
         if (total > a.tokens && a.given && me == 0) record_error(status, kErrKvTable, (uint32_t)max(n - 1, 0));
-        for (int64_t q0 = me; q0 * 4 < a.tokens; q0 += threads) {
+        for (int64_t q0 = threads - 1 - me; q0 * 4 < a.tokens; q0 += threads) {  // threads without entries first
             const int t0 = (int)(q0 * 4), here = min(4, a.tokens - t0);
             int pos[4];
             int64_t slot[4];

@@ -7,14 +7,19 @@
 // g: dw = sum r x h over all rows, and dx = r (w h - x r^2 mean(w h x)).  An angle
 // is a fraction of a turn: position times frequency modulo 1, which 64-bit integers
 // multiply exactly with the frequency in units of 2^-64 turns, however far the
-// position; sine and cosine of what is left are those of CUDA's sincospi.
+// position.  Of what is left, fp32 rows take CUDA's sincospif and the rounded
+// reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1, 2 units
+// in the last place) are a thousandth of the outputs' rounding and whose
+// instructions are fewer by 60 and 20.
 //
 // What bounds it.  Memory: every row is read once and written once (backward:
-// two and one), for about 10 operations an element.  So rows stay in registers:
-// L lanes share a row, each with two 16-byte vectors whose elements are each
-// other's partners in the rotation, so that it needs no exchange, and the norm
-// log2 L shuffles.  A CTA takes all heads of a few tokens, whose sines and cosines
-// it computes once, in shared memory, or a part of the heads where tokens are few.
+// two and one), for about 10 operations an element, so that instructions come
+// close.  L lanes share a row, each with two 16-byte vectors whose elements are
+// each other's partners in the rotation, so that it needs no exchange, and the norm
+// log2 L shuffles.  A CTA takes consecutive rows of one of the tensors, which
+// leaves it one set of strides and weights, and computes their tokens' sines and
+// cosines once, in shared memory; its threads copy the rows to come, each its own
+// vectors, three steps ahead.
 #include <algorithm>
 
 #include "kv_quant.cuh"
@@ -36,65 +41,105 @@ __device__ __forceinline__ uint32_t pack_pair(__half, float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two fp32 numbers side by side, which one instruction works on.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 open_f2(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum_f2(F2 a) {
+    const float2 x = open_f2(a);
+    return x.x + x.y;
+}
+// a - b c.
+__device__ __forceinline__ F2 less2(F2 a, F2 b, F2 c) { return fma2(b * c, f2(-1.0f, -1.0f), a); }
+
 // Eight elements as they lie in memory, and as fp32.
 template <typename T> struct Eight {
     uint4 v[sizeof(T) / 2];
     static constexpr int kVecs = sizeof(T) / 2;
     // The copies of eight elements to vectors v and on of a ring's stage (zeros where
-    // there are none), and they from there.
-    template <typename R> static __device__ __forceinline__ void copy(const R& ring, int stage, int v, const T* p, bool in) {
+    // bytes is 0), and they from there.
+    template <typename R> static __device__ __forceinline__ void copy(const R& ring, int stage, int v, const T* p, int bytes) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) ring.copy(stage, v + i, reinterpret_cast<const uint4*>(p) + i, in);
+        for (int i = 0; i < kVecs; ++i) ring.copy(stage, v + i, reinterpret_cast<const uint4*>(p) + i, bytes);
     }
     template <typename R> __device__ __forceinline__ Eight(const R& ring, int stage, int at) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = ring.get(stage, at + i);
     }
-    __device__ __forceinline__ void open(float (&x)[8]) const {
+    __device__ __forceinline__ void open(F2 (&x)[4]) const {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                x[4 * i] = __uint_as_float(v[i].x);
-                x[4 * i + 1] = __uint_as_float(v[i].y);
-                x[4 * i + 2] = __uint_as_float(v[i].z);
-                x[4 * i + 3] = __uint_as_float(v[i].w);
+                x[2 * i] = f2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                x[2 * i + 1] = f2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
             }
         } else {
             const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 a = open_pair<T>(w[i]);
-                x[2 * i] = a.x;
-                x[2 * i + 1] = a.y;
+                x[i] = f2(a.x, a.y);
             }
         }
     }
-    static __device__ __forceinline__ void store(T* p, const float (&x)[8]) {
+    static __device__ __forceinline__ void store(T* p, const F2 (&x)[4]) {
+        float2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = open_f2(x[i]);
         if constexpr (sizeof(T) == 4) {
-            stg_vec(p, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
-            stg_vec(p + 4, make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])));
+            stg_vec(p, make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y)));
+            stg_vec(p + 4, make_uint4(__float_as_uint(f[2].x), __float_as_uint(f[2].y), __float_as_uint(f[3].x), __float_as_uint(f[3].y)));
         } else {
-            stg_vec(p, make_uint4(pack_pair(T(), x[0], x[1]), pack_pair(T(), x[2], x[3]), pack_pair(T(), x[4], x[5]), pack_pair(T(), x[6], x[7])));
+            stg_vec(p, make_uint4(pack_pair(T(), f[0].x, f[0].y), pack_pair(T(), f[1].x, f[1].y), pack_pair(T(), f[2].x, f[2].y), pack_pair(T(), f[3].x, f[3].y)));
         }
     }
 };
+__device__ __forceinline__ void floats(const F2 (&x)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = open_f2(x[i]);
+        f[2 * i] = a.x;
+        f[2 * i + 1] = a.y;
+    }
+}
 
 // A lane's own vectors of the rows to come, in shared memory: only the thread that
 // copied them reads them, so nothing but its own copies is waited for.  NV vectors
 // of 16 bytes a row, S rows.
 template <int NV, int S> struct Ring {
-    uint32_t base, step;
-    __device__ __forceinline__ Ring(void* smem) : base((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16), step(blockDim.x * 16) {}
+    uint32_t base;
+    __device__ __forceinline__ Ring(void* smem)
+        : base((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x / 32) * (S * NV * 512) + threadIdx.x % 32 * 16) {}
     static size_t bytes(int threads) { return (size_t)NV * S * threads * 16; }
-    __device__ __forceinline__ void copy(int stage, int v, const void* from, bool in) const {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + (stage * NV + v) * step), "l"(from), "r"(in ? 16 : 0) : "memory");
+    __device__ __forceinline__ void copy(int stage, int v, const void* from, int bytes) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + (stage * NV + v) * 512), "l"(from), "r"(bytes) : "memory");
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory"); }
     static __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
     __device__ __forceinline__ uint4 get(int stage, int v) const {
         uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + (stage * NV + v) * step) : "memory");
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + (stage * NV + v) * 512) : "memory");
         return x;
     }
 };
@@ -108,14 +153,27 @@ struct Layout {
     __device__ __forceinline__ int second(int p) const { return p < pairs ? p + pairs : 2 * p + 1; }
 };
 
-// How the work is cut: a CTA has `tokens` tokens and `heads` heads of them.
-struct Cut {
-    int tokens, heads, splits;
-    FastDiv by_heads;
+// A lane's part of a group's rows, every `groups`th one: where its first vector is.
+struct Walk {
+    const char* at;
+    int head;
+    int64_t step, wrap;  // to the next row; more, where that is another token's
+    __device__ __forceinline__ Walk(const char* base, int64_t token_stride, int64_t head_stride, int size, int64_t token, int head_, int heads, int step_tokens, int step_heads,
+                                    int first)
+        : at(base + (token * token_stride + head_ * head_stride + first) * size), head(head_),
+          step((step_tokens * token_stride + step_heads * head_stride) * size), wrap((token_stride - heads * head_stride) * size) {}
+    // Whether the next row is another token's (beside step_tokens).
+    __device__ __forceinline__ bool next(int heads, int step_heads) {
+        head += step_heads;
+        const bool over = head >= heads;
+        at += over ? step + wrap : step;
+        head -= over ? heads : 0;
+        return over;
+    }
 };
 
-// Shared memory: cosines and sines of the CTA's tokens, and the weights of q and k,
-// each in four planes of float4: plane j of lane p has a lane's numbers 4 j and on.
+// Shared memory: cosines and sines of the tokens at hand, and the weights, each in
+// four planes of float4: plane j of lane p has a lane's numbers 4 j and on.
 struct Tables {
     float4 *turn, *weight;
     int pairs, lanes;
@@ -123,66 +181,80 @@ struct Tables {
         turn = static_cast<float4*>(smem);
         weight = turn + (size_t)tokens * 4 * pairs;
     }
-    __device__ __forceinline__ void* end() const { return weight + 8 * lanes; }
-    static size_t bytes(int vecs, int pairs, int tokens) { return ((size_t)tokens * 4 * pairs + 8 * ((vecs + 1) / 2)) * 16; }
-    __device__ __forceinline__ void get(const float4* plane, int stride, int p, float (&x)[8], float (&y)[8]) const {
+    __device__ __forceinline__ void* end() const { return weight + 4 * lanes; }
+    static size_t bytes(const Layout& l, int tokens) { return ((size_t)tokens * 4 * l.pairs + 4 * ((l.vecs + 1) / 2)) * 16; }
+    __device__ __forceinline__ void get(const float4* plane, int stride, int p, F2 (&x)[4], F2 (&y)[4]) const {
         const float4 v[4] = {plane[p], plane[stride + p], plane[2 * stride + p], plane[3 * stride + p]};
-        x[0] = v[0].x; x[1] = v[0].y; x[2] = v[0].z; x[3] = v[0].w; x[4] = v[1].x; x[5] = v[1].y; x[6] = v[1].z; x[7] = v[1].w;
-        y[0] = v[2].x; y[1] = v[2].y; y[2] = v[2].z; y[3] = v[2].w; y[4] = v[3].x; y[5] = v[3].y; y[6] = v[3].z; y[7] = v[3].w;
-    }
-    __device__ __forceinline__ void turns_of(int token, int p, float (&c)[8], float (&s)[8]) const { get(turn + (size_t)token * 4 * pairs, pairs, p, c, s); }
-    __device__ __forceinline__ void weights_of(int k, int p, float (&a)[8], float (&b)[8]) const { get(weight + k * 4 * lanes, lanes, p, a, b); }
-
-    __device__ __forceinline__ void fill_turns(const QkRope& a, int64_t t0, int tokens) const {
-        const int per = pairs * 8;
-        for (int i = threadIdx.x; i < tokens * per; i += blockDim.x) {
-            const int t = i / per, m = i - t * per, p = m >> 3, j = m & 7;
-            const int f = !a.interleaved ? m : j < 4 ? 4 * p + j : 4 * (p + pairs) + j - 4;
-            const long long x = (long long)(a.turns[f] * (unsigned long long)(long long)a.positions[t0 + t]);
-            float s, c;
-            sincospif((float)x * 0x1p-63f, &s, &c);
-            float* to = reinterpret_cast<float*>(turn + (size_t)t * 4 * pairs + (j >> 2) * pairs + p) + (j & 3);
-            to[0] = c;
-            to[8 * pairs] = s;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[2 * i] = f2(v[i].x, v[i].y);
+            x[2 * i + 1] = f2(v[i].z, v[i].w);
+            y[2 * i] = f2(v[2 + i].x, v[2 + i].y);
+            y[2 * i + 1] = f2(v[2 + i].z, v[2 + i].w);
         }
     }
-    __device__ __forceinline__ void fill_weights(const QkRope& a, const Layout& l) const {
-        for (int i = threadIdx.x; i < 32 * lanes; i += blockDim.x) {
-            const int k = i / (16 * lanes), m = i - k * 16 * lanes, p = m >> 4, j = m & 15;
-            const int vec = j < 8 ? l.first(p) : l.second(p), d = vec * 8 + (j & 7);
-            const char* w = k ? a.k.weight : a.q.weight;
+    __device__ __forceinline__ void turns_of(int token, int p, F2 (&c)[4], F2 (&s)[4]) const { get(turn + token * 4 * pairs, pairs, p, c, s); }
+    __device__ __forceinline__ void weights_of(int p, F2 (&a)[4], F2 (&b)[4]) const { get(weight, lanes, p, a, b); }
+
+    // A thread has one of the frequencies, and every few tokens.
+    template <bool FINE> __device__ __forceinline__ void fill_turns(const QkRope& a, int64_t t0, int tokens) const {
+        const int per = pairs * 8, side = blockDim.x / per, m = threadIdx.x % per, p = m >> 3, j = m & 7;
+        if ((int)threadIdx.x >= side * per) return;
+        const unsigned long long f = a.turns[!a.interleaved ? m : j < 4 ? 4 * p + j : 4 * (p + pairs) + j - 4];
+        float* to = reinterpret_cast<float*>(turn + (j >> 2) * pairs + p) + (j & 3);
+        for (int t = threadIdx.x / per; t < tokens; t += side) {
+            const int at = a.positions[t0 + t];
+            float s, c;
+            if (FINE) {
+                sincospif((float)(long long)(f * (unsigned long long)(long long)at) * 0x1p-63f, &s, &c);
+            } else {  // the product's high half
+                const uint32_t low = (uint32_t)f, high = (uint32_t)(f >> 32) * (uint32_t)at + __umulhi(low, (uint32_t)at) - (at < 0 ? low : 0u);
+                __sincosf((float)(int)high * (0x1p-31f * 3.14159265358979f), &s, &c);
+            }
+            to[t * 16 * pairs] = c;
+            to[t * 16 * pairs + 8 * pairs] = s;
+        }
+    }
+    __device__ __forceinline__ void fill_weights(const char* w, KvElem type, const Layout& l) const {
+        for (int i = threadIdx.x; i < 16 * lanes; i += blockDim.x) {
+            const int p = i >> 4, j = i & 15, vec = j < 8 ? l.first(p) : l.second(p), d = vec * 8 + (j & 7);
             float x = 1.0f;
             if (w && vec < l.vecs) {
-                x = a.weight_type == KvElem::F32    ? reinterpret_cast<const float*>(w)[d]
-                    : a.weight_type == KvElem::BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[d])
-                                                    : __half2float(reinterpret_cast<const __half*>(w)[d]);
+                x = type == KvElem::F32    ? reinterpret_cast<const float*>(w)[d]
+                    : type == KvElem::BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[d])
+                                           : __half2float(reinterpret_cast<const __half*>(w)[d]);
             }
-            reinterpret_cast<float*>(weight + k * 4 * lanes + (j >> 2) * lanes + p)[j & 3] = x;
+            reinterpret_cast<float*>(weight + (j >> 2) * lanes + p)[j & 3] = x;
         }
     }
 };
 
-// Turns a lane's 16 elements by their angles, or back (SIGN -1).
-template <int SIGN> __device__ __forceinline__ void turn16(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8], bool interleaved) {
+// Turns a lane's 16 elements by their angles, or back.
+template <bool BACK> __device__ __forceinline__ void turn16(F2 (&a)[4], F2 (&b)[4], const F2 (&c)[4], const F2 (&s)[4], bool interleaved) {
     if (!interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i], z = SIGN * s[i];
-            a[i] = x * c[i] - y * z;
-            b[i] = y * c[i] + x * z;
+        for (int i = 0; i < 4; ++i) {
+            const F2 x = a[i], y = b[i];
+            a[i] = BACK ? fma2(y, s[i], x * c[i]) : less2(x * c[i], y, s[i]);
+            b[i] = BACK ? less2(y * c[i], x, s[i]) : fma2(x, s[i], y * c[i]);
         }
     } else {
+        auto turn = [](F2& z, float co, float si) {
+            const float2 x = open_f2(z);
+            const float w = BACK ? -si : si;
+            z = f2(x.x * co - x.y * w, x.y * co + x.x * w);
+        };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float x = a[2 * i], y = a[2 * i + 1], z = SIGN * s[i];
-            a[2 * i] = x * c[i] - y * z;
-            a[2 * i + 1] = y * c[i] + x * z;
-            const float u = b[2 * i], v = b[2 * i + 1], w = SIGN * s[4 + i];
-            b[2 * i] = u * c[4 + i] - v * w;
-            b[2 * i + 1] = v * c[4 + i] + u * w;
+            const float2 ca = open_f2(c[i / 2]), sa = open_f2(s[i / 2]), cb = open_f2(c[2 + i / 2]), sb = open_f2(s[2 + i / 2]);
+            turn(a[i], i % 2 ? ca.y : ca.x, i % 2 ? sa.y : sa.x);
+            turn(b[i], i % 2 ? cb.y : cb.x, i % 2 ? sb.y : sb.x);
         }
     }
 }
+
+template <typename T> constexpr bool kFine = sizeof(T) == 4;
+template <bool FINE> __device__ __forceinline__ float inverse_root(float x) { return FINE ? __frsqrt_rn(x) : rsqrtf(x); }
 
 template <int L> __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -199,28 +271,31 @@ struct Place {
 };
 
 template <int BITS, typename T>
-__device__ __forceinline__ void store_cached(const KvPages& c, const Place& to, bool is_v, int h, const Layout& l, int p, bool in, const float (&a)[8], const float (&b)[8]) {
+__device__ __forceinline__ void store_cached(const KvPages& c, const Place& to, bool is_v, int h, const Layout& l, int p, bool in, const F2 (&a2)[4], const F2 (&b2)[4]) {
     char* pool = is_v ? c.v : c.k;
     const int64_t at = to.at + (int64_t)h * c.head_stride;
     const float* scales = is_v ? c.v_scale : c.k_scale;
     const int first = l.first(p), second = l.second(p);
     if constexpr (BITS == 16) {
         if (!in) return;
-        Eight<T>::store(reinterpret_cast<T*>(pool) + at + first * 8, a);
-        if (second < l.vecs) Eight<T>::store(reinterpret_cast<T*>(pool) + at + second * 8, b);
+        Eight<T>::store(reinterpret_cast<T*>(pool) + at + first * 8, a2);
+        if (second < l.vecs) Eight<T>::store(reinterpret_cast<T*>(pool) + at + second * 8, b2);
     } else if constexpr (BITS == 8) {
         if (!in) return;
         const float s = scales ? scales[h] : 1.0f, inverse = inverse_of(s);
-        auto put = [&](int vec, const float (&x)[8]) {
-            float y[8];
+        auto put = [&](int vec, const F2 (&x2)[4]) {
+            float x[8], y[8];
+            floats(x2, x);
             quotients(x, s, inverse, y);
             *reinterpret_cast<uint2*>(pool + at + vec * 8) = make_uint2(quant4(y[0], y[1], y[2], y[3]), quant4(y[4], y[5], y[6], y[7]));
         };
-        put(first, a);
-        if (second < l.vecs) put(second, b);
+        put(first, a2);
+        if (second < l.vecs) put(second, b2);
     } else {
         const float inverse = scales && in ? __frcp_rn(scales[h]) : 1.0f;
-        float y[16], ma = 0.0f, mb = 0.0f;
+        float a[8], b[8], y[16], ma = 0.0f, mb = 0.0f;
+        floats(a2, a);
+        floats(b2, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             y[i] = a[i] * inverse;
@@ -249,243 +324,276 @@ __device__ __forceinline__ void store_cached(const KvPages& c, const Place& to, 
     }
 }
 
+// The CTAs of each tensor.  A row's number is token * heads + head.
+struct Jobs {
+    int ctas[3];   // of q, k and v
+    int steps[3];  // of a CTA: a row for every group
+    int chunk[3];  // steps between two fillings of the tables
+    FastDiv by_heads[3];
+};
+// Selected, not indexed: parameters that are would be copied to local memory.
+template <typename X> __device__ __forceinline__ X pick(const X (&x)[3], int i) { return i == 0 ? x[0] : i == 1 ? x[1] : x[2]; }
+
+// What a CTA does: `kind` 0, 1 or 2 for q, k or v, and consecutive rows of it, of
+// which a thread's group has every `groups`th.
+struct Share {
+    int kind, heads, steps, chunk, token, head, step_tokens, step_heads;
+    int64_t t0;
+    bool last;  // whether the last step has a row for this group
+    __device__ __forceinline__ Share(const QkRope& a, const Jobs& jobs, int group, int groups) {
+        const int c = blockIdx.x;
+        kind = c < jobs.ctas[0] ? 0 : c < jobs.ctas[0] + jobs.ctas[1] ? 1 : 2;
+        heads = kind == 0 ? a.q.heads : kind == 1 ? a.k.heads : a.v.heads;
+        const FastDiv by_heads = pick(jobs.by_heads, kind);
+        const int most = pick(jobs.steps, kind) * groups;
+        const int64_t begin = (int64_t)(c - (kind == 0 ? 0 : kind == 1 ? jobs.ctas[0] : jobs.ctas[0] + jobs.ctas[1])) * most;
+        chunk = pick(jobs.chunk, kind);
+        t0 = begin < 0x7fffffff ? by_heads.div((int)begin) : begin / heads;
+        head0 = (int)(begin - t0 * heads);
+        rows = (int)min((int64_t)most, a.tokens * heads - begin);
+        steps = (rows + groups - 1) / groups;
+        last = (steps - 1) * groups + group < rows;
+        step_tokens = by_heads.div(groups);
+        step_heads = groups - step_tokens * heads;
+        token = by_heads.div(head0 + group);
+        head = head0 + group - token * heads;
+    }
+    int head0, rows;
+    // The tokens, from t0 on, of the rows of steps [k, k + chunk).
+    __device__ __forceinline__ int2 tokens(const Jobs& jobs, int k, int groups) const {
+        const FastDiv by_heads = pick(jobs.by_heads, kind);
+        const int from = by_heads.div(head0 + k * groups);
+        return make_int2(from, by_heads.div(head0 + min((k + chunk) * groups, rows) - 1) - from + 1);
+    }
+};
+
 // BITS 0: rows go to tensors; else k's and v's go to a cache of so many bits.
 template <typename T, int L, int BITS>
-__global__ void __launch_bounds__(kMostThreads) k_qk_rope(QkRope a, Layout l, Cut cut, float inv_dim, KvPages c, const int64_t* slots, FastDiv page, uint32_t* status) {
+__global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 4) k_qk_rope(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, KvPages c, const int64_t* slots, FastDiv page,
+                                                          uint32_t* status) {
     constexpr bool CACHE = BITS > 0;
+    constexpr int kVecs = Eight<T>::kVecs, S = kStages<T>;
     extern __shared__ float4 s_tables[];
-    __shared__ Place s_place[CACHE ? kMostThreads : 1];
-    const Tables tables(s_tables, l, cut.tokens);
-    const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L;
-    const int64_t t0 = (int64_t)(blockIdx.x / cut.splits) * cut.tokens;
-    const int h0 = (int)(blockIdx.x % cut.splits) * cut.heads;
-    const int tokens = (int)min((int64_t)cut.tokens, a.tokens - t0);
-    const int heads = min(cut.heads, a.q.heads + a.k.heads + a.v.heads - h0);
-    const int rows = tokens * heads, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
-    const int mine = tid / L;  // this lane's rows: mine, mine + groups, ...
-    constexpr int kVecs = Eight<T>::kVecs;
-    const Ring<2 * kVecs, kStages<T>> ring(tables.end());
-    struct Row {
-        const QkRows* of;
-        int token, head;
-        bool in;
+    __shared__ Place s_place[CACHE ? kMostThreads / L + 2 : 1];
+    const Tables tables(s_tables, l, most_tokens);
+    const Ring<2 * kVecs, S> ring(tables.end());
+    const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
+    const Share me(a, jobs, tid / L, groups);
+    const bool is_q = me.kind == 0, is_v = CACHE && me.kind == 2;
+    const QkRows& of = is_q ? a.q : is_v ? a.v : a.k;
+    const bool one = p < lanes, two = one && second < l.vecs;
+    // Lanes without a vector take zeros, and rows behind the last what is there.
+    const int one_bytes = one ? 16 : 0, two_bytes = two ? 16 : 0, apart = two ? (second - first) * 8 : 0;
+    auto walk = [&](const char* base, int64_t token_stride, int64_t head_stride) {
+        return Walk(base, token_stride, head_stride, sizeof(T), me.t0 + me.token, me.head, me.heads, me.step_tokens, me.step_heads, one ? first * 8 : 0);
     };
-    auto row_at = [&](int r) {
-        Row x{&a.q, 0, h0, r < rows && p < lanes};
-        if (r < rows) {
-            x.token = cut.by_heads.div(r);
-            x.head = h0 + r - x.token * heads;
+    Walk from = walk(of.x, of.token_stride, of.head_stride), to = walk(of.y, of.y_token_stride, of.y_head_stride);
+    auto issue = [&](int k, int stage) {
+        if (k + 1 < me.steps || me.last) {
+            const T* x = reinterpret_cast<const T*>(from.at);
+            Eight<T>::copy(ring, stage, 0, x, one_bytes);
+            Eight<T>::copy(ring, stage, kVecs, x + apart, two_bytes);
         }
-        if (x.head >= a.q.heads) {
-            x.head -= a.q.heads;
-            x.of = &a.k;
-            if (CACHE && x.head >= a.k.heads) {
-                x.head -= a.k.heads;
-                x.of = &a.v;
-            }
-        }
-        return x;
-    };
-    auto issue = [&](int r, int stage) {
-        const Row x = row_at(r);
-        const T* from = reinterpret_cast<const T*>(x.of->x) + (t0 + x.token) * x.of->token_stride + x.head * x.of->head_stride;
-        Eight<T>::copy(ring, stage, 0, x.in ? from + first * 8 : reinterpret_cast<const T*>(a.positions), x.in);
-        const bool both = x.in && second < l.vecs;
-        Eight<T>::copy(ring, stage, kVecs, both ? from + second * 8 : reinterpret_cast<const T*>(a.positions), both);
+        from.next(me.heads, me.step_heads);
     };
     begin_dependent();
     // the first rows are on their way while the tables are filled
 #pragma unroll
-    for (int k = 0; k < kStages<T> - 1; ++k) {
-        if (mine / (32 / L) * (32 / L) + k * groups < rows) issue(mine + k * groups, k);
+    for (int k = 0; k < S - 1; ++k) {
+        if (k < me.steps) issue(k, k);
         ring.commit();
     }
-    tables.fill_turns(a, t0, tokens);
-    tables.fill_weights(a, l);
-    if constexpr (CACHE) {
-        if (tid < tokens) {
-            const int64_t slot = slots[t0 + tid], all = c.num_pages * c.page_size;
-            Place to{-1, -1};
-            if (slot >= 0 && slot < all) {
-                const int64_t at = slot < 0x7fffffff ? page.div((int)slot) : slot / c.page_size, s = slot - at * c.page_size;
-                to.at = at * c.page_stride + s * c.slot_stride;
-                to.row = at * c.kv_heads * c.page_size + s;
-            } else if (slot >= all) {
-                record_error(status, kErrKvTable, (uint32_t)(t0 + tid));
-            }
-            s_place[tid] = to;
-        }
-    }
-    __syncthreads();
+    F2 wa[4] = {}, wb[4] = {};
+    if (!is_v) tables.fill_weights(of.weight, a.weight_type, l);
 
-    int stage = 0;
-    for (int r0 = tid / 32 * (32 / L); r0 < rows; r0 += groups) {  // the same for a warp
-        const Row row = row_at(r0 + tid % 32 / L);
+    // The row's token among those of the tables, the first of which is `done`, and the next filling.
+    int stage = 0, token = 0, done = 0, fill = 0;
+    for (int k = 0; k < me.steps; ++k) {
+        if (k == fill) {
+            const int2 range = me.tokens(jobs, k, groups);
+            if (k > 0) __syncthreads();
+            if (!is_v) tables.template fill_turns<kFine<T>>(a, me.t0 + range.x, range.y);
+            if constexpr (CACHE) {
+                for (int i = tid; !is_q && i < range.y; i += blockDim.x) {
+                    const int64_t t = me.t0 + range.x + i, slot = slots[t], all = c.num_pages * c.page_size;
+                    Place at{-1, -1};
+                    if (slot >= 0 && slot < all) {
+                        const int64_t index = slot < 0x7fffffff ? page.div((int)slot) : slot / c.page_size, s = slot - index * c.page_size;
+                        at.at = index * c.page_stride + s * c.slot_stride;
+                        at.row = index * c.kv_heads * c.page_size + s;
+                    } else if (slot >= all) {
+                        record_error(status, kErrKvTable, (uint32_t)t);
+                    }
+                    s_place[i] = at;
+                }
+            }
+            __syncthreads();
+            if (k == 0) {
+                token = me.token;
+                if (one && !is_v) tables.weights_of(p, wa, wb);
+            } else {
+                token -= range.x - done;
+            }
+            done = range.x;
+            fill += me.chunk;
+        }
+        // A step: a row of every group.
+        const bool in = (k + 1 < me.steps || me.last) && one;
         ring.wait();
-        float x[8], y[8];
+        F2 x[4], y[4];
         Eight<T>(ring, stage, 0).open(x);
         Eight<T>(ring, stage, kVecs).open(y);
         // the stage read in the last step is filled again
-        const int next = r0 + (kStages<T> - 1) * groups;
-        if (next < rows) issue(next + tid % 32 / L, stage == 0 ? kStages<T> - 1 : stage - 1);
+        if (k + S - 1 < me.steps) issue(k + S - 1, stage == 0 ? S - 1 : stage - 1);
         ring.commit();
-        stage = stage + 1 == kStages<T> ? 0 : stage + 1;
-
-        const bool is_q = row.of == &a.q, is_k = row.of == &a.k, is_v = CACHE && row.of == &a.v;
-        float sum = 0.0f;
+        stage = stage + 1 == S ? 0 : stage + 1;
+        if (!is_v) {
+            F2 sum = x[0] * x[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
-        sum = row_sum<L>(sum);
-        if (row.in && !is_v) {
-            const float inv = __frsqrt_rn(sum * inv_dim + a.eps);
-            float wa[8], wb[8];
-            tables.weights_of(is_k ? 1 : 0, p, wa, wb);
+            for (int i = 0; i < 4; ++i) {
+                if (i) sum = fma2(x[i], x[i], sum);
+                sum = fma2(y[i], y[i], sum);
+            }
+            const float inv = inverse_root<kFine<T>>(row_sum<L>(sum_f2(sum)) * inv_dim + a.eps);
+            const F2 both = f2(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] *= inv * wa[i];
-                y[i] *= inv * wb[i];
+            for (int i = 0; i < 4; ++i) {
+                x[i] = x[i] * (wa[i] * both);
+                y[i] = y[i] * (wb[i] * both);
             }
-            if (p < l.pairs) {
-                float co[8], si[8];
-                tables.turns_of(row.token, p, co, si);
-                turn16<1>(x, y, co, si, a.interleaved);
+            if (p < l.pairs && in) {
+                F2 co[4], si[4];
+                tables.turns_of(token, p, co, si);
+                turn16<false>(x, y, co, si, a.interleaved);
             }
         }
-        if constexpr (CACHE) {
-            const Place to = s_place[row.token];
-            const bool put = row.in && !is_q && to.at >= 0;
-            if (!is_q || BITS == 4) store_cached<BITS, T>(c, to, is_v, put ? row.head : 0, l, p, put, x, y);  // 4 bits: lanes exchange largest elements
-            if (put && is_k && p == 0 && c.weight) c.weight[to.row + (int64_t)row.head * c.page_size] = 0.0f;
-            if (!is_q) continue;
+        if (is_q || !CACHE) {
+            if (in) {
+                T* y_row = reinterpret_cast<T*>(const_cast<char*>(to.at));
+                Eight<T>::store(y_row, x);
+                if (two) Eight<T>::store(y_row + apart, y);
+            }
+        } else if constexpr (CACHE) {
+            const Place at = s_place[in ? token : 0];
+            const bool put = in && at.at >= 0;
+            store_cached<BITS, T>(c, at, is_v, put ? to.head : 0, l, p, put, x, y);
+            if (put && !is_v && p == 0 && c.weight) c.weight[at.row + (int64_t)to.head * c.page_size] = 0.0f;
         }
-        if (row.in) {
-            T* to = reinterpret_cast<T*>(row.of->y) + (t0 + row.token) * row.of->y_token_stride + row.head * row.of->y_head_stride;
-            Eight<T>::store(to + first * 8, x);
-            if (second < l.vecs) Eight<T>::store(to + second * 8, y);
-        }
+        token += me.step_tokens + (to.next(me.heads, me.step_heads) ? 1 : 0);
     }
     ring.wait_all();
 }
 
 // ---- backward ----
 
-// A CTA has rows of q or of k alone, tiles of `per` tokens of them, and leaves its
-// share of the weight's gradient in `parts`, head_dim numbers; which tiles are
-// whose, and so the order of all sums, is fixed.  The first q_ctas CTAs have q's.
+// A CTA has consecutive rows of q or of k, and leaves its share of the weight's
+// gradient in `parts`, head_dim numbers: which rows are whose, and so the order of
+// all sums, is fixed.
 template <typename T, int L>
-__global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout l, int q_ctas, int per_q, int per_k, FastDiv by_q, FastDiv by_k, float inv_dim, float* parts) {
+__global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, float* parts) {
     extern __shared__ float4 s_tables[];
-    const bool is_k = blockIdx.x >= q_ctas;
-    const QkRows& of = is_k ? a.k : a.q;
-    const FastDiv by_heads = is_k ? by_k : by_q;
-    const int per = is_k ? per_k : per_q, cta = is_k ? blockIdx.x - q_ctas : blockIdx.x, ctas = is_k ? gridDim.x - q_ctas : q_ctas;
-    const Tables tables(s_tables, l, max(per_q, per_k));
-    constexpr int kVecs = Eight<T>::kVecs;
-    const Ring<4 * kVecs, kStages<T>> ring(tables.end());
+    constexpr int kVecs = Eight<T>::kVecs, S = kStages<T>;
+    const Tables tables(s_tables, l, most_tokens);
+    const Ring<4 * kVecs, S> ring(tables.end());
     const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
-    const int64_t tiles = (a.tokens + per - 1) / per;
+    const Share me(a, jobs, tid / L, groups);
+    const QkRows& of = me.kind == 0 ? a.q : a.k;
+    const bool one = p < lanes, two = one && second < l.vecs;
+    const int one_bytes = one ? 16 : 0, two_bytes = two ? 16 : 0, apart = two ? (second - first) * 8 : 0;
+    auto walk = [&](const char* base, int64_t token_stride, int64_t head_stride) {
+        return Walk(base, token_stride, head_stride, sizeof(T), me.t0 + me.token, me.head, me.heads, me.step_tokens, me.step_heads, one ? first * 8 : 0);
+    };
+    Walk from = walk(of.x, of.token_stride, of.head_stride), grad = walk(of.g, of.g_token_stride, of.g_head_stride), to = walk(of.y, of.y_token_stride, of.y_head_stride);
+    auto issue = [&](int k, int stage) {
+        if (k + 1 < me.steps || me.last) {
+            const T *x = reinterpret_cast<const T*>(from.at), *g = reinterpret_cast<const T*>(grad.at);
+            Eight<T>::copy(ring, stage, 0, x, one_bytes);
+            Eight<T>::copy(ring, stage, kVecs, x + apart, two_bytes);
+            Eight<T>::copy(ring, stage, 2 * kVecs, g, one_bytes);
+            Eight<T>::copy(ring, stage, 3 * kVecs, g + apart, two_bytes);
+        }
+        from.next(me.heads, me.step_heads);
+        grad.next(me.heads, me.step_heads);
+    };
     begin_dependent();
-    // A step is one row of every group; the steps of all tiles are one sequence, so
-    // that the ring does not run empty between them.
-    struct At {
-        int64_t tile;
-        int r0;  // of the warp's first row
-    };
-    auto rows_in = [&](int64_t tile) { return (int)min((int64_t)per, a.tokens - tile * per) * of.heads; };
-    const int warp_row = tid / 32 * (32 / L);
-    auto settle = [&](At& x) {  // on to the next tile that has rows for this warp
-        while (x.tile < tiles && x.r0 >= rows_in(x.tile)) {
-            x.tile += ctas;
-            x.r0 = warp_row;
-        }
-    };
-    auto issue = [&](const At& at, int stage) {
-        const int r = at.r0 + tid % 32 / L;
-        const bool in = r < rows_in(at.tile) && p < lanes, both = in && second < l.vecs;
-        const int token = in ? by_heads.div(r) : 0, head = in ? r - token * of.heads : 0;
-        const int64_t t = at.tile * per + token;
-        const T* x = reinterpret_cast<const T*>(of.x) + t * of.token_stride + head * of.head_stride;
-        const T* g = reinterpret_cast<const T*>(of.g) + t * of.g_token_stride + head * of.g_head_stride;
-        const T* any = reinterpret_cast<const T*>(a.positions);
-        Eight<T>::copy(ring, stage, 0, in ? x + first * 8 : any, in);
-        Eight<T>::copy(ring, stage, kVecs, both ? x + second * 8 : any, both);
-        Eight<T>::copy(ring, stage, 2 * kVecs, in ? g + first * 8 : any, in);
-        Eight<T>::copy(ring, stage, 3 * kVecs, both ? g + second * 8 : any, both);
-    };
-    At ld{cta, warp_row};
 #pragma unroll
-    for (int k = 0; k < kStages<T> - 1; ++k) {
-        settle(ld);
-        if (ld.tile < tiles) {
-            issue(ld, k);
-            ld.r0 += groups;
-        }
+    for (int k = 0; k < S - 1; ++k) {
+        if (k < me.steps) issue(k, k);
         ring.commit();
     }
-    tables.fill_weights(a, l);
-    __syncthreads();
-    float wa[8] = {}, wb[8] = {}, da[8] = {}, db[8] = {};
-    if (p < lanes) tables.weights_of(is_k ? 1 : 0, p, wa, wb);
-    int stage = 0;
-    for (int64_t tile = cta; tile < tiles; tile += ctas) {
-        const int64_t t0 = tile * per;
-        const int tokens = (int)min((int64_t)per, a.tokens - t0), rows = tokens * of.heads;
-        __syncthreads();
-        tables.fill_turns(a, t0, tokens);
-        __syncthreads();
-        for (int r0 = warp_row; r0 < rows; r0 += groups) {
-            const int r = r0 + tid % 32 / L;
-            const bool in = r < rows && p < lanes;
-            const int token = in ? by_heads.div(r) : 0, head = in ? r - token * of.heads : 0;
-            ring.wait();
-            float x[8], y[8], g[8], h[8];
-            Eight<T>(ring, stage, 0).open(x);
-            Eight<T>(ring, stage, kVecs).open(y);
-            Eight<T>(ring, stage, 2 * kVecs).open(g);
-            Eight<T>(ring, stage, 3 * kVecs).open(h);
-            settle(ld);
-            if (ld.tile < tiles) {
-                issue(ld, stage == 0 ? kStages<T> - 1 : stage - 1);
-                ld.r0 += groups;
+    tables.fill_weights(of.weight, a.weight_type, l);
+    F2 wa[4] = {}, wb[4] = {}, da[4] = {}, db[4] = {};
+    int stage = 0, token = 0, done = 0, fill = 0;
+    for (int k = 0; k < me.steps; ++k) {
+        if (k == fill) {
+            const int2 range = me.tokens(jobs, k, groups);
+            if (k > 0) __syncthreads();
+            tables.template fill_turns<kFine<T>>(a, me.t0 + range.x, range.y);
+            __syncthreads();
+            if (k == 0) {
+                token = me.token;
+                if (one) tables.weights_of(p, wa, wb);
+            } else {
+                token -= range.x - done;
             }
-            ring.commit();
-            stage = stage + 1 == kStages<T> ? 0 : stage + 1;
-            if (p < l.pairs) {
-                float co[8], si[8];
-                tables.turns_of(token, p, co, si);
-                turn16<-1>(g, h, co, si, a.interleaved);
-            }
-            float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sum += x[i] * x[i] + y[i] * y[i];
-                dot += g[i] * wa[i] * x[i] + h[i] * wb[i] * y[i];
-            }
-            sum = row_sum<L>(sum);
-            dot = row_sum<L>(dot);
-            if (!in) continue;
-            const float inv = __frsqrt_rn(sum * inv_dim + a.eps), mean = inv * inv * dot * inv_dim;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                da[i] += g[i] * (x[i] * inv);
-                db[i] += h[i] * (y[i] * inv);
-                x[i] = inv * (g[i] * wa[i] - x[i] * mean);
-                y[i] = inv * (h[i] * wb[i] - y[i] * mean);
-            }
-            T* to = reinterpret_cast<T*>(of.y) + (t0 + token) * of.y_token_stride + head * of.y_head_stride;
-            Eight<T>::store(to + first * 8, x);
-            if (second < l.vecs) Eight<T>::store(to + second * 8, y);
+            done = range.x;
+            fill += me.chunk;
         }
+        const bool in = (k + 1 < me.steps || me.last) && one;
+        ring.wait();
+        F2 x[4], y[4], g[4], h[4];
+        Eight<T>(ring, stage, 0).open(x);
+        Eight<T>(ring, stage, kVecs).open(y);
+        Eight<T>(ring, stage, 2 * kVecs).open(g);
+        Eight<T>(ring, stage, 3 * kVecs).open(h);
+        if (k + S - 1 < me.steps) issue(k + S - 1, stage == 0 ? S - 1 : stage - 1);
+        ring.commit();
+        stage = stage + 1 == S ? 0 : stage + 1;
+        if (p < l.pairs && in) {
+            F2 co[4], si[4];
+            tables.turns_of(token, p, co, si);
+            turn16<true>(g, h, co, si, a.interleaved);
+        }
+        F2 sum = x[0] * x[0], dot = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i) sum = fma2(x[i], x[i], sum);
+            sum = fma2(y[i], y[i], sum);
+            dot = fma2(g[i] * wa[i], x[i], dot);
+            dot = fma2(h[i] * wb[i], y[i], dot);
+        }
+        const float squares = row_sum<L>(sum_f2(sum)), dots = row_sum<L>(sum_f2(dot));
+        if (in) {
+            const float inv = inverse_root<kFine<T>>(squares * inv_dim + a.eps), mean = -inv * inv * dots * inv_dim;
+            const F2 both = f2(inv, inv), means = f2(mean, mean);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = x[i] * both;
+                y[i] = y[i] * both;
+                da[i] = fma2(g[i], x[i], da[i]);
+                db[i] = fma2(h[i], y[i], db[i]);
+                x[i] = fma2(x[i], means, (g[i] * wa[i]) * both);
+                y[i] = fma2(y[i], means, (h[i] * wb[i]) * both);
+            }
+            T* y_row = reinterpret_cast<T*>(const_cast<char*>(to.at));
+            Eight<T>::store(y_row, x);
+            if (two) Eight<T>::store(y_row + apart, y);
+        }
+        token += me.step_tokens + (to.next(me.heads, me.step_heads) ? 1 : 0);
     }
     ring.wait_all();
     // the CTA's groups, added up in their order
     float* s_sums = reinterpret_cast<float*>(s_tables);  // groups x lanes x 16
     __syncthreads();
-    if (p < lanes) {
+    if (one) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s_sums[(tid / L * lanes + p) * 16 + i] = da[i];
-            s_sums[(tid / L * lanes + p) * 16 + 8 + i] = db[i];
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = open_f2(da[i]), y = open_f2(db[i]);
+            float* at = s_sums + (tid / L * lanes + p) * 16 + 2 * i;
+            at[0] = x.x;
+            at[1] = x.y;
+            at[8] = y.x;
+            at[9] = y.y;
         }
     }
     __syncthreads();
@@ -519,8 +627,32 @@ __global__ void __launch_bounds__(1024) k_qk_rope_weights(const float* parts, in
 
 Layout layout_of(const QkRope& a) { return Layout{a.head_dim / 8, a.rotary_dim / 16}; }
 
-constexpr int kBackThreads = 256;
-constexpr int kBackMostPerSm = 4;
+constexpr int kSteps = 16;  // most rows of a group between two fillings of the tables
+// CTAs for each that fits the GPU at a time: some tensors' rows take longer than
+// others', and waves even that out (16384 x 40 rows 59.5 us with one, 56.2 with two,
+// 56.2 four, 57.4 eight; 20000 x 48 into an 8-bit cache 111.7, 91.0, 83.6 with three,
+// 90.2 four, 88.1 eight).
+constexpr int waves_of(int bits) { return bits ? 3 : 2; }
+constexpr int kBackThreads = 256, kBackMostPerSm = 4;
+
+// Rows over about `most` CTAs, whole steps each, and the tokens that a filling of the
+// tables has at most: groups and two.
+Jobs jobs_of(const QkRope& a, int groups, int64_t most, int* grid, int* tokens) {
+    const int heads[3] = {a.q.heads, a.k.heads, a.v.heads};
+    Jobs jobs;
+    *grid = *tokens = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t all = a.tokens * heads[i], share = std::max<int64_t>(1, most * heads[i] / (heads[0] + heads[1] + heads[2]));
+        const int64_t steps = std::min<int64_t>(std::max<int64_t>(1, (all + share * groups - 1) / (share * groups)), 1 << 20), rows = steps * groups;
+        jobs.steps[i] = (int)steps;
+        jobs.chunk[i] = (int)std::min<int64_t>(steps, std::max(1, std::min(kSteps, heads[i])));
+        jobs.ctas[i] = (int)((all + rows - 1) / rows);
+        jobs.by_heads[i] = FastDiv(std::max(1, heads[i]));
+        *grid += jobs.ctas[i];
+        if (all > 0) *tokens = std::max(*tokens, (jobs.chunk[i] * groups + heads[i] - 2) / heads[i] + 1);
+    }
+    return jobs;
+}
 
 template <typename F> cudaError_t for_lanes(int lanes, F&& f) {
     if (lanes <= 2) return f(std::integral_constant<int, 2>());
@@ -537,48 +669,34 @@ template <typename F> cudaError_t for_type(KvElem type, F&& f) {
 template <typename T, int L, int BITS>
 cudaError_t run(const QkRope& a, const KvPages& c, const int64_t* slots, int sms, uint32_t* status, cudaStream_t s) {
     const Layout l = layout_of(a);
-    const int heads = a.q.heads + a.k.heads + a.v.heads;
-    Cut cut;
-    int threads = 256;
-    cut.tokens = std::max(1, std::min(16, 256 / heads));
-    cut.splits = 1;
-    while (cut.tokens > 1 && (a.tokens + cut.tokens - 1) / cut.tokens < 4 * (int64_t)sms) cut.tokens /= 2;
-    if (a.tokens < 2 * (int64_t)sms) {  // few tokens: a part of the heads each
-        threads = 128;
-        cut.splits = (int)std::min<int64_t>((heads + threads / L - 1) / (threads / L), std::max<int64_t>(1, 2 * sms / a.tokens));
-    }
-    cut.heads = (heads + cut.splits - 1) / cut.splits;
-    cut.splits = (heads + cut.heads - 1) / cut.heads;
-    cut.by_heads = FastDiv(cut.heads);
     auto* kern = k_qk_rope<T, L, BITS>;
-    const size_t smem = Tables::bytes(l.vecs, l.pairs, cut.tokens) + Ring<2 * Eight<T>::kVecs, kStages<T>>::bytes(threads);
+    using Rows = Ring<2 * Eight<T>::kVecs, kStages<T>>;
     KernelSetup su;
-    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kMostThreads, Tables::bytes(32, 16, 16) + Ring<2 * Eight<T>::kVecs, kStages<T>>::bytes(kMostThreads), &su);
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kMostThreads, Tables::bytes(Layout{2 * L, L}, kMostThreads / L + 2) + Rows::bytes(kMostThreads), &su);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, (size_t)((a.tokens + cut.tokens - 1) / cut.tokens) * cut.splits, threads, smem, 1, s, a, l, cut, 1.0f / a.head_dim, c, slots,
+    // Few rows: small CTAs of one step each; more: CTAs that fill the GPU once.
+    const int64_t rows = a.tokens * (a.q.heads + a.k.heads + a.v.heads);
+    const int threads = rows < (int64_t)sms * 4 * (kMostThreads / L) ? 128 : kMostThreads;
+    int grid = 0, tokens = 0;
+    const Jobs jobs = jobs_of(a, threads / L, (int64_t)sms * su.blocks_per_sm * (kMostThreads / threads) * waves_of(BITS), &grid, &tokens);
+    return launch_dependent(kern, (size_t)grid, threads, Tables::bytes(l, tokens) + Rows::bytes(threads), 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, c, slots,
                             FastDiv(BITS ? c.page_size : 1), status);
 }
 
 template <typename T, int L> cudaError_t run_back(const QkRope& a, float* dq_weight, float* dk_weight, float* parts, int sms, cudaStream_t s) {
     const Layout l = layout_of(a);
     auto* kern = k_qk_rope_back<T, L>;
-    const int lanes = (l.vecs + 1) / 2, most_tokens = 16;
-    // tiles of about 8 rows a group
-    auto tokens_of = [&](int heads) { return std::max(1, std::min(most_tokens, 8 * kBackThreads / L / std::max(1, heads))); };
-    const int per_q = tokens_of(a.q.heads), per_k = tokens_of(a.k.heads);
-    const size_t ring = Ring<4 * Eight<T>::kVecs, kStages<T>>::bytes(kBackThreads);
-    const size_t smem = std::max(Tables::bytes(l.vecs, l.pairs, std::max(per_q, per_k)) + ring, (size_t)kBackThreads / L * lanes * 16 * 4);
+    const int lanes = (l.vecs + 1) / 2, groups = kBackThreads / L;
+    using Rows = Ring<4 * Eight<T>::kVecs, kStages<T>>;
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kBackThreads, std::max(Tables::bytes(32, 16, most_tokens) + ring, (size_t)kBackThreads * 64), &su);
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kBackThreads, Tables::bytes(Layout{2 * L, L}, kBackThreads / L + 2) + Rows::bytes(kBackThreads), &su);
     if (e != cudaSuccess) return e;
-    // CTAs for q and for k by their rows
-    const int64_t most = (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), heads = a.q.heads + a.k.heads;
-    auto ctas_of = [&](int h, int per) { return h == 0 ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>((a.tokens + per - 1) / per, most * h / heads)); };
-    const int q_ctas = ctas_of(a.q.heads, per_q), ctas = q_ctas + ctas_of(a.k.heads, per_k);
-    e = launch_dependent(kern, ctas, kBackThreads, smem, 1, s, a, l, q_ctas, per_q, per_k, FastDiv(std::max(1, a.q.heads)), FastDiv(std::max(1, a.k.heads)), 1.0f / a.head_dim,
-                         parts);
+    int grid = 0, tokens = 0;
+    const Jobs jobs = jobs_of(a, groups, (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), &grid, &tokens);
+    const size_t smem = std::max(Tables::bytes(l, tokens) + Rows::bytes(kBackThreads), (size_t)groups * lanes * 16 * 4);
+    e = launch_dependent(kern, grid, kBackThreads, smem, 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, parts);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), q_ctas, ctas, a.head_dim, dq_weight, dk_weight);
+    return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), jobs.ctas[0], grid, a.head_dim, dq_weight, dk_weight);
 }
 
 }  // namespace
