@@ -231,3 +231,16 @@ def test_evict_after_decode_steps_in_4_bits(ss):
             w = np.exp(x - x.max())
             want = (w / w.sum()) @ v64[idx, h]
             assert (np.abs(out[b, j] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(v64[:, h]).max()).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "e2m1"])
+def test_example_serves_requests(cache):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_steps.py")
+    spec = importlib.util.spec_from_file_location("serve_steps", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.run(batch=5, heads=2, group=2, dim=64, prompt=70, steps=40, ends=0.05, cache=cache)
+    assert got["device_lens"] == got["lens"] and got["finite"] and got["ended"] > 0
+    assert got["free"] == got["pages"] - sum(-(-n // got["page"]) for n in got["lens"])
