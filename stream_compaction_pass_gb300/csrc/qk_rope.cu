@@ -7,10 +7,11 @@
 // g: dw = sum r x h over all rows, and dx = r (w h - x r^2 mean(w h x)).  An angle
 // is a fraction of a turn: position times frequency modulo 1, which 64-bit integers
 // multiply exactly with the frequency in units of 2^-64 turns, however far the
-// position.  Of what is left, fp32 rows take CUDA's sincospif and the rounded
-// reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1, 2 units
-// in the last place) are a thousandth of the outputs' rounding and whose
-// instructions are fewer by 60 and 20.
+// position.  Of what is left, fp32 rows and those for narrow caches (where a value
+// beside a tie of two codes moves by a whole step) take CUDA's sincospif and the
+// rounded reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1,
+// 2 units in the last place) are a thousandth of the outputs' rounding and whose
+// instructions are fewer (57.5 us without, 55.4 with them, of 16384 x 40 rows).
 //
 // What bounds it.  Memory: every row is read once and written once (backward:
 // two and one), for about 10 operations an element, so that instructions come
@@ -253,7 +254,6 @@ template <bool BACK> __device__ __forceinline__ void turn16(F2 (&a)[4], F2 (&b)[
     }
 }
 
-template <typename T> constexpr bool kFine = sizeof(T) == 4;
 template <bool FINE> __device__ __forceinline__ float inverse_root(float x) { return FINE ? __frsqrt_rn(x) : rsqrtf(x); }
 
 template <int L> __device__ __forceinline__ float row_sum(float x) {
@@ -371,7 +371,7 @@ struct Share {
 template <typename T, int L, int BITS>
 __global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 4) k_qk_rope(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, KvPages c, const int64_t* slots, FastDiv page,
                                                           uint32_t* status) {
-    constexpr bool CACHE = BITS > 0;
+    constexpr bool CACHE = BITS > 0, kFine = sizeof(T) == 4 || BITS == 8 || BITS == 4;
     constexpr int kVecs = Eight<T>::kVecs, S = kStages<T>;
     extern __shared__ float4 s_tables[];
     __shared__ Place s_place[CACHE ? kMostThreads / L + 2 : 1];
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 
         if (k == fill) {
             const int2 range = me.tokens(jobs, k, groups);
             if (k > 0) __syncthreads();
-            if (!is_v) tables.template fill_turns<kFine<T>>(a, me.t0 + range.x, range.y);
+            if (kFine && sizeof(T) < 4 && is_q) tables.template fill_turns<false>(a, me.t0 + range.x, range.y);
+            else if (!is_v) tables.template fill_turns<kFine>(a, me.t0 + range.x, range.y);
             if constexpr (CACHE) {
                 for (int i = tid; !is_q && i < range.y; i += blockDim.x) {
                     const int64_t t = me.t0 + range.x + i, slot = slots[t], all = c.num_pages * c.page_size;
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 
                 if (i) sum = fma2(x[i], x[i], sum);
                 sum = fma2(y[i], y[i], sum);
             }
-            const float inv = inverse_root<kFine<T>>(row_sum<L>(sum_f2(sum)) * inv_dim + a.eps);
+            const float inv = inverse_root<kFine>(row_sum<L>(sum_f2(sum)) * inv_dim + a.eps);
             const F2 both = f2(inv, inv);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout 
         if (k == fill) {
             const int2 range = me.tokens(jobs, k, groups);
             if (k > 0) __syncthreads();
-            tables.template fill_turns<kFine<T>>(a, me.t0 + range.x, range.y);
+            tables.template fill_turns<sizeof(T) == 4>(a, me.t0 + range.x, range.y);
             __syncthreads();
             if (k == 0) {
                 token = me.token;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(kMostThreads) k_qk_rope_back(QkRope a, Layout 
         }
         const float squares = row_sum<L>(sum_f2(sum)), dots = row_sum<L>(sum_f2(dot));
         if (in) {
-            const float inv = inverse_root<kFine<T>>(squares * inv_dim + a.eps), mean = -inv * inv * dots * inv_dim;
+            const float inv = inverse_root<sizeof(T) == 4>(squares * inv_dim + a.eps), mean = -inv * inv * dots * inv_dim;
             const F2 both = f2(inv, inv), means = f2(mean, mean);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
