@@ -93,12 +93,15 @@ __device__ __forceinline__ void move_rows(const KvPages& c, const KvTable& t, co
                 const int64_t src_row = ((int64_t)from * c.kv_heads + h) * c.page_size + fs, dst_row = ((int64_t)to * d.kv_heads + h) * d.page_size + ts;
                 if (d.weight) d.weight[dst_row] = c.weight[src_row];
                 if (c.type == KvElem::E2M1) {  // the blocks' scales: 4, 8 or 16 bytes of k and of v
-                    const int words = c.head_dim / 64;
-                    auto words_of = [&](uint8_t* p, int64_t row) { return reinterpret_cast<uint32_t*>(p) + row * words; };
-                    for (int i = 0; i < words; ++i) {
-                        words_of(d.k_block, dst_row)[i] = words_of(c.k_block, src_row)[i];
-                        words_of(d.v_block, dst_row)[i] = words_of(c.v_block, src_row)[i];
-                    }
+                    auto copy = [&](auto x) {
+                        using X = decltype(x);
+                        const X k = reinterpret_cast<const X*>(c.k_block)[src_row], v = reinterpret_cast<const X*>(c.v_block)[src_row];
+                        reinterpret_cast<X*>(d.k_block)[dst_row] = k;
+                        reinterpret_cast<X*>(d.v_block)[dst_row] = v;
+                    };
+                    if (c.head_dim == 64) copy(uint32_t());
+                    else if (c.head_dim == 128) copy(uint2());
+                    else copy(uint4());
                 }
             }
         }
