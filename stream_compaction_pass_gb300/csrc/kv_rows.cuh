@@ -341,9 +341,12 @@ template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
         __device__ __forceinline__ void word(int i, uint32_t (&f)[4]) const {
             const uint4& x = w[i / 4];
             e2m1x8_f16(i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w, f);
-            const uint32_t scale = __byte_perm(s[i / 4], 0, i / 2 % 2 ? 0x3232 : 0x1010);
+            const __half2 both = *reinterpret_cast<const __half2*>(&s[i / 4]), scale = i / 2 % 2 ? __high2half2(both) : __low2half2(both);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = mul_f16x2(f[k], scale);
+            for (int k = 0; k < 4; ++k) {
+                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&f[k]), scale);
+                f[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
         }
     };
     static constexpr int kKeyWords = DP / 32;
@@ -523,14 +526,24 @@ template <typename QT, int BITS, int DP, int T> struct Rows16 : RowsBase<QT, BIT
             }
         }
         const bool whole = t.whole(p0, T);
+        if (BITS == 4 && whole) {  // instructions bound 4-bit tiles: no selects where nothing is hidden (477 / 445 us)
 #pragma unroll
-        for (int pt = 0; pt < kPT; ++pt)
+            for (int pt = 0; pt < kPT; ++pt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool see = whole || t.visible(p0 + (BITS == 4 ? row4(2 * q4 + e) : 2 * q4 + e) + pt * 8);
-                x[pt][e] = see ? x[pt][e] * sl0 : -INFINITY;
-                x[pt][2 + e] = see ? x[pt][2 + e] * sl1 : -INFINITY;
-            }
+                for (int e = 0; e < 2; ++e) {
+                    x[pt][e] *= sl0;
+                    x[pt][2 + e] *= sl1;
+                }
+        } else {
+#pragma unroll
+            for (int pt = 0; pt < kPT; ++pt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool see = whole || t.visible(p0 + (BITS == 4 ? row4(2 * q4 + e) : 2 * q4 + e) + pt * 8);
+                    x[pt][e] = see ? x[pt][e] * sl0 : -INFINITY;
+                    x[pt][2 + e] = see ? x[pt][2 + e] * sl1 : -INFINITY;
+                }
+        }
         if (scores) {
 #pragma unroll
             for (int pt = 0; pt < kPT; ++pt) {
@@ -807,13 +820,20 @@ template <typename QT, int BITS, int DP, int T> struct Rows8 : RowsBase<QT, BITS
         }
         const bool whole = t.whole(p0, T);
         const int at = BITS == 4 ? row4(g) : g;  // position of this lane's rows
+        if (BITS == 4 && whole) {  // as in Rows16
 #pragma unroll
-        for (int h = 0; h < kHB; ++h)
+            for (int h = 0; h < kHB; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool see = whole || t.visible(p0 + 16 * h + at + (e >> 1) * 8);
-                x[h][e] = see ? (kSplit ? x[h][e] + z[kSplit ? h : 0][e] : x[h][e]) * (e & 1 ? sl1 : sl0) : -INFINITY;
-            }
+                for (int e = 0; e < 4; ++e) x[h][e] *= e & 1 ? sl1 : sl0;
+        } else {
+#pragma unroll
+            for (int h = 0; h < kHB; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool see = whole || t.visible(p0 + 16 * h + at + (e >> 1) * 8);
+                    x[h][e] = see ? (kSplit ? x[h][e] + z[kSplit ? h : 0][e] : x[h][e]) * (e & 1 ? sl1 : sl0) : -INFINITY;
+                }
+        }
         if (scores) {
 #pragma unroll
             for (int h = 0; h < kHB; ++h)
