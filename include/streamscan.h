@@ -287,6 +287,8 @@ ss_status ss_moe_counts_offsets(const int32_t *topk_ids, size_t m, int32_t num_e
  *     scratch would have to grow while its stream is being captured (or that
  *     is the first on that stream) returns SS_ERR_NO_MEMORY and enqueues
  *     nothing; one that makes it grow later leaves a captured graph its own.
+ *     Graphs captured from one stream share its scratch, and are replayed one
+ *     after the other.
  */
 typedef enum ss_elem { SS_BF16 = 0, SS_F16 = 1, SS_E4M3 = 2, SS_E2M1 = 3, SS_ELEM_F32 = 4 } ss_elem;
 
@@ -406,15 +408,16 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  * those of the inputs (dq and dk: the rows of an input or of a gradient of their
  * own, or apart from all) and of the weights, summed over all tokens and heads
  * in a fixed order (fp32, head_dim numbers each, or NULL).  The partial sums lie
- * in the stream's workspace: make one call before capturing a stream into a graph.
+ * in the stream's workspace: make one call before capturing a stream into a graph,
+ * and replay graphs that were captured from one stream one after the other.
  *
  * ss_kv_append_rope: the same with k's and v's rows written into a cache, v's as
  * they are: token t's to slot slots[t] (page * page_size + slot in the page, as
  * ss_kv_assign gives them; a negative one: nowhere).  What the cache holds is as
  * after ss_kv_append of y, which is not rounded to `type` before; the slots'
  * weights become 0.  Slots behind the pool are reported with the token.  No two
- * tokens share a slot.  type: SS_BF16 or SS_F16; rotary_dim a multiple of 32 for
- * an SS_E2M1 cache.
+ * tokens share a slot, and q_out no memory with the cache.  type: SS_BF16 or SS_F16;
+ * rotary_dim a multiple of 32 for an SS_E2M1 cache.
  */
 typedef struct ss_rows {
     void *data;
@@ -475,8 +478,8 @@ ss_status ss_kv_append_rope(const ss_kv_pages *cache, const int64_t *slots, cons
  * time, each cut below 2^-24 of its sum), exponentials are good to 2^-22, and
  * out is rounded once.  In the sum over v a weight has 16 bits (bf16 caches) or
  * 22 (fp16, e4m3 and e2m1 caches), and up to 2^-38 of the row's largest weight
- * more (fp16); it has 11 bits where q is bf16, the cache e4m3 or e2m1, and
- * head_dim at most 64 or q_heads more than 8 per key-value head.  lse and the
+ * more (fp16); it has 11 bits where q is bf16 and the cache e2m1, or e4m3
+ * with head_dim at most 64 or q_heads more than 8 per key-value head.  lse and the
  * gathered weights are of the fp32 scores.  bf16 queries of an e4m3 or e2m1 cache
  * are held to 2^-32 of their row's largest element.
  * q_heads <= 65536, at most 128 per key-value head, and (max_len / 16 + 1) *

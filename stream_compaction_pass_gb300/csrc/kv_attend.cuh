@@ -52,7 +52,7 @@ namespace cg = cooperative_groups;
 //     (21) 26.2 / 30.0, 1 x 48000 (31) 37.2 / 39.3; with weights 1 x 8000 (5)
 //     14.6 / 17.3, 1 x 16000 22.5 / 20.0, 4 x 8000 (10, on twice the SMs) 31.7 /
 //     33.2, 1 x 32000 41.3 / 35.4, 1 head x 16000 22.2 / 23.8.
-// 8-bit rows, groups above 8 and head_dim 256, whose tiles take a warp longer or
+// Narrow rows, groups above 8 and head_dim 256, whose tiles take a warp longer or
 // whose CTAs have fewer warps (`slow`), have lower limits, but where the clusters
 // hold three quarters of the SMs:
 //   8-bit: 1 x 16000 (5) 16.9 / 20.6, 1 x 32000 (10) 25.0 / 23.2, 1 x 64000 41.5
@@ -69,7 +69,6 @@ constexpr SmallLimits small_limits(bool slow, bool weights) {
     return slow ? (weights ? SmallLimits{5, 8} : SmallLimits{12, 24}) : weights ? SmallLimits{12, 12} : SmallLimits{24, 24};
 }
 constexpr int kSmallTiles = 24;  // the largest of them
-constexpr int small_tiles(int limit, int tile) { return tile == 64 ? limit / 2 : limit; }  // they are of tiles of 16 or 32
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightThreads = 256;
@@ -882,8 +881,8 @@ cudaError_t small_plan(const void* kern, size_t smem, const KvPages& c, const Kv
         if (units <= most) break;
     }
     const SmallLimits limits = small_limits(slow, a.weight_out != nullptr);
-    if (ranks == 0 || tiles > small_tiles(limits.many, tile) * ranks * warps) return cudaSuccess;
-    if (tiles > small_tiles(limits.few, tile) * ranks * warps) {
+    if (ranks == 0 || tiles > limits.many * ranks * warps) return cudaSuccess;
+    if (tiles > limits.few * ranks * warps) {
         KernelSetup su;
         const cudaError_t e = kernel_setup(kern, warps * 32, smem, &su);
         if (e != cudaSuccess || units * ranks * 4 < (int64_t)su.sms * 3) return e;
@@ -908,7 +907,7 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
     static_assert(smem <= 227 * 1024, "the ring does not fit in shared memory");
     auto* one = Small::small_kernel();
     static_assert(Small::kSmem <= 227 * 1024, "the ring does not fit in shared memory");
-    static_assert(small_tiles(kSmallTiles, Small::kTile) <= Small::RowsOf::kChain, "a small call sets nothing aside");
+    static_assert(kSmallTiles <= Small::RowsOf::kChain, "a small call sets nothing aside");
     constexpr bool slow = BITS < 16 || Rows::kHeads == 16 || DP == 256;
     SmallPlan small;
     cudaError_t e = small_plan(reinterpret_cast<const void*>(one), Small::kSmem, c, t, a, Rows::kHeads, Small::kWarps, Small::kTile, slow, &small);

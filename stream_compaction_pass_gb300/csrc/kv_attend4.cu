@@ -11,11 +11,11 @@ namespace {
 // and large ones spread what a tile costs at least: of 64 positions, with as many
 // warps, in fours for the SM's four schedulers, as registers and shared memory
 // allow, two stages each.  2.2 million positions of 8 x 8 heads of 128: tiles of 64
-// with 12 warps 477 us, 11 507, 8 580 (with two terms of P); of 32 with 16 warps
-// 530, 12 556, of 16 with 16 797 (at first).  32 x 4000 to 8000 positions, tiles of
-// 64 / 32: 16 heads of 64 59.7 / 70.6 us (16 warps), 16 query heads a key-value head
-// 76.8 / 84.4 (8 warps), of 64 84.7 / 96.5 (12); heads of 256, tiles of 32 / 16 58.0
-// / 69.7 (8).
+// with 12 warps 445 us, 11 482; of 32 with 16 warps 522, 12 507.  The ragged batch
+// with weights is the other way round, 85.6 / 84.8 / 84.6 / 82.0 us.  32 x 4000 to 8000
+// positions, tiles of 64 / 32 (at first): 16 heads of 64 59.7 / 70.6 us (16 warps),
+// 16 query heads a key-value head 76.8 / 84.4 (8 warps), of 64 84.7 / 96.5 (12); heads
+// of 256, tiles of 32 / 16 58.0 / 69.7 (8), with 16 query heads 93.6 / 112.0 (7).
 // Calls of one launch want few warps to start and more of them at work, hence
 // tiles of 32 with 8 warps: 1021 positions 6.8 us (12 warps 7.0, 16 9.0, tiles of 64
 // 8.3), 4000 8.3, 16,000 16.4.
@@ -27,7 +27,7 @@ template <typename QT> cudaError_t run_dim(const KvPages& c, const KvTable& t, c
     }
     if (c.head_dim == 64) return run<QT, Rows16<QT, 4, 64, 64>, 4, 64, 64, 12, 2, Shape<Rows16<QT, 4, 64, 32>, 4, 64, 32, 8, 3>>(c, t, a, mem, status, s);
     if (c.head_dim == 128) return run<QT, Rows16<QT, 4, 128, 64>, 4, 128, 64, 8, 2, Shape<Rows16<QT, 4, 128, 32>, 4, 128, 32, 8, 3>>(c, t, a, mem, status, s);
-    return run<QT, Rows16<QT, 4, 256, 16>, 4, 256, 16, 7, 5>(c, t, a, mem, status, s);
+    return run<QT, Rows16<QT, 4, 256, 32>, 4, 256, 32, 7, 2, Shape<Rows16<QT, 4, 256, 16>, 4, 256, 16, 7, 5>>(c, t, a, mem, status, s);
 }
 
 }  // namespace

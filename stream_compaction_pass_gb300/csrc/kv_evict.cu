@@ -11,13 +11,14 @@
 // counts.  The move copies the kept rows.
 //
 // What bounds it.  The move reads and writes every kept row once and is bound
-// by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  The
-// selection reads 4 bytes a position and is bound by latency: three passes, each
-// with a histogram, a scan and a barrier.  A row is one CTA's; where there are
-// few rows it is split over a cluster of up to 8 CTAs, which add up their
-// histograms in L2 and exchange counts through distributed shared memory.  128
-// rows of 60 to 131 thousand positions take 77 us, 118 where all weights are
-// equal, 192 rows of up to 9001 16 us, 8 rows of 2049 10 us.
+// by memory: 2.1 GB of 8-bit rows in 326 us, 0.95 of the copy rate.  Of 4-bit rows a
+// row's thread moves the block scales with the weight, 329 us for these rows,
+// selection and all (402 of 8 bits).  The selection reads 4 bytes a position and is
+// bound by latency: three passes, each with a histogram, a scan and a barrier.  A
+// row is one CTA's; where there are few rows it is split over a cluster of up to 8
+// CTAs, which add up their histograms in L2 and exchange counts through distributed
+// shared memory.  128 rows of 60 to 131 thousand positions take 77 us, 118 where all
+// weights are equal, 192 rows of up to 9001 16 us, 8 rows of 2049 10 us.
 #include <cooperative_groups.h>
 
 #include "kv.cuh"

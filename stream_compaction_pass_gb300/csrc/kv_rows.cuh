@@ -229,7 +229,6 @@ template <int BITS, int DP> __device__ __forceinline__ int v_at(int row, int v) 
     return row * kRowBytes + u * 16;
 }
 
-
 // The position, within its 16, of a product's row i over a 4-bit cache: of the
 // rows 0, 2, 4, 6 that one access to the values reads, half are odd positions,
 // and so are one of each two neighbours, for the keys.
@@ -258,16 +257,23 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
     return pack2<__half>(u.x * factor, u.y * factor);
 }
 
-// What both forms share.  8-bit caches multiply in fp16, which holds every
-// e4m3 value.  P enters the product with V as two 16-bit terms (kTwo), good to
-// 2^-16 of itself in bf16 and 2^-22 in fp16, below the rounding of out (2^-8,
+// What both forms share.  8- and 4-bit caches multiply in fp16, which holds every
+// e4m3 value, and every e2m1 value times an e4m3 scale (2 and 4 bits).  P enters
+// the product with V as two 16-bit terms (kTwo), good to 2^-16 of itself in bf16 and 2^-22 in fp16, below the rounding of out (2^-8,
 // 2^-11): 0.28 % of the ragged bf16 batch's outputs round to the other neighbour,
 // 0.13 % of an 8-bit cache's, against 0.07 and 0.12 % with fp32 weights.  One fp16
 // term, 2^-11, is left to bf16 outputs of 8-bit caches where two cost much (16
 // query heads a key-value head 84 / 95 us, head_dim 64 71 / 77): 7 % of them
 // round to the other neighbour, with the same error against the formula,
 // 1.65e-3.  (At head_dim 128 two terms cost nothing of 100 us, at 256 123 / 124.5,
-// at 80 60.7 / 64.4.)
+// at 80 60.7 / 64.4.)  So it is for all bf16 outputs of 4-bit caches, where the
+// instructions bound and two terms take 13 % (530 / 609 us of 2.2 million positions).
+//
+// 4-bit rows.  A code is opened by its conversion to fp16 and one multiplication by
+// its block's scale; keys in pairs of dimensions, as they lie, values in pairs of
+// positions, whose nibbles are put side by side first (4 instructions for 16).  That
+// makes 10 instructions for the 16 codes that one product takes of a lane's rows,
+// and 1170 a tile of 64 positions x 128, half of them these: 5.8 TB/s of 6.8.
 //
 // O is added up in the products' accumulators, which cut what falls below 24
 // bits instead of rounding it: an error of one sign, up to 2^-24 a product.  So
@@ -287,7 +293,6 @@ template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
     static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
     static constexpr int kRowBytes = DP * BITS / 8, kKS = DP / 16;
     static constexpr int kBlocks = DP / 16;  // scales of a 4-bit row; a tile's keys' scales follow its values, then the values'
-
 
     // Four elements of a query row for a narrow cache.  The products' index runs
     // over head_dim in another order there: step ks of lane q4 holds the four
