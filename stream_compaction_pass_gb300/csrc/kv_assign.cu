@@ -180,8 +180,8 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
             int pos[4];
             int64_t slot[4];
             int b = -1, end = 0, first = 0, old = 0, held = 0, index = -1;
-            int64_t base = -1;
-            bool ok = false;
+            int64_t base = 0;  // slot of the sequence's position 0, were all its pages like this one
+            bool ok = false, on_page = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int at = t0 + k;
@@ -208,9 +208,10 @@ template <Finish F> __global__ void __launch_bounds__(kThreads) k_kv_assign(KvTa
                 if (i != index) {
                     index = i;
                     const int page = checked(i < held ? t.pages[(int64_t)b * t.row_stride + i] : a.ring[ring_at(take[b] + i - held)], b);
-                    base = page < 0 ? -1 : ((int64_t)page - i) * a.page_size;
+                    on_page = page >= 0;
+                    base = ((int64_t)page - i) * a.page_size;
                 }
-                slot[k] = base == -1 ? -1 : base + pos[k];
+                slot[k] = on_page ? base + pos[k] : -1;
             }
             if (a.vectors && here == 4) {
                 if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);

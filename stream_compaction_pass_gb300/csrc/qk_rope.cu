@@ -695,6 +695,7 @@ template <typename T, int L> cudaError_t run_back(const QkRope& a, float* dq_wei
     if (e != cudaSuccess) return e;
     int grid = 0, tokens = 0;
     const Jobs jobs = jobs_of(a, groups, (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), &grid, &tokens);
+    if (grid > sms * kBackMostPerSm + 2) return cudaErrorInvalidValue;  // more rows than memory can hold
     const size_t smem = std::max(Tables::bytes(l, tokens) + Rows::bytes(kBackThreads), (size_t)groups * lanes * 16 * 4);
     e = launch_dependent(kern, grid, kBackThreads, smem, 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, parts);
     if (e != cudaSuccess) return e;

@@ -147,6 +147,22 @@ def test_many_tokens(ss, in_place):
     run(ss, lens, 32, counts, None, 4000, 100, in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_of_one_token(ss, in_place):
+    """A page number says nothing about the position that it holds: also page i - 1
+    at place i of a row."""
+    import torch
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = i32([[9, 0, 1, 2, 3, 4, 5, 6, 7, 8, 10, 11], [12, 13, 14, 15, 16, 17, 18, 19, 20, 21, 22, 23]])
+    lens, ring, state = i32([3, 0]), i32([2, 3, 4, 5, 6, 7] + [40 + i for i in range(6)]), i32([0, 12])
+    into = None if in_place else ss.KVTable(table.clone(), lens.clone())
+    left = None if in_place else state.clone()
+    slots, positions = torch.full((9,), -9, dtype=torch.int64, device="cuda"), torch.full((9,), -9, dtype=torch.int32, device="cuda")
+    ss.ss_kv_assign(ss.KVTable(table, lens), ss.KVFree(ring, state, num_pages=60), 1, counts=i32([6, 3]), into=into, left=left, positions=positions, slots=slots)
+    ok(ss)
+    assert slots.tolist() == [2, 3, 4, 5, 6, 7, 40, 41, 42] and positions.tolist() == [3, 4, 5, 6, 7, 8, 0, 1, 2]
+
+
 @pytest.mark.parametrize("given", [(), ("offsets",), ("positions",), ("slots",), ("positions", "slots")])
 def test_optional_outputs(ss, given):
     run(ss, [3, 40, 0], 16, [2, 30, 1], None, 9, given=given)
