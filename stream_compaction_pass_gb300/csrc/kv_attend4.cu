@@ -11,9 +11,9 @@ namespace {
 // and large ones spread what a tile costs at least: of 64 positions, with as many
 // warps, in fours for the SM's four schedulers, as registers and shared memory
 // allow, two stages each.  2.2 million positions of 8 x 8 heads of 128: tiles of 64
-// with 12 warps 445 us, 11 482; of 32 with 16 warps 522, 12 507.  The ragged batch
-// with weights is the other way round, 85.6 / 84.8 / 84.6 / 82.0 us.  32 x 4000 to 8000
-// positions, tiles of 64 / 32 (at first): 16 heads of 64 59.7 / 70.6 us (16 warps),
+// with 12 warps 445 us, 11 482; of 32 with 16 warps 522, 12 507.  (A ragged batch
+// with weights was the other way round, 85.6 / 84.8 / 84.6 / 82.0 us, until shares
+// counted the starts of rows: 72.6.)  32 x 4000 to 8000 positions, tiles of 64 / 32: 16 heads of 64 59.7 / 70.6 us (16 warps),
 // 16 query heads a key-value head 76.8 / 84.4 (8 warps), of 64 84.7 / 96.5 (12); heads
 // of 256, tiles of 32 / 16 58.0 / 69.7 (8), with 16 query heads 93.6 / 112.0 (7).
 // Calls of one launch want few warps to start and more of them at work, hence
