@@ -766,27 +766,30 @@ def _row_kind(name: str, dtype) -> int:
     return kind
 
 
+def _place(name: str, t):
+    """Address and strides of a (tokens, heads, head_dim) tensor."""
+    token, head, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t.data_ptr(), token, head
+
+
 def _rows(name: str, t, shape, dtype, device: int):
-    """Address and strides of a (tokens, heads, head_dim) tensor; shape None: no heads."""
+    """The place of rows whose shape, type and device are checked; shape None: no heads."""
     if t is None or shape is None:
         if (t is None) != (shape is None):
             raise ValueError(f"{name} is missing" if t is None else f"{name} has no input")
         return _NO_ROWS
-    if t.shape != shape or t.dtype is not dtype:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {str(dtype)[6:]} of shape {tuple(shape)}, got {str(t.dtype)[6:]} {tuple(t.shape)}")
-    token, head, unit = t.stride()
-    if unit != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
     if t.get_device() != device:
         raise _elsewhere(name, t, device)
-    return t.data_ptr(), token, head
+    return _place(name, t)
 
 
-def _weight(name: str, t, dim: int, dtype, device: int) -> int:
-    if t is None:
-        return 0
-    if t.dim() != 1 or t.shape[0] != dim or t.dtype is not dtype or (dim > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be contiguous, of shape {(dim,)}, and of the other weight's type")
+def _weight(name: str, t, dim, dtype, device: int) -> int:
+    if t.dtype is not dtype or t.shape != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {dim}, and of the other weight's type")
     if t.get_device() != device:
         raise _elsewhere(name, t, device)
     return t.data_ptr()
@@ -797,23 +800,32 @@ def _qk(q, k, q_weight, k_weight, rope, positions, eps: float):
     one = k if q is None else q
     if one is None:
         raise ValueError("q and k are both None")
-    if one.dim() != 3 or (k is not None and k.dim() != 3):
+    shape, dtype, device = one.shape, one.dtype, one.get_device()
+    q_shape, k_shape = None if q is None else shape, None if k is None else k.shape
+    if len(shape) != 3 or (k is not None and len(k_shape) != 3):
         raise ValueError("q and k must be (tokens, heads, head_dim)")
-    tokens, _, dim = one.shape
-    dtype, device = one.dtype, one.get_device()
-    q_shape, k_shape = None if q is None else q.shape, None if k is None else k.shape
-    if k is not None and (k_shape[0] != tokens or k_shape[2] != dim):
-        raise ValueError(f"q and k must be of the same tokens and head_dim, got {tuple(one.shape)} and {tuple(k_shape)}")
+    tokens, heads, dim = shape
+    kv_heads = 0
+    if k is not None:
+        of, kv_heads, wide = k_shape
+        if of != tokens or wide != dim or k.dtype is not dtype:
+            raise ValueError(f"q and k must be of the same tokens, head_dim and type, got {str(dtype)[6:]} {tuple(shape)} and {str(k.dtype)[6:]} {tuple(k_shape)}")
+        if k.get_device() != device:
+            raise _elsewhere("k", k, device)
     if device < 0:
         raise ValueError("q and k are not on a GPU")
     if rope.device != device:
         raise _elsewhere("rope", rope.turns, device)
-    weight = k_weight if q_weight is None else q_weight
-    weight_type = None if weight is None else weight.dtype
-    c = _QK.pack(_row_kind("q" if q is not None else "k", dtype), SS_ELEM_F32 if weight is None else _row_kind("q_weight", weight_type), dim,
-                 0 if q is None else q_shape[1], 0 if k is None else k_shape[1], eps, tokens, *_rows("q", q, q_shape, dtype, device),
-                 *_rows("k", k, k_shape, dtype, device), _weight("q_weight", q_weight, dim, weight_type, device), _weight("k_weight", k_weight, dim, weight_type, device),
-                 _like("positions", positions, (tokens,), "int32", device), *rope._c)
+    kind, weight, d_q, d_k = _row_kind("q" if q is not None else "k", dtype), SS_ELEM_F32, 0, 0
+    if q_weight is not None or k_weight is not None:
+        weight_type = (k_weight if q_weight is None else q_weight).dtype
+        weight = kind if weight_type is dtype else _row_kind("q_weight", weight_type)
+        if q_weight is not None:
+            d_q = _weight("q_weight", q_weight, (dim,), weight_type, device)
+        if k_weight is not None:
+            d_k = _weight("k_weight", k_weight, (dim,), weight_type, device)
+    c = _QK.pack(kind, weight, dim, 0 if q is None else heads, kv_heads, eps, tokens, *(_NO_ROWS if q is None else _place("q", q)),
+                 *(_NO_ROWS if k is None else _place("k", k)), d_q, d_k, _like("positions", positions, (tokens,), "int32", device), *rope._c)
     return c, q_shape, k_shape, dtype, device
 
 

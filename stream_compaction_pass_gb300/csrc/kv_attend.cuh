@@ -174,7 +174,7 @@ struct Cursor {
 };
 
 // DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros in shared
-// memory).  T positions per tile (16 or 32), NW warps of a CTA, S stages of
+// memory).  T positions per tile (16, 32 or 64), NW warps of a CTA, S stages of
 // each warp's ring.  Rows: Rows8 or Rows16.
 template <typename Rows, int BITS, int DP, int T, int NW, int S, bool SMALL>
 __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status);
