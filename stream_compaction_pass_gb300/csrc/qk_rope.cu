@@ -11,7 +11,8 @@
 // beside a tie of two codes moves by a whole step) take CUDA's sincospif and the
 // rounded reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1,
 // 2 units in the last place) are a thousandth of the outputs' rounding and whose
-// instructions are fewer (57.5 us without, 55.4 with them, of 16384 x 40 rows).
+// instructions are fewer (57.5 us without, 55.4 with them, of 16384 x 40 rows, in
+// CTAs of 256).
 //
 // What bounds it.  Memory: every row is read once and written once (backward:
 // two and one), for about 10 operations an element, so that instructions come
@@ -20,10 +21,10 @@
 // log2 L shuffles.  A CTA takes consecutive rows of one of the tensors, which
 // leaves it one set of strides and weights, and computes their tokens' sines and
 // cosines once, in shared memory; its threads copy the rows to come, each its own
-// vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 55.9
-// us, 0.88 of the copy rate, issuing in 80 % of the cycles; the gradients 89.3, 0.83,
-// which 111 registers and so two CTAs an SM bound; 20000 x 48 into an 8-bit cache
-// 87.7, 0.75, by quantisation's instructions (issue 77 %).
+// vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 54.9
+// us, 0.90 of the copy rate, issuing in 80 % of the cycles; the gradients 84.8, 0.87,
+// with the 16 warps an SM that 110 registers leave; 20000 x 48 into an 8-bit cache
+// 83.2, 0.79, by quantisation's instructions.
 #include <algorithm>
 
 #include "kv_quant.cuh"
@@ -32,9 +33,14 @@ namespace ss {
 
 namespace {
 
-constexpr int kMostThreads = 256;
+// Small CTAs: as many warps wait at a barrier as share its tables, and a rotation by
+// all 256 elements has a thread for each of its 128 angles.  Threads of 128 / 256, as
+// many warps an SM: backward 84.6 / 90.1 us, forward 55.3 / 56.1, into an 8-bit cache
+// 84.4 / 88.4 (64: 85.2, 55.7, 86.0).  With 20 warps backward instead of 16 96
+// registers are too few: 117.
+constexpr int kThreads = 128;
 // Rows of a ring: those on their way, and the one at hand.  Of tensors 3 (backward
-// 89.7 us, 4 92.6, 5 93.4; forward 55.8, 56.4, 60.7), into a cache 4 (88.3, 3 94.9).
+// 84.6 us, 4 87.1; forward 55.3, 54.9), into a cache 4 (84.4, 3 91.1, 5 86.6).
 template <int BITS> constexpr int kStages = BITS > 0 ? 4 : 3;
 
 __device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16, float x, float y) {
@@ -373,12 +379,12 @@ struct Share {
 
 // BITS 0: rows go to tensors; else k's and v's go to a cache of so many bits.
 template <typename T, int L, int BITS>
-__global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 4) k_qk_rope(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, KvPages c, const int64_t* slots, FastDiv page,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : BITS ? 6 : 8) k_qk_rope(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, KvPages c, const int64_t* slots, FastDiv page,
                                                           uint32_t* status) {
     constexpr bool CACHE = BITS > 0, kFine = sizeof(T) == 4 || BITS == 8 || BITS == 4;
     constexpr int kVecs = Eight<T>::kVecs, S = kStages<BITS>;
     extern __shared__ float4 s_tables[];
-    __shared__ Place s_place[CACHE ? kMostThreads / L + 2 : 1];
+    __shared__ Place s_place[CACHE ? kThreads / L + 2 : 1];
     const Tables tables(s_tables, l, most_tokens);
     const Ring<2 * kVecs, S> ring(tables.end());
     const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 2 : BITS ? 3 : 
 // gradient in `parts`, head_dim numbers: which rows are whose, and so the order of
 // all sums, is fixed.
 template <typename T, int L>
-__global__ void __launch_bounds__(kMostThreads, sizeof(T) == 4 ? 1 : 2) k_qk_rope_back(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, float* parts) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) k_qk_rope_back(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, float* parts) {
     extern __shared__ float4 s_tables[];
     constexpr int kVecs = Eight<T>::kVecs, S = kStages<0>;
     const Tables tables(s_tables, l, most_tokens);
@@ -632,17 +638,18 @@ __global__ void __launch_bounds__(1024) k_qk_rope_weights(const float* parts, in
 
 Layout layout_of(const QkRope& a) { return Layout{a.head_dim / 8, a.rotary_dim / 16}; }
 
-constexpr int kSteps = 16;  // most rows of a group between two fillings of the tables
+// Most rows of a group between two fillings of the tables (into an 8-bit cache 83.3 us,
+// 84.4 with 16, 85.3 with 8; backward 84.6 with 16, 86.2 with 32).
+constexpr int kSteps = 32, kBackSteps = 16;
 // CTAs for each that fits the GPU at a time: some tensors' rows take longer than
-// others', and waves even that out (16384 x 40 rows 59.5 us with one, 56.2 with two,
-// 56.2 four, 57.4 eight; 20000 x 48 into an 8-bit cache, whose k rows took approximate
-// sines then, 111.7, 91.0, 83.6 with three, 90.2 four, 88.1 eight).
+// others', and waves even that out (16384 x 40 rows 59.2 us with one, 55.3 with two,
+// 55.1 four; 20000 x 48 into an 8-bit cache 84.4 with three, 85.9 four, 86.6 six).
 constexpr int waves_of(int bits) { return bits ? 3 : 2; }
-constexpr int kBackThreads = 256, kBackMostPerSm = 4;
+constexpr int kBackMostPerSm = 4;
 
 // Rows over about `most` CTAs, whole steps each, and the tokens that a filling of the
 // tables has at most: groups and two.
-Jobs jobs_of(const QkRope& a, int groups, int64_t most, int* grid, int* tokens) {
+Jobs jobs_of(const QkRope& a, int groups, int most_steps, int64_t most, int* grid, int* tokens) {
     const int heads[3] = {a.q.heads, a.k.heads, a.v.heads};
     Jobs jobs;
     *grid = *tokens = 0;
@@ -650,7 +657,7 @@ Jobs jobs_of(const QkRope& a, int groups, int64_t most, int* grid, int* tokens) 
         const int64_t all = a.tokens * heads[i], share = std::max<int64_t>(1, most * heads[i] / (heads[0] + heads[1] + heads[2]));
         const int64_t steps = std::min<int64_t>(std::max<int64_t>(1, (all + share * groups - 1) / (share * groups)), 1 << 20), rows = steps * groups;
         jobs.steps[i] = (int)steps;
-        jobs.chunk[i] = (int)std::min<int64_t>(steps, std::max(1, std::min(kSteps, heads[i])));
+        jobs.chunk[i] = (int)std::min<int64_t>(steps, std::max(1, std::min(most_steps, heads[i])));
         jobs.ctas[i] = (int)((all + rows - 1) / rows);
         jobs.by_heads[i] = FastDiv(std::max(1, heads[i]));
         *grid += jobs.ctas[i];
@@ -677,30 +684,28 @@ cudaError_t run(const QkRope& a, const KvPages& c, const int64_t* slots, int sms
     auto* kern = k_qk_rope<T, L, BITS>;
     using Rows = Ring<2 * Eight<T>::kVecs, kStages<BITS>>;
     KernelSetup su;
-    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kMostThreads, Tables::bytes(Layout{2 * L, L}, kMostThreads / L + 2) + Rows::bytes(kMostThreads), &su);
+    constexpr int groups = kThreads / L;
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables::bytes(Layout{2 * L, L}, groups + 2) + Rows::bytes(kThreads), &su);
     if (e != cudaSuccess) return e;
-    // Few rows: small CTAs of one step each; more: CTAs that fill the GPU once.
-    const int64_t rows = a.tokens * (a.q.heads + a.k.heads + a.v.heads);
-    const int threads = rows < (int64_t)sms * 4 * (kMostThreads / L) ? 128 : kMostThreads;
     int grid = 0, tokens = 0;
-    const Jobs jobs = jobs_of(a, threads / L, (int64_t)sms * su.blocks_per_sm * (kMostThreads / threads) * waves_of(BITS), &grid, &tokens);
-    return launch_dependent(kern, (size_t)grid, threads, Tables::bytes(l, tokens) + Rows::bytes(threads), 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, c, slots,
+    const Jobs jobs = jobs_of(a, groups, kSteps, (int64_t)sms * su.blocks_per_sm * waves_of(BITS), &grid, &tokens);
+    return launch_dependent(kern, (size_t)grid, kThreads, Tables::bytes(l, tokens) + Rows::bytes(kThreads), 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, c, slots,
                             FastDiv(BITS ? c.page_size : 1), status);
 }
 
 template <typename T, int L> cudaError_t run_back(const QkRope& a, float* dq_weight, float* dk_weight, float* parts, int sms, cudaStream_t s) {
     const Layout l = layout_of(a);
     auto* kern = k_qk_rope_back<T, L>;
-    const int lanes = (l.vecs + 1) / 2, groups = kBackThreads / L;
+    const int lanes = (l.vecs + 1) / 2, groups = kThreads / L;
     using Rows = Ring<4 * Eight<T>::kVecs, kStages<0>>;
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kBackThreads, Tables::bytes(Layout{2 * L, L}, kBackThreads / L + 2) + Rows::bytes(kBackThreads), &su);
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables::bytes(Layout{2 * L, L}, kThreads / L + 2) + Rows::bytes(kThreads), &su);
     if (e != cudaSuccess) return e;
     int grid = 0, tokens = 0;
-    const Jobs jobs = jobs_of(a, groups, (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), &grid, &tokens);
+    const Jobs jobs = jobs_of(a, groups, kBackSteps, (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), &grid, &tokens);
     if (grid > sms * kBackMostPerSm + 2) return cudaErrorInvalidValue;  // more rows than memory can hold
-    const size_t smem = std::max(Tables::bytes(l, tokens) + Rows::bytes(kBackThreads), (size_t)groups * lanes * 16 * 4);
-    e = launch_dependent(kern, grid, kBackThreads, smem, 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, parts);
+    const size_t smem = std::max(Tables::bytes(l, tokens) + Rows::bytes(kThreads), (size_t)groups * lanes * 16 * 4);
+    e = launch_dependent(kern, grid, kThreads, smem, 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, parts);
     if (e != cudaSuccess) return e;
     return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), jobs.ctas[0], grid, a.head_dim, dq_weight, dk_weight);
 }

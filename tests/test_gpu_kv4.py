@@ -127,6 +127,14 @@ def test_attend_window_and_sinks(ss, window, sinks, weights, many):
     check_attend(ss, Cache4(LENS + [500] + ([300, 77] * 50 if many else []), dim=128, page=16, seed=6), 2, "bf16", window, sinks, weights)
 
 
+@pytest.mark.filterwarnings("ignore:All-NaN")
+@pytest.mark.parametrize("lens", [[0] * 200, [0] * 150 + [900, 3] + [0] * 100, [900] + [0, 1] * 90 + [1, 2, 3] * 30, [1] * 300], ids=["none", "two", "mixed", "ones"])
+@pytest.mark.parametrize("window,weights", [(0, "add"), (40, "apart")])
+def test_attend_padded_batches(ss, lens, window, weights):
+    """Sequences without a position, and rows that are shorter than a warp's share."""
+    check_attend(ss, Cache4(lens, dim=64, page=16, seed=16), 3, "bf16", window, 2, weights)
+
+
 @pytest.mark.parametrize("n,heads,group,dim", [(30011, 1, 8, 128), (20000, 2, 1, 64), (12007, 1, 5, 256), (15000, 1, 12, 128)])
 @pytest.mark.parametrize("weights", ["add", None])
 def test_attend_one_long_sequence(ss, n, heads, group, dim, weights):
