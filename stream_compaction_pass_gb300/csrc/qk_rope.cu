@@ -21,10 +21,10 @@
 // log2 L shuffles.  A CTA takes consecutive rows of one of the tensors, which
 // leaves it one set of strides and weights, and computes their tokens' sines and
 // cosines once, in shared memory; its threads copy the rows to come, each its own
-// vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 54.9
-// us, 0.90 of the copy rate, issuing in 80 % of the cycles; the gradients 84.8, 0.87,
+// vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 53.7
+// us, 0.92 of the copy rate, issuing in 80 % of the cycles; the gradients 83.8, 0.88,
 // with the 16 warps an SM that 110 registers leave; 20000 x 48 into an 8-bit cache
-// 83.2, 0.79, by quantisation's instructions.
+// 81.4, 0.81, by quantisation's instructions, into 4 bits 90, into bf16 78, 0.92.
 #include <algorithm>
 
 #include "kv_quant.cuh"
@@ -36,11 +36,11 @@ namespace {
 // Small CTAs: as many warps wait at a barrier as share its tables, and a rotation by
 // all 256 elements has a thread for each of its 128 angles.  Threads of 128 / 256, as
 // many warps an SM: backward 84.6 / 90.1 us, forward 55.3 / 56.1, into an 8-bit cache
-// 84.4 / 88.4 (64: 85.2, 55.7, 86.0).  With 20 warps backward instead of 16 96
-// registers are too few: 117.
+// 84.4 / 88.4 (64: 85.2, 55.7, 86.0).  20 warps an SM backward, for 16, leave 96
+// registers, which are too few: 117.
 constexpr int kThreads = 128;
 // Rows of a ring: those on their way, and the one at hand.  Of tensors 3 (backward
-// 84.6 us, 4 87.1; forward 55.3, 54.9), into a cache 4 (84.4, 3 91.1, 5 86.6).
+// 83.8 us, 4 86.5; forward 55.8, 55.9), into a cache 4 (84.4, 3 91.1, 5 86.6).
 template <int BITS> constexpr int kStages = BITS > 0 ? 4 : 3;
 
 __device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16, float x, float y) {
@@ -89,11 +89,11 @@ template <typename T> struct Eight {
     static constexpr int kVecs = sizeof(T) / 2;
     // The copies of eight elements to vectors v and on of a ring's stage (zeros where
     // bytes is 0), and they from there.
-    template <typename R> static __device__ __forceinline__ void copy(const R& ring, int stage, int v, const T* p, int bytes) {
+    template <typename R> static __device__ __forceinline__ void copy(const R& ring, uint32_t stage, int v, const T* p, int bytes) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) ring.copy(stage, v + i, reinterpret_cast<const uint4*>(p) + i, bytes);
     }
-    template <typename R> __device__ __forceinline__ Eight(const R& ring, int stage, int at) {
+    template <typename R> __device__ __forceinline__ Eight(const R& ring, uint32_t stage, int at) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = ring.get(stage, at + i);
     }
@@ -136,21 +136,23 @@ __device__ __forceinline__ void floats(const F2 (&x)[4], float (&f)[8]) {
 
 // A lane's own vectors of the rows to come, in shared memory: only the thread that
 // copied them reads them, so nothing but its own copies is waited for.  NV vectors
-// of 16 bytes a row, S rows.
+// of 16 bytes a row, S rows; a row's stage is given by its offset.
 template <int NV, int S> struct Ring {
     uint32_t base;
     __device__ __forceinline__ Ring(void* smem)
         : base((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x / 32) * (S * NV * 512) + threadIdx.x % 32 * 16) {}
     static size_t bytes(int threads) { return (size_t)NV * S * threads * 16; }
-    __device__ __forceinline__ void copy(int stage, int v, const void* from, int bytes) const {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + (stage * NV + v) * 512), "l"(from), "r"(bytes) : "memory");
+    static constexpr uint32_t kStage = NV * 512;
+    static __device__ __forceinline__ uint32_t after(uint32_t stage) { return stage == (S - 1) * kStage ? 0 : stage + kStage; }
+    __device__ __forceinline__ void copy(uint32_t stage, int v, const void* from, int bytes) const {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + stage + v * 512), "l"(from), "r"(bytes) : "memory");
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory"); }
     static __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-    __device__ __forceinline__ uint4 get(int stage, int v) const {
+    __device__ __forceinline__ uint4 get(uint32_t stage, int v) const {
         uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + (stage * NV + v) * 512) : "memory");
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(base + stage + v * 512) : "memory");
         return x;
     }
 };
@@ -183,19 +185,19 @@ struct Walk {
     }
 };
 
-// Shared memory: cosines and sines of the tokens at hand, and the weights, each in
-// four planes of float4: plane j of lane p has a lane's numbers 4 j and on.
-struct Tables {
-    float4 *turn, *weight;
+// Shared memory: the weights, and cosines and sines of the tokens at hand, each in
+// four planes of L float4: plane j of lane p has a lane's numbers 4 j and on.
+template <int L> struct Tables {
+    float4 *weight, *turn;
     int pairs, lanes;
-    __device__ __forceinline__ Tables(void* smem, const Layout& l, int tokens) : pairs(l.pairs), lanes((l.vecs + 1) / 2) {
-        turn = static_cast<float4*>(smem);
-        weight = turn + (size_t)tokens * 4 * pairs;
+    __device__ __forceinline__ Tables(void* smem, const Layout& l) : pairs(l.pairs), lanes((l.vecs + 1) / 2) {
+        weight = static_cast<float4*>(smem);
+        turn = weight + 4 * L;
     }
-    __device__ __forceinline__ void* end() const { return weight + 4 * lanes; }
-    static size_t bytes(const Layout& l, int tokens) { return ((size_t)tokens * 4 * l.pairs + 4 * ((l.vecs + 1) / 2)) * 16; }
-    __device__ __forceinline__ void get(const float4* plane, int stride, int p, F2 (&x)[4], F2 (&y)[4]) const {
-        const float4 v[4] = {plane[p], plane[stride + p], plane[2 * stride + p], plane[3 * stride + p]};
+    __device__ __forceinline__ void* end(int tokens) const { return turn + tokens * 4 * L; }
+    static size_t bytes(int tokens) { return ((size_t)tokens + 1) * 4 * L * 16; }
+    static __device__ __forceinline__ void get(const float4* plane, F2 (&x)[4], F2 (&y)[4]) {
+        const float4 v[4] = {plane[0], plane[L], plane[2 * L], plane[3 * L]};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             x[2 * i] = f2(v[i].x, v[i].y);
@@ -204,15 +206,15 @@ struct Tables {
             y[2 * i + 1] = f2(v[2 + i].z, v[2 + i].w);
         }
     }
-    __device__ __forceinline__ void turns_of(int token, int p, F2 (&c)[4], F2 (&s)[4]) const { get(turn + token * 4 * pairs, pairs, p, c, s); }
-    __device__ __forceinline__ void weights_of(int p, F2 (&a)[4], F2 (&b)[4]) const { get(weight, lanes, p, a, b); }
+    __device__ __forceinline__ void turns_of(int token, int p, F2 (&c)[4], F2 (&s)[4]) const { get(turn + token * 4 * L + p, c, s); }
+    __device__ __forceinline__ void weights_of(int p, F2 (&a)[4], F2 (&b)[4]) const { get(weight + p, a, b); }
 
     // A thread has one of the frequencies, and every few tokens.
     template <bool FINE> __device__ __forceinline__ void fill_turns(const QkRope& a, int64_t t0, int tokens) const {
         const int per = pairs * 8, side = blockDim.x / per, m = threadIdx.x % per, p = m >> 3, j = m & 7;
         if ((int)threadIdx.x >= side * per) return;
         const unsigned long long f = a.turns[!a.interleaved ? m : j < 4 ? 4 * p + j : 4 * (p + pairs) + j - 4];
-        float* to = reinterpret_cast<float*>(turn + (j >> 2) * pairs + p) + (j & 3);
+        float* to = reinterpret_cast<float*>(turn + (j >> 2) * L + p) + (j & 3);
         for (int t = threadIdx.x / per; t < tokens; t += side) {
             const int at = a.positions[t0 + t];
             float s, c;
@@ -222,8 +224,8 @@ struct Tables {
                 const uint32_t low = (uint32_t)f, high = (uint32_t)(f >> 32) * (uint32_t)at + __umulhi(low, (uint32_t)at) - (at < 0 ? low : 0u);
                 __sincosf((float)(int)high * (0x1p-31f * 3.14159265358979f), &s, &c);
             }
-            to[t * 16 * pairs] = c;
-            to[t * 16 * pairs + 8 * pairs] = s;
+            to[t * 16 * L] = c;
+            to[t * 16 * L + 8 * L] = s;
         }
     }
     __device__ __forceinline__ void fill_weights(const char* w, KvElem type, const Layout& l) const {
@@ -235,7 +237,7 @@ struct Tables {
                     : type == KvElem::BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[d])
                                            : __half2float(reinterpret_cast<const __half*>(w)[d]);
             }
-            reinterpret_cast<float*>(weight + (j >> 2) * lanes + p)[j & 3] = x;
+            reinterpret_cast<float*>(weight + (j >> 2) * L + p)[j & 3] = x;
         }
     }
 };
@@ -385,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : BITS ? 6 : 8) k
     constexpr int kVecs = Eight<T>::kVecs, S = kStages<BITS>;
     extern __shared__ float4 s_tables[];
     __shared__ Place s_place[CACHE ? kThreads / L + 2 : 1];
-    const Tables tables(s_tables, l, most_tokens);
-    const Ring<2 * kVecs, S> ring(tables.end());
+    const Tables<L> tables(s_tables, l);
+    using Rows = Ring<2 * kVecs, S>;
+    const Rows ring(tables.end(most_tokens));
     const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
     const Share me(a, jobs, tid / L, groups);
     const bool is_q = me.kind == 0, is_v = CACHE && me.kind == 2;
@@ -398,8 +401,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : BITS ? 6 : 8) k
         return Walk(base, token_stride, head_stride, sizeof(T), me.t0 + me.token, me.head, me.heads, me.step_tokens, me.step_heads, one ? first * 8 : 0);
     };
     Walk from = walk(of.x, of.token_stride, of.head_stride), to = walk(of.y, of.y_token_stride, of.y_head_stride);
-    auto issue = [&](int k, int stage) {
-        if (k + 1 < me.steps || me.last) {
+    const int mine = me.last ? me.steps : me.steps - 1;  // rows of this group
+    auto issue = [&](int k, uint32_t stage) {
+        if (k < mine) {
             const T* x = reinterpret_cast<const T*>(from.at);
             Eight<T>::copy(ring, stage, 0, x, one_bytes);
             Eight<T>::copy(ring, stage, kVecs, x + apart, two_bytes);
@@ -410,14 +414,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : BITS ? 6 : 8) k
     // the first rows are on their way while the tables are filled
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-        if (k < me.steps) issue(k, k);
+        issue(k, k * Rows::kStage);
         ring.commit();
     }
     F2 wa[4] = {}, wb[4] = {};
     if (!is_v) tables.fill_weights(of.weight, a.weight_type, l);
 
     // The row's token among those of the tables, the first of which is `done`, and the next filling.
-    int stage = 0, token = 0, done = 0, fill = 0;
+    uint32_t stage = 0, refilled = (S - 1) * Rows::kStage;  // at hand, and read in the last step
+    int token = 0, done = 0, fill = 0;
     for (int k = 0; k < me.steps; ++k) {
         if (k == fill) {
             const int2 range = me.tokens(jobs, k, groups);
@@ -449,15 +454,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : BITS ? 6 : 8) k
             fill += me.chunk;
         }
         // A step: a row of every group.
-        const bool in = (k + 1 < me.steps || me.last) && one;
+        const bool in = k < mine && one;
         ring.wait();
         F2 x[4], y[4];
         Eight<T>(ring, stage, 0).open(x);
         Eight<T>(ring, stage, kVecs).open(y);
-        // the stage read in the last step is filled again
-        if (k + S - 1 < me.steps) issue(k + S - 1, stage == 0 ? S - 1 : stage - 1);
+        issue(k + S - 1, refilled);
         ring.commit();
-        stage = stage + 1 == S ? 0 : stage + 1;
+        refilled = stage;
+        stage = Rows::after(stage);
         if (!is_v) {
             F2 sum = x[0] * x[0];
 #pragma unroll
@@ -504,8 +509,9 @@ template <typename T, int L>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) k_qk_rope_back(QkRope a, Layout l, Jobs jobs, int most_tokens, float inv_dim, float* parts) {
     extern __shared__ float4 s_tables[];
     constexpr int kVecs = Eight<T>::kVecs, S = kStages<0>;
-    const Tables tables(s_tables, l, most_tokens);
-    const Ring<4 * kVecs, S> ring(tables.end());
+    const Tables<L> tables(s_tables, l);
+    using Rows = Ring<4 * kVecs, S>;
+    const Rows ring(tables.end(most_tokens));
     const int tid = threadIdx.x, p = tid % L, groups = blockDim.x / L, lanes = (l.vecs + 1) / 2, first = l.first(p), second = l.second(p);
     const Share me(a, jobs, tid / L, groups);
     const QkRows& of = me.kind == 0 ? a.q : a.k;
@@ -515,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) k_qk_rope_ba
         return Walk(base, token_stride, head_stride, sizeof(T), me.t0 + me.token, me.head, me.heads, me.step_tokens, me.step_heads, one ? first * 8 : 0);
     };
     Walk from = walk(of.x, of.token_stride, of.head_stride), grad = walk(of.g, of.g_token_stride, of.g_head_stride), to = walk(of.y, of.y_token_stride, of.y_head_stride);
-    auto issue = [&](int k, int stage) {
-        if (k + 1 < me.steps || me.last) {
+    const int mine = me.last ? me.steps : me.steps - 1;  // rows of this group
+    auto issue = [&](int k, uint32_t stage) {
+        if (k < mine) {
             const T *x = reinterpret_cast<const T*>(from.at), *g = reinterpret_cast<const T*>(grad.at);
             Eight<T>::copy(ring, stage, 0, x, one_bytes);
             Eight<T>::copy(ring, stage, kVecs, x + apart, two_bytes);
@@ -529,12 +536,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) k_qk_rope_ba
     begin_dependent();
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-        if (k < me.steps) issue(k, k);
+        issue(k, k * Rows::kStage);
         ring.commit();
     }
     tables.fill_weights(of.weight, a.weight_type, l);
     F2 wa[4] = {}, wb[4] = {}, da[4] = {}, db[4] = {};
-    int stage = 0, token = 0, done = 0, fill = 0;
+    uint32_t stage = 0, refilled = (S - 1) * Rows::kStage;  // at hand, and read in the last step
+    int token = 0, done = 0, fill = 0;
     for (int k = 0; k < me.steps; ++k) {
         if (k == fill) {
             const int2 range = me.tokens(jobs, k, groups);
@@ -550,16 +558,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) k_qk_rope_ba
             done = range.x;
             fill += me.chunk;
         }
-        const bool in = (k + 1 < me.steps || me.last) && one;
+        const bool in = k < mine && one;
         ring.wait();
         F2 x[4], y[4], g[4], h[4];
         Eight<T>(ring, stage, 0).open(x);
         Eight<T>(ring, stage, kVecs).open(y);
         Eight<T>(ring, stage, 2 * kVecs).open(g);
         Eight<T>(ring, stage, 3 * kVecs).open(h);
-        if (k + S - 1 < me.steps) issue(k + S - 1, stage == 0 ? S - 1 : stage - 1);
+        issue(k + S - 1, refilled);
         ring.commit();
-        stage = stage + 1 == S ? 0 : stage + 1;
+        refilled = stage;
+        stage = Rows::after(stage);
         if (p < l.pairs && in) {
             F2 co[4], si[4];
             tables.turns_of(token, p, co, si);
@@ -642,9 +651,9 @@ Layout layout_of(const QkRope& a) { return Layout{a.head_dim / 8, a.rotary_dim /
 // 84.4 with 16, 85.3 with 8; backward 84.6 with 16, 86.2 with 32).
 constexpr int kSteps = 32, kBackSteps = 16;
 // CTAs for each that fits the GPU at a time: some tensors' rows take longer than
-// others', and waves even that out (16384 x 40 rows 59.2 us with one, 55.3 with two,
-// 55.1 four; 20000 x 48 into an 8-bit cache 84.4 with three, 85.9 four, 86.6 six).
-constexpr int waves_of(int bits) { return bits ? 3 : 2; }
+// others', and waves even that out (16384 x 40 rows 59.2 us with one, 55.8 with two,
+// 53.7 four; 20000 x 48 into an 8-bit cache 84.4 with three, 85.9 four, 86.6 six).
+constexpr int waves_of(int bits) { return bits ? 3 : 4; }
 constexpr int kBackMostPerSm = 4;
 
 // Rows over about `most` CTAs, whole steps each, and the tokens that a filling of the
@@ -685,11 +694,11 @@ cudaError_t run(const QkRope& a, const KvPages& c, const int64_t* slots, int sms
     using Rows = Ring<2 * Eight<T>::kVecs, kStages<BITS>>;
     KernelSetup su;
     constexpr int groups = kThreads / L;
-    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables::bytes(Layout{2 * L, L}, groups + 2) + Rows::bytes(kThreads), &su);
+    const cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables<L>::bytes(groups + 2) + Rows::bytes(kThreads), &su);
     if (e != cudaSuccess) return e;
     int grid = 0, tokens = 0;
     const Jobs jobs = jobs_of(a, groups, kSteps, (int64_t)sms * su.blocks_per_sm * waves_of(BITS), &grid, &tokens);
-    return launch_dependent(kern, (size_t)grid, kThreads, Tables::bytes(l, tokens) + Rows::bytes(kThreads), 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, c, slots,
+    return launch_dependent(kern, (size_t)grid, kThreads, Tables<L>::bytes(tokens) + Rows::bytes(kThreads), 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, c, slots,
                             FastDiv(BITS ? c.page_size : 1), status);
 }
 
@@ -699,12 +708,12 @@ template <typename T, int L> cudaError_t run_back(const QkRope& a, float* dq_wei
     const int lanes = (l.vecs + 1) / 2, groups = kThreads / L;
     using Rows = Ring<4 * Eight<T>::kVecs, kStages<0>>;
     KernelSetup su;
-    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables::bytes(Layout{2 * L, L}, kThreads / L + 2) + Rows::bytes(kThreads), &su);
+    cudaError_t e = kernel_setup(reinterpret_cast<const void*>(kern), kThreads, Tables<L>::bytes(kThreads / L + 2) + Rows::bytes(kThreads), &su);
     if (e != cudaSuccess) return e;
     int grid = 0, tokens = 0;
     const Jobs jobs = jobs_of(a, groups, kBackSteps, (int64_t)sms * std::min(su.blocks_per_sm, kBackMostPerSm), &grid, &tokens);
     if (grid > sms * kBackMostPerSm + 2) return cudaErrorInvalidValue;  // more rows than memory can hold
-    const size_t smem = std::max(Tables::bytes(l, tokens) + Rows::bytes(kThreads), (size_t)groups * lanes * 16 * 4);
+    const size_t smem = std::max(Tables<L>::bytes(tokens) + Rows::bytes(kThreads), (size_t)groups * lanes * 16 * 4);
     e = launch_dependent(kern, grid, kThreads, smem, 1, s, a, l, jobs, tokens, 1.0f / a.head_dim, parts);
     if (e != cudaSuccess) return e;
     return launch_dependent(k_qk_rope_weights, (2 * a.head_dim + 31) / 32, 1024, 0, 1, s, static_cast<const float*>(parts), jobs.ctas[0], grid, a.head_dim, dq_weight, dk_weight);
