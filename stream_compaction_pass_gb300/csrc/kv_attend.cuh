@@ -16,18 +16,18 @@
 // positions in all (8 x 4 heads of 128, bf16): 102 us for 634 MB, 6.2 TB/s,
 // tensor pipe 12 %; without the arithmetic about 4 us less.
 //
-// Split.  The tiles of every (sequence, unit), a unit being 8 or 16 query
-// heads of one key-value head, form one long list; a warp takes one contiguous
-// share of it, all shares equal to within a tile (or an entry that stands for the
-// start of a row, kOpen), whatever the lengths are.  So
-// a single long sequence and a ragged batch both fill every SM, and the host
-// needs no lengths.  A warp works alone: it owns a ring of tiles in shared
-// memory that only it fills and reads, so the main loop has no barrier.  Rows
-// that lie within one warp's share are written at once; a share's first and
-// last row may be parts, which go to scratch, and the second launch joins
-// them (7 us for 2048 rows of 3.6 parts).  Where weights are kept, the first
-// launch leaves X (fp32) in scratch and the third turns it into weights, since
-// they need the joined sums (10 us for 1.2 million positions x 4 heads).
+// Split.  The tiles of every (sequence, unit), a unit being 8 or 16 query heads
+// of one key-value head, form one long list; a warp takes one contiguous share
+// of it, all shares equal to within a tile (or an entry that stands for the
+// start of a row, kOpen), whatever the lengths are.  So a single long sequence
+// and a ragged batch both fill every SM, and the host needs no lengths.  A warp
+// works alone: it owns a ring of tiles in shared memory that only it fills and
+// reads, so the main loop has no barrier.  Rows that lie within one warp's share
+// are written at once; a share's first and last row may be parts, which go to
+// scratch, and the second launch joins them (7 us for 2048 rows of 3.6 parts).
+// Where weights are kept, the first launch leaves X (fp32) in scratch and the
+// third turns it into weights, since they need the joined sums (10 us for 1.2
+// million positions x 4 heads).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -66,6 +66,9 @@ template <int BITS> constexpr int kOpen = BITS == 4 ? 1 : 0;
 //   8-bit: 1 x 16000 (5) 16.9 / 20.6, 1 x 32000 (10) 25.0 / 23.2, 1 x 64000 41.5
 //     / 32.9, 4 x 16000 (10) 26.9 / 31.8; with weights 1 x 8000 (3) 18.0 / 22.8,
 //     1 x 16000 27.1 / 24.9, 1 x 32000 43.0 / 27.8, 4 x 8000 (5) 27.4 / 27.8.
+//   4-bit: 1 x 16000 (8, of 32 positions) 15.6 / 18.0, 1 x 32000 (16) 25.3 / 20.9,
+//     16 x 1000 (2) 9.9 / 16.2; with weights 1 x 8000 (4) 15.5 / 17.6, 1 x 16000 24.6
+//     / 24.0, 1 x 32000 42.4 / 26.5, 4 x 4000 (4) 16.0 / 21.8.
 //   256: 1 x 4000 (8) 11.5 / 13.1, 1 x 8000 (16) 18.0 / 15.2, 32 x 1000 (16) 23.4
 //     / 31.4; with weights 1 x 2000 (4) 11.3 / 13.1, 1 x 6000 (12) 22.2 / 16.9.
 //   group 12: 1 x 8000 (8) 13.8 / 16.8, 1 x 16000 (16) 21.1 / 17.7, 32 x 2000 (16)

@@ -258,16 +258,17 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 }
 
 // What both forms share.  8- and 4-bit caches multiply in fp16, which holds every
-// e4m3 value, and every e2m1 value times an e4m3 scale (2 and 4 bits).  P enters
-// the product with V as two 16-bit terms (kTwo), good to 2^-16 of itself in bf16 and 2^-22 in fp16, below the rounding of out (2^-8,
-// 2^-11): 0.28 % of the ragged bf16 batch's outputs round to the other neighbour,
-// 0.13 % of an 8-bit cache's, against 0.07 and 0.12 % with fp32 weights.  One fp16
-// term, 2^-11, is left to bf16 outputs of 8-bit caches where two cost much (16
-// query heads a key-value head 84 / 95 us, head_dim 64 71 / 77): 7 % of them
-// round to the other neighbour, with the same error against the formula,
-// 1.65e-3.  (At head_dim 128 two terms cost nothing of 100 us, at 256 123 / 124.5,
-// at 80 60.7 / 64.4.)  So it is for all bf16 outputs of 4-bit caches, where the
-// instructions bound and two terms take 13 % (530 / 609 us of 2.2 million positions).
+// e4m3 value, and every e2m1 value times an e4m3 scale (2 and 4 bits).  P enters the
+// product with V as two 16-bit terms (kTwo), good to 2^-16 of itself in bf16 and
+// 2^-22 in fp16, below the rounding of out (2^-8, 2^-11): 0.28 % of the ragged bf16
+// batch's outputs round to the other neighbour, 0.13 % of an 8-bit cache's, against
+// 0.07 and 0.12 % with fp32 weights.  One fp16 term, 2^-11, is left to bf16 outputs
+// of 8-bit caches where two cost much (16 query heads a key-value head 84 / 95 us,
+// head_dim 64 71 / 77): 7 % of them round to the other neighbour, with the same
+// error against the formula, 1.65e-3.  (At head_dim 128 two terms cost nothing of
+// 100 us, at 256 123 / 124.5, at 80 60.7 / 64.4.)  So it is for all bf16 outputs of
+// 4-bit caches, where the instructions bound and two terms take 13 % (530 / 609 us
+// of 2.2 million positions).
 //
 // 4-bit rows.  A code is opened by its conversion to fp16 and one multiplication by
 // its block's scale; keys in pairs of dimensions, as they lie, values in pairs of
