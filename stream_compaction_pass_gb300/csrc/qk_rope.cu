@@ -8,8 +8,10 @@
 // is a fraction of a turn: position times frequency modulo 1, which 64-bit integers
 // multiply exactly with the frequency in units of 2^-64 turns, however far the
 // position.  Of what is left, fp32 rows and those for narrow caches (where a value
-// beside a tie of two codes moves by a whole step) take CUDA's sincospif and the
-// rounded reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1,
+// beside a tie of two codes moves by a whole step) take CUDA's sincospif, with what
+// the angle's rounding to fp32 leaves out added by the derivatives (of 164 million
+// e4m3 codes 233 differ from those of 64 bits, 358 without), and the rounded
+// reciprocal root; 16-bit ones the approximations, whose errors (2^-21 of 1,
 // 2 units in the last place) are a thousandth of the outputs' rounding and whose
 // instructions are fewer (57.5 us without, 55.4 with them, of 16384 x 40 rows, in
 // CTAs of 256).
@@ -24,7 +26,7 @@
 // vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 53.7
 // us, 0.92 of the copy rate, issuing in 80 % of the cycles; the gradients 83.8, 0.88,
 // with the 16 warps an SM that 110 registers leave; 20000 x 48 into an 8-bit cache
-// 81.4, 0.81, by quantisation's instructions, into 4 bits 90, into bf16 78, 0.92.
+// 82.2, 0.80, by quantisation's instructions, into 4 bits 91, into bf16 79, 0.91.
 #include <algorithm>
 
 #include "kv_quant.cuh"
@@ -80,8 +82,8 @@ __device__ __forceinline__ float sum_f2(F2 a) {
     const float2 x = open_f2(a);
     return x.x + x.y;
 }
-// a - b c.
-__device__ __forceinline__ F2 less2(F2 a, F2 b, F2 c) { return fma2(b * c, f2(-1.0f, -1.0f), a); }
+// a - b c, rounded once.
+__device__ __forceinline__ F2 less2(F2 a, F2 b, F2 c) { return fma2(b * f2(-1.0f, -1.0f), c, a); }
 
 // Eight elements as they lie in memory, and as fp32.
 template <typename T> struct Eight {
@@ -219,7 +221,13 @@ template <int L> struct Tables {
             const int at = a.positions[t0 + t];
             float s, c;
             if (FINE) {
-                sincospif((float)(long long)(f * (unsigned long long)(long long)at) * 0x1p-63f, &s, &c);
+                // and what rounding the angle to fp32 leaves out, by the derivatives
+                const long long turns = (long long)(f * (unsigned long long)(long long)at);
+                const float near = __ll2float_rn(turns), rest = __ll2float_rn(turns - __float2ll_rn(near)) * (0x1p-63f * 3.14159265358979f);
+                float s0, c0;
+                sincospif(near * 0x1p-63f, &s0, &c0);
+                s = fmaf(c0, rest, s0);
+                c = fmaf(-s0, rest, c0);
             } else {  // the product's high half
                 const uint32_t low = (uint32_t)f, high = (uint32_t)(f >> 32) * (uint32_t)at + __umulhi(low, (uint32_t)at) - (at < 0 ? low : 0u);
                 __sincosf((float)(int)high * (0x1p-31f * 3.14159265358979f), &s, &c);
