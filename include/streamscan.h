@@ -478,10 +478,10 @@ ss_status ss_kv_append_rope(const ss_kv_pages *cache, const int64_t *slots, cons
  * time, each cut below 2^-24 of its sum), exponentials are good to 2^-22, and
  * out is rounded once.  In the sum over v a weight has 16 bits (bf16 caches) or
  * 22 (fp16, e4m3 and e2m1 caches), and up to 2^-38 of the row's largest weight
- * more (fp16); it has 11 bits where q is bf16 and the cache e2m1, or e4m3
- * with head_dim at most 64 or q_heads more than 8 per key-value head.  lse and the
- * gathered weights are of the fp32 scores.  bf16 queries of an e4m3 or e2m1 cache
- * are held to 2^-32 of their row's largest element.
+ * more (fp16); it has 11 bits where q is bf16 and the cache e4m3 with head_dim at
+ * most 64 or q_heads more than 8 per key-value head.  lse and the gathered
+ * weights are of the fp32 scores.  bf16 queries of an e4m3 or e2m1 cache are held
+ * to 2^-32 of their row's largest element.
  * q_heads <= 65536, at most 128 per key-value head, and (max_len / 16 + 1) *
  * q_heads < 2^31.
  */

@@ -266,9 +266,11 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 // of 8-bit caches where two cost much (16 query heads a key-value head 84 / 95 us,
 // head_dim 64 71 / 77): 7 % of them round to the other neighbour, with the same
 // error against the formula, 1.65e-3.  (At head_dim 128 two terms cost nothing of
-// 100 us, at 256 123 / 124.5, at 80 60.7 / 64.4.)  So it is for all bf16 outputs of
-// 4-bit caches, where the instructions bound and two terms take 13 % (530 / 609 us
-// of 2.2 million positions).
+// 100 us, at 256 123 / 124.5, at 80 60.7 / 64.4.)  4-bit caches take two terms
+// everywhere: one would be 10 % faster (444 / 495 us of 2.2 million positions, 8 x 8
+// heads of 128), but its bf16 outputs were 4.8e-4 from those of fp32 weights on a ragged
+// batch, where two leave 0.8e-4: 0.09 to 0.15 % of them round to another neighbour than
+// the formula's, of fp32 weights and sums in another order 0.10 to 0.23 %.
 //
 // 4-bit rows.  A code is opened by its conversion to fp16 and one multiplication by
 // its block's scale; keys in pairs of dimensions, as they lie, values in pairs of
@@ -289,7 +291,7 @@ template <typename QT, int BITS, int DP, int T, int HEADS> struct RowsBase {
     using MT = typename std::conditional<kNarrow, __half, QT>::type;
     static constexpr float kShift = std::is_same<MT, __half>::value ? 15.0f : -24.0f;
     static constexpr int kHeads = HEADS;
-    static constexpr bool kTwo = !kNarrow || std::is_same<QT, __half>::value || (BITS == 8 && HEADS == 8 && DP > 64);
+    static constexpr bool kTwo = BITS != 8 || std::is_same<QT, __half>::value || (HEADS == 8 && DP > 64);
     static constexpr bool kFit = kNarrow && !std::is_same<QT, __half>::value;
     static constexpr int kChain = 128 / (T / 16 * (kTwo ? 2 : 1));
     static constexpr int kRowBytes = DP * BITS / 8, kKS = DP / 16;

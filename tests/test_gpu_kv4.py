@@ -248,6 +248,50 @@ def test_pool_past_32_bit_offsets(ss):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("many", [False, True], ids=["small", "many"])
+def test_attend_is_off_by_the_rounding_of_out_alone(ss, kind, dim, group, many):
+    """No weight is rounded to fewer bits than a softmax weight keeps.  Queries have
+    one element that is not 0, so that a score's product is exact; X = score * log2 e
+    is at most 8 (0.25 * 1.25 * 11.25 * 1.5 * log2 e = 7.7).  X is then off by four
+    roundings, 2^-24 each of 8, and its difference to a reference that lies up to 32
+    away by 2^-20: 2^-19 + 2^-20, so that a weight is off by ln 2 times that and the
+    exponential's 2^-22, below 1.2 * 2^-19 of itself, and a quotient of sums of them by
+    twice that.  The products' accumulators cut 2^-23 at each of 14 steps (100
+    positions, two terms) and the sums of fp32 weights, the scaling and the quotient
+    take less than 16 roundings: 2^-19 + 2^-19.2 more.  Together less than 2^-17 of sum w
+    |v|, besides half a unit of out's own last place."""
+    import torch
+    lens = [2, 3, 100, 17, 64] + ([1, 31, 90, 5] * 60 if many else [])
+    c = Cache4(lens, dim=dim, page=16, seed=41)
+    rng = np.random.default_rng(42)
+    heads = c.heads * group
+    q = np.zeros((len(lens), heads, dim), np.float32)
+    b, j = np.meshgrid(np.arange(len(lens)), np.arange(heads), indexing="ij")
+    q[b, j, rng.integers(0, dim, b.shape)] = rng.uniform(0.5, 1.25, b.shape) * rng.choice([-1, 1], b.shape)
+    q = torch.from_numpy(q).to(torch_type(kind))
+    assert float(q.float().abs().max()) <= 1.25
+    out = torch.full(q.shape, math.nan, dtype=q.dtype, device="cuda")
+    pages, table = c.ss(ss)
+    ss.ss_kv_attend(pages, table, q.cuda(), out, scale=0.25)
+    ok(ss)
+    got, q = out.double().cpu().numpy(), q.double().numpy()
+    bits = 8 if kind == "bf16" else 11
+    for b, n in enumerate(lens):
+        for j in range(heads):
+            h = j // group
+            k, v = c.rows(c.k_host, b, h) * c.scale(c.ks, h), c.rows(c.v_host, b, h) * c.scale(c.vs, h)
+            x = 0.25 * (k @ q[b, j])
+            w = np.exp(x - x.max())
+            w /= w.sum()
+            want, tol = w @ v, 2.0 ** -17 * (w @ np.abs(v))
+            half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want) + tol, 2.0 ** -14))) - bits)
+            off = np.abs(got[b, j] - want)
+            assert (off <= half + tol).all(), (b, j, n, float(((off - half) / np.maximum(tol, 1e-300)).max()))
+
+
 # ---- append ----
 
 def check_append(ss, lens, news, heads, dim, page, src, layout="hnd", strided=False, offsets=True, values=None, scales=True):
