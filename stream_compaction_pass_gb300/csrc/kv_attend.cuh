@@ -49,8 +49,10 @@ namespace cg = cooperative_groups;
 // What a row costs the warp that begins it, in tiles, where tiles are cheap enough
 // for that to matter: so many entries of the list stand before the row's own, and
 // shares of many short rows have fewer tiles.  Over 4 bits, 64 sequences of 100 to
-// 16,001 positions, weights kept: none 86.2 us, 1 72.6, 2 73.2, 3 73.8, 5 75.5; 32
-// of 4000 to 8000, 16 heads of 64: 56.8, 57.6, 57.4, 57.6, 58.4.
+// 16,001 positions, weights kept: none 89.7 us, 1 76.1, 2 76.5, 3 76.8, 5 79.5; 32
+// of 4000 to 8000, 16 heads of 64: 61.9, 62.8, 62.9, 63.2, 64.3.
+// The later launches have it as a constant too (OPEN): with a member of Scratch for
+// it, 16-bit caches with weights took 721 us for 706 (32 of 20,000 to 50,000).
 template <int BITS> constexpr int kOpen = BITS == 4 ? 1 : 0;
 
 // Tiles of a warp up to which a call whose units fit the GPU takes the form of
@@ -66,9 +68,9 @@ template <int BITS> constexpr int kOpen = BITS == 4 ? 1 : 0;
 //   8-bit: 1 x 16000 (5) 16.9 / 20.6, 1 x 32000 (10) 25.0 / 23.2, 1 x 64000 41.5
 //     / 32.9, 4 x 16000 (10) 26.9 / 31.8; with weights 1 x 8000 (3) 18.0 / 22.8,
 //     1 x 16000 27.1 / 24.9, 1 x 32000 43.0 / 27.8, 4 x 8000 (5) 27.4 / 27.8.
-//   4-bit: 1 x 16000 (8, of 32 positions) 15.6 / 18.0, 1 x 32000 (16) 25.3 / 20.9,
-//     16 x 1000 (2) 9.9 / 16.2; with weights 1 x 8000 (4) 15.5 / 17.6, 1 x 16000 24.6
-//     / 24.0, 1 x 32000 42.4 / 26.5, 4 x 4000 (4) 16.0 / 21.8.
+//   4-bit: 1 x 16000 (8, of 32 positions) 17.0 / 18.6, 1 x 32000 (16) 28.2 / 21.9,
+//     16 x 1000 (2) 10.7 / 16.3; with weights 1 x 8000 (4) 16.2 / 17.1, 1 x 16000 25.9
+//     / 23.0, 1 x 32000 44.7 / 26.4, 4 x 4000 (4) 16.6 / 21.3.
 //   256: 1 x 4000 (8) 11.5 / 13.1, 1 x 8000 (16) 18.0 / 15.2, 32 x 1000 (16) 23.4
 //     / 31.4; with weights 1 x 2000 (4) 11.3 / 13.1, 1 x 6000 (12) 22.2 / 16.9.
 //   group 12: 1 x 8000 (8) 13.8 / 16.8, 1 x 16000 (16) 21.1 / 17.7, 32 x 2000 (16)
@@ -95,7 +97,6 @@ struct Scratch {
     float* logits;  // per (sequence, key-value head) tile: group x 16 scores, log2 units; or null
     int group, units, rows, workers;  // units per sequence, of `heads` query heads; rows = min(group, heads)
     int heads;
-    int open;                         // entries of a row before its tiles
     int ranks, max_tiles;             // small calls: CTAs of a unit's cluster, tiles of the longest sequence
     int shift;                        // tiles have 2^shift positions
     FastDiv page;                     // by page_size
@@ -621,11 +622,11 @@ __global__ void __launch_bounds__(NW * 32, 1) k_kv_attend(KvPages c, KvTable t, 
 struct Parts {
     int w0, count;
     // `before` entries precede the sequence in a unit's list, it has `tiles`, all sequences have `all`.
-    __device__ __forceinline__ Parts(const Scratch& sc, int before, int tiles, int all, int unit) {
+    __device__ __forceinline__ Parts(const Scratch& sc, int before, int tiles, int all, int unit, int open) {
         const int total = all * sc.units;
         const Shares shares(total, min(sc.workers, total));
         const int s0 = before * sc.units + unit * tiles;
-        w0 = shares.holder(s0 + sc.open);
+        w0 = shares.holder(s0 + open);
         count = shares.holder(s0 + tiles - 1) - w0 + 1;
     }
     // The first part is its worker's last row, the others are their workers' first ones.
@@ -690,7 +691,7 @@ template <int DP> struct RowSum {
 
 // The second launch finishes the rows that were cut and those without a
 // visible position: a team of TEAM warps (1, 4 or all 16) a row.
-template <typename QT, int DP, int TEAM>
+template <typename QT, int DP, int TEAM, int OPEN>
 __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, KvAttention a, Scratch sc) {
     __shared__ float4 s_o[kJoinWarps][DP / 4];
     __shared__ float2 s_ml[kJoinWarps];
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
         if (tiles == 0) {
             empty_row<QT>(a, b, j, c.head_dim, member * 32 + lane, TEAM * 32);
         } else {
-            const Parts p(sc, before, tiles, all, unit(j));
+            const Parts p(sc, before, tiles, all, unit(j), OPEN);
             wide = TEAM < kJoinWarps && p.count > 32 * TEAM;
             joined = p.count > 1 && !wide;
             if (joined) {
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
         if (!__syncthreads_or(wide && mine == k)) continue;
         const int rk = blockIdx.x * kPer + k, b = rk / a.q_heads, j = rk % a.q_heads, before = sc.pre[b];
         RowSum<DP> sum;
-        sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j)), j % sc.group % sc.heads, warp, kJoinWarps, lane);
+        sum.add(sc, Parts(sc, before, sc.pre[b + 1] - before, all, unit(j), OPEN), j % sc.group % sc.heads, warp, kJoinWarps, lane);
         keep(sum);
         __syncthreads();
         store(rk, 0, kJoinWarps, tid, kJoinThreads);
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(KvPages c, KvTable t, 
 // positions of one tile, and every tile finds its sequence and head by itself,
 // so that short sequences cost no more than long ones.  Accumulated in place,
 // only visible positions change.
-template <int V>
+template <int V, int OPEN>
 __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTable t, KvAttention a, Scratch sc, uint32_t* status) {
     __shared__ int s_pre[kMaxBatch<16, 0> + 1];
     begin_dependent();
@@ -777,8 +778,8 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTabl
         const int tile_at = (int)(at / per_tile), in = (int)(at % per_tile) * V;
         const int b = find_sequence(s_pre, t.batch, c.kv_heads, tile_at);
         const int tiles = s_pre[b + 1] - s_pre[b];
-        const int in_b = tile_at - s_pre[b] * c.kv_heads, h = in_b / tiles, j = in_b - h * tiles - (only_visible ? sc.open : 0);
-        if (j < 0) continue;
+        const int in_b = tile_at - s_pre[b] * c.kv_heads, h = in_b / tiles, j = in_b - h * tiles - (only_visible ? OPEN : 0);
+        if (OPEN > 0 && j < 0) continue;
         const Tiles tl(kv_len(t, b, status), a.window, a.sinks, sc.shift);
         const int tile = only_visible ? tl.tile(j) : j;
         const int p = (tile << sc.shift) + in;
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(kWeightThreads) k_kv_weights(KvPages c, KvTabl
         }
         if (tile < tl.nsink || tile >= tl.first) {  // the tile has scores
             const int before = only_visible ? s_pre[b] : sc.pre[b];
-            const int64_t jv = (int64_t)before * c.kv_heads + (int64_t)h * (tl.count + sc.open) + (tile < tl.nsink ? tile : tl.nsink + tile - tl.first);
+            const int64_t jv = (int64_t)before * c.kv_heads + (int64_t)h * (tl.count + OPEN) + (tile < tl.nsink ? tile : tl.nsink + tile - tl.first);
             const float* x = sc.logits + jv * sc.group * T + in;
             const float* lse = sc.lse2 + (int64_t)b * a.q_heads + h * sc.group;
 #pragma unroll 4
@@ -858,7 +859,6 @@ Plan make_plan(const KvPages& c, const KvTable& t, const KvAttention& a, int mos
     p.sc.heads = heads;
     p.sc.units = c.kv_heads * ((p.sc.group + heads - 1) / heads);
     p.sc.rows = p.sc.group < heads ? p.sc.group : heads;
-    p.sc.open = open;
     const size_t tiles = most_tiles(t, a, tile) + open;
     const size_t seq_logits = a.weight_out ? tiles * a.q_heads * tile * 4 : 0;
     const size_t seqs = t.batch < most_batch ? t.batch : most_batch;
@@ -983,14 +983,14 @@ cudaError_t run(const KvPages& c, const KvTable& t, const KvAttention& a, const 
         // units than workers are whole.
         const int64_t rows = (int64_t)u.batch * a.q_heads, units = (int64_t)u.batch * p.sc.units;
         const int team = units * 8 >= p.sc.workers ? 1 : units * 32 >= p.sc.workers ? 4 : kJoinWarps, per = kJoinWarps / team;
-        auto* join = team == 1 ? k_kv_join<QT, DP, 1> : team == 4 ? k_kv_join<QT, DP, 4> : k_kv_join<QT, DP, kJoinWarps>;
+        auto* join = team == 1 ? k_kv_join<QT, DP, 1, kOpen<BITS>> : team == 4 ? k_kv_join<QT, DP, 4, kOpen<BITS>> : k_kv_join<QT, DP, kJoinWarps, kOpen<BITS>>;
         e = launch_dependent(join, (rows + per - 1) / per, kJoinThreads, 0, 1, s, c, u, v, p.sc);
         if (e != cudaSuccess) return e;
         if (a.weight_out == nullptr) continue;
         const bool vec4 = c.page_size % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.weight_in) | reinterpret_cast<uintptr_t>(a.weight_out)) & 15u) == 0;
         const size_t tiles = ((size_t)t.max_len + T - 1) / T * u.batch * c.kv_heads;
         const size_t blocks = (tiles * (vec4 ? T / 4 : T) + kWeightThreads - 1) / kWeightThreads, most = (size_t)su.sms * 8;
-        e = launch_dependent(vec4 ? k_kv_weights<4> : k_kv_weights<1>, blocks < most ? blocks < 1 ? 1 : blocks : most, kWeightThreads, 0, 1, s, c, u, v, p.sc, status);
+        e = launch_dependent(vec4 ? k_kv_weights<4, kOpen<BITS>> : k_kv_weights<1, kOpen<BITS>>, blocks < most ? blocks < 1 ? 1 : blocks : most, kWeightThreads, 0, 1, s, c, u, v, p.sc, status);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
