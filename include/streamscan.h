@@ -373,7 +373,8 @@ ss_status ss_kv_append(const ss_kv_pages *cache, const ss_kv_table *seqs, ss_ele
  *              counts than room are reported.
  * Lengths, counts and page numbers are checked on the device, as for the other
  * calls.  batch <= 8192, batch * max_pages < 2^31, and all counts' sum is below
- * 2^31 (reported otherwise).
+ * 2^31 (reported otherwise).  What it reports lies in the stream's workspace: make one
+ * call before capturing a stream into a graph.
  */
 typedef struct ss_kv_free {
     int32_t *pages;
@@ -402,7 +403,8 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  *   positions  device, a token each; may be negative.
  *   q_out, k_out  each is its own input's rows, or shares no memory with either.
  *   head_dim a multiple of 8, at most 256; rotary_dim a positive multiple of 16,
- *   at most head_dim.  tokens == 0 is a no-op.
+ *   at most head_dim.  tokens == 0 is a no-op.  The call takes no scratch and may be
+ *   the first one on a stream that is being captured.
  *
  * ss_qk_norm_rope_backward: from the gradients of the outputs, dq_out and dk_out,
  * those of the inputs (dq and dk: the rows of an input or of a gradient of their
@@ -417,7 +419,8 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  * after ss_kv_append of y, which is not rounded to `type` before; the slots'
  * weights become 0.  Slots behind the pool are reported with the token.  No two
  * tokens share a slot, and q_out no memory with the cache.  type: SS_BF16 or SS_F16;
- * rotary_dim a multiple of 32 for an SS_E2M1 cache.
+ * rotary_dim a multiple of 32 for an SS_E2M1 cache.  Make one call before capturing a
+ * stream into a graph, as for ss_kv_assign.
  */
 typedef struct ss_rows {
     void *data;

@@ -702,10 +702,10 @@ ss_status ss_qk_norm_rope(const ss_qk* x, const ss_rows* q_out, const ss_rows* k
     if (st != SS_OK) return st;
     a.q = qk_rows(q, yq, x->q_weight, x->q_heads);
     a.k = qk_rows(k, yk, x->k_weight, x->kv_heads);
-    Workspace* w = nullptr;
-    st = get_workspace((cudaStream_t)stream, &w, false);
-    if (st != SS_OK) return st;
-    cudaError_t e = ss::launch_qk_rope(a, device_sms(w->device), (cudaStream_t)stream);
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    e = ss::launch_qk_rope(a, device_sms(device), (cudaStream_t)stream);
     return e == cudaSuccess ? SS_OK : cuda_fail(e, "norm and rotation launch");
 } catch (...) {  // of the host's own allocations
     g_detail.clear();

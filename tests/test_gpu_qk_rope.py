@@ -338,6 +338,33 @@ def test_a_first_call_in_a_capture_is_refused(ss):
         y.zero_()
 
 
+def test_forward_first_in_a_capture(ss):
+    """The call needs nothing that a call before the capture would have to make."""
+    import torch
+    tokens, hq, hk, dim = 90, 6, 2, 64
+    host, (q, k) = make(tokens, (hq, hk), dim, "bf16", 33)
+    wq, wk = weights(dim, "bf16", 34)
+    freq = frequencies(dim)
+    rope = ss.Rope(torch.from_numpy(freq).cuda())
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    yq, yk = (torch.full((tokens, h, dim), math.nan, dtype=torch.bfloat16, device="cuda") for h in (hq, hk))
+    dev = wq.cuda(), wk.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ss.ss_qk_norm_rope(q, k, *dev, rope, pos, yq, yk, stream=side)
+    for shift in (0, 1000):
+        pos.copy_(torch.arange(shift, shift + tokens))
+        yq.fill_(math.nan)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        at = np.arange(shift, shift + tokens)
+        check_rows(yq.double().cpu().numpy(), wide(host[0]), wide(wq), at, freq, False, 1e-6, "bf16")
+        check_rows(yk.double().cpu().numpy(), wide(host[1]), wide(wk), at, freq, False, 1e-6, "bf16")
+
+
 # ---- into the cache ----
 
 def check_append(ss, tokens, hq, hk, dim, rot, kind, cache, page=16, layout="hnd", interleaved=False, skip=(), scales=True, seed=41):
