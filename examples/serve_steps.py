@@ -41,7 +41,7 @@ def make_cache(kind, pages, heads, page, dim):
 
 def run(batch=64, heads=8, group=4, dim=128, page=16, prompt=1000, steps=300, ends=0.01, cache="e2m1", seed=0):
     gen, rng, hidden = torch.Generator(device="cuda").manual_seed(seed), random.Random(seed), 512
-    width = -(-(prompt + steps) // page)
+    width = -(-(prompt + 1 + steps) // page)  # a prompt, the step before the capture, the replays
     pool = make_cache(cache, batch * width, heads, page, dim)
     i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
     seqs = ss.KVTable(i32(batch, width), i32(batch))

@@ -244,3 +244,22 @@ def test_example_serves_requests(cache):
     got = example.run(batch=5, heads=2, group=2, dim=64, prompt=70, steps=40, ends=0.05, cache=cache)
     assert got["device_lens"] == got["lens"] and got["finite"] and got["ended"] > 0
     assert got["free"] == got["pages"] - sum(-(-n // got["page"]) for n in got["lens"])
+
+
+def load_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_steps.py")
+    spec = importlib.util.spec_from_file_location("serve_steps", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    return example
+
+
+@pytest.mark.parametrize("prompt,steps", [(1, 14), (1, 15), (1, 16), (2, 30)])
+def test_example_has_room_for_its_longest_request(prompt, steps):
+    """A prompt, the step before the capture and every replay add a token to a
+    request that never ends, and its last page may be full."""
+    got = load_example().run(batch=3, heads=2, group=2, dim=64, prompt=prompt, steps=steps, ends=0.0, cache="bf16")
+    assert got["device_lens"] == got["lens"] and got["finite"] and max(got["lens"]) <= prompt + 1 + steps
+    assert got["free"] == got["pages"] - sum(-(-n // got["page"]) for n in got["lens"])
