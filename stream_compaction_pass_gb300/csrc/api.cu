@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -541,16 +542,39 @@ ss_status rows_arg(const ss_rows* in, const char* name, int64_t tokens, int head
     return SS_OK;
 }
 
-// Whether two row tensors share memory: their ranges do, and they are not
-// columns of one buffer beside each other.
+// Whether a row that lies x behind another one meets it, or does for any two of
+// their tokens (whose rows are `step` apart).
+bool rows_meet(int64_t x, int64_t step, int64_t tokens, int64_t row) {
+    const int64_t near = step > 0 ? x / step : 0;
+    for (int64_t m = near - 1; m <= near + 1; ++m)
+        if (m > -tokens && m < tokens && std::abs(x - m * step) < row) return true;
+    return false;
+}
+
+// Whether two row tensors share memory.  Of tensors whose ranges do, those of one
+// token stride may still be columns of one buffer beside each other, or lie between
+// each other's heads (as q and k of a [head][q, k, v] projection); others are said to.
 bool rows_clash(const ss_rows& a, int a_heads, const ss_rows& b, int b_heads, int64_t tokens, int dim, int size) {
     if (a_heads == 0 || b_heads == 0) return false;
     if (!overlaps(a.data, rows_bytes(a, tokens, a_heads, dim, size), b.data, rows_bytes(b, tokens, b_heads, dim, size))) return false;
-    if (tokens == 1 || a.token_stride != b.token_stride || a.token_stride == 0) return true;
-    const int64_t step = a.token_stride * size, a_span = (int64_t)rows_bytes(a, 1, a_heads, dim, size), b_span = (int64_t)rows_bytes(b, 1, b_heads, dim, size);
-    int64_t d = ((int64_t)reinterpret_cast<intptr_t>(b.data) - (int64_t)reinterpret_cast<intptr_t>(a.data)) % step;
-    if (d < 0) d += step;
-    return d < a_span || d + b_span > step;
+    if (a.token_stride != b.token_stride) return true;
+    const int64_t step = a.token_stride * size, row = (int64_t)dim * size, a_head = a.head_stride * size, b_head = b.head_stride * size;
+    const int64_t apart = (int64_t)reinterpret_cast<intptr_t>(b.data) - (int64_t)reinterpret_cast<intptr_t>(a.data);
+    if (tokens > 1 && step > 0) {  // columns: a span of a, then one of b
+        int64_t d = apart % step;
+        if (d < 0) d += step;
+        if (d >= (int64_t)rows_bytes(a, 1, a_heads, dim, size) && d + (int64_t)rows_bytes(b, 1, b_heads, dim, size) <= step) return false;
+    }
+    if (a_head == b_head) {
+        for (int64_t h = 1 - a_heads; h < b_heads; ++h)
+            if (rows_meet(apart + h * a_head, step, tokens, row)) return true;
+        return false;
+    }
+    if ((int64_t)a_heads * b_heads > 1 << 12) return true;  // rather than look at every pair
+    for (int64_t i = 0; i < a_heads; ++i)
+        for (int64_t j = 0; j < b_heads; ++j)
+            if (rows_meet(apart + j * b_head - i * a_head, step, tokens, row)) return true;
+    return false;
 }
 bool same_rows(const ss_rows& a, const ss_rows& b) { return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride; }
 

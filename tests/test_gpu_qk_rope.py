@@ -186,6 +186,61 @@ def test_rows_of_zeros_infinities_and_nan(ss):
     assert bad[2, 2] and bad.sum() == 2  # inf / inf, and 0 for its row's others or NaN with it
 
 
+def interleaved_rows(tokens, heads, dim, kind, seed, layout):
+    """q, k and v of as many heads, beside each other in every head of one buffer."""
+    import torch
+    gen = torch.Generator().manual_seed(seed)
+    host = torch.randn(tokens, heads, 3, dim, generator=gen).to(kind_of(kind))
+    if layout == "token":  # [token][head][q, k, v]
+        dev = host.cuda()
+    elif layout == "head":  # [head][q, k, v][token]
+        dev = host.permute(1, 2, 0, 3).contiguous().cuda().permute(2, 0, 1, 3)
+    else:  # the same in rows that are padded
+        dev = torch.full((tokens, heads * 3 * dim + 24), math.nan, dtype=host.dtype, device="cuda")
+        dev[:, 8:8 + heads * 3 * dim] = host.flatten(1).cuda()
+        dev = dev[:, 8:8 + heads * 3 * dim].unflatten(1, (heads, 3, dim))
+    return [host[:, :, i] for i in range(3)], [dev[:, :, i] for i in range(3)]
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 50])
+@pytest.mark.parametrize("layout", ["token", "head", "padded"])
+@pytest.mark.parametrize("heads", [1, 5])
+def test_rows_beside_each_other_in_every_head(ss, tokens, layout, heads):
+    """Rows that share no memory, though their ranges do, are taken in place."""
+    import torch
+    dim, kind = 64, "bf16"
+    host, (q, k, v) = interleaved_rows(tokens, heads, dim, kind, 61, layout)
+    w = weights(dim, kind, 62)
+    freq = frequencies(dim)
+    rope = ss.Rope(torch.from_numpy(freq).cuda())
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    ss.ss_qk_norm_rope(q, k, w[0].cuda(), w[1].cuda(), rope, pos, q, k)
+    ok(ss)
+    at = np.arange(tokens)
+    for x, y, wi in ((q, host[0], w[0]), (k, host[1], w[1])):
+        check_rows(x.double().cpu().numpy(), wide(y), wide(wi), at, freq, False, 1e-6, kind)
+    assert torch.equal(v.cpu(), host[2])
+    # the gradients, in place of the gradients of the outputs, which lie as the inputs do
+    _, (gq, gk, _) = interleaved_rows(tokens, heads, dim, kind, 63, layout)
+    _, (xq, xk, _) = interleaved_rows(tokens, heads, dim, kind, 61, layout)
+    apart = [torch.empty(tokens, heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dws = [torch.empty(dim, device="cuda") for _ in range(4)]
+    call = lambda dq, dk, dw: ss.ss_qk_norm_rope_backward(gq, gk, xq, xk, w[0].cuda(), w[1].cuda(), rope, pos, dq, dk, *dw)  # noqa: E731
+    call(*apart, dws[:2])
+    call(gq, gk, dws[2:])
+    ok(ss)
+    assert torch.equal(gq, apart[0]) and torch.equal(gk, apart[1]) and torch.equal(dws[0], dws[2]) and torch.equal(dws[1], dws[3])
+    # queries in place, keys and values into a cache
+    _, (q, k, v) = interleaved_rows(tokens, heads, dim, kind, 61, layout)
+    pool = [torch.zeros(4, heads, 16, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ss.ss_kv_append_rope(ss.KVPages(*pool), torch.arange(tokens, device="cuda"), q, k, v, w[0].cuda(), w[1].cuda(), rope, pos, q)
+    ok(ss)
+    check_rows(q.double().cpu().numpy(), wide(host[0]), wide(w[0]), at, freq, False, 1e-6, kind)
+    rows = [x.transpose(1, 2).reshape(64, heads, dim)[:tokens] for x in pool]
+    check_rows(rows[0].double().cpu().numpy(), wide(host[1]), wide(w[1]), at, freq, False, 1e-6, kind)
+    assert torch.equal(rows[1].cpu(), host[2]) and torch.equal(k.cpu(), host[1])
+
+
 # ---- gradients ----
 
 def check_backward(ss, tokens, hq, hk, dim, rot, kind, interleaved=False, layout="packed", eps=1e-6, weighted=True, in_place=None, seed=11, positions=None, stream=None):

@@ -123,6 +123,23 @@ def test_rotation_outputs(lib, bad):
     assert forward(lib, **bad) == INV
 
 
+@pytest.mark.parametrize("bad", [
+    # [token][head][q, k, v] of 2 heads of 64 (192 elements a head): k_out on q, across q and k, and behind the last one's row on the next token's q
+    dict(q_heads=2, q=(0x100000, 384, 192), k=(0x100080, 384, 192), q_out=(0x100000, 384, 192), k_out=(0x100000, 384, 192)),
+    dict(q_heads=2, q=(0x100000, 384, 192), k=(0x100080, 384, 192), q_out=(0x100000, 384, 192), k_out=(0x1000c0, 384, 192)),
+    dict(q_heads=2, q=(0x100000, 384, 192), k=(0x100080, 384, 192), q_out=(0x100000, 384, 192), k_out=(0x100140, 384, 192)),
+    dict(q_heads=2, q=(0x100000, 384, 192), k=(0x100080, 384, 192), q_out=(0x100080, 384, 192)),
+    # [head][q, k][token] of 3 tokens: k_out on the last token's q
+    dict(q_heads=2, q=(0x100000, 64, 384), k=(0x100180, 64, 384), q_out=(0x100000, 64, 384), k_out=(0x100100, 64, 384)),
+    # one token: rows of k between, and on, those of q
+    dict(tokens=1, q=(0x100000, 0, 128), q_out=(0x100000, 0, 128), k_out=(0x1000c0, 0, 128)),
+    # other strides, whose third token meets
+    dict(q_heads=1, kv_heads=1, q=(0x100000, 64, 64), q_out=(0x100000, 64, 64), k_out=(0x100100, 128, 64))], ids=str)
+def test_rotation_outputs_between_other_rows(lib, bad):
+    assert forward(lib, **bad) == INV
+    assert "overlaps" in ss.ss_last_error_detail()
+
+
 @pytest.mark.parametrize("bad", [dict(gq=(0, 512, 64)), dict(gk=(0x600004, 256, 64)), dict(dq=(0, 512, 64)), dict(dq=(0x500080, 512, 64)), dict(dk=(0x500000, 512, 64)),
                                  dict(dk=(0x300000, 256, 64)), dict(dqw=0x1002), dict(dqw=0x8000, dkw=0x8010)], ids=str)
 def test_rotation_gradients_arguments(lib, bad):
