@@ -42,10 +42,11 @@ def make_cache(kind, pages, heads, page, dim):
 def run(batch=64, heads=8, group=4, dim=128, page=16, prompt=1000, steps=300, ends=0.01, cache="e2m1", seed=0):
     gen, rng, hidden = torch.Generator(device="cuda").manual_seed(seed), random.Random(seed), 512
     width = -(-(prompt + 1 + steps) // page)  # a prompt, the step before the capture, the replays
-    pool = make_cache(cache, batch * width, heads, page, dim)
+    pages = batch * (width - (-2 // page))  # and the first ones of requests that take places over, whose pages come back a step later
+    pool = make_cache(cache, pages, heads, page, dim)
     i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
     seqs = ss.KVTable(i32(batch, width), i32(batch))
-    free = ss.KVFree(torch.arange(batch * width, dtype=torch.int32, device="cuda"), torch.tensor([0, batch * width], dtype=torch.int32, device="cuda"))
+    free = ss.KVFree(torch.arange(pages, dtype=torch.int32, device="cuda"), torch.tensor([0, pages], dtype=torch.int32, device="cuda"))
     rope = ss.Rope(10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64, device="cuda") / dim))
     weights = [torch.ones(dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     project = torch.randn(hidden, (group + 2) * heads * dim, generator=gen, device="cuda", dtype=torch.bfloat16) * hidden ** -0.5
@@ -101,7 +102,7 @@ def run(batch=64, heads=8, group=4, dim=128, page=16, prompt=1000, steps=300, en
         seconds = time.perf_counter() - t0
     status, where = ss.ss_stream_status(side)
     assert status == ss.SS_OK, (status, where, ss.ss_last_error_detail())
-    return {"lens": lens, "device_lens": seqs.lens.tolist(), "free": int(free.state[1]), "pages": batch * width, "page": page, "ended": served,
+    return {"lens": lens, "device_lens": seqs.lens.tolist(), "free": int(free.state[1]), "pages": pages, "page": page, "ended": served,
             "us_per_step": seconds / max(steps, 1) * 1e6, "finite": bool(torch.isfinite(out.float()).all())}
 
 

@@ -263,3 +263,15 @@ def test_example_has_room_for_its_longest_request(prompt, steps):
     got = load_example().run(batch=3, heads=2, group=2, dim=64, prompt=prompt, steps=steps, ends=0.0, cache="bf16")
     assert got["device_lens"] == got["lens"] and got["finite"] and max(got["lens"]) <= prompt + 1 + steps
     assert got["free"] == got["pages"] - sum(-(-n // got["page"]) for n in got["lens"])
+
+
+@pytest.mark.parametrize("page,steps,seed", [(16, 16, 64), (1, 6, 5)])
+def test_example_has_pages_for_a_request_that_takes_a_place_over(page, steps, seed):
+    """The one request ends at the last step, when it holds all but none or one of
+    the pages that its table has places for; they come back after that step."""
+    ends = random.Random(seed)
+    ends.randrange(1, 2)  # the prompt
+    assert [ends.random() < 0.05 for _ in range(steps)] == [False] * (steps - 1) + [True]
+    got = load_example().run(batch=1, heads=2, group=2, dim=64, page=page, prompt=1, steps=steps, ends=0.05, cache="bf16", seed=seed)
+    assert got["device_lens"] == got["lens"] == [2]
+    assert got["free"] == got["pages"] - -(-2 // page)
