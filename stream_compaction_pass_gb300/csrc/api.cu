@@ -526,6 +526,15 @@ size_t rows_bytes(const ss_rows& r, int64_t tokens, int heads, int dim, int size
     return (size_t)((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + dim) * size;
 }
 
+// Whether a row that lies x behind another one meets it, or does for any two of
+// their tokens (whose rows are `step` apart).
+bool rows_meet(int64_t x, int64_t step, int64_t tokens, int64_t row) {
+    const int64_t near = step > 0 ? x / step : 0;
+    for (int64_t m = near - 1; m <= near + 1; ++m)
+        if (m > -tokens && m < tokens && std::abs(x - m * step) < row) return true;
+    return false;
+}
+
 // Rows (token, head) of one tensor: null where it has no heads.  Strides that
 // nothing steps by become 0.
 ss_status rows_arg(const ss_rows* in, const char* name, int64_t tokens, int heads, int dim, int size, bool written, ss_rows* out) {
@@ -537,18 +546,13 @@ ss_status rows_arg(const ss_rows* in, const char* name, int64_t tokens, int head
     for (const int64_t x : {out->token_stride, out->head_stride})
         if (x < 0 || x % (16 / size) || x > 1ll << 33)
             return fail(SS_ERR_INVALID_ARG, std::string(name) + ": strides must be non-negative multiples of 16 bytes, at most 2^33 elements");
-    if (written && ((tokens > 1 && out->token_stride < dim) || (heads > 1 && out->head_stride < dim)))
-        return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
+    if (!written) return SS_OK;
+    const int64_t span = (heads - 1) * out->head_stride + dim;  // of a token
+    if ((heads == 1 || out->head_stride >= dim) && (tokens == 1 || out->token_stride >= span)) return SS_OK;
+    bool meet = tokens > 1 && out->token_stride < dim;
+    for (int64_t h = 1; h < heads && !meet; ++h) meet = rows_meet(h * out->head_stride, out->token_stride, tokens, dim);
+    if (meet) return fail(SS_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
     return SS_OK;
-}
-
-// Whether a row that lies x behind another one meets it, or does for any two of
-// their tokens (whose rows are `step` apart).
-bool rows_meet(int64_t x, int64_t step, int64_t tokens, int64_t row) {
-    const int64_t near = step > 0 ? x / step : 0;
-    for (int64_t m = near - 1; m <= near + 1; ++m)
-        if (m > -tokens && m < tokens && std::abs(x - m * step) < row) return true;
-    return false;
 }
 
 // Whether two row tensors share memory.  Of tensors whose ranges do, those of one

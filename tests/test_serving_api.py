@@ -140,6 +140,16 @@ def test_rotation_outputs_between_other_rows(lib, bad):
     assert "overlaps" in ss.ss_last_error_detail()
 
 
+@pytest.mark.parametrize("out", [(0x300000, 96, 64), (0x300000, 64, 96), (0x300000, 64, 64), (0x300000, 64, 128), (0x300000, 128, 64), (0x300000, 120, 160)], ids=str)
+def test_rotation_outputs_whose_own_rows_meet(lib, out):
+    """Each stride reaches past a row, but a token's rows meet another's."""
+    shape = dict(q_heads=3, kv_heads=3, q=(0x100000, 192, 64), k=(0x200000, 192, 64), k_out=(0x400000, 192, 64))
+    for call in (lambda **kw: forward(lib, q_out=out, **kw), lambda **kw: forward(lib, **{**kw, "q_out": (0x500000, 192, 64), "k_out": out}),
+                 lambda **kw: backward(lib, gq=(0x600000, 192, 64), gk=(0x700000, 192, 64), dq=out, dk=(0x800000, 192, 64), **{k: v for k, v in kw.items() if k != "k_out"})):
+        assert call(**shape) == INV
+        assert "overlap" in ss.ss_last_error_detail()
+
+
 @pytest.mark.parametrize("bad", [dict(gq=(0, 512, 64)), dict(gk=(0x600004, 256, 64)), dict(dq=(0, 512, 64)), dict(dq=(0x500080, 512, 64)), dict(dk=(0x500000, 512, 64)),
                                  dict(dk=(0x300000, 256, 64)), dict(dqw=0x1002), dict(dqw=0x8000, dkw=0x8010)], ids=str)
 def test_rotation_gradients_arguments(lib, bad):
