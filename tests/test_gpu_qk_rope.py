@@ -543,3 +543,128 @@ def test_append_slots_behind_the_pool_are_reported(ss):
         ss.ss_kv_append_rope(ss.KVPages(*pool), slots, q, k, v, None, None, rope, pos, torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda"))
         assert ss.ss_stream_status() == (ss.SS_ERR_INVALID_ARG, 2)
         assert torch.equal((pool[1] != 0).any(-1).flatten().nonzero().flatten().cpu(), torch.tensor([0, 5, 47]))
+
+
+# ---- more rows than a CTA's tables hold ----
+
+# A CTA of 128 threads has 128 / L groups, L = 16 lanes a row of 256, 8 of 128, 4 of 64, and
+# every group a row a step.  The tables are filled again after min(32, heads) steps
+# (backward min(16, heads)).  No SM holds more than 16 such CTAs, and no call launches more
+# than four waves of them, backward one of four an SM.
+
+def least_steps(rows, dim, ctas_per_sm):
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    lanes = {64: 4, 128: 8, 256: 16}[dim]
+    return rows / (sms * ctas_per_sm * (128 // lanes))
+
+
+def large_rows(tokens, heads, dim, kind, seed):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return [torch.randn(tokens, h, dim, generator=gen, device="cuda").to(kind_of(kind)) for h in heads]
+
+
+@pytest.mark.parametrize("tokens,hq,hk,dim,kind", [(170_000, 33, 5, 128, "bf16"), (230_000, 3, 1, 128, "f16"), (120_000, 3, 2, 256, "f32")])
+def test_forward_of_more_rows_than_the_tables_hold(ss, tokens, hq, hk, dim, kind):
+    """The rows of one large call are those of calls of 999 tokens, which fill the tables
+    once, bit by bit; some are compared with the formula."""
+    import torch
+    assert least_steps(tokens * (hq + hk), dim, 64) > min(32, hq)
+    q, k = large_rows(tokens, (hq, hk), dim, kind, 81)
+    w = [x.cuda() for x in weights(dim, kind, 82)]
+    freq = frequencies(dim)
+    rope = ss.Rope(torch.from_numpy(freq).cuda())
+    pos = (torch.arange(tokens, device="cuda") * 7919 % 100_003).to(torch.int32)
+    yq, yk = torch.full_like(q, math.nan), torch.full_like(k, math.nan)
+    ss.ss_qk_norm_rope(q, k, *w, rope, pos, yq, yk)
+    pq, pk = torch.full_like(q, math.nan), torch.full_like(k, math.nan)
+    for t in range(0, tokens, 999):
+        s = slice(t, t + 999)
+        ss.ss_qk_norm_rope(q[s], k[s], *w, rope, pos[s], pq[s], pk[s])
+    ok(ss)
+    assert torch.equal(yq, pq) and torch.equal(yk, pk)
+    some = torch.arange(0, tokens, 997, device="cuda")
+    at = pos[some].cpu().numpy()
+    for x, y, wi in ((q, yq, w[0]), (k, yk, w[1])):
+        check_rows(y[some].double().cpu().numpy(), x[some].double().cpu().numpy(), wi.double().cpu().numpy(), at, freq, False, 1e-6, kind)
+
+
+@pytest.mark.parametrize("tokens,hq,hk,dim,kind", [(20_000, 32, 8, 64, "bf16"), (30_000, 33, 5, 128, "f16"), (60_000, 3, 1, 128, "bf16"), (30_000, 3, 2, 256, "f32")])
+def test_backward_of_more_rows_than_the_tables_hold(ss, tokens, hq, hk, dim, kind):
+    """The gradients of the rows are those of calls of 99 tokens, bit by bit.  Those of the
+    weights are the formula's sums, whose terms meet the rows of a group (below N / 5000 of
+    N rows here, 32 groups or fewer), 32 groups, 32 shares of CTAs and 5 of a warp."""
+    import torch
+    assert least_steps(tokens * (hq + hk), dim, 4) > min(16, hq)
+    q, k = large_rows(tokens, (hq, hk), dim, kind, 83)
+    gq, gk = large_rows(tokens, (hq, hk), dim, kind, 84)
+    w = [x.cuda() for x in weights(dim, kind, 85)]
+    freq = frequencies(dim)
+    rope = ss.Rope(torch.from_numpy(freq).cuda())
+    pos = (torch.arange(tokens, device="cuda") * 7919 % 100_003).to(torch.int32)
+    dq, dk = torch.full_like(q, math.nan), torch.full_like(k, math.nan)
+    dw = [torch.full((dim,), math.nan, device="cuda") for _ in range(2)]
+    ss.ss_qk_norm_rope_backward(gq, gk, q, k, *w, rope, pos, dq, dk, *dw)
+    pq, pk = torch.full_like(q, math.nan), torch.full_like(k, math.nan)
+    for t in range(0, tokens, 99):
+        s = slice(t, t + 99)
+        ss.ss_qk_norm_rope_backward(gq[s], gk[s], q[s], k[s], *w, rope, pos[s], pq[s], pk[s])
+    ok(ss)
+    assert torch.equal(dq, pq) and torch.equal(dk, pk)
+    half, n = dim // 2, (dim / 2 + 8) * E
+    for x, g, got, h in ((q, gq, dw[0], hq), (k, gk, dw[1], hk)):
+        want, terms, off = (torch.zeros(dim, dtype=torch.float64, device="cuda") for _ in range(3))
+        for t in range(0, tokens, 4096):
+            s = slice(t, t + 4096)
+            u = x[s].double()
+            u = u / (u.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+            angle = (pos[s].double()[:, None] * torch.from_numpy(freq).cuda())[:, None]
+            z = torch.complex(g[s][..., :half].double(), g[s][..., half:].double()) * torch.exp(-1j * angle)
+            hh = torch.cat([z.real, z.imag], -1)
+            want += (u * hh).sum((0, 1))
+            terms += (u * hh).abs().sum((0, 1))
+            pair = g[s][..., :half].double().abs() + g[s][..., half:].double().abs()
+            error = (angle_error(kind) + 2.0 ** -51 * angle.abs().amax(-1, keepdim=True) + 4 * E) * torch.cat([pair, pair], -1)
+            off += (u.abs() * error).sum((0, 1))
+        tol = off + n * terms + (100 + tokens * h / 5000) * E * terms
+        assert bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "e2m1"])
+@pytest.mark.parametrize("tokens,hq,hk", [(75_000, 3, 1), (53_000, 1, 3)])
+def test_append_of_more_rows_than_the_tables_hold(ss, cache, tokens, hq, hk):
+    """The queries and the cache of one large call, some of whose tokens go nowhere, are
+    those of calls of 999 tokens, bit by bit."""
+    import torch
+    dim, page = 128, 16
+    assert least_steps(tokens * (hq + 2 * hk), dim, 48) > min(32, max(hq, hk))
+    q, k, v = large_rows(tokens, (hq, hk, hk), dim, "bf16", 86)
+    w = [x.cuda() for x in weights(dim, "bf16", 87)]
+    rope = ss.Rope(torch.from_numpy(frequencies(dim)).cuda())
+    pos = (torch.arange(tokens, device="cuda") * 7919 % 100_003).to(torch.int32)
+    pages_n = -(-tokens // page) + 3
+    gen = torch.Generator(device="cuda").manual_seed(88)
+    slots = torch.randperm(pages_n * page, generator=gen, device="cuda")[:tokens]
+    slots[::7] = -1
+    scale = torch.full((hk,), 1 / 32 if cache == "e4m3" else 1.0, device="cuda")
+
+    def run(step):
+        shape = (pages_n, hk, page)
+        size = {"bf16": 2 * dim, "e4m3": dim, "e2m1": dim // 2}[cache]
+        held = [torch.full((*shape, size), 0x3a, dtype=torch.uint8, device="cuda") for _ in range(2)] + [torch.full(shape, 2.5, device="cuda")]
+        if cache == "e2m1":
+            held += [torch.full((*shape, dim // 16), 0x33, dtype=torch.uint8, device="cuda") for _ in range(2)]
+            pages = ss.KVPages(*held[:2], weight=held[2], k_scale=scale, v_scale=scale, k_block=held[3].view(torch.float8_e4m3fn), v_block=held[4].view(torch.float8_e4m3fn))
+        else:
+            scales = dict(k_scale=scale, v_scale=scale) if cache == "e4m3" else {}
+            pages = ss.KVPages(*(x.view(torch_type(cache)) for x in held[:2]), weight=held[2], **scales)
+        y = torch.full_like(q, math.nan)
+        for t in range(0, tokens, step):
+            s = slice(t, t + step)
+            ss.ss_kv_append_rope(pages, slots[s], q[s], k[s], v[s], *w, rope, pos[s], y[s])
+        ok(ss)
+        return [y, *held]
+
+    for large, small in zip(run(tokens), run(999)):
+        assert torch.equal(large, small)
