@@ -184,3 +184,48 @@ def angle_error(kind):
     """How far the sine or cosine of an angle may be off: that of 2^-24 of half a
     turn and two units of fp32, or the 2^-20 of the approximations that 16-bit rows take."""
     return math.pi * 2.0 ** -24 + 2.0 ** -22 if kind == "f32" else 2.0 ** -20
+
+
+class QuarterTurns:
+    """Rows of which the first half becomes small: pairs (+-w, 0) turned by nearly a
+    quarter, whose cosines, 2^-8 to 2^-19, take angles that are good to far more than
+    fp32 holds of them.  Elements are +-1, so that the norm of 2^k of them is 1 in any
+    precision, and the weights of the other halves 0."""
+
+    POSITIONS = np.array([1, -1, 3, -3, 5, -7, 9, 1])
+
+    def __init__(self, tokens, heads, dim, seed):
+        rng = np.random.default_rng(seed)
+        half = dim // 2
+        self.x = rng.choice([-1.0, 1.0], (tokens, heads, dim))
+        self.weight = np.concatenate([1 + rng.integers(0, 128, half) / 128, np.zeros(half)])
+        blocks = np.linspace(-8, -19, half // 16)  # of about one size each, for a block's scale
+        self.freq = np.pi / 2 - 2.0 ** np.repeat(blocks, 16) * (1 + np.tile(np.arange(16), half // 16) / 32)
+        self.positions = self.POSITIONS[np.arange(tokens) % len(self.POSITIONS)]
+
+    def rows(self, angle=lambda x: x):
+        """Rows of k, their angles passed through `angle`."""
+        a = angle(self.positions[:, None] * self.freq)[:, None]
+        u = (self.x * self.weight)[..., :len(self.freq)]
+        return np.concatenate([u * np.cos(a), u * np.sin(a)], -1)
+
+
+def e4m3_between(got, y, error):
+    """Whether every e4m3 value is that of a number within a factor 1 +- error of y."""
+    return (e4m3_reference(y - error * np.abs(y)) <= got) & (got <= e4m3_reference(y + error * np.abs(y)))
+
+
+def codes_between(codes, blocks, y, error):
+    """The same of e2m1 codes with their blocks' scales; NaN-free rows of numbers."""
+    most = np.abs(y).reshape(*blocks.shape, 16).max(-1)
+    b = e4m3_value(blocks)
+    cut = lambda x: e4m3_reference(np.minimum(x / 6, 448.0))  # noqa: E731
+    good = (cut(most * (1 - error)) <= b) & (b <= cut(most * (1 + error)))
+    got = np.abs(np.stack([e2m1_value(codes & 15), e2m1_value(codes >> 4)], -1).reshape(y.shape))
+    z = np.abs(y) / np.repeat(b, 16, -1)
+
+    def nearest(a, up):  # of the codes beside it the nearer one; at a tie the higher or lower one
+        middle = (E2M1[1:] + E2M1[:-1]) / 2
+        return E2M1[np.searchsorted(middle, a, side="right" if up else "left")]
+
+    return (nearest(z * (1 - error), False) <= got) & (got <= nearest(z * (1 + error), True)) & np.repeat(good, 16, -1)

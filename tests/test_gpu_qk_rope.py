@@ -545,6 +545,42 @@ def test_append_slots_behind_the_pool_are_reported(ss):
         assert torch.equal((pool[1] != 0).any(-1).flatten().nonzero().flatten().cpu(), torch.tensor([0, 5, 47]))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("cache", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_append_of_keys_turned_by_nearly_a_quarter(ss, kind, cache, dim):
+    """Narrow caches take sines and cosines of fp32, of angles that are good to more.
+    The norm is 1 and the partner 0, so that a key is w cos: off by two units of the
+    cosine (2^-22 of it), the angle's remainder in fp32 (2^-24 times 2^-25 / 2^-19 of it,
+    and its derivative's 2^-22), the product, the scale's division or inverse and
+    product: below 2^-20 of it.  An angle in fp32, 2^-25, is 2^-6 of a cosine of 2^-19."""
+    import torch
+    from serving_helpers import QuarterTurns, codes_between, e4m3_between, e4m3_value
+    tokens, heads, page = 203, 3, 16
+    rows = QuarterTurns(tokens, heads, dim, 71)
+    k = torch.from_numpy(rows.x).to(kind_of(kind)).cuda()
+    w = torch.from_numpy(rows.weight).to(kind_of(kind)).cuda()
+    rope = ss.Rope(torch.from_numpy(rows.freq).cuda())
+    pos = torch.from_numpy(rows.positions.astype(np.int32)).cuda()
+    pages_n = -(-tokens // page)
+    scale = torch.full((heads,), 2.0 ** -16, device="cuda")
+    size = dim if cache == "e4m3" else dim // 2
+    kc, vc = (torch.zeros(pages_n, heads, page, size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    if cache == "e4m3":
+        pages = ss.KVPages(kc.view(torch.float8_e4m3fn), vc.view(torch.float8_e4m3fn), k_scale=scale, v_scale=scale)
+    else:
+        kb, vb = (torch.zeros(pages_n, heads, page, dim // 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+        pages = ss.KVPages(kc, vc, k_scale=scale, v_scale=scale, k_block=kb.view(torch.float8_e4m3fn), v_block=vb.view(torch.float8_e4m3fn))
+    ss.ss_kv_append_rope(pages, torch.arange(tokens, device="cuda"), None, k, k, None, w, rope, pos, None, eps=0.0)
+    ok(ss)
+    y = rope_reference(rows.x, rows.weight, rows.positions, rows.freq, False, 0.0) * 2.0 ** 16
+    read = lambda x: x.cpu().numpy().swapaxes(1, 2).reshape(pages_n * page, heads, -1)[:tokens]  # noqa: E731
+    if cache == "e4m3":
+        assert e4m3_between(e4m3_value(read(kc)), y, 2.0 ** -20).all()
+    else:
+        assert codes_between(read(kc), read(kb), y, 2.0 ** -20).all()
+
+
 # ---- more rows than a CTA's tables hold ----
 
 # A CTA of 128 threads has 128 / L groups, L = 16 lanes a row of 256, 8 of 128, 4 of 64, and

@@ -9,8 +9,8 @@ import pytest
 
 import stream_compaction_pass_gb300 as ss
 from kv_helpers import e4m3_reference
-from serving_helpers import (E2M1, assign_reference, e2m1_value, e4m3_value, frequencies, open4, quantise4, rope_gradients, rope_reference,
-                             turn_reference)
+from serving_helpers import (E2M1, QuarterTurns, assign_reference, codes_between, e2m1_value, e4m3_between, e4m3_value, frequencies, open4, quantise4,
+                             rope_gradients, rope_reference, turn_reference)
 
 INV, UNS = ss.SS_ERR_INVALID_ARG, ss.SS_ERR_UNSUPPORTED
 
@@ -297,3 +297,23 @@ def test_rope_reference(interleaved):
         v = np.zeros(24)
         v[i[2]] = 1e-5
         assert abs((f(x, w + v) - f(x, w - v)) / 2e-5 - dw[i[2]]) < 1e-7
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_rows_turned_by_a_quarter_show_angles_of_fp32(dim):
+    """What the GPU's caches are held to: the formula's rows pass, also with fp32
+    roundings of the cosines; those of angles in fp32, or of cosines off by 2^-21, do not."""
+    rows = QuarterTurns(40, 3, dim, 5)
+    y = rope_reference(rows.x, rows.weight, rows.positions, rows.freq, False, 0.0)
+    assert np.allclose(y, rows.rows(), rtol=1e-9, atol=0)
+    s = 2.0 ** -16
+    rng = np.random.default_rng(6)
+    fine = rows.rows() * (1 + rng.uniform(-1, 1, y.shape) * 2.0 ** -21)
+    rounded = rows.rows(lambda x: x.astype(np.float32).astype(np.float64))
+    near = rows.rows() + rng.uniform(-1, 1, y.shape) * 2.0 ** -21
+    for z, good in ((fine, True), (rounded, False), (near, False)):
+        got = e4m3_between(e4m3_reference(np.clip(z / s, -448, 448)), y / s, 2.0 ** -20)
+        assert got.all() == good, got.mean()
+        codes, blocks = quantise4(z, np.full(3, s, np.float32))
+        got = codes_between(codes, blocks, y / s, 2.0 ** -20)
+        assert got.all() == good, got.mean()
