@@ -393,7 +393,12 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  * interleaved, i < r/2, by the angle of position p, and leaves elements from r =
  * rotary_dim on as they are:  (a, b) -> (a cos - b sin, b cos + a sin).  Angles
  * are p * turns[i] / 2^64 turns modulo 1, exact for every p; sums and products
- * are fp32, and y is rounded once.
+ * are fp32, and y is rounded once.  Sines and cosines of SS_ELEM_F32 rows, and of
+ * k's on their way into an SS_E4M3 or SS_E2M1 cache, are good to 2^-22 of their own
+ * value, and the reciprocal root to half a unit in the last place; those of other
+ * rows to 2^-20 (absolute, of pairs whose lengths are 1) and to two units, so that
+ * where a cos and b sin nearly cancel an SS_F16 output may be off by more than its
+ * rounding.
  *   type       of q, k and the outputs: SS_BF16, SS_F16 or SS_ELEM_F32.
  *   q, k       rows (token, head) of head_dim consecutive elements; strides in
  *              elements, multiples of 16 bytes, at most 2^33, 16-byte aligned.
@@ -401,7 +406,9 @@ ss_status ss_kv_assign(const ss_kv_table *seqs, const ss_kv_table *into, int32_t
  *   q_weight, k_weight  device, head_dim numbers of weight_type (SS_BF16, SS_F16
  *              or SS_ELEM_F32), or NULL: ones.
  *   positions  device, a token each; may be negative.
- *   q_out, k_out  each is its own input's rows, or shares no memory with either.
+ *   q_out, k_out  each is its own input's rows, or shares no memory with either
+ *              (rows may lie between each other's; tensors of two token strides whose
+ *              ranges meet are taken for overlapping).
  *   head_dim a multiple of 8, at most 256; rotary_dim a positive multiple of 16,
  *   at most head_dim.  tokens == 0 is a no-op.  The call takes no scratch and may be
  *   the first one on a stream that is being captured.

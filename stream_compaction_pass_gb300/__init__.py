@@ -731,7 +731,8 @@ class Rope:
     """The rotation's frequencies (ss_rope).
 
     inv_freq     the angles of one position in radians, (rotary_dim / 2,), on the
-                 GPU; best float64, as far positions multiply its error.
+                 GPU; best float64, as far positions multiply its error.  What is
+                 derived from it is made on the current stream.
     interleaved  pairs are adjacent elements (else rotary_dim / 2 apart).
     """
 

@@ -3,10 +3,11 @@
 // one to e2m1 with a scale of every 16 elements beside it.  Bound by memory: each
 // row is read once and written once.  A CTA takes a few (token, head) rows: one
 // thread a row finds its page and slot, then all threads move 16-byte vectors of
-// the result, every load issued before the first store.  108 thousand tokens of 8
-// heads of 128, bf16 to e4m3: 62 us, 0.84 of the copy rate (96 with a look-up for
-// every 64 rows, 102 with IEEE divisions, which made it instruction-bound); to e2m1,
-// 19 % fewer bytes and more instructions, 63.8 us, 0.82; 64 tokens 2.5 us.
+// the result, every load issued before the first store.  57,382 tokens of 8 heads
+// of 128, bf16 to e4m3: 62 us, 0.84 of the copy rate (96 with a look-up for every 64
+// rows, 102 with IEEE divisions, which made it instruction-bound); to e2m1, 15 % fewer
+// bytes and more instructions (issued in 71 % of the cycles, with 28 warps an SM
+// waiting for loads), 63.2 us, 0.71; 64 tokens 2.5 us.
 #include "kv_quant.cuh"
 
 namespace ss {

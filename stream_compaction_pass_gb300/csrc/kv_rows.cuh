@@ -1,6 +1,6 @@
-// kv_rows.cuh -- one unit of query heads against tiles of 16 or 32 positions:
+// kv_rows.cuh -- one unit of query heads against tiles of 16, 32 or 64 positions:
 // the products, the running softmax and the outputs of the attention kernel
-// (kv_attend.cu), in two forms.
+// (kv_attend.cuh), in two forms.
 //
 //   Rows16  query heads are the rows of the products: X = Q K^T is two m16n8
 //           products per 16 of head_dim and 16 positions, O += P V.  For groups
@@ -275,8 +275,8 @@ template <typename QT> __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t
 // 4-bit rows.  A code is opened by its conversion to fp16 and one multiplication by
 // its block's scale; keys in pairs of dimensions, as they lie, values in pairs of
 // positions, whose nibbles are put side by side first (4 instructions for 16).  That
-// makes 10 instructions for the 16 codes that one product takes of a lane's rows,
-// and 1170 a tile of 64 positions x 128, half of them these: 5.8 TB/s of 6.8.
+// makes 8 and 10 instructions for the 8 codes that one product takes of a lane's rows,
+// 576 of the 1254 of a tile of 64 positions x 128: 5.2 TB/s of 6.8.
 //
 // O is added up in the products' accumulators, which cut what falls below 24
 // bits instead of rounding it: an error of one sign, up to 2^-24 a product.  So
@@ -534,7 +534,7 @@ template <typename QT, int BITS, int DP, int T> struct Rows16 : RowsBase<QT, BIT
             }
         }
         const bool whole = t.whole(p0, T);
-        if (BITS == 4 && whole) {  // instructions bound 4-bit tiles: no selects where nothing is hidden (477 / 445 us)
+        if (BITS == 4 && whole) {  // no selects where nothing is hidden (477 / 445 us, when P was one term)
 #pragma unroll
             for (int pt = 0; pt < kPT; ++pt)
 #pragma unroll

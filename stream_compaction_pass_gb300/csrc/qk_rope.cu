@@ -24,9 +24,11 @@
 // leaves it one set of strides and weights, and computes their tokens' sines and
 // cosines once, in shared memory; its threads copy the rows to come, each its own
 // vectors, two steps ahead (three into a cache).  bf16 rows of 128, 16384 x 40: 53.7
-// us, 0.92 of the copy rate, issuing in 80 % of the cycles; the gradients 83.8, 0.88,
-// with the 16 warps an SM that 110 registers leave; 20000 x 48 into an 8-bit cache
-// 82.2, 0.80, by quantisation's instructions, into 4 bits 91, into bf16 79, 0.91.
+// us, 0.92 of the copy rate, issuing in 82 % of the cycles; the gradients 83.8, 0.88,
+// with the 16 warps an SM that 109 registers leave; 20000 x 48 into an 8-bit cache
+// 82.3, 0.80, by quantisation's instructions, into 4 bits 91.8, 0.69, by the same (both
+// issue in 78 % of the cycles), into bf16 79, 0.91.  fp32 rows, 16384 x 40: 148 us,
+// 0.67, waiting for shared memory with the 16 warps that 100 registers leave.
 #include <algorithm>
 
 #include "kv_quant.cuh"
